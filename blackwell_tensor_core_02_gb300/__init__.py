@@ -393,3 +393,18 @@ def pipeline_trace(depth: int, initial_phase: int, steps: int) -> list[tuple[int
     if rc != 0:
         raise GemmError(rc, "gemm_f16_pipeline_trace")
     return [(st[i], ph[i]) for i in range(steps)]
+
+
+# The operators around the product of a linear layer (they need torch, as every call above does).
+_LINEAR = ("layer_norm", "layer_norm_backward", "Fp4Tensor", "quantize_fp4", "dequantize_fp4", "gemm_fp4_nt", "Fp4Options",
+           "describe_fp4", "fp4_device_status", "load_linear")
+__all__ += list(_LINEAR)
+
+
+def __getattr__(name):
+    if name in _LINEAR:
+        from . import linear
+
+        globals().update({n: getattr(linear, n) for n in _LINEAR})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

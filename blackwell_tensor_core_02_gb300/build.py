@@ -3,7 +3,9 @@
 The result is ``blackwell_tensor_core_02_gb300/_build/libgemm_f16.so``; it
 exports exactly the C ABI declared in ``include/gemm_f16.h``.  A second build
 of the same source with the device range checks compiled in
-(``-DGEMM_F16_DEVICE_CHECKS=1``), ``libgemm_f16_checked.so``, is for tests.
+(``-DGEMM_F16_DEVICE_CHECKS=1``), ``libgemm_f16_checked.so``, is for tests.  The
+operators around a linear layer's product (``csrc/linear/``) are a library of
+their own, ``liblinear_ops.so``, with the C ABI of ``include/linear_ops.h``.
 """
 from __future__ import annotations
 
@@ -20,6 +22,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libgemm_f16.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 CHECKED_LIB_PATH = os.path.join(BUILD_DIR, "libgemm_f16_checked.so")
+LINEAR_LIB_PATH = os.path.join(BUILD_DIR, "liblinear_ops.so")
+LINEAR_CSRC = os.path.join(CSRC, "linear")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,14 +39,24 @@ def sources() -> list[str]:
                   glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "gemm_f16.h")])
 
 
+def linear_sources() -> list[str]:
+    return sorted(glob.glob(os.path.join(LINEAR_CSRC, "*.cu")) + glob.glob(os.path.join(LINEAR_CSRC, "*.cuh")) +
+                  glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
+                  glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
 def is_stale(path: str = LIB_PATH) -> bool:
     if not os.path.exists(path):
         return True
     built = os.path.getmtime(path)
-    return any(os.path.getmtime(s) > built for s in sources())
+    return any(os.path.getmtime(s) > built for s in (linear_sources() if path == LINEAR_LIB_PATH else sources()))
 
 
-def _command(path: str, checked: bool, verbose: bool) -> list[str]:
+def _command(path: str, checked: bool, verbose: bool, target: str = LIB_PATH) -> list[str]:
+    if target == LINEAR_LIB_PATH:
+        return [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "--threads", "0",
+                *(["-Xptxas", "-v"] if verbose else []), "-I", INCLUDE, "-I", LINEAR_CSRC,
+                *sorted(glob.glob(os.path.join(LINEAR_CSRC, "*.cu"))), "-o", path]
     return [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
             *(["-DGEMM_F16_DEVICE_CHECKS=1"] if checked else []), *(["-Xptxas", "-v"] if verbose else []),
             "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "gemm_f16.cu"), "-o", path]
@@ -57,7 +71,7 @@ def build_many(targets: list[tuple[str, bool]], force: bool = False, verbose: bo
     procs = []
     for path, checked in todo:
         tmp = f"{path}.{os.getpid()}.tmp"
-        cmd = _command(tmp, checked, verbose)
+        cmd = _command(tmp, checked, verbose, path)
         procs.append((path, tmp, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
     errors = []
     for path, tmp, cmd, proc in procs:
@@ -79,12 +93,19 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
     return path
 
 
+def build_linear(force: bool = False, verbose: bool = False) -> str:
+    """Compile the linear layer's operators if missing or older than their sources; return the path."""
+    build_many([(LINEAR_LIB_PATH, False)], force=force, verbose=verbose)
+    return LINEAR_LIB_PATH
+
+
 def build_all(force: bool = False, verbose: bool = False) -> None:
-    """Both builds, compiled side by side."""
-    build_many([(LIB_PATH, False), (CHECKED_LIB_PATH, True)], force=force, verbose=verbose)
+    """Every library, compiled side by side."""
+    build_many([(LIB_PATH, False), (CHECKED_LIB_PATH, True), (LINEAR_LIB_PATH, False)], force=force, verbose=verbose)
 
 
 if __name__ == "__main__":
     build_all(force=True, verbose=True)
     print(LIB_PATH)
     print(CHECKED_LIB_PATH)
+    print(LINEAR_LIB_PATH)

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../ptx.cuh"
 #include "linear_ops.h"
 
@@ -44,6 +46,56 @@ struct alignas(VEC * sizeof(T)) Pack {
 // Elements of a 16-byte unit.
 template <typename T>
 constexpr int kUnit = 16 / static_cast<int>(sizeof(T));
+
+// Two values to and from their packed form, one rounding each.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<float> {
+    using Raw = float2;
+    static __device__ __forceinline__ float2 widen(Raw r) { return r; }
+    static __device__ __forceinline__ Raw narrow(float2 v) { return v; }
+};
+template <>
+struct Pair<__half> {
+    using Raw = __half2;
+    static __device__ __forceinline__ float2 widen(Raw r) { return __half22float2(r); }
+    static __device__ __forceinline__ Raw narrow(float2 v) { return __floats2half2_rn(v.x, v.y); }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+    using Raw = __nv_bfloat162;
+    static __device__ __forceinline__ float2 widen(Raw r) { return __bfloat1622float2(r); }
+    static __device__ __forceinline__ Raw narrow(float2 v) { return __floats2bfloat162_rn(v.x, v.y); }
+};
+
+// N pairs from and to consecutive memory, in 16-byte units where they fill them.
+template <typename T, int N>
+__device__ __forceinline__ void load_pairs(const T *p, float2 *v) {
+    constexpr int kPer = 2 * N * sizeof(T) > 16 ? kUnit<T> / 2 : N;  // pairs of a load
+#pragma unroll
+    for (int i = 0; i < N; i += kPer) {
+        struct alignas(kPer * sizeof(typename Pair<T>::Raw)) Unit {
+            typename Pair<T>::Raw v[kPer];
+        };
+        const Unit u = *reinterpret_cast<const Unit *>(p + 2 * i);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[i + j] = Pair<T>::widen(u.v[j]);
+    }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_pairs(T *p, const float2 *v) {
+    constexpr int kPer = 2 * N * sizeof(T) > 16 ? kUnit<T> / 2 : N;
+#pragma unroll
+    for (int i = 0; i < N; i += kPer) {
+        struct alignas(kPer * sizeof(typename Pair<T>::Raw)) Unit {
+            typename Pair<T>::Raw v[kPer];
+        } u;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) u.v[j] = Pair<T>::narrow(v[i + j]);
+        *reinterpret_cast<Unit *>(p + 2 * i) = u;
+    }
+}
 
 // A load of data that is read once: it leaves the L1 cache to what is read
 // again (the weights, which every row reads).
@@ -89,34 +141,88 @@ __device__ __forceinline__ void store_f32(T *p, const float (&in)[VEC]) {
     }
 }
 
-// N sums over the threads of one row, every thread getting them.  The row's
-// threads are the x dimension of the CTA (a power of two of at least 32, whole
-// warps); `slot` is this row's own N * 32 floats of shared memory.  The order
-// of the additions is fixed.  Rows that share a CTA call it together (it holds
-// CTA barriers when a row has several warps); a second call on the same slot
-// needs other shared memory or a barrier between.
-template <int N>
+// Two fp32 values in one 64-bit register pair: Blackwell adds, multiplies and
+// fuses both in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+          "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// N sums over the TPR threads of one row (threadIdx.x; whole warps), every
+// thread getting them, in a fixed order.  ROWS rows (threadIdx.y) share the CTA
+// and each has a barrier of its own; `slot` is this row's own N * 32 floats of
+// shared memory, 16-byte aligned.  A second call on the same slot needs a call
+// on another slot, or a barrier, between.
+template <int TPR, int ROWS>
+__device__ __forceinline__ void row_barrier() {
+    if constexpr (ROWS == 1) {
+        __syncthreads();
+    } else {
+        asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1u), "n"(TPR) : "memory");
+    }
+}
+
+template <int N, int TPR, int ROWS>
 __device__ __forceinline__ void row_sum(float (&v)[N], float *slot) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
-    const int warps = static_cast<int>(blockDim.x) / 32;
-    if (warps == 1) return;
-    const int warp = static_cast<int>(threadIdx.x) / 32, lane = static_cast<int>(threadIdx.x) % 32;
-    if (lane == 0) {
+    constexpr int kWarps = TPR / 32;
+    if constexpr (kWarps > 1) {
+        const int warp = static_cast<int>(threadIdx.x) / 32;
+        if (threadIdx.x % 32 == 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) slot[i * 32 + warp] = v[i];
-    }
-    __syncthreads();
+            for (int i = 0; i < N; ++i) slot[i * 32 + warp] = v[i];
+        }
+        row_barrier<TPR, ROWS>();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        // a power of two of warps: lanes beyond repeat the first ones' values
-        float t = slot[i * 32 + (lane & (warps - 1))];
-        for (int o = warps / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        v[i] = t;
+        for (int i = 0; i < N; ++i) {
+            constexpr int kPer = kWarps < 4 ? kWarps : 4;
+            float t = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; w += kPer) {
+                const Pack<float, kPer> p = *reinterpret_cast<const Pack<float, kPer> *>(slot + i * 32 + w);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) t += p.v[j];
+            }
+            v[i] = t;
+        }
     }
+}
+
+// 16 bytes of global memory on their way to shared memory; or `bytes` of them, the
+// rest zeroed.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ------------------------------------------------------------------- host --
@@ -140,6 +246,23 @@ inline int64_t span_bytes(int64_t rows, int64_t cols, int64_t stride, int64_t si
 
 // The current device is a GB300 (checked once per device); its SM count.
 int gb300_sms(int *sms);
+
+constexpr int kMaxDevices = 64;
+
+// The kernel's dynamic shared memory, allowed once per device.
+template <typename K>
+inline bool allow_smem(K *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    const uint64_t bit = uint64_t(1) << dev;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 // A grid of CTAs that may start while the previous kernel of the stream ends
 // (every kernel here waits for it, griddepcontrol.wait, before its first

@@ -14,7 +14,6 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
 constexpr int64_t kDefaultTimeoutNs = 4000000000LL;
-constexpr int kMaxDevices = 64;
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static std::once_flag once;
@@ -61,21 +60,6 @@ bool encode_d(CUtensorMap *map, void *ptr, int64_t M, int64_t N) {
     return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, ptr, dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The kernel's dynamic shared memory, allowed once per device.
-template <typename K>
-bool allow_smem(K *kernel, int bytes, std::atomic<uint64_t> &done) {
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
-    const uint64_t bit = uint64_t(1) << dev;
-    if (done.load(std::memory_order_relaxed) & bit) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    done.fetch_or(bit, std::memory_order_relaxed);
-    return true;
 }
 
 template <typename... P>

@@ -1,0 +1,269 @@
+// norm_forward.cu -- layer norm (see linear_ops.h and norm_rows.cuh).
+#include <cmath>
+
+#include "norm_rows.cuh"
+
+namespace linear_ops {
+namespace {
+
+struct NormArgs {
+    const void *x, *weight, *bias;
+    void *y;
+    float *mean, *rstd;
+    int64_t x_stride, y_stride;
+    int32_t rows, cols;
+    float eps, inv_cols;
+};
+
+constexpr int kStages = 4;
+
+template <typename T, typename W, int E, bool WIDE, int TPR, int THREADS, int PER_SM>
+__global__ void __launch_bounds__(THREADS, PER_SM) norm_forward_ring_kernel(const NormArgs a) {
+    constexpr int ROWS = THREADS / TPR;
+    using Ring = RowRing<T, E, WIDE, TPR, 1, kStages>;
+    __shared__ __align__(16) float slots[2][ROWS][32];
+    extern __shared__ __align__(16) uint8_t ring_mem[];
+    if (threadIdx.x == 0 && threadIdx.y == 0) ptx::griddep_launch_dependents();
+    Ring ring(ring_mem, a.cols);
+    int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.y;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+    const T *x = static_cast<const T *>(a.x) + row * a.x_stride;  // of this row
+    T *y = static_cast<T *>(a.y) + row * a.y_stride;
+    const int64_t x_step = step * a.x_stride, y_step = step * a.y_stride;
+    ptx::griddep_wait();
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        if (row + s * step < a.rows) ring.copy(s, 0, x + s * x_step);
+        cp_async_commit();
+    }
+    float2 w[E / 2], b[E / 2];
+    ring.gather(static_cast<const W *>(a.weight), 1.f, w);
+    ring.gather(static_cast<const W *>(a.bias), 0.f, b);
+    for (; row < a.rows; row += step, x += x_step, y += y_step) {
+        cp_async_wait<kStages - 2>();
+        if constexpr (!WIDE) row_barrier<TPR, ROWS>();
+        float2 v[E / 2];
+        ring.read(0, x, v);
+        if (row + (kStages - 1) * step < a.rows) ring.copy(ring.slot_behind(), 0, x + (kStages - 1) * x_step);
+        cp_async_commit();
+        ring.next();
+        float2 s2 = both(0.f);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) s2 = add2(s2, v[i]);
+        float sum[1] = {s2.x + s2.y};
+        row_sum<1, TPR, ROWS>(sum, slots[0][threadIdx.y]);
+        const float mean = sum[0] * a.inv_cols;
+        s2 = both(0.f);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            v[i] = add2(v[i], both(-mean));
+            // elements past the row's end are no deviations
+            if constexpr (WIDE) {
+                if (ring.holds(2 * i)) s2 = fma2(v[i], v[i], s2);
+            } else {
+                if (ring.holds(2 * i)) s2.x += v[i].x * v[i].x;
+                if (ring.holds(2 * i + 1)) s2.y += v[i].y * v[i].y;
+            }
+        }
+        float var[1] = {s2.x + s2.y};
+        row_sum<1, TPR, ROWS>(var, slots[1][threadIdx.y]);
+        const float rstd = 1.f / sqrtf(var[0] * a.inv_cols + a.eps);
+        if (threadIdx.x == 0 && a.mean) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) v[i] = fma2(mul2(v[i], both(rstd)), w[i], b[i]);
+        ring.scatter(y, v);
+    }
+}
+
+// Rows past the ring's, of whole units: a CTA of 256 threads a row, which holds it
+// as it came from memory (16-bit pairs: half the registers of fp32 values).
+template <typename T, typename W, int VEC, int NV>
+__global__ void __launch_bounds__(256) norm_forward_kernel(const NormArgs a) {
+    __shared__ __align__(16) float slots[2][32];
+    if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+    const int64_t row = blockIdx.x;
+    const int first = static_cast<int>(threadIdx.x) * VEC;
+    constexpr int step = 256 * VEC;
+    const T *x = static_cast<const T *>(a.x) + row * a.x_stride + first;
+    ptx::griddep_wait();
+    Pack<T, VEC> raw[NV];
+    float sum[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (first + i * step < a.cols) raw[i] = load_once<T, VEC>(x + i * step);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (first + i * step < a.cols) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum[0] += to_f32(raw[i].v[j]);
+        }
+    }
+    row_sum<1, 256, 1>(sum, slots[0]);
+    const float mean = sum[0] * a.inv_cols;
+    float var[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (first + i * step < a.cols) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float d = to_f32(raw[i].v[j]) - mean;
+                var[0] += d * d;
+            }
+        }
+    }
+    row_sum<1, 256, 1>(var, slots[1]);
+    const float rstd = 1.f / sqrtf(var[0] * a.inv_cols + a.eps);
+    if (threadIdx.x == 0 && a.mean) {
+        a.mean[row] = mean;
+        a.rstd[row] = rstd;
+    }
+    T *y = static_cast<T *>(a.y) + row * a.y_stride + first;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (first + i * step < a.cols) {
+            float w[VEC], b[VEC], out[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) w[j] = 1.f, b[j] = 0.f;
+            if (a.weight) load_f32<W, VEC>(static_cast<const W *>(a.weight) + first + i * step, w);
+            if (a.bias) load_f32<W, VEC>(static_cast<const W *>(a.bias) + first + i * step, b);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) out[j] = (to_f32(raw[i].v[j]) - mean) * rstd * w[j] + b[j];
+            store_f32<T, VEC>(y + i * step, out);
+        }
+    }
+}
+
+// Rows too long for registers: one CTA of 1024 threads passes over its row
+// three times (sum, centred squares, output), the second and third from L2.
+template <typename T, typename W>
+__global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs a) {
+    __shared__ __align__(16) float slots[2][32];
+    if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+    const int64_t row = blockIdx.x;
+    const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
+    T *y = static_cast<T *>(a.y) + row * a.y_stride;
+    ptx::griddep_wait();
+    float sum[1] = {0.f}, var[1] = {0.f};
+    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) sum[0] += to_f32(x[c]);
+    row_sum<1, 1024, 1>(sum, slots[0]);
+    const float mean = sum[0] * a.inv_cols;
+    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
+        const float d = to_f32(x[c]) - mean;
+        var[0] += d * d;
+    }
+    row_sum<1, 1024, 1>(var, slots[1]);
+    const float rstd = 1.f / sqrtf(var[0] * a.inv_cols + a.eps);
+    if (threadIdx.x == 0 && a.mean) {
+        a.mean[row] = mean;
+        a.rstd[row] = rstd;
+    }
+    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
+        const float w = a.weight ? to_f32(static_cast<const W *>(a.weight)[c]) : 1.f;
+        const float b = a.bias ? to_f32(static_cast<const W *>(a.bias)[c]) : 0.f;
+        y[c] = from_f32<T>((to_f32(x[c]) - mean) * rstd * w + b);
+    }
+}
+
+// ------------------------------------------------------------------- host --
+
+template <typename T, typename W, int E, bool WIDE, int TPR, int THREADS, int PER_SM>
+int forward_ring(const NormArgs &a, int sms, cudaStream_t stream) {
+    constexpr int ROWS = THREADS / TPR;
+    auto *kernel = norm_forward_ring_kernel<T, W, E, WIDE, TPR, THREADS, PER_SM>;
+    constexpr int kBytes = ROWS * RowRing<T, E, WIDE, TPR, 1, kStages>::BYTES;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(kernel, kBytes, done)) return GEMM_ERR_CUDA;
+    return launch(kernel, dim3(grid_of(a.rows, ROWS, PER_SM * sms)), dim3(TPR, ROWS), kBytes, stream, a);
+}
+
+template <typename T, typename W, bool WIDE>
+int forward_rows(const NormArgs &a, int sms, cudaStream_t stream) {
+    if (a.cols <= 32 * 8) return forward_ring<T, W, 8, WIDE, 32, 256, 4>(a, sms, stream);
+    if (a.cols <= 32 * 16) return forward_ring<T, W, 16, WIDE, 32, 256, 3>(a, sms, stream);
+    if (a.cols <= 64 * 16) return forward_ring<T, W, 16, WIDE, 64, 256, 3>(a, sms, stream);
+    if (a.cols <= 128 * 16) return forward_ring<T, W, 16, WIDE, 128, 256, 3>(a, sms, stream);
+    if (a.cols <= 256 * 16) return forward_ring<T, W, 16, WIDE, 256, 256, 3>(a, sms, stream);
+    if (a.cols <= kRingCols) return forward_ring<T, W, 16, WIDE, 512, 512, 1>(a, sms, stream);
+    if constexpr (WIDE) {
+        constexpr int U = kUnit<T>;
+        const dim3 grid(a.rows), block(256);
+        if (a.cols <= 256 * 8 * U) return launch(norm_forward_kernel<T, W, U, 8>, grid, block, 0, stream, a);
+        if (a.cols <= 256 * 16 * U) return launch(norm_forward_kernel<T, W, U, 16>, grid, block, 0, stream, a);
+    }
+    return launch(norm_forward_long_kernel<T, W>, dim3(a.rows), dim3(1024), 0, stream, a);
+}
+
+template <typename T, typename W>
+int forward_as(const NormArgs &a, int sms, cudaStream_t stream) {
+    constexpr int U = kUnit<T>;
+    const bool wide = a.cols % U == 0 && a.x_stride % U == 0 && a.y_stride % U == 0 && aligned(a.x, 16) &&
+                      aligned(a.y, 16) && (!a.weight || aligned(a.weight, 16)) && (!a.bias || aligned(a.bias, 16));
+    return wide ? forward_rows<T, W, true>(a, sms, stream) : forward_rows<T, W, false>(a, sms, stream);
+}
+
+}  // namespace
+
+int gb300_sms(int *sms) {
+    static thread_local int last_dev = -1, last_sms = 0;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_NO_DEVICE;
+    }
+    if (dev != last_dev) {
+        int major = 0, minor = 0, n = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_NO_DEVICE;
+        }
+        if (major != 10 || minor != 3) return GEMM_ERR_ARCH;
+        last_dev = dev;
+        last_sms = n;
+    }
+    *sms = last_sms;
+    return GEMM_OK;
+}
+
+}  // namespace linear_ops
+
+using namespace linear_ops;
+
+extern "C" {
+
+int layer_norm_forward(const void *x, int64_t x_stride, const void *weight, const void *bias, void *y, int64_t y_stride,
+                       float *mean, float *rstd, int64_t rows, int64_t cols, float eps, int32_t type,
+                       int32_t weight_type, void *stream) {
+    if (!sizes_ok(rows, cols) || !type_ok(type) || (weight_type != type && weight_type != LINEAR_F32) ||
+        !(eps >= 0.f) || std::isinf(eps) || x_stride < 0 || !mean != !rstd) {
+        return GEMM_ERR_INVALID_ARG;
+    }
+    if (rows > kMaxDim || cols > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return GEMM_OK;
+    if (!x || !y || (rows > 1 && y_stride < cols)) return GEMM_ERR_INVALID_ARG;
+    const int64_t size = type_size(type), wsize = type_size(weight_type);
+    if (!aligned(x, size) || !aligned(y, size) || !aligned(weight, wsize) || !aligned(bias, wsize) || !aligned(mean, 4) ||
+        !aligned(rstd, 4)) {
+        return GEMM_ERR_MISALIGNED;
+    }
+    if (rows == 1) x_stride = y_stride = 0;
+    const int64_t y_bytes = span_bytes(rows, cols, y_stride, size);
+    if (overlap(y, y_bytes, x, span_bytes(rows, cols, x_stride, size)) || overlap(y, y_bytes, weight, cols * wsize) ||
+        overlap(y, y_bytes, bias, cols * wsize) || overlap(y, y_bytes, mean, rows * 4) ||
+        overlap(y, y_bytes, rstd, rows * 4)) {
+        return GEMM_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    const int st = gb300_sms(&sms);
+    if (st != GEMM_OK) return st;
+    const NormArgs a = {x,    weight,   bias,     y,   mean, rstd, x_stride, y_stride, static_cast<int32_t>(rows),
+                        static_cast<int32_t>(cols), eps, 1.f / static_cast<float>(cols)};
+    return LINEAR_BY_TYPE(type, weight_type, forward_as, a, sms, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,167 @@
+// norm_rows.cuh -- rows of layer norm and its gradient: their sizes, and a ring of
+// rows on their way into shared memory.
+//
+// Both operators are bound by memory: forward reads a row and writes one, its
+// gradient reads two and writes one, at 8 and 14 operations an element.  So each
+// element is read from memory once and held in registers while its row's sums
+// are formed (the variance from the centred values: E[x^2] - mean^2 loses what
+// an offset of the row costs), and a persistent grid keeps the next rows on
+// their way meanwhile.
+#pragma once
+
+#include "common.cuh"
+
+namespace linear_ops {
+
+// The columns of a row that the TPR threads of threadIdx.x hold, E each, as pairs.
+//   WIDE   rows are whole 16-byte units: thread t holds units t, t + TPR, ...
+//   else   rows start anywhere: thread t holds columns t, t + TPR, ...
+template <typename T, int E, bool WIDE, int TPR>
+struct RowShare {
+    static constexpr int U = kUnit<T>;
+    static constexpr int NV = E / U;  // units of a thread
+    static_assert(E % U == 0, "whole units");
+    int cols;
+    // the first column, and whether element e (a constant) is one of the row
+    __device__ __forceinline__ int column(int e) const {
+        return WIDE ? (e / U * TPR + static_cast<int>(threadIdx.x)) * U + e % U : e * TPR + static_cast<int>(threadIdx.x);
+    }
+    __device__ __forceinline__ bool holds(int e) const { return column(WIDE ? e / U * U : e) < cols; }
+
+    // this thread's values of a vector by columns, `fill` past its end
+    template <typename W>
+    __device__ __forceinline__ void gather(const W *from, float fill, float2 (&v)[E / 2]) const {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) v[i] = both(fill);
+        if (!from) return;
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (holds(i * U)) load_pairs<W, U / 2>(from + column(i * U), v + i * U / 2);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                if (holds(2 * i)) v[i].x = to_f32(from[column(2 * i)]);
+                if (holds(2 * i + 1)) v[i].y = to_f32(from[column(2 * i + 1)]);
+            }
+        }
+    }
+    template <typename W>
+    __device__ __forceinline__ void scatter(W *to, const float2 (&v)[E / 2]) const {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (holds(i * U)) store_pairs<W, U / 2>(to + column(i * U), v + i * U / 2);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                if (holds(2 * i)) to[column(2 * i)] = from_f32<W>(v[i].x);
+                if (holds(2 * i + 1)) to[column(2 * i + 1)] = from_f32<W>(v[i].y);
+            }
+        }
+    }
+};
+
+// Some rows of OPS operands on their way from global to shared memory: STAGES
+// slots for each row of a CTA.
+//   WIDE   a thread copies and reads its own units, so no barrier guards the ring
+//   else   the 16-byte units that hold the row are copied (the first may start
+//          with bytes that lie before the row; they share an aligned 16 bytes
+//          with it, so its allocation; the last is cut at the row's end), and a
+//          barrier is due between copying and reading, and between reading and
+//          the next copy into that slot
+template <typename T, int E, bool WIDE, int TPR, int OPS, int STAGES>
+struct RowRing : RowShare<T, E, WIDE, TPR> {
+    using Share = RowShare<T, E, WIDE, TPR>;
+    using Share::cols;
+    using Share::NV;
+    using Share::U;
+    static constexpr uint32_t SLOT = (NV * TPR + (WIDE ? 0 : 1)) * 16;
+    static constexpr uint32_t BYTES = STAGES * OPS * SLOT;  // of one row's ring
+    uint32_t base;
+    int slot = 0;
+
+    __device__ __forceinline__ RowRing(void *ring, int cols_) : Share{cols_} {
+        base = ptx::smem_u32(ring) + threadIdx.y * BYTES;
+    }
+    __device__ __forceinline__ void copy(int s, int op, const T *row) const {
+        const uint32_t dst = base + static_cast<uint32_t>(s * OPS + op) * SLOT;
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (this->holds(i * U)) cp_async_16(dst + (i * TPR + threadIdx.x) * 16u, row + this->column(i * U));
+            }
+        } else {
+            const uint32_t head = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) % 16);
+            const char *from = reinterpret_cast<const char *>(row) - head;
+            const int end = static_cast<int>(head) + cols * static_cast<int>(sizeof(T));
+#pragma unroll
+            for (int i = 0; i <= NV; ++i) {
+                const int at = (i * TPR + static_cast<int>(threadIdx.x)) * 16;
+                if (at < end) cp_async_16(dst + at, from + at, static_cast<uint32_t>(end - at < 16 ? end - at : 16));
+            }
+        }
+    }
+    // this thread's elements of the current slot; zeros past the row's end
+    __device__ __forceinline__ void read(int op, const T *row, float2 (&v)[E / 2]) const {
+        const uint32_t src = base + static_cast<uint32_t>(slot * OPS + op) * SLOT;
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                uint4 raw = make_uint4(0, 0, 0, 0);
+                if (this->holds(i * U)) raw = ptx::ld_shared_v4(src + (i * TPR + threadIdx.x) * 16u);
+                using Raw = typename Pair<T>::Raw;
+                const Raw *p = reinterpret_cast<const Raw *>(&raw);
+#pragma unroll
+                for (int j = 0; j < U / 2; ++j) v[i * U / 2 + j] = Pair<T>::widen(p[j]);
+            }
+        } else {
+            const uint32_t at = src + static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) % 16) +
+                                threadIdx.x * static_cast<uint32_t>(sizeof(T));
+            float f[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                f[e] = 0.f;
+                if (this->holds(e)) {
+                    if constexpr (sizeof(T) == 4) {
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[e]) : "r"(at + e * TPR * 4u) : "memory");
+                    } else {
+                        uint16_t u;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at + e * TPR * 2u) : "memory");
+                        f[e] = to_f32(*reinterpret_cast<const T *>(&u));
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+        }
+    }
+    __device__ __forceinline__ void next() { slot = slot + 1 == STAGES ? 0 : slot + 1; }
+    __device__ __forceinline__ int slot_behind() const { return slot == 0 ? STAGES - 1 : slot - 1; }
+};
+
+// ------------------------------------------------------------------- host --
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
+
+// The ring kernels hold rows of up to 512 threads x 16 elements.
+constexpr int kRingCols = 512 * 16;
+
+inline int grid_of(int64_t rows, int per_cta, int ctas) {
+    const int64_t groups = (rows + per_cta - 1) / per_cta;
+    return static_cast<int>(groups < ctas ? groups : ctas);
+}
+
+// The element type and the weights' as template arguments.
+#define LINEAR_BY_TYPE(type, weight_type, FN, ...)                                                              \
+    ((type) == LINEAR_F32 ? FN<float, float>(__VA_ARGS__)                                                       \
+     : (type) == LINEAR_F16                                                                                     \
+         ? ((weight_type) == LINEAR_F32 ? FN<__half, float>(__VA_ARGS__) : FN<__half, __half>(__VA_ARGS__))     \
+         : ((weight_type) == LINEAR_F32 ? FN<__nv_bfloat16, float>(__VA_ARGS__)                                 \
+                                        : FN<__nv_bfloat16, __nv_bfloat16>(__VA_ARGS__)))
+
+inline bool sizes_ok(int64_t rows, int64_t cols) { return rows >= 0 && cols >= 1; }
+
+}  // namespace linear_ops

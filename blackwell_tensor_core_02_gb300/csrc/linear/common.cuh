@@ -174,7 +174,9 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // on another slot, or a barrier, between.
 template <int TPR, int ROWS>
 __device__ __forceinline__ void row_barrier() {
-    if constexpr (ROWS == 1) {
+    if constexpr (TPR == 32) {
+        __syncwarp();
+    } else if constexpr (ROWS == 1) {
         __syncthreads();
     } else {
         asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1u), "n"(TPR) : "memory");
@@ -198,7 +200,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float *slot) {
         row_barrier<TPR, ROWS>();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            constexpr int kPer = kWarps < 4 ? kWarps : 4;
+            constexpr int kPer = kWarps % 4 == 0 ? 4 : (kWarps % 2 == 0 ? 2 : 1);
             float t = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; w += kPer) {

@@ -5,6 +5,9 @@
 namespace linear_ops {
 namespace {
 
+// Parts of the weights' gradient: at most two CTAs for each of 152 SMs.
+constexpr int kMaxParts = 304;
+
 // Floats from a fold's dweight to its dbias: whole units.
 __host__ __device__ constexpr int fold_stride(int cols) { return (cols + 3) / 4 * 4; }
 
@@ -18,25 +21,36 @@ struct GradArgs {
     float inv_cols;
 };
 
-// Stages of the ring; fp32 rows are larger, and three let two CTAs of 4096 columns
-// share an SM.
-template <typename T>
-constexpr int kStages = sizeof(T) == 4 ? 3 : 4;
+// A persistent grid, one CTA an SM: each of its rows of threads takes a row, then
+// further ones a grid apart, and keeps its columns' sums of dweight and dbias in
+// registers until the end, when the CTA's are added up in shared memory and go
+// out as one part.
+//
+// A row is read from the ring twice, once for its sums and once for dx: holding
+// h and g in between takes 64 registers more a thread, which halves the rows at
+// work on an SM, and a row's time is the latency of its sums (8192 x 4096 bf16:
+// 40.1 us with them held, see the table of times at norm_backward_join).
+template <typename T, int E, bool WIDE, int TPR>
+struct GradShape {
+    static constexpr int STAGES = 3;
+    static constexpr int ROW_BYTES = RowRing<T, E, WIDE, TPR, 2, STAGES>::BYTES;
+    static constexpr int BY_SMEM = 200 * 1024 / ROW_BYTES, BY_THREADS = E == 8 ? 512 / TPR : 384 / TPR;
+    static constexpr int ROWS = BY_SMEM < BY_THREADS ? BY_SMEM : BY_THREADS;  // at most
+    // the rows' sums meet in the ring's memory, half of them at a time
+    static_assert(ROWS == 1 || ROWS * ROW_BYTES >= (ROWS / 2) * 2 * 4 * TPR * E, "room for the sums");
+};
 
-// A persistent grid: each CTA takes ROWS rows, then further ones a grid apart, and
-// keeps its columns' sums of dweight and dbias in registers until the end.  Then
-// the sums of its other rows join those of its first one, one row after the other
-// through shared memory, and go out as one part.
-template <typename T, typename W, int E, bool WIDE, int TPR, int THREADS, int PER_SM>
-__global__ void __launch_bounds__(THREADS, PER_SM) norm_backward_ring_kernel(const GradArgs a) {
-    constexpr int ROWS = THREADS / TPR, STAGES = kStages<T>;
+template <typename T, typename W, int E, bool WIDE, int TPR>
+__global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
+    norm_backward_ring_kernel(const GradArgs a) {
+    constexpr int ROWS = GradShape<T, E, WIDE, TPR>::ROWS, STAGES = GradShape<T, E, WIDE, TPR>::STAGES;
     using Ring = RowRing<T, E, WIDE, TPR, 2, STAGES>;
     __shared__ __align__(16) float slots[2][ROWS][64];
     extern __shared__ __align__(16) uint8_t ring_mem[];
     if (threadIdx.x == 0 && threadIdx.y == 0) ptx::griddep_launch_dependents();
     Ring ring(ring_mem, a.cols);
-    int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.y;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
     const T *x = static_cast<const T *>(a.x) + row * a.x_stride, *dy = static_cast<const T *>(a.dy) + row * a.dy_stride;
     T *dx = static_cast<T *>(a.dx) + row * a.dx_stride;
     const int64_t x_step = step * a.x_stride, dy_step = step * a.dy_stride, dx_step = step * a.dx_stride;
@@ -59,55 +73,72 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_backward_ring_kernel(con
     for (; row < a.rows; row += step, x += x_step, dy += dy_step, dx += dx_step) {
         cp_async_wait<STAGES - 2>();
         if constexpr (!WIDE) row_barrier<TPR, ROWS>();
-        const float2 m = both(-mean), rs = both(rstd);
-        float2 h[E / 2], g[E / 2];
-        ring.read(0, x, h);
-        ring.read(1, dy, g);
         if (row + (STAGES - 1) * step < a.rows) {
             ring.copy(ring.slot_behind(), 0, x + (STAGES - 1) * x_step);
             ring.copy(ring.slot_behind(), 1, dy + (STAGES - 1) * dy_step);
         }
         cp_async_commit();
-        ring.next();
+        const float2 m = both(-mean), rs = both(rstd);
         if (row + step < a.rows) mean = a.mean[row + step], rstd = a.rstd[row + step];
         float2 s0 = both(0.f), s1 = both(0.f);
+        constexpr int U = Ring::U;
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            // past the row's end dy is 0, and so is what h there is multiplied with
-            h[i] = mul2(add2(h[i], m), rs);
-            sw[i] = fma2(g[i], h[i], sw[i]);
-            sb[i] = add2(sb[i], g[i]);
-            g[i] = mul2(g[i], w[i]);
-            s0 = add2(s0, g[i]);
-            s1 = fma2(g[i], h[i], s1);
+        for (int u = 0; u < Ring::NV; ++u) {
+            float2 h[U / 2], g[U / 2];
+            ring.read_some(0, x, u, h);
+            ring.read_some(1, dy, u, g);
+#pragma unroll
+            for (int i = 0; i < U / 2; ++i) {
+                // past the row's end dy is 0, and so is what h there is multiplied with
+                float2 &swi = sw[u * U / 2 + i], &sbi = sb[u * U / 2 + i];
+                h[i] = mul2(add2(h[i], m), rs);
+                swi = fma2(g[i], h[i], swi);
+                sbi = add2(sbi, g[i]);
+                g[i] = mul2(g[i], w[u * U / 2 + i]);
+                s0 = add2(s0, g[i]);
+                s1 = fma2(g[i], h[i], s1);
+            }
         }
         float sums[2] = {s0.x + s0.y, s1.x + s1.y};
         row_sum<2, TPR, ROWS>(sums, slots[flip][threadIdx.y]);
         flip ^= 1;
         const float2 c1 = both(-sums[0] * a.inv_cols), c2 = both(-sums[1] * a.inv_cols);
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) g[i] = mul2(fma2(h[i], c2, add2(g[i], c1)), rs);
-        ring.scatter(dx, g);
+        for (int u = 0; u < Ring::NV; ++u) {
+            float2 h[U / 2], g[U / 2];
+            ring.read_some(0, x, u, h);
+            ring.read_some(1, dy, u, g);
+#pragma unroll
+            for (int i = 0; i < U / 2; ++i) {
+                h[i] = mul2(add2(h[i], m), rs);
+                g[i] = mul2(fma2(h[i], c2, fma2(g[i], w[u * U / 2 + i], c1)), rs);
+            }
+            ring.scatter_some(dx, u, g);
+        }
+        ring.next();
     }
     if (!a.partial) return;
     cp_async_wait<0>();
-    float *fold = reinterpret_cast<float *>(ring_mem), *fold_b = fold + fold_stride(a.cols);  // the ring's memory
-    for (int r = 1; r < ROWS; ++r) {
+    const int dbias_at = fold_stride(a.cols);
+    for (int n = static_cast<int>(blockDim.y); n > 1;) {
+        const int keep = (n + 1) / 2, r = static_cast<int>(threadIdx.y);
+        float *fold = reinterpret_cast<float *>(ring_mem) + (r < keep ? r : r - keep) * 2 * dbias_at;
         __syncthreads();
-        if (static_cast<int>(threadIdx.y) == r) {
+        if (r >= keep && r < n) {
             ring.scatter(fold, sw);
-            ring.scatter(fold_b, sb);
+            ring.scatter(fold + dbias_at, sb);
         }
         __syncthreads();
-        if (threadIdx.y == 0) {
+        if (r < n - keep) {
             float2 o[E / 2];
             ring.gather(static_cast<const float *>(fold), 0.f, o);
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) sw[i] = add2(sw[i], o[i]);
-            ring.gather(static_cast<const float *>(fold_b), 0.f, o);
+            ring.gather(static_cast<const float *>(fold + dbias_at), 0.f, o);
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) sb[i] = add2(sb[i], o[i]);
         }
+        n = keep;
     }
     if (threadIdx.y != 0) return;
     float *part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
@@ -171,8 +202,14 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float *partial, i
     float sum = 0.f;
     if (col < cols) {
         const float *p = partial + static_cast<int64_t>(blockIdx.y) * cols + col;
-#pragma unroll 4
-        for (int i = threadIdx.y; i < parts; i += 32) sum += p[static_cast<int64_t>(i) * 2 * cols];
+        float v[(kMaxParts + 31) / 32];  // every load on its way before the first sum
+#pragma unroll
+        for (int k = 0; k < (kMaxParts + 31) / 32; ++k) {
+            const int i = k * 32 + static_cast<int>(threadIdx.y);
+            v[k] = i < parts ? p[static_cast<int64_t>(i) * 2 * cols] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < (kMaxParts + 31) / 32; ++k) sum += v[k];
     }
     s[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
@@ -185,29 +222,25 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float *partial, i
 
 // ------------------------------------------------------------------- host --
 
-// Parts of the weights' gradient: at most two CTAs for each of 152 SMs.
-constexpr int kMaxParts = 304;
-
-template <typename T, typename W, int E, bool WIDE, int TPR, int THREADS, int PER_SM>
+template <typename T, typename W, int E, bool WIDE, int TPR>
 int backward_ring(const GradArgs &a, int sms, int *parts, cudaStream_t stream) {
-    constexpr int ROWS = THREADS / TPR;
-    auto *kernel = norm_backward_ring_kernel<T, W, E, WIDE, TPR, THREADS, PER_SM>;
-    constexpr int kBytes = ROWS * RowRing<T, E, WIDE, TPR, 2, kStages<T>>::BYTES;
-    static_assert(kBytes >= 2 * 4 * TPR * E || ROWS == 1, "the ring's memory holds two rows of sums");
+    using S = GradShape<T, E, WIDE, TPR>;
+    auto *kernel = norm_backward_ring_kernel<T, W, E, WIDE, TPR>;
     static std::atomic<uint64_t> done{0};
-    if (!allow_smem(kernel, kBytes, done)) return GEMM_ERR_CUDA;
-    *parts = grid_of(a.rows, ROWS, PER_SM * sms < kMaxParts ? PER_SM * sms : kMaxParts);
-    return launch(kernel, dim3(*parts), dim3(TPR, ROWS), kBytes, stream, a);
+    if (!allow_smem(kernel, S::ROWS * S::ROW_BYTES, done)) return GEMM_ERR_CUDA;
+    // few rows: spread over the SMs before they share one
+    const int ctas = sms < kMaxParts ? sms : kMaxParts;
+    const int64_t each = (a.rows + static_cast<int64_t>(ctas) - 1) / ctas;
+    const int rows = each < S::ROWS ? static_cast<int>(each) : S::ROWS;
+    *parts = grid_of(a.rows, rows, ctas);
+    return launch(kernel, dim3(*parts), dim3(TPR, rows), rows * S::ROW_BYTES, stream, a);
 }
 
 template <typename T, typename W, bool WIDE>
 int backward_rows(const GradArgs &a, int sms, int *parts, cudaStream_t stream) {
-    if (a.cols <= 32 * 8) return backward_ring<T, W, 8, WIDE, 32, 256, 2>(a, sms, parts, stream);
-    if (a.cols <= 32 * 16) return backward_ring<T, W, 16, WIDE, 32, 256, 2>(a, sms, parts, stream);
-    if (a.cols <= 64 * 16) return backward_ring<T, W, 16, WIDE, 64, 256, 2>(a, sms, parts, stream);
-    if (a.cols <= 128 * 16) return backward_ring<T, W, 16, WIDE, 128, 256, 2>(a, sms, parts, stream);
-    if (a.cols <= 256 * 16) return backward_ring<T, W, 16, WIDE, 256, 256, 2>(a, sms, parts, stream);
-    if (a.cols <= kRingCols) return backward_ring<T, W, 16, WIDE, 512, 512, 1>(a, sms, parts, stream);
+#define LINEAR_CASE(E, TPR) return backward_ring<T, W, E, WIDE, TPR>(a, sms, parts, stream)
+    LINEAR_ROW_SHAPES(LINEAR_CASE)
+#undef LINEAR_CASE
     int st = launch(norm_backward_long_kernel<T, W>, dim3(a.rows), dim3(1024), 0, stream, a);
     if (st == GEMM_OK && a.partial) {
         *parts = grid_of(a.rows, 1, kMaxParts);

@@ -17,9 +17,20 @@ struct NormArgs {
 
 constexpr int kStages = 4;
 
-template <typename T, typename W, int E, bool WIDE, int TPR, int THREADS, int PER_SM>
-__global__ void __launch_bounds__(THREADS, PER_SM) norm_forward_ring_kernel(const NormArgs a) {
-    constexpr int ROWS = THREADS / TPR;
+// Rows of a CTA: 128 threads' worth; CTAs of an SM: 512 threads (32 elements, their
+// weights and biases take 100 registers) and what their rings leave room for.
+template <typename T, int E, bool WIDE, int TPR>
+struct NormShape {
+    static constexpr int ROWS = TPR < 128 ? 128 / TPR : 1;
+    static constexpr int BYTES = ROWS * RowRing<T, E, WIDE, TPR, 1, kStages>::BYTES;
+    static constexpr int BY_SMEM = 220 * 1024 / (BYTES + 2048), BY_THREADS = 512 / (ROWS * TPR);
+    static constexpr int PER_SM = BY_SMEM < BY_THREADS ? BY_SMEM : BY_THREADS;
+};
+
+template <typename T, typename W, int E, bool WIDE, int TPR>
+__global__ void __launch_bounds__(TPR *NormShape<T, E, WIDE, TPR>::ROWS, NormShape<T, E, WIDE, TPR>::PER_SM)
+    norm_forward_ring_kernel(const NormArgs a) {
+    constexpr int ROWS = NormShape<T, E, WIDE, TPR>::ROWS;
     using Ring = RowRing<T, E, WIDE, TPR, 1, kStages>;
     __shared__ __align__(16) float slots[2][ROWS][32];
     extern __shared__ __align__(16) uint8_t ring_mem[];
@@ -170,24 +181,20 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs 
 
 // ------------------------------------------------------------------- host --
 
-template <typename T, typename W, int E, bool WIDE, int TPR, int THREADS, int PER_SM>
+template <typename T, typename W, int E, bool WIDE, int TPR>
 int forward_ring(const NormArgs &a, int sms, cudaStream_t stream) {
-    constexpr int ROWS = THREADS / TPR;
-    auto *kernel = norm_forward_ring_kernel<T, W, E, WIDE, TPR, THREADS, PER_SM>;
-    constexpr int kBytes = ROWS * RowRing<T, E, WIDE, TPR, 1, kStages>::BYTES;
+    using S = NormShape<T, E, WIDE, TPR>;
+    auto *kernel = norm_forward_ring_kernel<T, W, E, WIDE, TPR>;
     static std::atomic<uint64_t> done{0};
-    if (!allow_smem(kernel, kBytes, done)) return GEMM_ERR_CUDA;
-    return launch(kernel, dim3(grid_of(a.rows, ROWS, PER_SM * sms)), dim3(TPR, ROWS), kBytes, stream, a);
+    if (!allow_smem(kernel, S::BYTES, done)) return GEMM_ERR_CUDA;
+    return launch(kernel, dim3(grid_of(a.rows, S::ROWS, S::PER_SM * sms)), dim3(TPR, S::ROWS), S::BYTES, stream, a);
 }
 
 template <typename T, typename W, bool WIDE>
 int forward_rows(const NormArgs &a, int sms, cudaStream_t stream) {
-    if (a.cols <= 32 * 8) return forward_ring<T, W, 8, WIDE, 32, 256, 4>(a, sms, stream);
-    if (a.cols <= 32 * 16) return forward_ring<T, W, 16, WIDE, 32, 256, 3>(a, sms, stream);
-    if (a.cols <= 64 * 16) return forward_ring<T, W, 16, WIDE, 64, 256, 3>(a, sms, stream);
-    if (a.cols <= 128 * 16) return forward_ring<T, W, 16, WIDE, 128, 256, 3>(a, sms, stream);
-    if (a.cols <= 256 * 16) return forward_ring<T, W, 16, WIDE, 256, 256, 3>(a, sms, stream);
-    if (a.cols <= kRingCols) return forward_ring<T, W, 16, WIDE, 512, 512, 1>(a, sms, stream);
+#define LINEAR_CASE(E, TPR) return forward_ring<T, W, E, WIDE, TPR>(a, sms, stream)
+    LINEAR_ROW_SHAPES(LINEAR_CASE)
+#undef LINEAR_CASE
     if constexpr (WIDE) {
         constexpr int U = kUnit<T>;
         const dim3 grid(a.rows), block(256);

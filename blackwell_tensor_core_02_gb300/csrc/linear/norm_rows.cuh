@@ -47,20 +47,24 @@ struct RowShare {
             }
         }
     }
+    // U of this thread's values (the i-th U of its E) to a vector by columns
     template <typename W>
-    __device__ __forceinline__ void scatter(W *to, const float2 (&v)[E / 2]) const {
+    __device__ __forceinline__ void scatter_some(W *to, int i, const float2 *v) const {
         if constexpr (WIDE) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (holds(i * U)) store_pairs<W, U / 2>(to + column(i * U), v + i * U / 2);
-            }
+            if (holds(i * U)) store_pairs<W, U / 2>(to + column(i * U), v);
         } else {
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-                if (holds(2 * i)) to[column(2 * i)] = from_f32<W>(v[i].x);
-                if (holds(2 * i + 1)) to[column(2 * i + 1)] = from_f32<W>(v[i].y);
+            for (int j = 0; j < U / 2; ++j) {
+                const int e = i * U + 2 * j;
+                if (holds(e)) to[column(e)] = from_f32<W>(v[j].x);
+                if (holds(e + 1)) to[column(e + 1)] = from_f32<W>(v[j].y);
             }
         }
+    }
+    template <typename W>
+    __device__ __forceinline__ void scatter(W *to, const float2 (&v)[E / 2]) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) scatter_some(to, i, v + i * U / 2);
     }
 };
 
@@ -104,39 +108,42 @@ struct RowRing : RowShare<T, E, WIDE, TPR> {
             }
         }
     }
-    // this thread's elements of the current slot; zeros past the row's end
-    __device__ __forceinline__ void read(int op, const T *row, float2 (&v)[E / 2]) const {
+    // U of this thread's elements (the i-th U of its E) of the current slot; zeros past
+    // the row's end
+    __device__ __forceinline__ void read_some(int op, const T *row, int i, float2 *v) const {
         const uint32_t src = base + static_cast<uint32_t>(slot * OPS + op) * SLOT;
         if constexpr (WIDE) {
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (this->holds(i * U)) raw = ptx::ld_shared_v4(src + (i * TPR + threadIdx.x) * 16u);
+            using Raw = typename Pair<T>::Raw;
+            const Raw *p = reinterpret_cast<const Raw *>(&raw);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                uint4 raw = make_uint4(0, 0, 0, 0);
-                if (this->holds(i * U)) raw = ptx::ld_shared_v4(src + (i * TPR + threadIdx.x) * 16u);
-                using Raw = typename Pair<T>::Raw;
-                const Raw *p = reinterpret_cast<const Raw *>(&raw);
-#pragma unroll
-                for (int j = 0; j < U / 2; ++j) v[i * U / 2 + j] = Pair<T>::widen(p[j]);
-            }
+            for (int j = 0; j < U / 2; ++j) v[j] = Pair<T>::widen(p[j]);
         } else {
             const uint32_t at = src + static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) % 16) +
                                 threadIdx.x * static_cast<uint32_t>(sizeof(T));
-            float f[E];
+            float f[U];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                f[e] = 0.f;
+            for (int j = 0; j < U; ++j) {
+                const int e = i * U + j;
+                f[j] = 0.f;
                 if (this->holds(e)) {
                     if constexpr (sizeof(T) == 4) {
-                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[e]) : "r"(at + e * TPR * 4u) : "memory");
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[j]) : "r"(at + e * TPR * 4u) : "memory");
                     } else {
                         uint16_t u;
                         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at + e * TPR * 2u) : "memory");
-                        f[e] = to_f32(*reinterpret_cast<const T *>(&u));
+                        f[j] = to_f32(*reinterpret_cast<const T *>(&u));
                     }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+            for (int j = 0; j < U / 2; ++j) v[j] = make_float2(f[2 * j], f[2 * j + 1]);
         }
+    }
+    __device__ __forceinline__ void read(int op, const T *row, float2 (&v)[E / 2]) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) read_some(op, row, i, v + i * U / 2);
     }
     __device__ __forceinline__ void next() { slot = slot + 1 == STAGES ? 0 : slot + 1; }
     __device__ __forceinline__ int slot_behind() const { return slot == 0 ? STAGES - 1 : slot - 1; }
@@ -146,8 +153,26 @@ struct RowRing : RowShare<T, E, WIDE, TPR> {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
 
-// The ring kernels hold rows of up to 512 threads x 16 elements.
-constexpr int kRingCols = 512 * 16;
+// Elements of a row that a thread holds, and the threads: a sum over a row costs
+// each warp some 50 instructions and a barrier, so few warps with many elements
+// are faster (8192 x 4096 bf16 forward, us: 8 elements 36.6, 16 25.4, 32 23.7;
+// gradient 66, 41.4, 41.7), and whole warps up to 8 serve each width up to 8192.
+constexpr int kEach = 32;
+constexpr int kRingCols = 256 * kEach;
+
+// CASE(E, threads) of the first shape that holds a.cols.
+#define LINEAR_ROW_SHAPES(CASE)          \
+    if (a.cols <= 32 * 8) CASE(8, 32);   \
+    switch ((a.cols + 1023) / 1024) {    \
+        case 1: CASE(kEach, 32);         \
+        case 2: CASE(kEach, 64);         \
+        case 3: CASE(kEach, 96);         \
+        case 4: CASE(kEach, 128);        \
+        case 5: CASE(kEach, 160);        \
+        case 6: CASE(kEach, 192);        \
+        case 7: CASE(kEach, 224);        \
+        case 8: CASE(kEach, 256);        \
+    }
 
 inline int grid_of(int64_t rows, int per_cta, int ctas) {
     const int64_t groups = (rows + per_cta - 1) / per_cta;

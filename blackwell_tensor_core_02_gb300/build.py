@@ -62,6 +62,43 @@ def _command(path: str, checked: bool, verbose: bool, target: str = LIB_PATH) ->
             "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "gemm_f16.cu"), "-o", path]
 
 
+def binding_path() -> str:
+    """The Python binding of the linear layer's operators, for this torch."""
+    from importlib.metadata import version
+
+    return os.path.join(BUILD_DIR, f"_linear_binding.torch{version('torch')}.so")
+
+
+def _binding_command(path: str) -> list[str]:
+    import importlib.util
+    import sysconfig
+
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    system = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+              os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+            *(a for d in system for a in ("-isystem", d)), "-I", INCLUDE, os.path.join(LINEAR_CSRC, "binding.cpp"), "-o", path,
+            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10",
+            "-lc10_cuda", "-L", BUILD_DIR, "-l:" + os.path.basename(LINEAR_LIB_PATH), "-Wl,-rpath,$ORIGIN",
+            "-Wl,-rpath," + os.path.join(torch_dir, "lib")]
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the Python binding if missing or older than its sources; return its path.  (It links
+    the operators' library, which is built first.)"""
+    build_linear()
+    path = binding_path()
+    sources = [os.path.join(LINEAR_CSRC, "binding.cpp"), os.path.join(INCLUDE, "linear_ops.h"), os.path.join(INCLUDE, "gemm_f16.h")]
+    if force or not os.path.exists(path) or any(os.path.getmtime(s) > os.path.getmtime(path) for s in sources):
+        tmp = f"{path}.{os.getpid()}.tmp"
+        r = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, path)
+    return path
+
+
 def build_many(targets: list[tuple[str, bool]], force: bool = False, verbose: bool = False) -> None:
     """Compile the (path, checked) targets that are missing or stale, in parallel."""
     todo = [(path, checked) for path, checked in targets if force or is_stale(path)]
@@ -102,6 +139,7 @@ def build_linear(force: bool = False, verbose: bool = False) -> str:
 def build_all(force: bool = False, verbose: bool = False) -> None:
     """Every library, compiled side by side."""
     build_many([(LIB_PATH, False), (CHECKED_LIB_PATH, True), (LINEAR_LIB_PATH, False)], force=force, verbose=verbose)
+    build_binding(force=force)
 
 
 if __name__ == "__main__":

@@ -116,6 +116,7 @@ int launch_single(const Call &c) {
     p.k_tiles = static_cast<int32_t>((c.K + 255) / 256);
     p.d_type = c.d_type;
     p.swap = swap;
+    p.wide_store = c.N % 4 == 0 && aligned(c.D, 4 * type_size(c.d_type));
     p.debug_flags = static_cast<uint32_t>(c.o.debug_flags);
     p.timeout_ns = static_cast<uint64_t>(c.o.timeout_ns);
     p.alpha = c.alpha;

@@ -152,6 +152,7 @@ struct Fp4Params {
     int32_t d_type;
     int32_t swap;                  // single-CTA tiles: the 128-row side is B
     int32_t tma_store;             // CTA pairs: D through its tensor map
+    int32_t wide_store;            // single-CTA tiles: D's rows are aligned units of four elements
     uint32_t debug_flags;
     uint64_t timeout_ns;
     float alpha;
@@ -177,6 +178,41 @@ __device__ __forceinline__ uint32_t pack16(int32_t type, float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Four consecutive elements of a row of D, of which `left` are in the row.
+__device__ __forceinline__ void store_d4(const Fp4Params &p, int64_t at, int32_t left, float4 v) {
+    if (p.wide_store) {  // rows of whole units of four, aligned
+        if (p.d_type == LINEAR_F32) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.D) + at) = v;
+        } else {
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.D) + at) =
+                make_uint2(pack16(p.d_type, v.x, v.y), pack16(p.d_type, v.z, v.w));
+        }
+        return;
+    }
+    store_d(p.D, p.d_type, at, v.x);
+    if (left > 1) store_d(p.D, p.d_type, at + 1, v.y);
+    if (left > 2) store_d(p.D, p.d_type, at + 2, v.z);
+    if (left > 3) store_d(p.D, p.d_type, at + 3, v.w);
+}
+
+// Four sums of a CTA of the cluster (of this CTA without a K split).
+template <int KS>
+__device__ __forceinline__ float4 load_sums(uint32_t addr) {
+    float4 v;
+    if constexpr (KS > 1) {
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(addr)
+                     : "memory");
+    } else {
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(addr)
+                     : "memory");
+    }
+    return v;
+}
+
 // ------------------------------------------------------- single-CTA tiles --
 //
 // One CTA of 6 warps per tile and K slice (warp 0 TMA producer, warp 1 MMA
@@ -198,9 +234,12 @@ struct Fp4Single {
     static constexpr int OFF_SFA = OFF_B + STAGES * S::B_BYTES;
     static constexpr int OFF_SFB = OFF_SFA + STAGES * S::SFA_BYTES;
     static constexpr int RING = OFF_SFB + STAGES * S::SFB_BYTES;
-    // the CTA's fp32 sums, in the ring once it is idle: row p of P at p * LD
-    static constexpr int LD = BN + 1;  // odd: columns and rows are free of bank conflicts
-    static constexpr int SUMS = 128 * LD * 4;
+    // The CTA's fp32 sums, in the ring once it is idle, in the order of D's rows: with
+    // swap row q of Q (128 sums) at q * LD_SWAP, else row p of P (BN sums) at p * LD.
+    // Rows are 16 bytes off a multiple of 128 bytes, so the 16-byte accesses of 8
+    // lanes in 8 rows meet no bank twice.
+    static constexpr int LD = BN + 4, LD_SWAP = 128 + 4;
+    static constexpr int SUMS = 4 * (128 * LD > BN * LD_SWAP ? 128 * LD : BN * LD_SWAP);
     static constexpr int OFF_BAR = RING > SUMS ? RING : (SUMS + 15) / 16 * 16;
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 1) * 8;
     static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
@@ -324,16 +363,23 @@ __global__ void __launch_bounds__(192, 2)
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (ok && *abort_flag == 0) {
             ptx::tcgen05_fence_after();
-            const int quarter = warp & 3;
-            float *row = reinterpret_cast<float *>(smem) + (quarter * 32 + lane) * C::LD;
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+            const int row = (warp & 3) * 32 + lane;  // of P
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll
             for (int c = 0; c < BN; c += 16) {
                 uint32_t v[16];
                 ptx::tmem_ld_32x32b_x16(taddr + c, v);
                 ptx::tmem_wait_ld();
+                if (p.swap) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) row[c + j] = __uint_as_float(v[j]);
+                    for (int j = 0; j < 16; ++j) {
+                        reinterpret_cast<float *>(smem)[(c + j) * C::LD_SWAP + row] = __uint_as_float(v[j]);
+                    }
+                } else {
+                    const uint32_t at = base + static_cast<uint32_t>(row * C::LD + c) * 4u;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) ptx::st_shared_v4(at + j * 4u, v[j], v[j + 1], v[j + 2], v[j + 3]);
+                }
             }
         }
     }
@@ -346,31 +392,28 @@ __global__ void __launch_bounds__(192, 2)
     }
     ptx::griddep_wait();
     if (*abort_flag == 0) {
-        const float *own = reinterpret_cast<const float *>(smem);
+        // Rows of D that this CTA adds up: with swap its share of Q's rows that
+        // exist, else of P's; four columns a thread and step.
+        const int d_rows = p.swap ? (p.M - q0 < BN ? p.M - q0 : BN) : (p.M - p0 < 128 ? p.M - p0 : 128);
+        const int first = d_rows * rank / KS, last = d_rows * (rank + 1) / KS;
+        const int per = p.swap ? 32 : BN / 4, ld = p.swap ? C::LD_SWAP : C::LD;  // threads and floats of a row
+        const int m0 = p.swap ? q0 : p0, n0 = p.swap ? p0 : q0;
         uint32_t peer[KS];
 #pragma unroll
-        for (int s = 0; s < KS; ++s) peer[s] = KS > 1 ? ptx::mapa(base, static_cast<uint32_t>(s)) : 0u;
-        constexpr int kRows = 128 / KS;  // rows of P
-        for (int u = static_cast<int>(threadIdx.x); u < kRows * BN; u += C::THREADS) {
-            // consecutive threads along the rows of D
-            const int pr = (p.swap ? u % kRows : u / BN) + rank * kRows, q = p.swap ? u / kRows : u % BN;
-            const int64_t m = p.swap ? q0 + q : p0 + pr, n = p.swap ? p0 + pr : q0 + q;
-            if (m >= p.M || n >= p.N) continue;
-            float v = 0.f;
-            if constexpr (KS > 1) {
-                float part[KS];
+        for (int s = 0; s < KS; ++s) peer[s] = KS > 1 ? ptx::mapa(base, static_cast<uint32_t>(s)) : base;
+        for (int u = first * per + static_cast<int>(threadIdx.x); u < last * per; u += C::THREADS) {
+            const int r = u / per, c = u % per * 4;
+            const int32_t n = n0 + c;
+            if (n >= p.N) continue;
+            const uint32_t at = static_cast<uint32_t>(r * ld + c) * 4u;
+            float4 part[KS];
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(part[s])
-                                 : "r"(peer[s] + static_cast<uint32_t>(pr * C::LD + q) * 4u));
-                }
+            for (int s = 0; s < KS; ++s) part[s] = load_sums<KS>(peer[s] + at);
+            float4 v = part[0];
 #pragma unroll
-                for (int s = 0; s < KS; ++s) v += part[s];
-            } else {
-                v = own[pr * C::LD + q];
-            }
-            store_d(p.D, p.d_type, m * p.N + n, v * p.alpha);
+            for (int s = 1; s < KS; ++s) v.x += part[s].x, v.y += part[s].y, v.z += part[s].z, v.w += part[s].w;
+            v.x *= p.alpha, v.y *= p.alpha, v.z *= p.alpha, v.w *= p.alpha;
+            store_d4(p, static_cast<int64_t>(m0 + r) * p.N + n, p.N - n, v);
         }
     }
     if constexpr (KS > 1) {

@@ -228,7 +228,7 @@ bool resolve(int64_t M, int64_t N, int64_t K, int sms, gemm_fp4_options *o) {
     const int64_t k_tiles = (K + 255) / 256;
     if (o->tile == 0 && o->swap == 0 && o->cluster_k == 0) {
         const int64_t pairs = (M + 255) / 256 * ((N + 255) / 256);
-        if (M > 128 && N > 128 && pairs * 2 >= sms) o->tile = 256;
+        if (M > 128 && N > 128 && pairs * 8 >= sms) o->tile = 256;
     }
     if (o->tile == 256) {
         o->cluster_k = 1;
@@ -242,7 +242,7 @@ bool resolve(int64_t M, int64_t N, int64_t K, int sms, gemm_fp4_options *o) {
     const int64_t tiles = (p_rows + 127) / 128 * ((q_rows + o->tile - 1) / o->tile);
     if (o->cluster_k == 0) {
         o->cluster_k = 8;
-        while (o->cluster_k > 1 && (tiles * o->cluster_k > 2 * sms || k_tiles < 2 * o->cluster_k)) o->cluster_k /= 2;
+        while (o->cluster_k > 1 && (tiles * o->cluster_k > 2 * sms || k_tiles < 4 * o->cluster_k)) o->cluster_k /= 2;
     }
     while (o->cluster_k > k_tiles) o->cluster_k /= 2;
     return true;

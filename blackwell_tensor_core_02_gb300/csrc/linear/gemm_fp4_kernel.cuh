@@ -195,6 +195,15 @@ __device__ __forceinline__ void store_d4(const Fp4Params &p, int64_t at, int32_t
     if (left > 3) store_d(p.D, p.d_type, at + 3, v.w);
 }
 
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
+    if constexpr (N == 32) {
+        ptx::tmem_ld_32x32b_x32(taddr, v);
+    } else {
+        ptx::tmem_ld_32x32b_x16(taddr, v);
+    }
+}
+
 // Four sums of a CTA of the cluster (of this CTA without a K split).
 template <int KS>
 __device__ __forceinline__ float4 load_sums(uint32_t addr) {
@@ -365,20 +374,21 @@ __global__ void __launch_bounds__(192, 2)
             ptx::tcgen05_fence_after();
             const int row = (warp & 3) * 32 + lane;  // of P
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            constexpr int kCols = BN < 32 ? 16 : 32;  // of a TMEM load
 #pragma unroll
-            for (int c = 0; c < BN; c += 16) {
-                uint32_t v[16];
-                ptx::tmem_ld_32x32b_x16(taddr + c, v);
+            for (int c = 0; c < BN; c += kCols) {
+                uint32_t v[kCols];
+                tmem_ld<kCols>(taddr + c, v);
                 ptx::tmem_wait_ld();
                 if (p.swap) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < kCols; ++j) {
                         reinterpret_cast<float *>(smem)[(c + j) * C::LD_SWAP + row] = __uint_as_float(v[j]);
                     }
                 } else {
                     const uint32_t at = base + static_cast<uint32_t>(row * C::LD + c) * 4u;
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) ptx::st_shared_v4(at + j * 4u, v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    for (int j = 0; j < kCols; j += 4) ptx::st_shared_v4(at + j * 4u, v[j], v[j + 1], v[j + 2], v[j + 3]);
                 }
             }
         }
@@ -450,7 +460,10 @@ struct Fp4Pair {
     static constexpr int OFF_D = OFF_B + STAGES * S::B_BYTES;
     static constexpr int EPI_BUF = 32 * 128;                    // 32 rows of 128 bytes
     static constexpr int EPI_BUFS = 2;
-    static constexpr int OFF_SFA = OFF_D + 4 * EPI_BUFS * EPI_BUF;
+    static constexpr int ROW_PITCH = 128 * 2 + 16;              // a row of 128 elements, shifted up to 7
+    static constexpr int EPI_WARP = 32 * ROW_PITCH;             // 32 such rows (the same memory as the buffers)
+    static_assert(EPI_WARP >= EPI_BUFS * EPI_BUF && OFF_D % 1024 == 0, "staging");
+    static constexpr int OFF_SFA = OFF_D + (4 * EPI_WARP + 1023) / 1024 * 1024;
     static constexpr int OFF_SFB = OFF_SFA + STAGES * S::SFA_BYTES;
     static constexpr int OFF_BAR = OFF_SFB + STAGES * S::SFB_BYTES;
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4) * 8;
@@ -458,6 +471,81 @@ struct Fp4Pair {
     static constexpr int THREADS = 192;
     static_assert(ACC1 + 256 <= SF_COL && SMEM_ALLOC <= 232448, "TMEM columns, 227 KiB");
 };
+
+// Half HALF (128 columns) of a slice of 32 rows x 256 16-bit elements, a row a lane
+// (packed in w; `before`: the row's two elements before them), to rows of D that
+// start anywhere; the two halves one after the other.  A lane stages its row with
+// the shift that its address has within 16 bytes, so the row's whole units are
+// aligned in both memories, and 16 lanes move the units of a row.  The unit that
+// the halves share stays in the staging between them; what the slice's first and
+// last unit hold of the row goes element by element.  One warp runs on each
+// scheduler here and nothing hides its latencies, so the index arithmetic counts:
+// 1000 x 1529 x 256 takes 6.9 us (5.0 at 1528 columns, by TMA); with the units of
+// the whole warp's rows indexed in general it took 12.0, with one lane moving a
+// row's units 9.0.
+template <int HALF, int PITCH>
+__device__ __forceinline__ void store_unaligned(const Fp4Params &p, uint32_t staging, const uint32_t (&w)[64],
+                                                uint32_t before, int lane, int32_t row0, int32_t col0) {
+    uint16_t *first = static_cast<uint16_t *>(p.D) + static_cast<int64_t>(row0) * p.N + col0;  // row 0, the slice's start
+    const int cols = p.N - col0 - HALF * 128;  // from this half on; may be negative
+    const uint32_t own = staging + static_cast<uint32_t>(lane * PITCH);
+    const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(first + static_cast<int64_t>(lane) * p.N) / 2) & 7);
+    if (HALF == 1) {  // the shared unit: last of the first half, first of this one
+        const uint4 v = ptx::ld_shared_v4(own + 256u);
+        ptx::st_shared_v4(own, v.x, v.y, v.z, v.w);
+    }
+    const uint32_t at = own + static_cast<uint32_t>(shift / 2 * 4), odd = static_cast<uint32_t>(shift & 1) * 16u;
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(__funnelshift_l(before, w[0], odd)) : "memory");
+#pragma unroll
+    for (int k = 1; k < 64; ++k) {
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + k * 4u), "r"(__funnelshift_l(w[k - 1], w[k], odd)) : "memory");
+    }
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 256u), "r"(__funnelshift_l(w[63], 0u, odd)) : "memory");
+    __syncwarp();
+    const int valid = cols < 128 ? (cols > 0 ? cols : 0) : 128;
+    {
+        // lane: unit lane % 16 of rows lane / 16, 2 + lane / 16, ...
+        const uint16_t *row = first + HALF * 128 + static_cast<int64_t>(lane >> 4) * p.N;
+        const int unit = lane & 15;
+        const uint32_t from = staging + static_cast<uint32_t>((lane >> 4) * PITCH + unit * 16);
+        const int rows = p.M - row0 - (lane >> 4);
+        const int64_t two = 2 * static_cast<int64_t>(p.N);
+#pragma unroll
+        for (int i = 0; i < 16; ++i, row += two) {
+            const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row) / 2 & 7);
+            // the first half's first unit is whole without a shift, the second's always
+            if (2 * i < rows && unit * 8 + 8 <= s + valid && (HALF == 1 || s == 0 || unit > 0)) {
+                const uint4 v = ptx::ld_shared_v4(from + i * 2 * PITCH);
+                ptx::st_global_v4(const_cast<uint16_t *>(row) + (unit * 8 - s), v.x, v.y, v.z, v.w);
+            }
+        }
+    }
+    // Elements outside the whole units: the first half's first ones; at the row's end,
+    // or the slice's, its last ones.
+    if (row0 + lane < p.M) {
+        uint16_t *to = first + static_cast<int64_t>(lane) * p.N + HALF * 128 - shift;
+        const int end = shift + valid;
+        if (HALF == 0 && shift > 0) {
+            const uint4 v = ptx::ld_shared_v4(own);
+            const uint32_t e2[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 1; e < 8; ++e) {
+                if (e >= shift && e < end) to[e] = static_cast<uint16_t>(e2[e / 2] >> (e % 2 * 16));
+            }
+        }
+        const int tail = end / 8 * 8;
+        // none here where the next half continues it, or where it is the first unit
+        if (valid > 0 && (HALF == 1 || valid < 128 || cols == 128) && (HALF == 1 || tail > 0 || shift == 0)) {
+            const uint4 v = ptx::ld_shared_v4(own + static_cast<uint32_t>(tail * 2));
+            const uint32_t e2[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 7; ++e) {
+                if (tail + e < end) to[tail + e] = static_cast<uint16_t>(e2[e / 2] >> (e % 2 * 16));
+            }
+        }
+    }
+    __syncwarp();
+}
 
 template <bool NV>
 __global__ void __launch_bounds__(192, 1)
@@ -586,6 +674,7 @@ __global__ void __launch_bounds__(192, 1)
     } else {
         const int quarter = warp & 3;
         const uint32_t stage_base = base + C::OFF_D + static_cast<uint32_t>((warp - 2) * C::EPI_BUFS * C::EPI_BUF);
+        const uint32_t rows_base = base + C::OFF_D + static_cast<uint32_t>((warp - 2) * C::EPI_WARP);
         const uint32_t share_leader = ptx::mapa(bar_share, 0);
         uint32_t buf = 0, seq = 0;
         for (int item = cluster; item < tiles; item += clusters, ++seq) {
@@ -611,7 +700,7 @@ __global__ void __launch_bounds__(192, 1)
                 if (lane == 0) ptx::mbar_arrive_cluster(share_leader);
             };
             constexpr int kShared = (C::OVER + 63) / 64;  // chunks that hold shared columns
-            if (p.tma_store) {
+            if (p.d_type != LINEAR_F32) {
                 // the whole slice in registers, rounded, before any of it is stored
                 uint32_t h[4][32];
 #pragma unroll
@@ -629,6 +718,23 @@ __global__ void __launch_bounds__(192, 1)
                         h[i][16 + j] = pack16(p.d_type, __uint_as_float(hi[2 * j]) * p.alpha,
                                               __uint_as_float(hi[2 * j + 1]) * p.alpha);
                     }
+                }
+                if (!p.tma_store) {
+                    uint32_t w[64];  // the low 128 columns, then the high ones
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        w[j] = second ? h[0][j] : h[3][j];
+                        w[32 + j] = second ? h[1][j] : h[2][j];
+                    }
+                    store_unaligned<0, C::ROW_PITCH>(p, rows_base, w, 0u, lane, row0, col0);
+                    const uint32_t before = w[63];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        w[j] = second ? h[2][j] : h[1][j];
+                        w[32 + j] = second ? h[3][j] : h[0][j];
+                    }
+                    store_unaligned<1, C::ROW_PITCH>(p, rows_base, w, before, lane, row0, col0);
+                    continue;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -651,9 +757,8 @@ __global__ void __launch_bounds__(192, 1)
                     buf = (buf + 1u) % C::EPI_BUFS;
                 }
             } else {
-                // fp32, or rows that are not whole 16-byte units: 32 columns at a time
-                // through 32 x 32 floats of staging (row r's column c at c ^ r), read
-                // back by rows, one element a lane
+                // fp32: 32 columns at a time through 32 x 32 floats of staging (row r's
+                // column c at c ^ r), read back by rows, one element a lane
                 float *stage = reinterpret_cast<float *>(smem + (stage_base - base));
 #pragma unroll 1
                 for (int i = 0; i < 8; ++i) {

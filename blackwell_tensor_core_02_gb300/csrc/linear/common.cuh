@@ -47,98 +47,80 @@ struct alignas(VEC * sizeof(T)) Pack {
 template <typename T>
 constexpr int kUnit = 16 / static_cast<int>(sizeof(T));
 
-// Two values to and from their packed form, one rounding each.
+// Two values to and from the 32-bit words that hold them (two for fp32), one
+// rounding each.  Words, not the 16-bit pair classes: arrays of those are copied
+// one by one, and a 16-byte store becomes four.
 template <typename T>
 struct Pair;
 template <>
 struct Pair<float> {
-    using Raw = float2;
-    static __device__ __forceinline__ float2 widen(Raw r) { return r; }
-    static __device__ __forceinline__ Raw narrow(float2 v) { return v; }
+    static constexpr int WORDS = 2;
+    static __device__ __forceinline__ float2 widen(const uint32_t *w) {
+        return make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    }
+    static __device__ __forceinline__ void narrow(float2 v, uint32_t *w) {
+        w[0] = __float_as_uint(v.x);
+        w[1] = __float_as_uint(v.y);
+    }
 };
 template <>
 struct Pair<__half> {
-    using Raw = __half2;
-    static __device__ __forceinline__ float2 widen(Raw r) { return __half22float2(r); }
-    static __device__ __forceinline__ Raw narrow(float2 v) { return __floats2half2_rn(v.x, v.y); }
+    static constexpr int WORDS = 1;
+    static __device__ __forceinline__ float2 widen(const uint32_t *w) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(w));
+    }
+    static __device__ __forceinline__ void narrow(float2 v, uint32_t *w) {
+        const __half2 h = __floats2half2_rn(v.x, v.y);
+        *w = *reinterpret_cast<const uint32_t *>(&h);
+    }
 };
 template <>
 struct Pair<__nv_bfloat16> {
-    using Raw = __nv_bfloat162;
-    static __device__ __forceinline__ float2 widen(Raw r) { return __bfloat1622float2(r); }
-    static __device__ __forceinline__ Raw narrow(float2 v) { return __floats2bfloat162_rn(v.x, v.y); }
+    static constexpr int WORDS = 1;
+    static __device__ __forceinline__ float2 widen(const uint32_t *w) {
+        return make_float2(__uint_as_float(*w << 16), __uint_as_float(*w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ void narrow(float2 v, uint32_t *w) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+        *w = *reinterpret_cast<const uint32_t *>(&h);
+    }
 };
 
-// N pairs from and to consecutive memory, in 16-byte units where they fill them.
+// N pairs from and to consecutive memory in 16-byte units (N pairs fill whole ones).
 template <typename T, int N>
 __device__ __forceinline__ void load_pairs(const T *p, float2 *v) {
-    constexpr int kPer = 2 * N * sizeof(T) > 16 ? kUnit<T> / 2 : N;  // pairs of a load
+    constexpr int kWords = N * Pair<T>::WORDS;
+    static_assert(kWords % 4 == 0, "whole units");
+    uint32_t w[kWords];
 #pragma unroll
-    for (int i = 0; i < N; i += kPer) {
-        struct alignas(kPer * sizeof(typename Pair<T>::Raw)) Unit {
-            typename Pair<T>::Raw v[kPer];
-        };
-        const Unit u = *reinterpret_cast<const Unit *>(p + 2 * i);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) v[i + j] = Pair<T>::widen(u.v[j]);
+    for (int i = 0; i < kWords; i += 4) {
+        const uint4 u = *(reinterpret_cast<const uint4 *>(p) + i / 4);
+        w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = Pair<T>::widen(w + i * Pair<T>::WORDS);
 }
 template <typename T, int N>
 __device__ __forceinline__ void store_pairs(T *p, const float2 *v) {
-    constexpr int kPer = 2 * N * sizeof(T) > 16 ? kUnit<T> / 2 : N;
+    constexpr int kWords = N * Pair<T>::WORDS;
+    static_assert(kWords % 4 == 0, "whole units");
+    uint32_t w[kWords];
 #pragma unroll
-    for (int i = 0; i < N; i += kPer) {
-        struct alignas(kPer * sizeof(typename Pair<T>::Raw)) Unit {
-            typename Pair<T>::Raw v[kPer];
-        } u;
+    for (int i = 0; i < N; ++i) Pair<T>::narrow(v[i], w + i * Pair<T>::WORDS);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) u.v[j] = Pair<T>::narrow(v[i + j]);
-        *reinterpret_cast<Unit *>(p + 2 * i) = u;
+    for (int i = 0; i < kWords; i += 4) {
+        *(reinterpret_cast<uint4 *>(p) + i / 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     }
 }
 
-// A load of data that is read once: it leaves the L1 cache to what is read
-// again (the weights, which every row reads).
-template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> load_once(const T *p) {
-    Pack<T, VEC> r;
-    if constexpr (VEC * sizeof(T) == 16) {
-        uint4 u;
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                     : "l"(p)
-                     : "memory");
-        *reinterpret_cast<uint4 *>(&r) = u;
-    } else {
-        r = *reinterpret_cast<const Pack<T, VEC> *>(p);
-    }
-    return r;
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void load_f32(const T *p, float (&out)[VEC]) {
-    // VEC elements of T may be two 16-byte units (fp32 weights beside 16-bit rows)
-    constexpr int kBytes = VEC * static_cast<int>(sizeof(T));
-    constexpr int kPer = kBytes > 16 ? kUnit<T> : VEC;
-#pragma unroll
-    for (int i = 0; i < VEC / kPer; ++i) {
-        const Pack<T, kPer> u = *reinterpret_cast<const Pack<T, kPer> *>(p + i * kPer);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) out[i * kPer + j] = to_f32(u.v[j]);
-    }
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_f32(T *p, const float (&in)[VEC]) {
-    constexpr int kBytes = VEC * static_cast<int>(sizeof(T));
-    constexpr int kPer = kBytes > 16 ? kUnit<T> : VEC;
-#pragma unroll
-    for (int i = 0; i < VEC / kPer; ++i) {
-        Pack<T, kPer> u;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) u.v[j] = from_f32<T>(in[i * kPer + j]);
-        *reinterpret_cast<Pack<T, kPer> *>(p + i * kPer) = u;
-    }
+// 16 bytes that are read once: they leave the L1 cache to what is read again.
+__device__ __forceinline__ uint4 load_unit(const void *p) {
+    uint4 u;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "l"(p)
+                 : "memory");
+    return u;
 }
 
 // Two fp32 values in one 64-bit register pair: Blackwell adds, multiplies and

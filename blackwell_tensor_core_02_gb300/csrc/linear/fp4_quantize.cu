@@ -2,9 +2,10 @@
 // linear_ops.h).
 //
 // Bound by memory: 2 or 4 bytes an element on one side, 0.53 to 0.56 on the
-// other.  A thread owns 16 consecutive elements of a row, which is a block of
-// FP4_NV and half of one of FP4_MX, and 8 bytes of data; a scale word (4
-// blocks of a row) is gathered from 4 or 8 lanes and stored once.
+// other, which at 16 bits an element leaves some ten instructions for each.  A
+// thread owns a unit of 16 consecutive elements of a row, which is a block of
+// FP4_NV and half of one of FP4_MX, and 8 bytes of data; a scale word (4 blocks
+// of a row) is gathered from 4 or 8 lanes and stored once.
 #include "common.cuh"
 #include "fp4.cuh"
 
@@ -14,13 +15,13 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
 constexpr int kThreads = 256;
 
-// 16 floats to E2M1, to nearest with ties to the even code, magnitudes past 6
+// 8 pairs of floats to E2M1, to nearest with ties to the even code, magnitudes past 6
 // to 6: element 2i in the low nibble of byte i.
-__device__ __forceinline__ uint2 to_e2m1(const float (&v)[16]) {
+__device__ __forceinline__ uint2 to_e2m1(const float2 (&v)[8]) {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float *f = v + 8 * i;
+        const float2 *f = v + 4 * i;
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
@@ -28,13 +29,13 @@ __device__ __forceinline__ uint2 to_e2m1(const float (&v)[16]) {
             "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
             "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
             : "=r"(w[i])
-            : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+            : "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y));
     }
     return make_uint2(w[0], w[1]);
 }
 
-// The 8 values of 4 bytes of E2M1 codes.
-__device__ __forceinline__ void from_e2m1(uint32_t w, float (&v)[8]) {
+// The 4 pairs of values of 4 bytes of E2M1 codes.
+__device__ __forceinline__ void from_e2m1(uint32_t w, float2 *v) {
     uint32_t h[4];
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -45,11 +46,7 @@ __device__ __forceinline__ void from_e2m1(uint32_t w, float (&v)[8]) {
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(w));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
 }
 
 // E4M3 code of t (finite, 0 <= t <= 448), to nearest even.
@@ -73,102 +70,154 @@ __device__ __forceinline__ float from_e8m0(uint32_t code) {
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// A row's units along threadIdx.x (8 to 256 of them, so a scale word's lanes are
+// neighbours) and blockIdx.y, rows along threadIdx.y and blockIdx.x.
+struct Grid {
+    dim3 grid, block;
+};
+
+Grid grid_for(int64_t rows, int64_t units) {
+    int x = 8;
+    while (x < kThreads && x < units) x *= 2;
+    const int y = kThreads / x;
+    const int64_t chunks = (units + x - 1) / x;
+    return {dim3(static_cast<unsigned>((rows + y - 1) / y), static_cast<unsigned>(chunks < 65535 ? chunks : 65535)),
+            dim3(x, y)};
+}
+
+// The 16 elements of each lane's unit, where rows start anywhere: the lanes of a
+// row read its elements one after the other and meet in shared memory.
+// `group`: lanes of a row in the warp; `seg`: their elements, from the first of
+// lane 0's unit on; `left`: how many there are.
+template <typename T>
+__device__ __forceinline__ void read_scattered(const T *seg, int left, int group, T *stage, float (&v)[16]) {
+    const int lane = static_cast<int>(threadIdx.x) % group;
+    T *own = stage + ((threadIdx.y * blockDim.x + threadIdx.x) % 32 - lane) * 16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int e = i * group + lane;
+        own[e] = e < left ? seg[e] : from_f32<T>(0.f);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; i += kUnit<T>) {
+        const Pack<T, kUnit<T>> p = *reinterpret_cast<const Pack<T, kUnit<T>> *>(own + lane * 16 + i);
+#pragma unroll
+        for (int j = 0; j < kUnit<T>; ++j) v[i + j] = to_f32(p.v[j]);
+    }
+    __syncwarp();
+}
+
 struct QuantArgs {
     const void *x;
     uint8_t *data, *scales;
     int64_t x_stride;
-    int64_t work;        // threads: rows (to whole scale tiles) x units
-    int32_t rows, cols, units, data_units;  // units of 16 a row: with the scale tiles' rest, and of data
-    int32_t tiles;       // scale tiles along a row
+    int32_t rows, cols;
+    int32_t units, data_units;  // units of a row: with the scale tiles' rest, and of data
+    int32_t tiles;              // scale tiles along a row
     int32_t exponent;
 };
 
 template <typename T, bool NV, bool WIDE>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
-    if (threadIdx.x == 0) ptx::griddep_launch_dependents();
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const bool live = id < a.work;  // units is a multiple of 4 (NV) or 8: the lanes of a scale word agree
-    const int row = live ? static_cast<int>(id / a.units) : 0;
-    const int unit = live ? static_cast<int>(id - static_cast<int64_t>(row) * a.units) : 0;
-    const int col = unit * 16;
+    __shared__ __align__(16) T stage[WIDE ? 1 : kThreads * 16];
+    if (threadIdx.x == 0 && threadIdx.y == 0) ptx::griddep_launch_dependents();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool inside = row < a.rows;
+    const T *x = static_cast<const T *>(a.x) + (inside ? row : 0) * a.x_stride;
+    const bool padded = row < (static_cast<int64_t>(a.rows) + kScaleTileRows - 1) / kScaleTileRows * kScaleTileRows;
     ptx::griddep_wait();
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    if (live && row < a.rows && col < a.cols) {
-        const T *x = static_cast<const T *>(a.x) + static_cast<int64_t>(row) * a.x_stride + col;
+    for (int base = static_cast<int>(blockIdx.y * blockDim.x); base < a.units; base += static_cast<int>(gridDim.y * blockDim.x)) {
+        // units is a multiple of 4 (FP4_NV) or 8: the lanes of a scale word agree on `live`
+        const int unit = base + static_cast<int>(threadIdx.x), col = unit * 16;
+        const bool live = padded && unit < a.units;
+        float v[16];
         if constexpr (WIDE) {
             constexpr int U = kUnit<T>;
-            Pack<T, U> p[16 / U];
+            uint4 raw[16 / U];
 #pragma unroll
             for (int i = 0; i < 16 / U; ++i) {
-                if (col + i * U < a.cols) p[i] = *reinterpret_cast<const Pack<T, U> *>(x + i * U);
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (inside && col + i * U < a.cols) raw[i] = load_unit(x + col + i * U);
             }
 #pragma unroll
             for (int i = 0; i < 16 / U; ++i) {
-                if (col + i * U < a.cols) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-                    for (int j = 0; j < U; ++j) v[i * U + j] = to_f32(p[i].v[j]);
+                for (int j = 0; j < U / 2; ++j) {
+                    const float2 f = Pair<T>::widen(w + j * Pair<T>::WORDS);
+                    v[i * U + 2 * j] = f.x;
+                    v[i * U + 2 * j + 1] = f.y;
                 }
             }
         } else {
+            const int group = blockDim.x < 32 ? static_cast<int>(blockDim.x) : 32;
+            const int first = (unit - unit % group) * 16;
+            read_scattered<T>(x + first, inside ? a.cols - first : 0, group,
+                              stage + (threadIdx.y * blockDim.x + threadIdx.x) / 32 * 512, v);
+        }
+        // the largest magnitude as bits: they order like the values, and an infinity or
+        // NaN is above every finite one
+        uint32_t amax = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (col + i < a.cols) v[i] = to_f32(x[i]);
+        for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+        if constexpr (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        const bool bad = amax >= 0x7f800000u;
+        uint32_t code;
+        float2 q[8];
+        if constexpr (NV) {
+            // A quotient has to be rounded as a quotient, ties included.  With a reciprocal
+            // i of s within an ulp, q = x * i is off by a few ulps; one step with the exact
+            // remainder x - q * s leaves an error far below half an ulp before its rounding.
+            // That gives a quotient that is a tie of E2M1 (or E4M3; they have few bits)
+            // exactly, and no other quotient of fp32 numbers lies within half an ulp of one.
+            const float m = __uint_as_float(amax);
+            constexpr float sixth = 1.f / 6.f;
+            const float t0 = m * sixth, t = fmaf(fmaf(-t0, 6.f, m), sixth, t0) * pow2(-a.exponent);
+            code = to_e4m3(fminf(fmaxf(t, 0x1p-9f), 448.f));
+            const float s = from_e4m3(code) * pow2(a.exponent);
+            float inv;
+            asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 xi = make_float2(v[2 * i], v[2 * i + 1]), q0 = mul2(xi, both(inv));
+                q[i] = fma2(fma2(q0, both(-s), xi), both(inv), q0);
             }
-        }
-    }
-    // the largest magnitude as bits: they order like the values, and an
-    // infinity or NaN is above every finite one
-    uint32_t amax = 0;
+            if (m > 8.f * s) {
+                // the scale ended at its largest: quotients may overflow, and their
+                // remainders with them, but past 8 the code is 6 either way
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
-    if constexpr (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    const bool bad = amax >= 0x7f800000u;
-    uint32_t code;
-    if constexpr (NV) {
-        // Element / scale has to be rounded as the quotient, ties included.  With
-        // i = 1 / s rounded, q = x * i is within two units in the last place; one
-        // step with the exact remainder x - q * s gives the quotient to nearest,
-        // and where the quotient is a tie of E2M1 (which has few bits) exactly it.
-        const float t = __fdiv_rn(__uint_as_float(amax), 6.f) * pow2(-a.exponent);
-        code = to_e4m3(fminf(fmaxf(t, 0x1p-9f), 448.f));
-        const float s = from_e4m3(code) * pow2(a.exponent);
-        const float inv = __frcp_rn(s);
+                for (int i = 0; i < 8; ++i) {
+                    if (fabsf(v[2 * i] * inv) >= 8.f) q[i].x = copysignf(8.f, v[2 * i]);
+                    if (fabsf(v[2 * i + 1] * inv) >= 8.f) q[i].y = copysignf(8.f, v[2 * i + 1]);
+                }
+            }
+            if (bad) code = 0x7fu;
+        } else {
+            const uint32_t e = amax >> 23;  // floor(log2(amax)) + 127; 0 for zeros and subnormal values
+            code = e > 2u ? e - 2u : 0u;
+            const float inv = pow2(127 - static_cast<int>(code));  // code <= 252: 2^-125 .. 2^127
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float q = v[i] * inv;
-            // past 8 the code is 6 either way (and an overflowed q has no remainder)
-            if (fabsf(q) < 8.f) v[i] = fmaf(fmaf(-q, s, v[i]), inv, q);
-            else v[i] = q;
+            for (int i = 0; i < 8; ++i) q[i] = mul2(make_float2(v[2 * i], v[2 * i + 1]), both(inv));
+            if (bad) code = 0xffu;
         }
-        if (bad) code = 0x7fu;
-    } else {
-        const uint32_t e = amax >> 23;  // floor(log2(amax)) + 127; 0 for zeros and subnormal values
-        code = e > 2u ? e - 2u : 0u;
-        const float inv = pow2(127 - static_cast<int>(code));  // code <= 252: 2^-125 .. 2^127
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] *= inv;
-        if (bad) code = 0xffu;
-    }
-    uint2 packed = to_e2m1(v);
-    if (bad) packed = make_uint2(0u, 0u);
-    if (live && row < a.rows && unit < a.data_units) {
-        *reinterpret_cast<uint2 *>(a.data + (static_cast<int64_t>(row) * a.data_units + unit) * 8) = packed;
-    }
-    // rows and blocks past the matrix have scale 0
-    if (row >= a.rows || unit >= a.data_units) code = 0u;
-    if constexpr (NV) {
-        uint32_t word = code | (__shfl_down_sync(0xffffffffu, code, 1) << 8);
-        word |= __shfl_down_sync(0xffffffffu, word, 2) << 16;
-        if (live && unit % 4 == 0) {
-            *reinterpret_cast<uint32_t *>(a.scales + fp4_scale_at(row, unit, a.tiles)) = word;
+        uint2 packed = to_e2m1(q);
+        if (bad) packed = make_uint2(0u, 0u);
+        if (inside && unit < a.data_units) {
+            *reinterpret_cast<uint2 *>(a.data + (row * a.data_units + unit) * 8) = packed;
         }
-    } else {
-        uint32_t word = code | (__shfl_down_sync(0xffffffffu, code, 2) << 8);
-        word |= __shfl_down_sync(0xffffffffu, word, 4) << 16;
-        if (live && unit % 8 == 0) {
-            *reinterpret_cast<uint32_t *>(a.scales + fp4_scale_at(row, unit / 2, a.tiles)) = word;
+        // rows and blocks past the matrix have scale 0
+        if (!inside || unit >= a.data_units) code = 0u;
+        if constexpr (NV) {
+            uint32_t word = code | (__shfl_down_sync(0xffffffffu, code, 1) << 8);
+            word |= __shfl_down_sync(0xffffffffu, word, 2) << 16;
+            if (live && unit % 4 == 0) *reinterpret_cast<uint32_t *>(a.scales + fp4_scale_at(row, unit, a.tiles)) = word;
+        } else {
+            uint32_t word = code | (__shfl_down_sync(0xffffffffu, code, 2) << 8);
+            word |= __shfl_down_sync(0xffffffffu, word, 4) << 16;
+            if (live && unit % 8 == 0) {
+                *reinterpret_cast<uint32_t *>(a.scales + fp4_scale_at(row, unit / 2, a.tiles)) = word;
+            }
         }
     }
 }
@@ -176,43 +225,56 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
 struct DequantArgs {
     const uint8_t *data, *scales;
     void *out;
-    int64_t out_stride, work;
-    int32_t cols, data_units, tiles, exponent;
+    int64_t out_stride;
+    int32_t rows, cols, data_units, tiles, exponent;
 };
 
 template <typename T, bool NV, bool WIDE>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs a) {
-    if (threadIdx.x == 0) ptx::griddep_launch_dependents();
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (id >= a.work) return;
-    const int64_t row = id / a.data_units;
-    const int unit = static_cast<int>(id - row * a.data_units);
-    const int col = unit * 16;
+    __shared__ __align__(16) T stage[WIDE ? 1 : kThreads * 16];
+    if (threadIdx.x == 0 && threadIdx.y == 0) ptx::griddep_launch_dependents();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool inside = row < a.rows;
     ptx::griddep_wait();
-    const uint2 packed = *reinterpret_cast<const uint2 *>(a.data + id * 8);
-    const uint32_t code = a.scales[fp4_scale_at(row, NV ? unit : unit / 2, a.tiles)];
-    const float s = NV ? from_e4m3(code) * pow2(a.exponent) : from_e8m0(code);
-    float lo[8], hi[8], v[16];
-    from_e2m1(packed.x, lo);
-    from_e2m1(packed.y, hi);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = lo[i] * s, v[8 + i] = hi[i] * s;
-    T *out = static_cast<T *>(a.out) + row * a.out_stride + col;
-    if constexpr (WIDE) {
-        constexpr int U = kUnit<T>;
-#pragma unroll
-        for (int i = 0; i < 16 / U; ++i) {
-            if (col + i * U < a.cols) {
-                float f[U];
-#pragma unroll
-                for (int j = 0; j < U; ++j) f[j] = v[i * U + j];
-                store_f32<T, U>(out + i * U, f);
-            }
+    for (int base = static_cast<int>(blockIdx.y * blockDim.x); base < a.data_units;
+         base += static_cast<int>(gridDim.y * blockDim.x)) {
+        const int unit = base + static_cast<int>(threadIdx.x), col = unit * 16;
+        const bool live = inside && unit < a.data_units;
+        uint2 packed = make_uint2(0u, 0u);
+        uint32_t code = 0;
+        if (live) {
+            packed = *reinterpret_cast<const uint2 *>(a.data + (row * a.data_units + unit) * 8);
+            code = a.scales[fp4_scale_at(row, NV ? unit : unit / 2, a.tiles)];
         }
-    } else {
+        const float s = NV ? from_e4m3(code) * pow2(a.exponent) : from_e8m0(code);
+        float2 v[8];
+        from_e2m1(packed.x, v);
+        from_e2m1(packed.y, v + 4);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (col + i < a.cols) out[i] = from_f32<T>(v[i]);
+        for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], both(s));
+        T *out = static_cast<T *>(a.out) + row * a.out_stride;
+        if constexpr (WIDE) {
+            constexpr int U = kUnit<T>;
+#pragma unroll
+            for (int i = 0; i < 16 / U; ++i) {
+                if (live && col + i * U < a.cols) store_pairs<T, U / 2>(out + col + i * U, v + i * U / 2);
+            }
+        } else {
+            // rows start anywhere: through shared memory, one element a lane after the other
+            const int group = blockDim.x < 32 ? static_cast<int>(blockDim.x) : 32, lane = static_cast<int>(threadIdx.x) % group;
+            const int thread = static_cast<int>(threadIdx.y * blockDim.x + threadIdx.x);
+            T *own = stage + (thread - lane) * 16;
+            store_pairs<T, 8>(own + lane * 16, v);
+            __syncwarp();
+            const int first = (unit - lane) * 16;
+            if (inside) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int e = i * group + lane;
+                    if (first + e < a.cols) out[first + e] = own[e];
+                }
+            }
+            __syncwarp();
         }
     }
 }
@@ -220,25 +282,25 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
 template <typename T>
 int quantize_as(const QuantArgs &a, bool nv, cudaStream_t stream) {
     const bool wide = a.cols % kUnit<T> == 0 && a.x_stride % kUnit<T> == 0 && aligned(a.x, 16);
-    const dim3 grid(static_cast<unsigned>((a.work + kThreads - 1) / kThreads));
+    const Grid g = grid_for((static_cast<int64_t>(a.rows) + kScaleTileRows - 1) / kScaleTileRows * kScaleTileRows, a.units);
     if (nv) {
-        return wide ? launch(quantize_kernel<T, true, true>, grid, dim3(kThreads), 0, stream, a)
-                    : launch(quantize_kernel<T, true, false>, grid, dim3(kThreads), 0, stream, a);
+        return wide ? launch(quantize_kernel<T, true, true>, g.grid, g.block, 0, stream, a)
+                    : launch(quantize_kernel<T, true, false>, g.grid, g.block, 0, stream, a);
     }
-    return wide ? launch(quantize_kernel<T, false, true>, grid, dim3(kThreads), 0, stream, a)
-                : launch(quantize_kernel<T, false, false>, grid, dim3(kThreads), 0, stream, a);
+    return wide ? launch(quantize_kernel<T, false, true>, g.grid, g.block, 0, stream, a)
+                : launch(quantize_kernel<T, false, false>, g.grid, g.block, 0, stream, a);
 }
 
 template <typename T>
 int dequantize_as(const DequantArgs &a, bool nv, cudaStream_t stream) {
     const bool wide = a.cols % kUnit<T> == 0 && a.out_stride % kUnit<T> == 0 && aligned(a.out, 16);
-    const dim3 grid(static_cast<unsigned>((a.work + kThreads - 1) / kThreads));
+    const Grid g = grid_for(a.rows, a.data_units);
     if (nv) {
-        return wide ? launch(dequantize_kernel<T, true, true>, grid, dim3(kThreads), 0, stream, a)
-                    : launch(dequantize_kernel<T, true, false>, grid, dim3(kThreads), 0, stream, a);
+        return wide ? launch(dequantize_kernel<T, true, true>, g.grid, g.block, 0, stream, a)
+                    : launch(dequantize_kernel<T, true, false>, g.grid, g.block, 0, stream, a);
     }
-    return wide ? launch(dequantize_kernel<T, false, true>, grid, dim3(kThreads), 0, stream, a)
-                : launch(dequantize_kernel<T, false, false>, grid, dim3(kThreads), 0, stream, a);
+    return wide ? launch(dequantize_kernel<T, false, true>, g.grid, g.block, 0, stream, a)
+                : launch(dequantize_kernel<T, false, false>, g.grid, g.block, 0, stream, a);
 }
 
 int check_matrix(int64_t rows, int64_t cols, int32_t format, int32_t exponent) {
@@ -246,11 +308,7 @@ int check_matrix(int64_t rows, int64_t cols, int32_t format, int32_t exponent) {
         (format == FP4_MX && exponent != 0)) {
         return GEMM_ERR_INVALID_ARG;
     }
-    // a thread's number times 256 has to fit a grid: 2^31 CTAs
-    if (rows > kMaxDim || cols > kMaxDim || (cols > 0 && rows + 128 > (int64_t(1) << 42) / (cols + 256))) {
-        return GEMM_ERR_UNSUPPORTED_SHAPE;
-    }
-    return GEMM_OK;
+    return rows > kMaxDim || cols > kMaxDim ? GEMM_ERR_UNSUPPORTED_SHAPE : GEMM_OK;
 }
 
 }  // namespace
@@ -300,7 +358,6 @@ int fp4_quantize(const void *x, int64_t x_stride, int64_t rows, int64_t cols, in
     a.tiles = static_cast<int32_t>(fp4_scale_tiles(cols, nv));
     a.units = a.tiles * (nv ? 4 : 8);
     a.data_units = static_cast<int32_t>(fp4_padded_cols(cols) / 16);
-    a.work = (rows + kScaleTileRows - 1) / kScaleTileRows * kScaleTileRows * a.units;
     a.exponent = exponent;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return type == LINEAR_F16    ? quantize_as<__half>(a, nv, s)
@@ -332,7 +389,7 @@ int fp4_dequantize(const void *data, const void *scales, int64_t rows, int64_t c
     a.cols = static_cast<int32_t>(cols);
     a.data_units = static_cast<int32_t>(fp4_padded_cols(cols) / 16);
     a.tiles = static_cast<int32_t>(fp4_scale_tiles(cols, format == FP4_NV));
-    a.work = rows * a.data_units;
+    a.rows = static_cast<int32_t>(rows);
     a.exponent = exponent;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool nv = format == FP4_NV;

@@ -91,41 +91,43 @@ __global__ void __launch_bounds__(TPR *NormShape<T, E, WIDE, TPR>::ROWS, NormSha
 
 // Rows past the ring's, of whole units: a CTA of 256 threads a row, which holds it
 // as it came from memory (16-bit pairs: half the registers of fp32 values).
-template <typename T, typename W, int VEC, int NV>
+template <typename T, typename W, int NV>
 __global__ void __launch_bounds__(256) norm_forward_kernel(const NormArgs a) {
+    constexpr int U = kUnit<T>, step = 256 * U, P = Pair<T>::WORDS;
     __shared__ __align__(16) float slots[2][32];
     if (threadIdx.x == 0) ptx::griddep_launch_dependents();
     const int64_t row = blockIdx.x;
-    const int first = static_cast<int>(threadIdx.x) * VEC;
-    constexpr int step = 256 * VEC;
+    const int first = static_cast<int>(threadIdx.x) * U;
     const T *x = static_cast<const T *>(a.x) + row * a.x_stride + first;
     ptx::griddep_wait();
-    Pack<T, VEC> raw[NV];
-    float sum[1] = {0.f};
+    uint32_t raw[NV][4];
+    float2 s2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (first + i * step < a.cols) raw[i] = load_once<T, VEC>(x + i * step);
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (first + i * step < a.cols) u = load_unit(x + i * step);
+        raw[i][0] = u.x, raw[i][1] = u.y, raw[i][2] = u.z, raw[i][3] = u.w;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (first + i * step < a.cols) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sum[0] += to_f32(raw[i].v[j]);
-        }
+        for (int j = 0; j < U / 2; ++j) s2 = add2(s2, Pair<T>::widen(&raw[i][j * P]));
     }
+    float sum[1] = {s2.x + s2.y};
     row_sum<1, 256, 1>(sum, slots[0]);
     const float mean = sum[0] * a.inv_cols;
-    float var[1] = {0.f};
+    s2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (first + i * step < a.cols) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float d = to_f32(raw[i].v[j]) - mean;
-                var[0] += d * d;
+            for (int j = 0; j < U / 2; ++j) {
+                const float2 d = add2(Pair<T>::widen(&raw[i][j * P]), both(-mean));
+                s2 = fma2(d, d, s2);
             }
         }
     }
+    float var[1] = {s2.x + s2.y};
     row_sum<1, 256, 1>(var, slots[1]);
     const float rstd = 1.f / sqrtf(var[0] * a.inv_cols + a.eps);
     if (threadIdx.x == 0 && a.mean) {
@@ -136,14 +138,16 @@ __global__ void __launch_bounds__(256) norm_forward_kernel(const NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (first + i * step < a.cols) {
-            float w[VEC], b[VEC], out[VEC];
+            float2 w[U / 2], b[U / 2], out[U / 2];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) w[j] = 1.f, b[j] = 0.f;
-            if (a.weight) load_f32<W, VEC>(static_cast<const W *>(a.weight) + first + i * step, w);
-            if (a.bias) load_f32<W, VEC>(static_cast<const W *>(a.bias) + first + i * step, b);
+            for (int j = 0; j < U / 2; ++j) w[j] = both(1.f), b[j] = both(0.f);
+            if (a.weight) load_pairs<W, U / 2>(static_cast<const W *>(a.weight) + first + i * step, w);
+            if (a.bias) load_pairs<W, U / 2>(static_cast<const W *>(a.bias) + first + i * step, b);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) out[j] = (to_f32(raw[i].v[j]) - mean) * rstd * w[j] + b[j];
-            store_f32<T, VEC>(y + i * step, out);
+            for (int j = 0; j < U / 2; ++j) {
+                out[j] = fma2(mul2(add2(Pair<T>::widen(&raw[i][j * P]), both(-mean)), both(rstd)), w[j], b[j]);
+            }
+            store_pairs<T, U / 2>(y + i * step, out);
         }
     }
 }
@@ -198,8 +202,8 @@ int forward_rows(const NormArgs &a, int sms, cudaStream_t stream) {
     if constexpr (WIDE) {
         constexpr int U = kUnit<T>;
         const dim3 grid(a.rows), block(256);
-        if (a.cols <= 256 * 8 * U) return launch(norm_forward_kernel<T, W, U, 8>, grid, block, 0, stream, a);
-        if (a.cols <= 256 * 16 * U) return launch(norm_forward_kernel<T, W, U, 16>, grid, block, 0, stream, a);
+        if (a.cols <= 256 * 8 * U) return launch(norm_forward_kernel<T, W, 8>, grid, block, 0, stream, a);
+        if (a.cols <= 256 * 16 * U) return launch(norm_forward_kernel<T, W, 16>, grid, block, 0, stream, a);
     }
     return launch(norm_forward_long_kernel<T, W>, dim3(a.rows), dim3(1024), 0, stream, a);
 }

@@ -115,10 +115,9 @@ struct RowRing : RowShare<T, E, WIDE, TPR> {
         if constexpr (WIDE) {
             uint4 raw = make_uint4(0, 0, 0, 0);
             if (this->holds(i * U)) raw = ptx::ld_shared_v4(src + (i * TPR + threadIdx.x) * 16u);
-            using Raw = typename Pair<T>::Raw;
-            const Raw *p = reinterpret_cast<const Raw *>(&raw);
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-            for (int j = 0; j < U / 2; ++j) v[j] = Pair<T>::widen(p[j]);
+            for (int j = 0; j < U / 2; ++j) v[j] = Pair<T>::widen(w + j * Pair<T>::WORDS);
         } else {
             const uint32_t at = src + static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) % 16) +
                                 threadIdx.x * static_cast<uint32_t>(sizeof(T));

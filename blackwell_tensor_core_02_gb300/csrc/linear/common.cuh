@@ -123,6 +123,115 @@ __device__ __forceinline__ uint4 load_unit(const void *p) {
     return u;
 }
 
+// 32 bytes at a 32-byte boundary: one access fills whole sectors.
+__device__ __forceinline__ void load_32(const void *p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void store_32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// OUT words from `bytes` (0 to 15) on in a run of at least OUT + 4 words.
+template <int OUT, int IN>
+__device__ __forceinline__ void shift_words(const uint32_t (&in)[IN], uint32_t bytes, uint32_t (&out)[OUT]) {
+    static_assert(IN >= OUT + 4, "up to four more words");
+    uint32_t a[OUT + 3], b[OUT + 1];
+#pragma unroll
+    for (int i = 0; i < OUT + 3; ++i) a[i] = bytes & 4u ? in[i + 1] : in[i];
+#pragma unroll
+    for (int i = 0; i < OUT + 1; ++i) b[i] = bytes & 8u ? a[i + 2] : a[i];
+#pragma unroll
+    for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(b[i], b[i + 1], (bytes & 3u) * 8u);
+}
+
+// W words of a row of T that starts anywhere, from `p` on, of which `left` elements
+// are the row's (the others come as zeros): by the aligned 16-byte units that hold
+// them.  The first may start before p; it shares an aligned 16 bytes with *p, so
+// its allocation.  A unit that goes past the row's end is read by elements.
+template <typename T, int W>
+__device__ __forceinline__ void load_shifted(const T *p, int left, uint32_t (&w)[W]) {
+    constexpr int U = kUnit<T>, kElements = W * 4 / static_cast<int>(sizeof(T));
+    const uint32_t head = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) % 16);
+    const T *from = p - head / sizeof(T);
+    const int end = left + static_cast<int>(head / sizeof(T));  // of the row, from `from` on
+    uint32_t raw[W + 4];
+#pragma unroll
+    for (int i = 0; i < W + 4; i += 4) {
+        const int first = i / 4 * U;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (left > 0 && first + U <= end) {
+            if (first < kElements || head > 0) u = *reinterpret_cast<const uint4 *>(from + first);
+        } else if (left > 0 && first < end) {
+            uint32_t e[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (first + j < end && (i > 0 || j * sizeof(T) >= head)) {
+                    if constexpr (sizeof(T) == 4) {
+                        e[j] = reinterpret_cast<const uint32_t *>(from)[first + j];
+                    } else {
+                        e[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(from)[first + j]) << (j % 2 * 16);
+                    }
+                }
+            }
+            u = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+        raw[i] = u.x, raw[i + 1] = u.y, raw[i + 2] = u.z, raw[i + 3] = u.w;
+    }
+    shift_words<W>(raw, head, w);
+    if (left < kElements) {
+        constexpr int kPer = 4 / static_cast<int>(sizeof(T));  // elements of a word
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if (i * kPer >= left) w[i] = 0u;
+            if (kPer == 2 && i * kPer + 1 >= left) w[i] &= 0xffffu;
+        }
+    }
+}
+
+// The other way: a thread's run of W words of a row of T, `valid` elements of it
+// the row's, to `p`, anywhere.  w: the four words before the run, then the run.
+// The 16-byte unit that the run shares with the one before belongs to this thread
+// if `before` (w then has that run's end), and the one it shares with the next run
+// to that one's thread if `after`; else each stores its own elements of it.
+template <typename T, int N>
+__device__ __forceinline__ void store_shifted(T *p, int valid, bool before, bool after, const uint32_t (&w)[N]) {
+    constexpr int W = N - 4, U = kUnit<T>;
+    const uint32_t head = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) % 16);
+    const int skip = static_cast<int>(head / sizeof(T));  // elements of the first unit before p
+    T *to = p - skip;
+    uint32_t run[W + 8], out[W + 4];  // out: the words of the aligned units
+#pragma unroll
+    for (int i = 0; i < W + 8; ++i) {
+        const uint32_t shifted = i < N ? w[i < N ? i : 0] : 0u, plain = i + 4 < N ? w[i + 4 < N ? i + 4 : 0] : 0u;
+        run[i] = head ? shifted : plain;
+    }
+    shift_words<W + 4>(run, (16u - head) % 16u, out);
+    const int start = before ? 0 : skip, end = skip + valid;
+#pragma unroll
+    for (int i = 0; i < W + 4; i += 4) {
+        const int at = i / 4 * U;
+        if (at >= start && at + U <= end) {
+            *reinterpret_cast<uint4 *>(to + at) = make_uint4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+        } else if (at < end && !(after && at + U > end)) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (at + j >= start && at + j < end) {
+                    if constexpr (sizeof(T) == 4) {
+                        reinterpret_cast<uint32_t *>(to)[at + j] = out[i + j];
+                    } else {
+                        reinterpret_cast<uint16_t *>(to)[at + j] = static_cast<uint16_t>(out[i + j / 2] >> (j % 2 * 16));
+                    }
+                }
+            }
+        }
+    }
+}
+
 // Two fp32 values in one 64-bit register pair: Blackwell adds, multiplies and
 // fuses both in one instruction.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {

@@ -14,6 +14,8 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
 constexpr int kThreads = 256;
+// Columns that a grid's 65535 chunks of 256 units (grid_for, for wide rows) cover.
+constexpr int64_t kMaxCols = int64_t(65535) * kThreads * 16;
 
 // 8 pairs of floats to E2M1, to nearest with ties to the even code, magnitudes past 6
 // to 6: element 2i in the low nibble of byte i.
@@ -76,36 +78,14 @@ struct Grid {
     dim3 grid, block;
 };
 
+// As many threads of a row as leave at most an eighth of them without a unit (of
+// 257 units 256 threads would take two turns).
 Grid grid_for(int64_t rows, int64_t units) {
-    int x = 8;
-    while (x < kThreads && x < units) x *= 2;
+    int x = kThreads;
+    while (x > 8 && (units + x - 1) / x * x * 8 > units * 9) x /= 2;
     const int y = kThreads / x;
     const int64_t chunks = (units + x - 1) / x;
-    return {dim3(static_cast<unsigned>((rows + y - 1) / y), static_cast<unsigned>(chunks < 65535 ? chunks : 65535)),
-            dim3(x, y)};
-}
-
-// The 16 elements of each lane's unit, where rows start anywhere: the lanes of a
-// row read its elements one after the other and meet in shared memory.
-// `group`: lanes of a row in the warp; `seg`: their elements, from the first of
-// lane 0's unit on; `left`: how many there are.
-template <typename T>
-__device__ __forceinline__ void read_scattered(const T *seg, int left, int group, T *stage, float (&v)[16]) {
-    const int lane = static_cast<int>(threadIdx.x) % group;
-    T *own = stage + ((threadIdx.y * blockDim.x + threadIdx.x) % 32 - lane) * 16;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int e = i * group + lane;
-        own[e] = e < left ? seg[e] : from_f32<T>(0.f);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 16; i += kUnit<T>) {
-        const Pack<T, kUnit<T>> p = *reinterpret_cast<const Pack<T, kUnit<T>> *>(own + lane * 16 + i);
-#pragma unroll
-        for (int j = 0; j < kUnit<T>; ++j) v[i + j] = to_f32(p.v[j]);
-    }
-    __syncwarp();
+    return {dim3(static_cast<unsigned>((rows + y - 1) / y), static_cast<unsigned>(chunks)), dim3(x, y)};
 }
 
 struct QuantArgs {
@@ -118,49 +98,90 @@ struct QuantArgs {
     int32_t exponent;
 };
 
-template <typename T, bool NV, bool WIDE>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
-    __shared__ __align__(16) T stage[WIDE ? 1 : kThreads * 16];
+// How rows lie in memory: elements anywhere, whole 16-byte units, or whole 16
+// elements of which each 32 bytes are aligned (one access then fills sectors).
+enum : int { kScattered = 0, kUnits = 1, kSectors = 2 };
+
+// The largest magnitude of a thread's elements as fp32 bits.  Bits order like the
+// magnitudes, and an infinity or NaN is above every finite one; 16-bit elements are
+// compared two at a time.
+template <typename T, int N>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&w)[N]) {
+    uint32_t m = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = max(m, w[i] & 0x7fffffffu);
+        return m;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w[i] & 0x7fff7fffu));
+        m = max(m & 0xffffu, m >> 16);
+        return __float_as_uint(Pair<T>::widen(&m).x);
+    }
+}
+
+// FP4_NV, with the longer arithmetic, runs on a grid of the CTAs that fit at once: a
+// thread takes rows a grid apart and loads its unit of the next row while it works
+// on this one (8192 x 4096 bf16: 17.4 us, a CTA for each row 18.7; FP4_MX 15.6 and
+// 15.4, so it takes a CTA for each row, and so do rows that start anywhere, whose
+// loads take more registers).
+template <typename T, bool NV, int LAYOUT>
+constexpr bool kAhead = NV && LAYOUT != kScattered;
+template <typename T, bool NV, int LAYOUT>
+constexpr int kQuantizePerSm = kAhead<T, NV, LAYOUT> || sizeof(T) == 4 ? 4 : 5;
+
+template <typename T, bool NV, int LAYOUT>
+__global__ void __launch_bounds__(kThreads, kQuantizePerSm<T, NV, LAYOUT>) quantize_kernel(const QuantArgs a) {
     if (threadIdx.x == 0 && threadIdx.y == 0) ptx::griddep_launch_dependents();
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    const bool inside = row < a.rows;
-    const T *x = static_cast<const T *>(a.x) + (inside ? row : 0) * a.x_stride;
-    const bool padded = row < (static_cast<int64_t>(a.rows) + kScaleTileRows - 1) / kScaleTileRows * kScaleTileRows;
-    ptx::griddep_wait();
-    for (int base = static_cast<int>(blockIdx.y * blockDim.x); base < a.units; base += static_cast<int>(gridDim.y * blockDim.x)) {
-        // units is a multiple of 4 (FP4_NV) or 8: the lanes of a scale word agree on `live`
-        const int unit = base + static_cast<int>(threadIdx.x), col = unit * 16;
-        const bool live = padded && unit < a.units;
-        float v[16];
-        if constexpr (WIDE) {
-            constexpr int U = kUnit<T>;
-            uint4 raw[16 / U];
+    const int64_t rows = (static_cast<int64_t>(a.rows) + kScaleTileRows - 1) / kScaleTileRows * kScaleTileRows;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    // units is a multiple of 4 (FP4_NV) or 8: the lanes of a scale word agree on `live`
+    const int unit = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x), col = unit * 16;
+    const bool live = unit < a.units;
+    constexpr int W = 16 * sizeof(T) / 4;
+    // this thread's unit of a row as it lies in memory, zeros past the matrix
+    auto fetch = [&](int64_t row, uint32_t (&w)[W]) {
 #pragma unroll
-            for (int i = 0; i < 16 / U; ++i) {
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (inside && col + i * U < a.cols) raw[i] = load_unit(x + col + i * U);
+        for (int i = 0; i < W; ++i) w[i] = 0u;
+        if (row >= a.rows) return;
+        const T *x = static_cast<const T *>(a.x) + row * a.x_stride + col;
+        if constexpr (LAYOUT == kSectors) {
+#pragma unroll
+            for (int i = 0; i < W; i += 8) {
+                if (col < a.cols) load_32(x + i * 4 / static_cast<int>(sizeof(T)), reinterpret_cast<uint32_t (&)[8]>(w[i]));
             }
+        } else if constexpr (LAYOUT == kUnits) {
 #pragma unroll
-            for (int i = 0; i < 16 / U; ++i) {
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-                for (int j = 0; j < U / 2; ++j) {
-                    const float2 f = Pair<T>::widen(w + j * Pair<T>::WORDS);
-                    v[i * U + 2 * j] = f.x;
-                    v[i * U + 2 * j + 1] = f.y;
+            for (int i = 0; i < W; i += 4) {
+                const int c = i * 4 / static_cast<int>(sizeof(T));
+                if (col + c < a.cols) {
+                    const uint4 u = load_unit(x + c);
+                    w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
                 }
             }
         } else {
-            const int group = blockDim.x < 32 ? static_cast<int>(blockDim.x) : 32;
-            const int first = (unit - unit % group) * 16;
-            read_scattered<T>(x + first, inside ? a.cols - first : 0, group,
-                              stage + (threadIdx.y * blockDim.x + threadIdx.x) / 32 * 512, v);
+            load_shifted<T>(x, a.cols - col, w);
         }
-        // the largest magnitude as bits: they order like the values, and an infinity or
-        // NaN is above every finite one
-        uint32_t amax = 0;
+    };
+    ptx::griddep_wait();
+    uint32_t next[W];
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.y;  // whole CTAs take part in the shuffles
+    if constexpr (kAhead<T, NV, LAYOUT>) fetch(first + threadIdx.y, next);
+    for (int64_t base = first; base < rows; base += step) {
+        const int64_t row = base + threadIdx.y;
+        const bool inside = row < a.rows;
+        uint32_t w[W];
+        if constexpr (kAhead<T, NV, LAYOUT>) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+            for (int i = 0; i < W; ++i) w[i] = next[i];
+            if (base + step < rows) fetch(row + step, next);
+        } else {
+            fetch(row, w);
+        }
+        float2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = Pair<T>::widen(w + i * Pair<T>::WORDS);
+        uint32_t amax = largest<T>(w);
         if constexpr (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         const bool bad = amax >= 0x7f800000u;
         uint32_t code;
@@ -177,19 +198,19 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
             code = to_e4m3(fminf(fmaxf(t, 0x1p-9f), 448.f));
             const float s = from_e4m3(code) * pow2(a.exponent);
             float inv;
-            asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 xi = make_float2(v[2 * i], v[2 * i + 1]), q0 = mul2(xi, both(inv));
-                q[i] = fma2(fma2(q0, both(-s), xi), both(inv), q0);
+                const float2 q0 = mul2(v[i], both(inv));
+                q[i] = fma2(fma2(q0, both(-s), v[i]), both(inv), q0);
             }
             if (m > 8.f * s) {
                 // the scale ended at its largest: quotients may overflow, and their
                 // remainders with them, but past 8 the code is 6 either way
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (fabsf(v[2 * i] * inv) >= 8.f) q[i].x = copysignf(8.f, v[2 * i]);
-                    if (fabsf(v[2 * i + 1] * inv) >= 8.f) q[i].y = copysignf(8.f, v[2 * i + 1]);
+                    if (fabsf(v[i].x * inv) >= 8.f) q[i].x = copysignf(8.f, v[i].x);
+                    if (fabsf(v[i].y * inv) >= 8.f) q[i].y = copysignf(8.f, v[i].y);
                 }
             }
             if (bad) code = 0x7fu;
@@ -198,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
             code = e > 2u ? e - 2u : 0u;
             const float inv = pow2(127 - static_cast<int>(code));  // code <= 252: 2^-125 .. 2^127
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = mul2(make_float2(v[2 * i], v[2 * i + 1]), both(inv));
+            for (int i = 0; i < 8; ++i) q[i] = mul2(v[i], both(inv));
             if (bad) code = 0xffu;
         }
         uint2 packed = to_e2m1(q);
@@ -211,11 +232,13 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
         if constexpr (NV) {
             uint32_t word = code | (__shfl_down_sync(0xffffffffu, code, 1) << 8);
             word |= __shfl_down_sync(0xffffffffu, word, 2) << 16;
-            if (live && unit % 4 == 0) *reinterpret_cast<uint32_t *>(a.scales + fp4_scale_at(row, unit, a.tiles)) = word;
+            if (live && row < rows && unit % 4 == 0) {
+                *reinterpret_cast<uint32_t *>(a.scales + fp4_scale_at(row, unit, a.tiles)) = word;
+            }
         } else {
             uint32_t word = code | (__shfl_down_sync(0xffffffffu, code, 2) << 8);
             word |= __shfl_down_sync(0xffffffffu, word, 4) << 16;
-            if (live && unit % 8 == 0) {
+            if (live && row < rows && unit % 8 == 0) {
                 *reinterpret_cast<uint32_t *>(a.scales + fp4_scale_at(row, unit / 2, a.tiles)) = word;
             }
         }
@@ -229,16 +252,14 @@ struct DequantArgs {
     int32_t rows, cols, data_units, tiles, exponent;
 };
 
-template <typename T, bool NV, bool WIDE>
+template <typename T, bool NV, int LAYOUT>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs a) {
-    __shared__ __align__(16) T stage[WIDE ? 1 : kThreads * 16];
     if (threadIdx.x == 0 && threadIdx.y == 0) ptx::griddep_launch_dependents();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool inside = row < a.rows;
     ptx::griddep_wait();
-    for (int base = static_cast<int>(blockIdx.y * blockDim.x); base < a.data_units;
-         base += static_cast<int>(gridDim.y * blockDim.x)) {
-        const int unit = base + static_cast<int>(threadIdx.x), col = unit * 16;
+    {
+        const int unit = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x), col = unit * 16;
         const bool live = inside && unit < a.data_units;
         uint2 packed = make_uint2(0u, 0u);
         uint32_t code = 0;
@@ -253,62 +274,87 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], both(s));
         T *out = static_cast<T *>(a.out) + row * a.out_stride;
-        if constexpr (WIDE) {
+        if constexpr (LAYOUT == kSectors) {
+            constexpr int P = Pair<T>::WORDS;
+            uint32_t w[8 * P];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) Pair<T>::narrow(v[i], w + i * P);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                if (live && col < a.cols) store_32(out + col + i * 8, reinterpret_cast<const uint32_t (&)[8]>(w[i * 8]));
+            }
+        } else if constexpr (LAYOUT == kUnits) {
             constexpr int U = kUnit<T>;
 #pragma unroll
             for (int i = 0; i < 16 / U; ++i) {
                 if (live && col + i * U < a.cols) store_pairs<T, U / 2>(out + col + i * U, v + i * U / 2);
             }
         } else {
-            // rows start anywhere: through shared memory, one element a lane after the other
-            const int group = blockDim.x < 32 ? static_cast<int>(blockDim.x) : 32, lane = static_cast<int>(threadIdx.x) % group;
-            const int thread = static_cast<int>(threadIdx.y * blockDim.x + threadIdx.x);
-            T *own = stage + (thread - lane) * 16;
-            store_pairs<T, 8>(own + lane * 16, v);
-            __syncwarp();
-            const int first = (unit - lane) * 16;
-            if (inside) {
+            // Rows start anywhere: a lane's unit and the end of the lane before's give it the
+            // aligned units of 16 bytes that begin in its unit or the one before; elements of
+            // no whole one go by themselves.
+            const int group = blockDim.x < 32 ? static_cast<int>(blockDim.x) : 32;  // lanes of this row
+            const bool first = threadIdx.x % group == 0, final = threadIdx.x % group == group - 1;
+            constexpr int P = Pair<T>::WORDS, W = 8 * P;
+            uint32_t w[W + 4];  // four words of the lane before, then this lane's
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int e = i * group + lane;
-                    if (first + e < a.cols) out[first + e] = own[e];
-                }
+            for (int i = 0; i < 8; ++i) Pair<T>::narrow(v[i], w + 4 + i * P);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, w[W + i], 1);
+            if (live && col < a.cols) {
+                store_shifted<T>(out + col, a.cols - col < 16 ? a.cols - col : 16, !first, !final && col + 16 < a.cols, w);
             }
-            __syncwarp();
         }
     }
 }
 
-template <typename T>
-int quantize_as(const QuantArgs &a, bool nv, cudaStream_t stream) {
-    const bool wide = a.cols % kUnit<T> == 0 && a.x_stride % kUnit<T> == 0 && aligned(a.x, 16);
-    const Grid g = grid_for((static_cast<int64_t>(a.rows) + kScaleTileRows - 1) / kScaleTileRows * kScaleTileRows, a.units);
-    if (nv) {
-        return wide ? launch(quantize_kernel<T, true, true>, g.grid, g.block, 0, stream, a)
-                    : launch(quantize_kernel<T, true, false>, g.grid, g.block, 0, stream, a);
-    }
-    return wide ? launch(quantize_kernel<T, false, true>, g.grid, g.block, 0, stream, a)
-                : launch(quantize_kernel<T, false, false>, g.grid, g.block, 0, stream, a);
+// The layout of rows at `p` with that stride.
+int layout_of(const void *p, int64_t stride, int64_t cols, int64_t size) {
+    if (cols % 16 == 0 && stride * size % 32 == 0 && aligned(p, 32)) return kSectors;
+    return cols * size % 16 == 0 && stride * size % 16 == 0 && aligned(p, 16) ? kUnits : kScattered;
 }
 
-template <typename T>
-int dequantize_as(const DequantArgs &a, bool nv, cudaStream_t stream) {
-    const bool wide = a.cols % kUnit<T> == 0 && a.out_stride % kUnit<T> == 0 && aligned(a.out, 16);
-    const Grid g = grid_for(a.rows, a.data_units);
-    if (nv) {
-        return wide ? launch(dequantize_kernel<T, true, true>, g.grid, g.block, 0, stream, a)
-                    : launch(dequantize_kernel<T, true, false>, g.grid, g.block, 0, stream, a);
+template <typename T, bool NV, int LAYOUT>
+int quantize_rows(const QuantArgs &a, int sms, cudaStream_t stream) {
+    Grid g = grid_for((static_cast<int64_t>(a.rows) + kScaleTileRows - 1) / kScaleTileRows * kScaleTileRows, a.units);
+    if (kAhead<T, NV, LAYOUT>) {
+        const unsigned fit = (kQuantizePerSm<T, NV, LAYOUT> * static_cast<unsigned>(sms) + g.grid.y - 1) / g.grid.y;
+        if (g.grid.x > fit) g.grid.x = fit;
     }
-    return wide ? launch(dequantize_kernel<T, false, true>, g.grid, g.block, 0, stream, a)
-                : launch(dequantize_kernel<T, false, false>, g.grid, g.block, 0, stream, a);
+    return launch(quantize_kernel<T, NV, LAYOUT>, g.grid, g.block, 0, stream, a);
 }
+
+template <typename T, bool NV>
+int quantize_as(const QuantArgs &a, int sms, cudaStream_t stream) {
+    switch (layout_of(a.x, a.x_stride, a.cols, sizeof(T))) {
+        case kSectors: return quantize_rows<T, NV, kSectors>(a, sms, stream);
+        case kUnits: return quantize_rows<T, NV, kUnits>(a, sms, stream);
+        default: return quantize_rows<T, NV, kScattered>(a, sms, stream);
+    }
+}
+
+template <typename T, bool NV>
+int dequantize_as(const DequantArgs &a, cudaStream_t stream) {
+    const Grid g = grid_for(a.rows, a.data_units);
+    switch (layout_of(a.out, a.out_stride, a.cols, sizeof(T))) {
+        case kSectors: return launch(dequantize_kernel<T, NV, kSectors>, g.grid, g.block, 0, stream, a);
+        case kUnits: return launch(dequantize_kernel<T, NV, kUnits>, g.grid, g.block, 0, stream, a);
+        default: return launch(dequantize_kernel<T, NV, kScattered>, g.grid, g.block, 0, stream, a);
+    }
+}
+
+// The element type and the format as template arguments.
+#define LINEAR_BY_FORMAT(type, nv, FN, ...)                                                    \
+    ((type) == LINEAR_F16    ? ((nv) ? FN<__half, true>(__VA_ARGS__) : FN<__half, false>(__VA_ARGS__)) \
+     : (type) == LINEAR_BF16 ? ((nv) ? FN<__nv_bfloat16, true>(__VA_ARGS__) : FN<__nv_bfloat16, false>(__VA_ARGS__)) \
+                             : ((nv) ? FN<float, true>(__VA_ARGS__) : FN<float, false>(__VA_ARGS__)))
 
 int check_matrix(int64_t rows, int64_t cols, int32_t format, int32_t exponent) {
     if (rows < 0 || cols < 0 || (format != FP4_MX && format != FP4_NV) || exponent < -100 || exponent > 100 ||
         (format == FP4_MX && exponent != 0)) {
         return GEMM_ERR_INVALID_ARG;
     }
-    return rows > kMaxDim || cols > kMaxDim ? GEMM_ERR_UNSUPPORTED_SHAPE : GEMM_OK;
+    return rows > kMaxDim || cols > kMaxCols ? GEMM_ERR_UNSUPPORTED_SHAPE : GEMM_OK;
 }
 
 }  // namespace
@@ -360,9 +406,7 @@ int fp4_quantize(const void *x, int64_t x_stride, int64_t rows, int64_t cols, in
     a.data_units = static_cast<int32_t>(fp4_padded_cols(cols) / 16);
     a.exponent = exponent;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return type == LINEAR_F16    ? quantize_as<__half>(a, nv, s)
-           : type == LINEAR_BF16 ? quantize_as<__nv_bfloat16>(a, nv, s)
-                                 : quantize_as<float>(a, nv, s);
+    return LINEAR_BY_FORMAT(type, nv, quantize_as, a, sms, s);
 }
 
 int fp4_dequantize(const void *data, const void *scales, int64_t rows, int64_t cols, int32_t format, int32_t exponent,
@@ -393,9 +437,7 @@ int fp4_dequantize(const void *data, const void *scales, int64_t rows, int64_t c
     a.exponent = exponent;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool nv = format == FP4_NV;
-    return type == LINEAR_F16    ? dequantize_as<__half>(a, nv, s)
-           : type == LINEAR_BF16 ? dequantize_as<__nv_bfloat16>(a, nv, s)
-                                 : dequantize_as<float>(a, nv, s);
+    return LINEAR_BY_FORMAT(type, nv, dequantize_as, a, s);
 }
 
 }  // extern "C"

@@ -13,6 +13,13 @@
 
 namespace linear_ops {
 
+// Elements of a row that a thread holds, and the threads: a sum over a row costs
+// each warp some 50 instructions and a barrier, so few warps with many elements
+// are faster (8192 x 4096 bf16 forward, us: 8 elements 36.6, 16 25.4, 32 23.7;
+// gradient 66, 41.4, 41.7), and whole warps up to 8 serve each width up to 8192.
+constexpr int kEach = 32;
+constexpr int kRingCols = 256 * kEach;
+
 // The columns of a row that the TPR threads of threadIdx.x hold, E each, as pairs.
 //   WIDE   rows are whole 16-byte units: thread t holds units t, t + TPR, ...
 //   else   rows start anywhere: thread t holds columns t, t + TPR, ...
@@ -22,11 +29,16 @@ struct RowShare {
     static constexpr int NV = E / U;  // units of a thread
     static_assert(E % U == 0, "whole units");
     int cols;
-    // the first column, and whether element e (a constant) is one of the row
+    // the column of element e (a constant after unrolling), and whether it is one of
+    // the row's: known without a comparison for what the narrowest row of this shape
+    // has (LINEAR_ROW_SHAPES: E elements for each thread but the last warp's)
     __device__ __forceinline__ int column(int e) const {
         return WIDE ? (e / U * TPR + static_cast<int>(threadIdx.x)) * U + e % U : e * TPR + static_cast<int>(threadIdx.x);
     }
-    __device__ __forceinline__ bool holds(int e) const { return column(WIDE ? e / U * U : e) < cols; }
+    __device__ __forceinline__ bool holds(int e) const {
+        const int past = WIDE ? (e / U + 1) * U * TPR : (e + 1) * TPR;  // every thread's element e lies before this
+        return (E == kEach && past <= (TPR - 32) * E) || column(WIDE ? e / U * U : e) < cols;
+    }
 
     // this thread's values of a vector by columns, `fill` past its end
     template <typename W>
@@ -151,13 +163,6 @@ struct RowRing : RowShare<T, E, WIDE, TPR> {
 // ------------------------------------------------------------------- host --
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
-
-// Elements of a row that a thread holds, and the threads: a sum over a row costs
-// each warp some 50 instructions and a barrier, so few warps with many elements
-// are faster (8192 x 4096 bf16 forward, us: 8 elements 36.6, 16 25.4, 32 23.7;
-// gradient 66, 41.4, 41.7), and whole warps up to 8 serve each width up to 8192.
-constexpr int kEach = 32;
-constexpr int kRingCols = 256 * kEach;
 
 // CASE(E, threads) of the first shape that holds a.cols.
 #define LINEAR_ROW_SHAPES(CASE)          \

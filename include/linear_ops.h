@@ -79,7 +79,8 @@ int64_t layer_norm_backward_workspace_size(int64_t rows, int64_t cols);
  */
 typedef enum fp4_format { FP4_MX = 0, FP4_NV = 1 } fp4_format_t;
 
-/* Bytes of data and scales of such a matrix; negative gemm_status_t on bad arguments. */
+/* Bytes of data and scales of such a matrix; negative gemm_status_t on bad arguments
+ * (GEMM_ERR_UNSUPPORTED_SHAPE for more than 2^31 - 1024 rows or 65535 * 4096 columns). */
 int64_t fp4_data_bytes(int64_t rows, int64_t cols);
 int64_t fp4_scale_bytes(int64_t rows, int64_t cols, int32_t format);
 
@@ -131,7 +132,7 @@ typedef struct gemm_fp4_options {
  * alpha (2^(exponent of A + exponent of B)).  A, B and their scales are
  * 16-byte aligned; D is aligned to its elements (16-byte aligned rows are
  * faster) and overlaps none of them.  M or N 0: nothing is launched; K 0:
- * D = 0.  M, N, K <= 2^31 - 1024.
+ * D = 0.  M, N <= 2^31 - 1024, K as the columns of a quantised matrix.
  */
 int gemm_fp4_nt(const void *A, const void *A_scales, const void *B, const void *B_scales, void *D, int64_t M, int64_t N,
                 int64_t K, int32_t format, int32_t d_type, float alpha, void *stream, const gemm_fp4_options *opts);

@@ -5,8 +5,8 @@
 namespace linear_ops {
 namespace {
 
-// Parts of the weights' gradient: at most two CTAs for each of 152 SMs.
-constexpr int kMaxParts = 304;
+// Parts of the weights' gradient: a CTA for each of 152 SMs.
+constexpr int kMaxParts = 152;
 
 // Floats from a fold's dweight to its dbias: whole units.
 __host__ __device__ constexpr int fold_stride(int cols) { return (cols + 3) / 4 * 4; }
@@ -190,34 +190,57 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const GradArgs a) {
     part[a.cols + col] = sb;
 }
 
-// dweight (blockIdx.y 0) or dbias (1) of 32 columns: thread row y adds every
-// 32nd part, then the 32 thread rows are added in order.
-template <typename W>
-__global__ void __launch_bounds__(1024) norm_join_kernel(const float *partial, int parts, int cols, W *dweight,
-                                                         W *dbias) {
-    __shared__ float s[32][33];
+// dweight (blockIdx.y 0) or dbias (1) of 32 columns: each thread adds four columns
+// of every 32nd part (all its loads on their way at once), then the part lanes of
+// a warp and the warps are added, in a fixed order.
+constexpr int kPartLanes = 32;
+
+template <typename W, bool WIDE>
+__global__ void __launch_bounds__(256) norm_join_kernel(const float *partial, int parts, int cols, W *dweight,
+                                                        W *dbias) {
+    __shared__ float4 s[8][8];
+    if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+    const int quad = static_cast<int>(threadIdx.x) % 8, lane = static_cast<int>(threadIdx.x) / 8;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + quad * 4;
+    const float *p = partial + static_cast<int64_t>(blockIdx.y) * cols + col;
+    constexpr int kEach = (kMaxParts + kPartLanes - 1) / kPartLanes;
+    float4 v[kEach];
     ptx::griddep_wait();
-    if (threadIdx.x == 0 && threadIdx.y == 0) ptx::griddep_launch_dependents();
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-    float sum = 0.f;
-    if (col < cols) {
-        const float *p = partial + static_cast<int64_t>(blockIdx.y) * cols + col;
-        float v[(kMaxParts + 31) / 32];  // every load on its way before the first sum
 #pragma unroll
-        for (int k = 0; k < (kMaxParts + 31) / 32; ++k) {
-            const int i = k * 32 + static_cast<int>(threadIdx.y);
-            v[k] = i < parts ? p[static_cast<int64_t>(i) * 2 * cols] : 0.f;
+    for (int k = 0; k < kEach; ++k) {
+        const int i = k * kPartLanes + lane;
+        const float *from = p + static_cast<int64_t>(i) * 2 * cols;
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < parts) {
+            if constexpr (WIDE) {
+                if (col < cols) v[k] = *reinterpret_cast<const float4 *>(from);
+            } else {
+                if (col < cols) v[k].x = from[0];
+                if (col + 1 < cols) v[k].y = from[1];
+                if (col + 2 < cols) v[k].z = from[2];
+                if (col + 3 < cols) v[k].w = from[3];
+            }
         }
-#pragma unroll
-        for (int k = 0; k < (kMaxParts + 31) / 32; ++k) sum += v[k];
     }
-    s[threadIdx.y][threadIdx.x] = sum;
-    __syncthreads();
-    float t = s[threadIdx.x][threadIdx.y];
+    float4 t = v[0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && out < cols) (blockIdx.y ? dbias : dweight)[out] = from_f32<W>(t);
+    for (int k = 1; k < kEach; ++k) t.x += v[k].x, t.y += v[k].y, t.z += v[k].z, t.w += v[k].w;
+#pragma unroll
+    for (int o = 8; o < 32; o *= 2) {
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+        t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+        t.z += __shfl_xor_sync(0xffffffffu, t.z, o);
+        t.w += __shfl_xor_sync(0xffffffffu, t.w, o);
+    }
+    if (threadIdx.x % 32 < 8) s[threadIdx.x / 32][quad] = t;
+    __syncthreads();
+    const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+    if (threadIdx.x < 32 && out < cols) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) sum += reinterpret_cast<const float *>(s[w])[threadIdx.x];
+        (blockIdx.y ? dbias : dweight)[out] = from_f32<W>(sum);
+    }
 }
 
 // ------------------------------------------------------------------- host --
@@ -261,7 +284,9 @@ int backward_as(const GradArgs &a, void *dweight, void *dbias, int sms, cudaStre
                             : backward_rows<T, W, false>(a, sms, &parts, stream);
         if (st != GEMM_OK || !dweight) return st;
     }
-    return launch(norm_join_kernel<W>, dim3((a.cols + 31) / 32, 2), dim3(32, 32), 0, stream, a.partial, parts, a.cols,
+    // parts lie 2 * cols floats apart, dbias cols after dweight
+    auto *join = a.cols % 4 == 0 ? norm_join_kernel<W, true> : norm_join_kernel<W, false>;
+    return launch(join, dim3((a.cols + 31) / 32, 2), dim3(256), 0, stream, a.partial, parts, a.cols,
                   static_cast<W *>(dweight), static_cast<W *>(dbias));
 }
 

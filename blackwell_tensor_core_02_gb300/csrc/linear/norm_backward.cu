@@ -146,48 +146,105 @@ __global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
     ring.scatter(part + a.cols, sb);
 }
 
-// Rows too long for registers: dx by one CTA per row in two passes, ...
-template <typename T, typename W>
+// Rows too long for registers: dx by one CTA per row in two passes, the second
+// from L2, ...
+template <typename T, typename W, bool WIDE>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const GradArgs a) {
+    constexpr int VEC = WIDE ? kUnit<T> : 2;  // of a thread and step; odd rows by pairs of any alignment
     __shared__ __align__(16) float slot[64];
     if (threadIdx.x == 0) ptx::griddep_launch_dependents();
     const int64_t row = blockIdx.x;
     const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
     const T *dy = static_cast<const T *>(a.dy) + row * a.dy_stride;
     T *dx = static_cast<T *>(a.dx) + row * a.dx_stride;
+    const W *weight = static_cast<const W *>(a.weight);
     ptx::griddep_wait();
-    const float m = a.mean[row], rs = a.rstd[row];
-    float sums[2] = {0.f, 0.f};
-    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
-        const float g = to_f32(dy[c]) * (a.weight ? to_f32(static_cast<const W *>(a.weight)[c]) : 1.f);
-        sums[0] += g;
-        sums[1] += g * ((to_f32(x[c]) - m) * rs);
+    const float2 m = both(-a.mean[row]), rs = both(a.rstd[row]);
+    // h and g of VEC columns from c on
+    auto fetch = [&](int64_t c, float2 (&h)[VEC / 2], float2 (&g)[VEC / 2]) {
+        if constexpr (WIDE) {
+            load_pairs<T, VEC / 2>(x + c, h);
+            load_pairs<T, VEC / 2>(dy + c, g);
+        } else {
+            const bool two = c + 1 < a.cols;
+            h[0] = make_float2(to_f32(x[c]), two ? to_f32(x[c + 1]) : 0.f);
+            g[0] = make_float2(to_f32(dy[c]), two ? to_f32(dy[c + 1]) : 0.f);
+        }
+        float2 w[VEC / 2];
+        if constexpr (WIDE) {
+            if (weight) load_pairs<W, VEC / 2>(weight + c, w);
+        } else {
+            if (weight) w[0] = make_float2(to_f32(weight[c]), c + 1 < a.cols ? to_f32(weight[c + 1]) : 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            h[i] = mul2(add2(h[i], m), rs);
+            if (weight) g[i] = mul2(g[i], w[i]);
+        }
+    };
+    float2 s0 = both(0.f), s1 = both(0.f);
+    for (int64_t c = static_cast<int64_t>(threadIdx.x) * VEC; c < a.cols; c += 1024 * VEC) {
+        float2 h[VEC / 2], g[VEC / 2];
+        fetch(c, h, g);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) s0 = add2(s0, g[i]), s1 = fma2(g[i], h[i], s1);
     }
+    float sums[2] = {s0.x + s0.y, s1.x + s1.y};
     row_sum<2, 1024, 1>(sums, slot);
-    const float c1 = sums[0] * a.inv_cols, c2 = sums[1] * a.inv_cols;
-    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
-        const float g = to_f32(dy[c]) * (a.weight ? to_f32(static_cast<const W *>(a.weight)[c]) : 1.f);
-        dx[c] = from_f32<T>(rs * (g - c1 - (to_f32(x[c]) - m) * rs * c2));
+    const float2 c1 = both(-sums[0] * a.inv_cols), c2 = both(-sums[1] * a.inv_cols);
+    for (int64_t c = static_cast<int64_t>(threadIdx.x) * VEC; c < a.cols; c += 1024 * VEC) {
+        float2 h[VEC / 2], g[VEC / 2];
+        fetch(c, h, g);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) g[i] = mul2(fma2(h[i], c2, add2(g[i], c1)), rs);
+        if constexpr (WIDE) {
+            store_pairs<T, VEC / 2>(dx + c, g);
+        } else {
+            dx[c] = from_f32<T>(g[0].x);
+            if (c + 1 < a.cols) dx[c + 1] = from_f32<T>(g[0].y);
+        }
     }
 }
 
 // ... and the weights' partial sums by columns: blockIdx.y takes every
-// gridDim.y-th row.
-template <typename T>
+// gridDim.y-th row, a thread VEC columns.
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) norm_columns_kernel(const GradArgs a) {
+    constexpr int VEC = WIDE ? kUnit<T> : 1;
     if (threadIdx.x == 0) ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t col = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * VEC;
     if (col >= a.cols) return;
-    float sw = 0.f, sb = 0.f;
-    for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-        const float d = to_f32(static_cast<const T *>(a.dy)[r * a.dy_stride + col]);
-        sw += d * ((to_f32(static_cast<const T *>(a.x)[r * a.x_stride + col]) - a.mean[r]) * a.rstd[r]);
-        sb += d;
+    float *part = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * a.cols + col;
+    if constexpr (WIDE) {
+        float2 sw[VEC / 2], sb[VEC / 2];
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) sw[i] = sb[i] = both(0.f);
+#pragma unroll 4
+        for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+            float2 h[VEC / 2], d[VEC / 2];
+            load_pairs<T, VEC / 2>(static_cast<const T *>(a.x) + r * a.x_stride + col, h);
+            load_pairs<T, VEC / 2>(static_cast<const T *>(a.dy) + r * a.dy_stride + col, d);
+            const float2 m = both(-a.mean[r]), rs = both(a.rstd[r]);
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                sw[i] = fma2(d[i], mul2(add2(h[i], m), rs), sw[i]);
+                sb[i] = add2(sb[i], d[i]);
+            }
+        }
+        store_pairs<float, VEC / 2>(part, sw);
+        store_pairs<float, VEC / 2>(part + a.cols, sb);
+    } else {
+        float sw = 0.f, sb = 0.f;
+#pragma unroll 4
+        for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+            const float d = to_f32(static_cast<const T *>(a.dy)[r * a.dy_stride + col]);
+            sw += d * ((to_f32(static_cast<const T *>(a.x)[r * a.x_stride + col]) - a.mean[r]) * a.rstd[r]);
+            sb += d;
+        }
+        part[0] = sw;
+        part[a.cols] = sb;
     }
-    float *part = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * a.cols;
-    part[col] = sw;
-    part[a.cols + col] = sb;
 }
 
 // dweight (blockIdx.y 0) or dbias (1) of 32 columns: each thread adds four columns
@@ -264,10 +321,11 @@ int backward_rows(const GradArgs &a, int sms, int *parts, cudaStream_t stream) {
 #define LINEAR_CASE(E, TPR) return backward_ring<T, W, E, WIDE, TPR>(a, sms, parts, stream)
     LINEAR_ROW_SHAPES(LINEAR_CASE)
 #undef LINEAR_CASE
-    int st = launch(norm_backward_long_kernel<T, W>, dim3(a.rows), dim3(1024), 0, stream, a);
+    int st = launch(norm_backward_long_kernel<T, W, WIDE>, dim3(a.rows), dim3(1024), 0, stream, a);
     if (st == GEMM_OK && a.partial) {
+        constexpr int kCols = 256 * (WIDE ? kUnit<T> : 1);
         *parts = grid_of(a.rows, 1, kMaxParts);
-        st = launch(norm_columns_kernel<T>, dim3((a.cols + 255) / 256, *parts), dim3(256), 0, stream, a);
+        st = launch(norm_columns_kernel<T, WIDE>, dim3((a.cols + kCols - 1) / kCols, *parts), dim3(256), 0, stream, a);
     }
     return st;
 }

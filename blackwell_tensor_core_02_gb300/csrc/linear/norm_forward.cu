@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(256) norm_forward_kernel(const NormArgs a) {
     }
 }
 
-// Rows too long for registers: one CTA of 1024 threads passes over its row
-// three times (sum, centred squares, output), the second and third from L2.
+// Rows too long for registers: one CTA of 1024 threads passes over its row three
+// times (sum, centred squares, output), the second and third from L2.
 template <typename T, typename W>
 __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs a) {
     __shared__ __align__(16) float slots[2][32];
@@ -163,9 +163,11 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs 
     T *y = static_cast<T *>(a.y) + row * a.y_stride;
     ptx::griddep_wait();
     float sum[1] = {0.f}, var[1] = {0.f};
+#pragma unroll 8
     for (int64_t c = threadIdx.x; c < a.cols; c += 1024) sum[0] += to_f32(x[c]);
     row_sum<1, 1024, 1>(sum, slots[0]);
     const float mean = sum[0] * a.inv_cols;
+#pragma unroll 8
     for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
         const float d = to_f32(x[c]) - mean;
         var[0] += d * d;
@@ -176,6 +178,7 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs 
         a.mean[row] = mean;
         a.rstd[row] = rstd;
     }
+#pragma unroll 4
     for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
         const float w = a.weight ? to_f32(static_cast<const W *>(a.weight)[c]) : 1.f;
         const float b = a.bias ? to_f32(static_cast<const W *>(a.bias)[c]) : 0.f;

@@ -8,14 +8,14 @@ namespace {
 // Parts of the weights' gradient: a CTA for each of 152 SMs.
 constexpr int kMaxParts = 152;
 
-// Floats from a fold's dweight to its dbias: whole units.
-__host__ __device__ constexpr int fold_stride(int cols) { return (cols + 3) / 4 * 4; }
+// Floats of a part's dweight, and of its dbias: whole 16-byte units.
+__host__ __device__ constexpr int64_t part_stride(int64_t cols) { return (cols + 3) / 4 * 4; }
 
 struct GradArgs {
     const void *dy, *x, *weight;
     const float *mean, *rstd;
     void *dx;
-    float *partial;  // [parts][2][cols]: sums over some rows of dy * h, then of dy
+    float *partial;  // [parts][2][part_stride(cols)]: sums over some rows of dy * h, then of dy
     int64_t dy_stride, x_stride, dx_stride;
     int32_t rows, cols;
     float inv_cols;
@@ -36,8 +36,7 @@ struct GradShape {
     static constexpr int ROW_BYTES = RowRing<T, E, WIDE, TPR, 2, STAGES>::BYTES;
     static constexpr int BY_SMEM = 200 * 1024 / ROW_BYTES, BY_THREADS = E == 8 ? 512 / TPR : 384 / TPR;
     static constexpr int ROWS = BY_SMEM < BY_THREADS ? BY_SMEM : BY_THREADS;  // at most
-    // the rows' sums meet in the ring's memory, half of them at a time
-    static_assert(ROWS == 1 || ROWS * ROW_BYTES >= (ROWS / 2) * 2 * 4 * TPR * E, "room for the sums");
+    static_assert(ROW_BYTES >= 2 * 4 * TPR * E, "a row's ring holds its sums");
 };
 
 template <typename T, typename W, int E, bool WIDE, int TPR>
@@ -118,32 +117,28 @@ __global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
         ring.next();
     }
     if (!a.partial) return;
-    cp_async_wait<0>();
-    const int dbias_at = fold_stride(a.cols);
-    for (int n = static_cast<int>(blockDim.y); n > 1;) {
-        const int keep = (n + 1) / 2, r = static_cast<int>(threadIdx.y);
-        float *fold = reinterpret_cast<float *>(ring_mem) + (r < keep ? r : r - keep) * 2 * dbias_at;
-        __syncthreads();
-        if (r >= keep && r < n) {
-            ring.scatter(fold, sw);
-            ring.scatter(fold + dbias_at, sb);
-        }
-        __syncthreads();
-        if (r < n - keep) {
-            float2 o[E / 2];
-            ring.gather(static_cast<const float *>(fold), 0.f, o);
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i) sw[i] = add2(sw[i], o[i]);
-            ring.gather(static_cast<const float *>(fold + dbias_at), 0.f, o);
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i) sb[i] = add2(sb[i], o[i]);
-        }
-        n = keep;
+    const int stride = static_cast<int>(part_stride(a.cols));
+    float *part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * stride;
+    if (blockDim.y == 1) {
+        ring.scatter(part, sw);
+        ring.scatter(part + stride, sb);
+        return;
     }
-    if (threadIdx.y != 0) return;
-    float *part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-    ring.scatter(part, sw);
-    ring.scatter(part + a.cols, sb);
+    // each row of threads puts its sums where its ring was, then all threads add them up
+    cp_async_wait<0>();
+    row_barrier<TPR, ROWS>();
+    float *own = reinterpret_cast<float *>(ring_mem + threadIdx.y * Ring::BYTES);
+    ring.scatter(own, sw);
+    ring.scatter(own + stride, sb);
+    __syncthreads();
+    for (int u = static_cast<int>(threadIdx.y * TPR + threadIdx.x); u < stride / 2; u += static_cast<int>(blockDim.y) * TPR) {
+        float4 t = *(reinterpret_cast<const float4 *>(ring_mem) + u);
+        for (int r = 1; r < static_cast<int>(blockDim.y); ++r) {
+            const float4 o = *(reinterpret_cast<const float4 *>(ring_mem + r * Ring::BYTES) + u);
+            t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
+        }
+        *(reinterpret_cast<float4 *>(part) + u) = t;
+    }
 }
 
 // Rows too long for registers: dx by one CTA per row in two passes, the second
@@ -215,7 +210,8 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const GradArgs a) {
     ptx::griddep_wait();
     const int64_t col = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * VEC;
     if (col >= a.cols) return;
-    float *part = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * a.cols + col;
+    const int64_t stride = part_stride(a.cols);
+    float *part = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * stride + col;
     if constexpr (WIDE) {
         float2 sw[VEC / 2], sb[VEC / 2];
 #pragma unroll
@@ -233,7 +229,7 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const GradArgs a) {
             }
         }
         store_pairs<float, VEC / 2>(part, sw);
-        store_pairs<float, VEC / 2>(part + a.cols, sb);
+        store_pairs<float, VEC / 2>(part + stride, sb);
     } else {
         float sw = 0.f, sb = 0.f;
 #pragma unroll 4
@@ -243,7 +239,7 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const GradArgs a) {
             sb += d;
         }
         part[0] = sw;
-        part[a.cols] = sb;
+        part[stride] = sb;
     }
 }
 
@@ -252,32 +248,23 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const GradArgs a) {
 // a warp and the warps are added, in a fixed order.
 constexpr int kPartLanes = 32;
 
-template <typename W, bool WIDE>
+template <typename W>
 __global__ void __launch_bounds__(256) norm_join_kernel(const float *partial, int parts, int cols, W *dweight,
                                                         W *dbias) {
     __shared__ float4 s[8][8];
     if (threadIdx.x == 0) ptx::griddep_launch_dependents();
     const int quad = static_cast<int>(threadIdx.x) % 8, lane = static_cast<int>(threadIdx.x) / 8;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + quad * 4;
-    const float *p = partial + static_cast<int64_t>(blockIdx.y) * cols + col;
+    const int64_t stride = part_stride(cols);
+    const float *p = partial + static_cast<int64_t>(blockIdx.y) * stride + col;
     constexpr int kEach = (kMaxParts + kPartLanes - 1) / kPartLanes;
     float4 v[kEach];
     ptx::griddep_wait();
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
         const int i = k * kPartLanes + lane;
-        const float *from = p + static_cast<int64_t>(i) * 2 * cols;
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < parts) {
-            if constexpr (WIDE) {
-                if (col < cols) v[k] = *reinterpret_cast<const float4 *>(from);
-            } else {
-                if (col < cols) v[k].x = from[0];
-                if (col + 1 < cols) v[k].y = from[1];
-                if (col + 2 < cols) v[k].z = from[2];
-                if (col + 3 < cols) v[k].w = from[3];
-            }
-        }
+        if (i < parts && col < cols) v[k] = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(i) * 2 * stride);
     }
     float4 t = v[0];
 #pragma unroll
@@ -342,9 +329,7 @@ int backward_as(const GradArgs &a, void *dweight, void *dbias, int sms, cudaStre
                             : backward_rows<T, W, false>(a, sms, &parts, stream);
         if (st != GEMM_OK || !dweight) return st;
     }
-    // parts lie 2 * cols floats apart, dbias cols after dweight
-    auto *join = a.cols % 4 == 0 ? norm_join_kernel<W, true> : norm_join_kernel<W, false>;
-    return launch(join, dim3((a.cols + 31) / 32, 2), dim3(256), 0, stream, a.partial, parts, a.cols,
+    return launch(norm_join_kernel<W>, dim3((a.cols + 31) / 32, 2), dim3(256), 0, stream, a.partial, parts, a.cols,
                   static_cast<W *>(dweight), static_cast<W *>(dbias));
 }
 
@@ -358,7 +343,7 @@ extern "C" {
 int64_t layer_norm_backward_workspace_size(int64_t rows, int64_t cols) {
     if (!sizes_ok(rows, cols)) return GEMM_ERR_INVALID_ARG;
     if (rows > kMaxDim || cols > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
-    return (rows < kMaxParts ? rows : kMaxParts) * 2 * cols * 4;
+    return (rows < kMaxParts ? rows : kMaxParts) * 2 * part_stride(cols) * 4;
 }
 
 int layer_norm_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride, const void *weight,

@@ -15,7 +15,7 @@ struct NormArgs {
     float eps, inv_cols;
 };
 
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 
 // Rows of a CTA: 128 threads' worth; CTAs of an SM: 512 threads (32 elements, their
 // weights and biases take 100 registers) and what their rings leave room for.

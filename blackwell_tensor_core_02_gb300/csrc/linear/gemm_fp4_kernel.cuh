@@ -45,6 +45,12 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// An arrival, possibly on the peer's barrier, that publishes no memory writes: a
+// release at cluster scope would first wait for all of the thread's.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // Shared-memory descriptor of one scale tile: no swizzle, 8 x 16-byte core
 // matrices 128 bytes apart (fields as in ptx::smem_desc_k_sw128).
 __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
@@ -117,11 +123,9 @@ struct Fp4Stage {
     static constexpr int SF_COLS = SFA_COLS + SFB_COLS;
     static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "1 KiB swizzle atoms");
 
-    // The copies of a stage's scales and its four MMAs.  B's rows start on a
-    // scale tile: the MMA takes its scales from a multiple of 4 columns on (an
-    // odd column is a misaligned address), so not from a tile's middle.
-    static __device__ __forceinline__ void issue(uint32_t sa, uint32_t sb, uint32_t ssfa, uint32_t ssfb, uint32_t tsf,
-                                                 uint32_t d, bool first) {
+    // The copies of a stage's scales to TMEM columns `tsf`, in order with the MMAs
+    // issued before and after them.
+    static __device__ __forceinline__ void copy_scales(uint32_t ssfa, uint32_t ssfb, uint32_t tsf) {
         const uint32_t tsfa = tsf, tsfb = tsf + SFA_COLS;
 #pragma unroll
         for (int j = 0; j < SF_TILES; ++j) {
@@ -132,6 +136,12 @@ struct Fp4Stage {
                                       ptx4::scale_desc(ssfb + (r * SF_TILES + j) * kScaleTileBytes));
             }
         }
+    }
+    // A stage's four MMAs.  B's rows start on a scale tile: the MMA takes its scales
+    // from a multiple of 4 columns on (an odd column is a misaligned address), so not
+    // from a tile's middle.
+    static __device__ __forceinline__ void multiply(uint32_t sa, uint32_t sb, uint32_t tsf, uint32_t d, bool first) {
+        const uint32_t tsfa = tsf, tsfb = tsf + SFA_COLS;
         const uint64_t a_desc = ptx::smem_desc_k_sw128(sa), b_desc = ptx::smem_desc_k_sw128(sb);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -351,10 +361,10 @@ __global__ void __launch_bounds__(192, 2)
                 }
                 ptx::tcgen05_fence_after();
                 const int s = ring.stage;
-                S::issue(base + C::OFF_A + s * S::A_BYTES, base + C::OFF_B + s * S::B_BYTES,
-                         base + C::OFF_SFA + s * S::SFA_BYTES, base + C::OFF_SFB + s * S::SFB_BYTES,
-                         tmem_base + C::SF_COL + (kt - kt_begin) % C::SF_BUFS * S::SF_COLS, tmem_base,
-                         kt == kt_begin);
+                const uint32_t tsf = tmem_base + C::SF_COL + (kt - kt_begin) % C::SF_BUFS * S::SF_COLS;
+                S::copy_scales(base + C::OFF_SFA + s * S::SFA_BYTES, base + C::OFF_SFB + s * S::SFB_BYTES, tsf);
+                S::multiply(base + C::OFF_A + s * S::A_BYTES, base + C::OFF_B + s * S::B_BYTES, tsf, tmem_base,
+                            kt == kt_begin);
                 ptx::mma_commit<1>(bar_empty + 8 * s, 0x1);
                 ring.advance();
             }
@@ -427,7 +437,10 @@ __global__ void __launch_bounds__(192, 2)
         }
     }
     if constexpr (KS > 1) {
-        ptx::cluster_sync();  // no CTA leaves while another reads its sums
+        // no CTA leaves while another reads its sums (they are in registers by now; the
+        // arrival need not wait for this thread's stores to D, as a release would)
+        ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
     } else {
         __syncthreads();
     }
@@ -642,13 +655,6 @@ __global__ void __launch_bounds__(192, 1)
             bool ok = true;
             uint32_t seq = 0, stage_seq = 0;
             for (int item = cluster; ok && item < tiles; item += clusters, ++seq) {
-                // the previous tile's epilogue has read the columns both accumulators share
-                if (!wait_bounded(bar_share, share.phase, abort_flag, p.timeout_ns, gemm_f16::kRoleMma, seq)) {
-                    ok = false;
-                    break;
-                }
-                share.advance();
-                ptx::tcgen05_fence_after();
                 const uint32_t d = tmem_base + (seq % 2 ? C::ACC1 : 0);
                 for (int kt = 0; kt < p.k_tiles; ++kt, ++stage_seq) {
                     if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns,
@@ -658,9 +664,18 @@ __global__ void __launch_bounds__(192, 1)
                     }
                     ptx::tcgen05_fence_after();
                     const int s = ring.stage;
-                    S::issue(base + C::OFF_A + s * S::A_BYTES, base + C::OFF_B + s * S::B_BYTES,
-                             base + C::OFF_SFA + s * S::SFA_BYTES, base + C::OFF_SFB + s * S::SFB_BYTES,
-                             tmem_base + C::SF_COL + stage_seq % C::SF_BUFS * S::SF_COLS, d, kt == 0);
+                    const uint32_t tsf = tmem_base + C::SF_COL + stage_seq % C::SF_BUFS * S::SF_COLS;
+                    S::copy_scales(base + C::OFF_SFA + s * S::SFA_BYTES, base + C::OFF_SFB + s * S::SFB_BYTES, tsf);
+                    if (kt == 0) {
+                        // the previous tile's epilogue has read the columns both accumulators share
+                        if (!wait_bounded(bar_share, share.phase, abort_flag, p.timeout_ns, gemm_f16::kRoleMma, seq)) {
+                            ok = false;
+                            break;
+                        }
+                        share.advance();
+                        ptx::tcgen05_fence_after();
+                    }
+                    S::multiply(base + C::OFF_A + s * S::A_BYTES, base + C::OFF_B + s * S::B_BYTES, tsf, d, kt == 0);
                     ptx::mma_commit<2>(bar_empty + 8 * s, 0x3);
                     ring.advance();
                 }
@@ -697,7 +712,7 @@ __global__ void __launch_bounds__(192, 1)
             auto hand_over = [&]() {
                 ptx::tcgen05_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(share_leader);
+                if (lane == 0) ptx4::mbar_arrive_cluster_relaxed(share_leader);
             };
             constexpr int kShared = (C::OVER + 63) / 64;  // chunks that hold shared columns
             if (p.d_type != LINEAR_F32) {
@@ -787,8 +802,11 @@ __global__ void __launch_bounds__(192, 1)
         if (lane == 0) ptx::bulk_wait_group_read<0>();
         __syncwarp();
     }
+    // the pair's CTAs done with TMEM and with each other's barriers (nothing in memory
+    // is published here, so the arrival waits for no store)
     ptx::tcgen05_fence_before();
-    ptx::cluster_sync();
+    ptx::cluster_arrive_relaxed();
+    ptx::cluster_wait();
     if (warp == 1) {
         ptx::tcgen05_fence_after();
         ptx::tmem_dealloc<2>(tmem_base, 512);

@@ -152,19 +152,21 @@ __device__ __forceinline__ void shift_words(const uint32_t (&in)[IN], uint32_t b
 // W words of a row of T that starts anywhere, from `p` on, of which `left` elements
 // are the row's (the others come as zeros): by the aligned 16-byte units that hold
 // them.  The first may start before p; it shares an aligned 16 bytes with *p, so
-// its allocation.  A unit that goes past the row's end is read by elements.
+// its allocation.  The last may go past the row's end, but not past the matrix's,
+// `all` elements from p on: that one unit is read by elements.
 template <typename T, int W>
-__device__ __forceinline__ void load_shifted(const T *p, int left, uint32_t (&w)[W]) {
+__device__ __forceinline__ void load_shifted(const T *p, int left, int64_t all, uint32_t (&w)[W]) {
     constexpr int U = kUnit<T>, kElements = W * 4 / static_cast<int>(sizeof(T));
     const uint32_t head = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) % 16);
     const T *from = p - head / sizeof(T);
     const int end = left + static_cast<int>(head / sizeof(T));  // of the row, from `from` on
+    const int64_t last = all + static_cast<int64_t>(head / sizeof(T));
     uint32_t raw[W + 4];
 #pragma unroll
     for (int i = 0; i < W + 4; i += 4) {
         const int first = i / 4 * U;
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (left > 0 && first + U <= end) {
+        if (left > 0 && first < end && first + U <= last) {
             if (first < kElements || head > 0) u = *reinterpret_cast<const uint4 *>(from + first);
         } else if (left > 0 && first < end) {
             uint32_t e[4] = {0, 0, 0, 0};

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, kQuantizePerSm<T, NV, LAYOUT>) quant
                 }
             }
         } else {
-            load_shifted<T>(x, a.cols - col, w);
+            load_shifted<T>(x, a.cols - col, (a.rows - 1 - row) * a.x_stride + a.cols - col, w);
         }
     };
     ptx::griddep_wait();

@@ -34,7 +34,7 @@ template <typename T, int E, bool WIDE, int TPR>
 struct GradShape {
     static constexpr int STAGES = 3;
     static constexpr int ROW_BYTES = RowRing<T, E, WIDE, TPR, 2, STAGES>::BYTES;
-    static constexpr int BY_SMEM = 200 * 1024 / ROW_BYTES, BY_THREADS = E == 8 ? 512 / TPR : 384 / TPR;
+    static constexpr int BY_SMEM = 200 * 1024 / ROW_BYTES, BY_THREADS = E <= 16 ? 512 / TPR : 384 / TPR;
     static constexpr int ROWS = BY_SMEM < BY_THREADS ? BY_SMEM : BY_THREADS;  // at most
     static_assert(ROW_BYTES >= 2 * 4 * TPR * E, "a row's ring holds its sums");
 };

@@ -29,15 +29,18 @@ struct RowShare {
     static constexpr int NV = E / U;  // units of a thread
     static_assert(E % U == 0, "whole units");
     int cols;
+    // Columns of the narrowest row of this shape, less one (LINEAR_ROW_SHAPES); for
+    // WIDE rows of one warp it is not used: the gradient of 8192 x 1024 took 18.3 us
+    // with it and takes 14.8 with the comparisons.
+    static constexpr int kFewest = TPR > 32 ? (TPR - 32) * E : (WIDE ? 0 : (E - 8) * 32);
     // the column of element e (a constant after unrolling), and whether it is one of
-    // the row's: known without a comparison for what the narrowest row of this shape
-    // has (LINEAR_ROW_SHAPES: E elements for each thread but the last warp's)
+    // the row's: known without a comparison for what the narrowest row has
     __device__ __forceinline__ int column(int e) const {
         return WIDE ? (e / U * TPR + static_cast<int>(threadIdx.x)) * U + e % U : e * TPR + static_cast<int>(threadIdx.x);
     }
     __device__ __forceinline__ bool holds(int e) const {
         const int past = WIDE ? (e / U + 1) * U * TPR : (e + 1) * TPR;  // every thread's element e lies before this
-        return (E == kEach && past <= (TPR - 32) * E) || column(WIDE ? e / U * U : e) < cols;
+        return past <= kFewest || column(WIDE ? e / U * U : e) < cols;
     }
 
     // this thread's values of a vector by columns, `fill` past its end
@@ -164,11 +167,16 @@ struct RowRing : RowShare<T, E, WIDE, TPR> {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
 
-// CASE(E, threads) of the first shape that holds a.cols.
+// CASE(E, threads) of the first shape that holds a.cols; a warp's rows come in steps
+// of 256 columns, longer ones in steps of 1024.
 #define LINEAR_ROW_SHAPES(CASE)          \
-    if (a.cols <= 32 * 8) CASE(8, 32);   \
+    switch ((a.cols + 255) / 256) {      \
+        case 1: CASE(8, 32);             \
+        case 2: CASE(16, 32);            \
+        case 3: CASE(24, 32);            \
+        case 4: CASE(32, 32);            \
+    }                                    \
     switch ((a.cols + 1023) / 1024) {    \
-        case 1: CASE(kEach, 32);         \
         case 2: CASE(kEach, 64);         \
         case 3: CASE(kEach, 96);         \
         case 4: CASE(kEach, 128);        \

@@ -63,11 +63,11 @@ bool encode_d(CUtensorMap *map, void *ptr, int64_t M, int64_t N) {
 }
 
 template <typename... P>
-cudaError_t launch_cluster(void (*kernel)(P...), unsigned ctas, unsigned cluster, size_t smem, cudaStream_t stream,
-                           const P &...args) {
+cudaError_t launch_cluster(void (*kernel)(P...), unsigned ctas, unsigned threads, unsigned cluster, size_t smem,
+                           cudaStream_t stream, const P &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(192);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -123,8 +123,8 @@ int launch_single(const Call &c) {
     p.D = c.D;
     const int64_t ctas = static_cast<int64_t>(p.m_tiles) * p.n_tiles * KS;
     if (ctas > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
-    return launch_cluster(fp4_single_kernel<BN, KS, NV>, static_cast<unsigned>(ctas), KS, C::SMEM_ALLOC, c.stream, tmP,
-                          tmQ, tmSP, tmSQ, p) == cudaSuccess
+    return launch_cluster(fp4_single_kernel<BN, KS, NV>, static_cast<unsigned>(ctas), C::THREADS, KS, C::SMEM_ALLOC,
+                          c.stream, tmP, tmQ, tmSP, tmSQ, p) == cudaSuccess
                ? GEMM_OK
                : GEMM_ERR_LAUNCH;
 }
@@ -183,8 +183,8 @@ int launch_pair(const Call &c) {
     }
     int64_t grid = m_tiles * n_tiles < clusters ? m_tiles * n_tiles : clusters;
     if (c.o.max_clusters > 0 && c.o.max_clusters < grid) grid = c.o.max_clusters;
-    return launch_cluster(fp4_pair_kernel<NV>, static_cast<unsigned>(2 * grid), 2, C::SMEM_ALLOC, c.stream, tmA, tmB,
-                          tmSA, tmSB, tmD, p) == cudaSuccess
+    return launch_cluster(fp4_pair_kernel<NV>, static_cast<unsigned>(2 * grid), C::THREADS, 2, C::SMEM_ALLOC, c.stream,
+                          tmA, tmB, tmSA, tmSB, tmD, p) == cudaSuccess
                ? GEMM_OK
                : GEMM_ERR_LAUNCH;
 }

@@ -238,7 +238,7 @@ __device__ __forceinline__ float4 load_sums(uint32_t addr) {
 // issuer and TMEM allocator, warps 2-5 read the accumulator).  The 128-row side
 // is called P, the other Q (BN rows): without swap P is A, with it P is B,
 // which for few rows of A streams the weights through the 128-row side.  Tiles
-// of BN < 128 are for a Q of at most BN rows (see Fp4Stage::issue).  KS
+// of BN < 128 are for a Q of at most BN rows (see Fp4Stage::multiply).  KS
 // CTAs of a cluster share a tile's K; their fp32 sums meet through distributed
 // shared memory, added in slice order, rounded once.
 template <int BN, int KS, bool NV>
@@ -471,97 +471,111 @@ struct Fp4Pair {
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * S::A_BYTES;
     static constexpr int OFF_D = OFF_B + STAGES * S::B_BYTES;
-    static constexpr int EPI_BUF = 32 * 128;                    // 32 rows of 128 bytes
-    static constexpr int EPI_BUFS = 2;
-    static constexpr int ROW_PITCH = 128 * 2 + 16;              // a row of 128 elements, shifted up to 7
-    static constexpr int EPI_WARP = 32 * ROW_PITCH;             // 32 such rows (the same memory as the buffers)
-    static_assert(EPI_WARP >= EPI_BUFS * EPI_BUF && OFF_D % 1024 == 0, "staging");
-    static constexpr int OFF_SFA = OFF_D + (4 * EPI_WARP + 1023) / 1024 * 1024;
+    static constexpr int EPI_WARPS = 8;                         // two for each quarter of the rows, 128 columns each
+    static constexpr int EPI_BUF = 32 * 128;                    // of a warp: 32 rows of 128 bytes
+    static constexpr int ROW_PITCH = 64 * 2 + 16;               // a row of 64 elements, shifted up to 7
+    static constexpr int EPI_ROWS = 32 * ROW_PITCH;             // 32 such rows (the same memory as the buffers)
+    static_assert(EPI_ROWS >= EPI_BUF && OFF_D % 1024 == 0 && EPI_WARPS * EPI_ROWS % 1024 == 0, "staging");
+    static constexpr int OFF_SFA = OFF_D + EPI_WARPS * EPI_ROWS;
     static constexpr int OFF_SFB = OFF_SFA + STAGES * S::SFA_BYTES;
     static constexpr int OFF_BAR = OFF_SFB + STAGES * S::SFB_BYTES;
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4) * 8;
-    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
-    static constexpr int THREADS = 192;
+    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 896;      // from a multiple of 128 bytes to one of 1024
+    static constexpr int THREADS = 64 + EPI_WARPS * 32;
     static_assert(ACC1 + 256 <= SF_COL && SMEM_ALLOC <= 232448, "TMEM columns, 227 KiB");
 };
 
-// Half HALF (128 columns) of a slice of 32 rows x 256 16-bit elements, a row a lane
+// An aligned word of a row of D from its place in the staging.
+template <typename U>
+__device__ __forceinline__ void move_edge(uint16_t *to, const uint8_t *from) {
+    *reinterpret_cast<U *>(to) = *reinterpret_cast<const U *>(from);
+}
+
+// Half HALF (64 columns) of a warp's 32 rows x 128 16-bit elements, a row a lane
 // (packed in w; `before`: the row's two elements before them), to rows of D that
 // start anywhere; the two halves one after the other.  A lane stages its row with
 // the shift that its address has within 16 bytes, so the row's whole units are
-// aligned in both memories, and 16 lanes move the units of a row.  The unit that
-// the halves share stays in the staging between them; what the slice's first and
-// last unit hold of the row goes element by element.  One warp runs on each
-// scheduler here and nothing hides its latencies, so the index arithmetic counts:
-// 1000 x 1529 x 256 takes 6.9 us (5.0 at 1528 columns, by TMA); with the units of
-// the whole warp's rows indexed in general it took 12.0, with one lane moving a
-// row's units 9.0.
+// aligned in both memories, and 8 lanes move the units of a row.  The unit that
+// the halves share stays in the staging between them; the one that the tile's two
+// warps share is moved by the left one, which reads the next eight columns too
+// (`after`).  What the tile's first and last unit hold of the row goes in aligned
+// words of 8, 4 and 2 bytes.  Two warps run on each scheduler here and little hides
+// their latencies, so the index arithmetic counts.
 template <int HALF, int PITCH>
-__device__ __forceinline__ void store_unaligned(const Fp4Params &p, uint32_t staging, const uint32_t (&w)[64],
-                                                uint32_t before, int lane, int32_t row0, int32_t col0) {
+__device__ __forceinline__ void store_unaligned(const Fp4Params &p, uint8_t *staging, const uint32_t (&w)[32],
+                                                uint32_t before, const uint32_t (&after)[4], bool left, int lane,
+                                                int32_t row0, int32_t col0) {
     uint16_t *first = static_cast<uint16_t *>(p.D) + static_cast<int64_t>(row0) * p.N + col0;  // row 0, the slice's start
-    const int cols = p.N - col0 - HALF * 128;  // from this half on; may be negative
-    const uint32_t own = staging + static_cast<uint32_t>(lane * PITCH);
+    const int cols = p.N - col0 > HALF * 64 ? p.N - col0 - HALF * 64 : 0;  // of the row from this half on
+    uint8_t *own = staging + lane * PITCH;
     const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(first + static_cast<int64_t>(lane) * p.N) / 2) & 7);
     if (HALF == 1) {  // the shared unit: last of the first half, first of this one
-        const uint4 v = ptx::ld_shared_v4(own + 256u);
-        ptx::st_shared_v4(own, v.x, v.y, v.z, v.w);
+        *reinterpret_cast<uint4 *>(own) = *reinterpret_cast<const uint4 *>(own + 128);
     }
-    const uint32_t at = own + static_cast<uint32_t>(shift / 2 * 4), odd = static_cast<uint32_t>(shift & 1) * 16u;
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(__funnelshift_l(before, w[0], odd)) : "memory");
+    uint32_t *at = reinterpret_cast<uint32_t *>(own) + shift / 2;
+    const uint32_t odd = static_cast<uint32_t>(shift & 1) * 16u;
+    at[0] = __funnelshift_l(before, w[0], odd);
 #pragma unroll
-    for (int k = 1; k < 64; ++k) {
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + k * 4u), "r"(__funnelshift_l(w[k - 1], w[k], odd)) : "memory");
+    for (int k = 1; k < 32; ++k) at[k] = __funnelshift_l(w[k - 1], w[k], odd);
+    if (HALF == 1 && left) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // up to the end of the unit
+            if (k + shift / 2 < 4) at[32 + k] = __funnelshift_l(k ? after[k - 1] : w[31], after[k], odd);
+        }
+    } else {
+        at[32] = __funnelshift_l(w[31], 0u, odd);
     }
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 256u), "r"(__funnelshift_l(w[63], 0u, odd)) : "memory");
     __syncwarp();
-    const int valid = cols < 128 ? (cols > 0 ? cols : 0) : 128;
     {
-        // lane: unit lane % 16 of rows lane / 16, 2 + lane / 16, ...
-        const uint16_t *row = first + HALF * 128 + static_cast<int64_t>(lane >> 4) * p.N;
-        const int unit = lane & 15;
-        const uint32_t from = staging + static_cast<uint32_t>((lane >> 4) * PITCH + unit * 16);
-        const int rows = p.M - row0 - (lane >> 4);
-        const int64_t two = 2 * static_cast<int64_t>(p.N);
+        // lane: unit lane % 8 of rows lane / 8, 4 + lane / 8, ...
+        uint16_t *row = first + HALF * 64 + static_cast<int64_t>(lane >> 3) * p.N;
+        const int unit = lane & 7;
+        const uint8_t *from = staging + (lane >> 3) * PITCH + unit * 16;
+        const int rows = p.M - row0 - (lane >> 3);
+        const int64_t four = 4 * static_cast<int64_t>(p.N);
 #pragma unroll
-        for (int i = 0; i < 16; ++i, row += two) {
+        for (int i = 0; i < 8; ++i, row += four) {
             const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row) / 2 & 7);
             // the first half's first unit is whole without a shift, the second's always
-            if (2 * i < rows && unit * 8 + 8 <= s + valid && (HALF == 1 || s == 0 || unit > 0)) {
-                const uint4 v = ptx::ld_shared_v4(from + i * 2 * PITCH);
-                ptx::st_global_v4(const_cast<uint16_t *>(row) + (unit * 8 - s), v.x, v.y, v.z, v.w);
+            if (4 * i < rows && unit * 8 + 8 <= s + cols && (HALF == 1 || s == 0 || unit > 0)) {
+                *reinterpret_cast<uint4 *>(row + (unit * 8 - s)) = *reinterpret_cast<const uint4 *>(from + i * 4 * PITCH);
             }
         }
     }
-    // Elements outside the whole units: the first half's first ones; at the row's end,
-    // or the slice's, its last ones.
+    // The rest of the lane's row: the tile's first elements; the unit that both warps
+    // share; at the row's end, or the tile's, the last ones.
     if (row0 + lane < p.M) {
-        uint16_t *to = first + static_cast<int64_t>(lane) * p.N + HALF * 128 - shift;
-        const int end = shift + valid;
-        if (HALF == 0 && shift > 0) {
-            const uint4 v = ptx::ld_shared_v4(own);
-            const uint32_t e2[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 1; e < 8; ++e) {
-                if (e >= shift && e < end) to[e] = static_cast<uint16_t>(e2[e / 2] >> (e % 2 * 16));
+        uint16_t *to = first + static_cast<int64_t>(lane) * p.N + HALF * 64 - shift;
+        const int past = HALF == 1 && left && shift > 0 ? 72 : shift + 64;  // this half's last element, and one
+        const int end = shift + cols < past ? shift + cols : past;
+        const int tail = end / 8 * 8;
+        if (HALF == 0 && left && shift > 0) {
+            if (end >= 8) {
+                if (shift & 1) move_edge<uint16_t>(to + shift, own + shift * 2);
+                const int even = shift + (shift & 1);
+                if (even & 2) move_edge<uint32_t>(to + even, own + even * 2);
+                if (shift <= 4) move_edge<uint2>(to + 4, own + 8);
+            } else {
+                for (int e = shift; e < end; ++e) move_edge<uint16_t>(to + e, own + e * 2);
             }
         }
-        const int tail = end / 8 * 8;
-        // none here where the next half continues it, or where it is the first unit
-        if (valid > 0 && (HALF == 1 || valid < 128 || cols == 128) && (HALF == 1 || tail > 0 || shift == 0)) {
-            const uint4 v = ptx::ld_shared_v4(own + static_cast<uint32_t>(tail * 2));
-            const uint32_t e2[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 7; ++e) {
-                if (tail + e < end) to[tail + e] = static_cast<uint16_t>(e2[e / 2] >> (e % 2 * 16));
-            }
+        if (HALF == 1 && end == 72) {
+            move_edge<uint4>(to + 64, own + 128);
+        } else if (cols > 0 && (HALF == 1 || (cols <= 64 && (tail > 0 || shift == 0)))) {
+            // not where the next half continues the unit, nor the first unit (above, or the left warp's)
+            uint16_t *d = to + tail;
+            const uint8_t *from = own + tail * 2;
+            const int n = end - tail;
+            if (n & 4) move_edge<uint2>(d, from);
+            if (n & 2) move_edge<uint32_t>(d + (n & 4), from + (n & 4) * 2);
+            if (n & 1) move_edge<uint16_t>(d + (n & 6), from + (n & 6) * 2);
         }
     }
     __syncwarp();
 }
 
 template <bool NV>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(Fp4Pair<NV>::THREADS, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                     const __grid_constant__ CUtensorMap tmD, const Fp4Params p) {
@@ -597,7 +611,7 @@ __global__ void __launch_bounds__(192, 1)
         }
         ptx::mbar_init(bar_tfull, 1);
         ptx::mbar_init(bar_tfull + 8, 1);
-        ptx::mbar_init(bar_share, 8);  // the epilogue warps of both CTAs
+        ptx::mbar_init(bar_share, 2 * C::EPI_WARPS);  // the epilogue warps of both CTAs
         ptx::mbar_init(bar_drain, 1);
         *abort_flag = 0;
         ptx::fence_mbarrier_init();
@@ -687,14 +701,14 @@ __global__ void __launch_bounds__(192, 1)
         }
         __syncwarp();
     } else {
-        const int quarter = warp & 3;
-        const uint32_t stage_base = base + C::OFF_D + static_cast<uint32_t>((warp - 2) * C::EPI_BUFS * C::EPI_BUF);
-        const uint32_t rows_base = base + C::OFF_D + static_cast<uint32_t>((warp - 2) * C::EPI_WARP);
+        const int quarter = warp & 3, half = (warp - 2) / 4;  // of the CTA's rows, of the tile's columns
+        const uint32_t rows_base = base + C::OFF_D + static_cast<uint32_t>((warp - 2) * C::EPI_ROWS);
+        const uint32_t stage_base = base + C::OFF_D + static_cast<uint32_t>((warp - 2) * C::EPI_BUF);
         const uint32_t share_leader = ptx::mapa(bar_share, 0);
-        uint32_t buf = 0, seq = 0;
+        uint32_t seq = 0;
         for (int item = cluster; item < tiles; item += clusters, ++seq) {
             const WorkItem w = tile_of(item);
-            const int32_t row0 = w.m_idx * 256 + rank * 128 + quarter * 32, col0 = w.n_idx * 256;
+            const int32_t row0 = w.m_idx * 256 + rank * 128 + quarter * 32, col0 = w.n_idx * 256 + half * 128;
             bool ok = true;
             if (lane == 0) {
                 ok = wait_bounded(bar_tfull + 8 * (seq % 2), seq / 2 % 2, abort_flag, p.timeout_ns,
@@ -705,27 +719,32 @@ __global__ void __launch_bounds__(192, 1)
             if (seq == 0) ptx::griddep_wait();
             ptx::tcgen05_fence_after();
             const bool second = seq % 2;
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (second ? C::ACC1 : 0);
-            // 64-column chunks, the shared columns first: the last ones of the first
-            // accumulator, the first ones of the second
-            auto chunk_at = [&](int i) { return second ? i : 3 - i; };
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (second ? C::ACC1 : 0) +
+                                   static_cast<uint32_t>(half * 128);
+            // 64-column chunks of this warp's half, the shared columns first: the last
+            // ones of the first accumulator, the first ones of the second.  The half
+            // without any hands over what it has read with the tile before.
+            const bool shares = half == (second ? 0 : 1);
+            auto chunk_at = [&](int i) { return second ? i : 1 - i; };
             auto hand_over = [&]() {
                 ptx::tcgen05_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx4::mbar_arrive_cluster_relaxed(share_leader);
             };
             constexpr int kShared = (C::OVER + 63) / 64;  // chunks that hold shared columns
+            static_assert(kShared <= 2, "in one half");
+            if (!shares) hand_over();
             if (p.d_type != LINEAR_F32) {
                 // the whole slice in registers, rounded, before any of it is stored
-                uint32_t h[4][32];
+                uint32_t h[2][32];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     const uint32_t col = static_cast<uint32_t>(chunk_at(i) * 64);
                     uint32_t lo[32], hi[32];
                     ptx::tmem_ld_32x32b_x32(taddr + col, lo);
                     ptx::tmem_ld_32x32b_x32(taddr + col + 32, hi);
                     ptx::tmem_wait_ld();
-                    if (i == kShared - 1) hand_over();
+                    if (shares && i == kShared - 1) hand_over();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         h[i][j] = pack16(p.d_type, __uint_as_float(lo[2 * j]) * p.alpha,
@@ -735,28 +754,34 @@ __global__ void __launch_bounds__(192, 1)
                     }
                 }
                 if (!p.tma_store) {
-                    uint32_t w[64];  // the low 128 columns, then the high ones
+                    uint32_t after[4] = {};
+                    if (half == 0) {
+                        uint32_t v[16];
+                        ptx::tmem_ld_32x32b_x16(taddr + 128, v);
+                        ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        w[j] = second ? h[0][j] : h[3][j];
-                        w[32 + j] = second ? h[1][j] : h[2][j];
+                        for (int j = 0; j < 4; ++j) {
+                            after[j] = pack16(p.d_type, __uint_as_float(v[2 * j]) * p.alpha,
+                                              __uint_as_float(v[2 * j + 1]) * p.alpha);
+                        }
                     }
-                    store_unaligned<0, C::ROW_PITCH>(p, rows_base, w, 0u, lane, row0, col0);
-                    const uint32_t before = w[63];
+                    uint8_t *rows = smem + (rows_base - base);
+                    uint32_t w[32];  // the low 64 columns, then the high ones
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        w[j] = second ? h[2][j] : h[1][j];
-                        w[32 + j] = second ? h[3][j] : h[0][j];
-                    }
-                    store_unaligned<1, C::ROW_PITCH>(p, rows_base, w, before, lane, row0, col0);
+                    for (int j = 0; j < 32; ++j) w[j] = second ? h[0][j] : h[1][j];
+                    store_unaligned<0, C::ROW_PITCH>(p, rows, w, 0u, after, half == 0, lane, row0, col0);
+                    const uint32_t before = w[31];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) w[j] = second ? h[1][j] : h[0][j];
+                    store_unaligned<1, C::ROW_PITCH>(p, rows, w, before, after, half == 0, lane, row0, col0);
                     continue;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     const int32_t col = col0 + chunk_at(i) * 64;
-                    if (lane == 0) ptx::bulk_wait_group_read<C::EPI_BUFS - 1>();
+                    if (lane == 0) ptx::bulk_wait_group_read<0>();
                     __syncwarp();
-                    const uint32_t row_addr = stage_base + buf * C::EPI_BUF + static_cast<uint32_t>(lane) * 128u;
+                    const uint32_t row_addr = stage_base + static_cast<uint32_t>(lane) * 128u;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const uint32_t unit = static_cast<uint32_t>(j) ^ (static_cast<uint32_t>(lane) & 7u);
@@ -766,22 +791,21 @@ __global__ void __launch_bounds__(192, 1)
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        if (row0 < p.M && col < p.N) ptx::tma_store_2d(&tmD, stage_base + buf * C::EPI_BUF, col, row0);
+                        if (row0 < p.M && col < p.N) ptx::tma_store_2d(&tmD, stage_base, col, row0);
                         ptx::bulk_commit_group();
                     }
-                    buf = (buf + 1u) % C::EPI_BUFS;
                 }
             } else {
                 // fp32: 32 columns at a time through 32 x 32 floats of staging (row r's
                 // column c at c ^ r), read back by rows, one element a lane
                 float *stage = reinterpret_cast<float *>(smem + (stage_base - base));
 #pragma unroll 1
-                for (int i = 0; i < 8; ++i) {
-                    const int c32 = second ? i : 7 - i;
+                for (int i = 0; i < 4; ++i) {
+                    const int c32 = second ? i : 3 - i;
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(taddr + c32 * 32, v);
                     ptx::tmem_wait_ld();
-                    if (i == 2 * kShared - 1) hand_over();
+                    if (shares && i == 2 * kShared - 1) hand_over();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) stage[lane * 32 + (j ^ lane)] = __uint_as_float(v[j]) * p.alpha;
                     __syncwarp();

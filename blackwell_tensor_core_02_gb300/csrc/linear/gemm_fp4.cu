@@ -222,27 +222,58 @@ int check_options(const gemm_fp4_options *opts, gemm_fp4_options *o) {
     return GEMM_OK;
 }
 
-// The tile, side and K split of a call; false where the options cannot serve
-// the shape (a tile narrower than 128 with more rows than that on that side).
+// CTAs that share a single-CTA tile's K: the most of 8, 4 and 2 that keep two CTAs
+// an SM, where the stages that it saves outweigh the cluster's start and the sums'
+// way through distributed shared memory, which grow with the tile and the clusters
+// at work.  Microseconds, FP4_MX:
+//   1 x 4096 x 2048:    1: 3.48   2: 3.51   4: 3.24   8: 3.38
+//   1 x 4096 x 14336:   1: 14.7   2: 9.7    4: 8.2    8: 7.3
+//   64 x 2048 x 8192:   1: 8.6    2: 7.1    4: 5.2    8: 6.2
+//   64 x 2048 x 14336:  1: 17.3   2: 11.7   4: 7.9    8: 7.3
+//   64 x 1000 x 8192:   1: 8.5    2: 7.1    4: 5.1    8: 4.9     (8 tiles)
+//   64 x 1000 x 2048:   1: 4.5    2: 5.1    4: 4.1    8: 4.5     (8 tiles)
+//   64 x 8192 x 2048:   1: 5.0    2: 5.7    4: 5.5    8: 11.0    (64 tiles)
+//   100 x 14336 x 2048: 1: 7.6    2: 8.0
+//   100 x 14336 x 4096: 1: 11.4   2: 10.4
+// More than two CTAs an SM is a second turn (1 x 28672 x 4096, 224 tiles: 11.3, and
+// 14.0 with two CTAs a tile).
+int split_of(int64_t tiles, int64_t k_tiles, int tile, int sms) {
+    const bool wide = tile >= 64;
+    if (tiles * 8 <= 2 * sms && k_tiles >= (wide && tiles * 16 > sms ? 48 : 32)) return 8;
+    if (tiles * 4 <= 2 * sms && k_tiles >= (wide && tiles * 8 > sms ? 16 : 8)) return 4;
+    if (tiles * 2 <= 2 * sms && k_tiles >= 16) return 2;
+    return 1;
+}
+
+// The tile, side and K split of a call; false where the options cannot serve the
+// shape (a tile narrower than 128 with more rows than that on that side).
+//
+// With more than 128 rows on both sides a CTA pair takes 256 x 256, unless 128 x 128
+// tiles leave enough SMs free for a split of a long K.  Microseconds, FP4_MX, pairs
+// and then 128 x 128 tiles with their best split:
+//   512 x 2048 x 1024 5.1, 5.7     512 x 1024 x 2048 6.2, 6.2     256 x 512 x 2048  6.1, 4.9
+//   500 x 1529 x 256  5.8, 7.0     500 x 1529 x 2048 7.7, 7.6     500 x 1529 x 4096 9.9, 8.5
+//   512 x 2048 x 4096 8.3, 8.3     512 x 2048 x 8192 13.0, 10.2
+//   384 x 4096 x 4096 8.5, 9.0     384 x 4096 x 8192 13.5, 12.8   2048 x 4096 x 4096 14.8, 21.4
 bool resolve(int64_t M, int64_t N, int64_t K, int sms, gemm_fp4_options *o) {
     const int64_t k_tiles = (K + 255) / 256;
-    if (o->tile == 0 && o->swap == 0 && o->cluster_k == 0) {
-        const int64_t pairs = (M + 255) / 256 * ((N + 255) / 256);
-        if (M > 128 && N > 128 && pairs * 8 >= sms) o->tile = 256;
+    if (o->tile == 0 && o->swap == 0 && o->cluster_k == 0 && M > 128 && N > 128) {
+        const int split = split_of((M + 127) / 128 * ((N + 127) / 128), k_tiles, 128, sms);
+        if (split < 4 && (split == 1 || k_tiles < 32)) o->tile = 256;
     }
     if (o->tile == 256) {
         o->cluster_k = 1;
         o->swap = 1;
         return true;
     }
+    // the side with more rows, the weights of a few tokens, streams through the tile's
+    // 128 rows; the other side's tile is the narrowest MMA that holds it
     if (o->swap == 0) o->swap = M < N ? 2 : 1;
     const int64_t p_rows = o->swap == 2 ? N : M, q_rows = o->swap == 2 ? M : N;
     if (o->tile == 0) o->tile = q_rows <= 16 ? 16 : (q_rows <= 32 ? 32 : (q_rows <= 64 ? 64 : 128));
     if (o->tile < 128 && q_rows > o->tile) return false;
-    const int64_t tiles = (p_rows + 127) / 128 * ((q_rows + o->tile - 1) / o->tile);
     if (o->cluster_k == 0) {
-        o->cluster_k = 8;
-        while (o->cluster_k > 1 && (tiles * o->cluster_k > 2 * sms || k_tiles < 4 * o->cluster_k)) o->cluster_k /= 2;
+        o->cluster_k = split_of((p_rows + 127) / 128 * ((q_rows + o->tile - 1) / o->tile), k_tiles, o->tile, sms);
     }
     while (o->cluster_k > k_tiles) o->cluster_k /= 2;
     return true;

@@ -28,15 +28,27 @@ struct GradArgs {
 //
 // A row is read from the ring twice, once for its sums and once for dx: holding
 // h and g in between takes 64 registers more a thread, which halves the rows at
-// work on an SM, and a row's time is the latency of its sums (8192 x 4096 bf16:
-// 40.1 us with them held, see the table of times at norm_backward_join).
+// work on an SM, and a row's time is the latency of its sums.  8192 x 4096 bf16
+// (the memory takes 29.6 us at the copy rate): 36.4 us, with them held 40.1; 31.8
+// without the weights' gradient, the rest is the parts' way to the join.  4096 x
+// 8192 fp16 42 us (parts twice as long), 4096 x 4096 fp32 34.7.  Of rows past 8192
+// columns one is at work on an SM: 2048 x 12288 bf16 33.4 us, and past 12288 of 16
+// bits the weights are read again with each row and the ring has two stages: 2048 x
+// 16384 53.7.  Whole rows in a second pass over memory (norm_backward_long_kernel)
+// took 84 and 93; fp32 rows past 12288 still do, their ring has no room.
+// The second pass of a row behind the first pass of the next, with one barrier a
+// row, gained nothing (8192 x 4096 36.9, 4096 x 8192 42.0, 8192 x 1024 16.4, 14.8
+// as it is).
 template <typename T, int E, bool WIDE, int TPR>
 struct GradShape {
-    static constexpr int STAGES = 3;
-    static constexpr int ROW_BYTES = RowRing<T, E, WIDE, TPR, 2, STAGES>::BYTES;
-    static constexpr int BY_SMEM = 200 * 1024 / ROW_BYTES, BY_THREADS = E <= 16 ? 512 / TPR : 384 / TPR;
-    static constexpr int ROWS = BY_SMEM < BY_THREADS ? BY_SMEM : BY_THREADS;  // at most
-    static_assert(ROW_BYTES >= 2 * 4 * TPR * E, "a row's ring holds its sums");
+    static constexpr int BUDGET = 200 * 1024;
+    static constexpr int ROW = RowRing<T, E, WIDE, TPR, 2, 1>::BYTES;  // of dy and x
+    static constexpr bool HELD = TPR <= 384;  // the weights, in registers
+    static constexpr int STAGES = 3 * ROW <= BUDGET && HELD ? 3 : 2;
+    static constexpr int ROW_BYTES = STAGES * ROW;
+    static constexpr int BY_SMEM = BUDGET / ROW_BYTES, BY_THREADS = E <= 16 ? 512 / TPR : (TPR < 384 ? 384 / TPR : 1);
+    static constexpr int ROWS = BY_SMEM < BY_THREADS ? BY_SMEM : BY_THREADS;  // at most; 0: no room for a row
+    static_assert(ROWS < 2 || ROW_BYTES >= 2 * 4 * TPR * E, "a row's ring holds its sums");
 };
 
 template <typename T, typename W, int E, bool WIDE, int TPR>
@@ -44,6 +56,7 @@ __global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
     norm_backward_ring_kernel(const GradArgs a) {
     constexpr int ROWS = GradShape<T, E, WIDE, TPR>::ROWS, STAGES = GradShape<T, E, WIDE, TPR>::STAGES;
     using Ring = RowRing<T, E, WIDE, TPR, 2, STAGES>;
+    constexpr int U = Ring::U;
     __shared__ __align__(16) float slots[2][ROWS][64];
     extern __shared__ __align__(16) uint8_t ring_mem[];
     if (threadIdx.x == 0 && threadIdx.y == 0) ptx::griddep_launch_dependents();
@@ -64,8 +77,16 @@ __global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
     }
     float mean = 0.f, rstd = 0.f;
     if (row < a.rows) mean = a.mean[row], rstd = a.rstd[row];
-    float2 w[E / 2], sw[E / 2], sb[E / 2];
-    ring.gather(static_cast<const W *>(a.weight), 1.f, w);
+    constexpr bool HELD = GradShape<T, E, WIDE, TPR>::HELD;
+    float2 w[HELD ? E / 2 : U / 2], sw[E / 2], sb[E / 2];
+    const W *weight = static_cast<const W *>(a.weight);
+    if constexpr (HELD) ring.gather(weight, 1.f, w);
+    // the weights of unit u: held, or read again
+    auto weights = [&](int u) -> const float2 * {
+        if constexpr (HELD) return w + u * U / 2;
+        ring.gather_some(weight, 1.f, u, w);
+        return w;
+    };
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) sw[i] = sb[i] = both(0.f);
     int flip = 0;
@@ -80,12 +101,12 @@ __global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
         const float2 m = both(-mean), rs = both(rstd);
         if (row + step < a.rows) mean = a.mean[row + step], rstd = a.rstd[row + step];
         float2 s0 = both(0.f), s1 = both(0.f);
-        constexpr int U = Ring::U;
 #pragma unroll
         for (int u = 0; u < Ring::NV; ++u) {
             float2 h[U / 2], g[U / 2];
             ring.read_some(0, x, u, h);
             ring.read_some(1, dy, u, g);
+            const float2 *wu = weights(u);
 #pragma unroll
             for (int i = 0; i < U / 2; ++i) {
                 // past the row's end dy is 0, and so is what h there is multiplied with
@@ -93,7 +114,7 @@ __global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
                 h[i] = mul2(add2(h[i], m), rs);
                 swi = fma2(g[i], h[i], swi);
                 sbi = add2(sbi, g[i]);
-                g[i] = mul2(g[i], w[u * U / 2 + i]);
+                g[i] = mul2(g[i], wu[i]);
                 s0 = add2(s0, g[i]);
                 s1 = fma2(g[i], h[i], s1);
             }
@@ -107,10 +128,11 @@ __global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
             float2 h[U / 2], g[U / 2];
             ring.read_some(0, x, u, h);
             ring.read_some(1, dy, u, g);
+            const float2 *wu = weights(u);
 #pragma unroll
             for (int i = 0; i < U / 2; ++i) {
                 h[i] = mul2(add2(h[i], m), rs);
-                g[i] = mul2(fma2(h[i], c2, fma2(g[i], w[u * U / 2 + i], c1)), rs);
+                g[i] = mul2(fma2(h[i], c2, fma2(g[i], wu[i], c1)), rs);
             }
             ring.scatter_some(dx, u, g);
         }
@@ -119,7 +141,7 @@ __global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
     if (!a.partial) return;
     const int stride = static_cast<int>(part_stride(a.cols));
     float *part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * stride;
-    if (blockDim.y == 1) {
+    if (ROWS == 1 || blockDim.y == 1) {
         ring.scatter(part, sw);
         ring.scatter(part + stride, sb);
         return;
@@ -142,7 +164,7 @@ __global__ void __launch_bounds__(TPR *GradShape<T, E, WIDE, TPR>::ROWS, 1)
 }
 
 // Rows too long for registers: dx by one CTA per row in two passes, the second
-// from L2, ...
+// from L2 (2048 x 20480 fp16 with the weights' gradient 114 us, 2.2 TB/s), ...
 template <typename T, typename W, bool WIDE>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const GradArgs a) {
     constexpr int VEC = WIDE ? kUnit<T> : 2;  // of a thread and step; odd rows by pairs of any alignment
@@ -305,7 +327,11 @@ int backward_ring(const GradArgs &a, int sms, int *parts, cudaStream_t stream) {
 
 template <typename T, typename W, bool WIDE>
 int backward_rows(const GradArgs &a, int sms, int *parts, cudaStream_t stream) {
-#define LINEAR_CASE(E, TPR) return backward_ring<T, W, E, WIDE, TPR>(a, sms, parts, stream)
+#define LINEAR_CASE(E, TPR)                                                      \
+    if constexpr (GradShape<T, E, WIDE, TPR>::ROWS > 0) {                        \
+        return backward_ring<T, W, E, WIDE, TPR>(a, sms, parts, stream);         \
+    }                                                                            \
+    break
     LINEAR_ROW_SHAPES(LINEAR_CASE)
 #undef LINEAR_CASE
     int st = launch(norm_backward_long_kernel<T, W, WIDE>, dim3(a.rows), dim3(1024), 0, stream, a);

@@ -15,10 +15,11 @@ namespace linear_ops {
 
 // Elements of a row that a thread holds, and the threads: a sum over a row costs
 // each warp some 50 instructions and a barrier, so few warps with many elements
-// are faster (8192 x 4096 bf16 forward, us: 8 elements 36.6, 16 25.4, 32 23.7;
-// gradient 66, 41.4, 41.7), and whole warps up to 8 serve each width up to 8192.
+// are faster (8192 x 4096 bf16 when it was chosen, us: 8 elements 36.6, 16 25.4,
+// 32 23.7; gradient 66, 41.4, 41.7).  Whole warps up to 8 serve the widths up to
+// 8192 and 12 and 16 those up to 16384; short rows of one warp take fewer elements
+// (4976 x 639: 32 each 6.8 us, 24 each 5.2).
 constexpr int kEach = 32;
-constexpr int kRingCols = 256 * kEach;
 
 // The columns of a row that the TPR threads of threadIdx.x hold, E each, as pairs.
 //   WIDE   rows are whole 16-byte units: thread t holds units t, t + TPR, ...
@@ -32,7 +33,7 @@ struct RowShare {
     // Columns of the narrowest row of this shape, less one (LINEAR_ROW_SHAPES); for
     // WIDE rows of one warp it is not used: the gradient of 8192 x 1024 took 18.3 us
     // with it and takes 14.8 with the comparisons.
-    static constexpr int kFewest = TPR > 32 ? (TPR - 32) * E : (WIDE ? 0 : (E - 8) * 32);
+    static constexpr int kFewest = TPR > 256 ? (TPR - 128) * E : (TPR > 32 ? (TPR - 32) * E : (WIDE ? 0 : (E - 8) * 32));
     // the column of element e (a constant after unrolling), and whether it is one of
     // the row's: known without a comparison for what the narrowest row has
     __device__ __forceinline__ int column(int e) const {
@@ -43,24 +44,28 @@ struct RowShare {
         return past <= kFewest || column(WIDE ? e / U * U : e) < cols;
     }
 
-    // this thread's values of a vector by columns, `fill` past its end
+    // U of this thread's values (the i-th U of its E) of a vector by columns, `fill`
+    // past its end and without a vector
+    template <typename W>
+    __device__ __forceinline__ void gather_some(const W *from, float fill, int i, float2 *v) const {
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) v[j] = both(fill);
+        if (!from) return;
+        if constexpr (WIDE) {
+            if (holds(i * U)) load_pairs<W, U / 2>(from + column(i * U), v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < U / 2; ++j) {
+                const int e = i * U + 2 * j;
+                if (holds(e)) v[j].x = to_f32(from[column(e)]);
+                if (holds(e + 1)) v[j].y = to_f32(from[column(e + 1)]);
+            }
+        }
+    }
     template <typename W>
     __device__ __forceinline__ void gather(const W *from, float fill, float2 (&v)[E / 2]) const {
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) v[i] = both(fill);
-        if (!from) return;
-        if constexpr (WIDE) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (holds(i * U)) load_pairs<W, U / 2>(from + column(i * U), v + i * U / 2);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-                if (holds(2 * i)) v[i].x = to_f32(from[column(2 * i)]);
-                if (holds(2 * i + 1)) v[i].y = to_f32(from[column(2 * i + 1)]);
-            }
-        }
+        for (int i = 0; i < NV; ++i) gather_some(from, fill, i, v + i * U / 2);
     }
     // U of this thread's values (the i-th U of its E) to a vector by columns
     template <typename W>
@@ -168,7 +173,7 @@ struct RowRing : RowShare<T, E, WIDE, TPR> {
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
 
 // CASE(E, threads) of the first shape that holds a.cols; a warp's rows come in steps
-// of 256 columns, longer ones in steps of 1024.
+// of 256 columns, longer ones in steps of 1024 and, past 8192, of 4096.
 #define LINEAR_ROW_SHAPES(CASE)          \
     switch ((a.cols + 255) / 256) {      \
         case 1: CASE(8, 32);             \
@@ -184,6 +189,14 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
         case 6: CASE(kEach, 192);        \
         case 7: CASE(kEach, 224);        \
         case 8: CASE(kEach, 256);        \
+        case 9:                          \
+        case 10:                         \
+        case 11:                         \
+        case 12: CASE(kEach, 384);       \
+        case 13:                         \
+        case 14:                         \
+        case 15:                         \
+        case 16: CASE(kEach, 512);       \
     }
 
 inline int grid_of(int64_t rows, int per_cta, int ctas) {

@@ -276,11 +276,18 @@ int layer_norm_forward(const void *x, int64_t x_stride, const void *weight, cons
         return GEMM_ERR_MISALIGNED;
     }
     if (rows == 1) x_stride = y_stride = 0;
-    const int64_t y_bytes = span_bytes(rows, cols, y_stride, size);
-    if (overlap(y, y_bytes, x, span_bytes(rows, cols, x_stride, size)) || overlap(y, y_bytes, weight, cols * wsize) ||
-        overlap(y, y_bytes, bias, cols * wsize) || overlap(y, y_bytes, mean, rows * 4) ||
-        overlap(y, y_bytes, rstd, rows * 4)) {
-        return GEMM_ERR_INVALID_ARG;
+    const struct {
+        const void *p;
+        int64_t bytes;
+    } outs[3] = {{y, span_bytes(rows, cols, y_stride, size)}, {mean, rows * 4}, {rstd, rows * 4}},
+      ins[3] = {{x, span_bytes(rows, cols, x_stride, size)}, {weight, cols * wsize}, {bias, cols * wsize}};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < 3; ++j) {
+            if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return GEMM_ERR_INVALID_ARG;
+        }
+        for (int j = 0; j < i; ++j) {
+            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return GEMM_ERR_INVALID_ARG;
+        }
     }
     int sms = 0;
     const int st = gb300_sms(&sms);

@@ -33,8 +33,9 @@ typedef enum linear_dtype { LINEAR_F16 = 0, LINEAR_BF16 = 1, LINEAR_F32 = 2 } li
  * x and y have type `type`; weight and bias (either may be NULL: 1 and 0) have
  * type `weight_type`, which is `type` or LINEAR_F32.  mean and rstd (fp32,
  * `rows` each) may both be NULL.  Sums are fp32, the variance from the centred
- * values; y is rounded once.  cols >= 1, rows >= 0.  y must not overlap x,
- * weight or bias, nor its own rows (y_stride >= cols).  eps >= 0 and finite.
+ * values; y is rounded once.  cols >= 1, rows >= 0.  y, mean and rstd must not
+ * overlap x, weight, bias or each other, nor y its own rows (y_stride >= cols).
+ * eps >= 0 and finite.
  * Any alignment of whole elements is accepted; 16-byte aligned rows are faster.
  */
 int layer_norm_forward(const void *x, int64_t x_stride, const void *weight, const void *bias, void *y, int64_t y_stride,

@@ -177,6 +177,23 @@ def test_pairs_over_several_tiles(g, fmt, dtype, N, clusters):
     check_product(g, 900, N, 1300, fmt, dtype, g.Fp4Options(tile=256, max_clusters=clusters))
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("N", [1, 6, 63, 64, 65, 127, 129, 135, 191, 193, 250, 257, 263, 320, 385, 511, 513])
+def test_pairs_store_rows_that_start_anywhere(g, N, dtype):
+    """D at each offset within 16 bytes holds the bits of whole aligned rows' product, and nothing
+    beside it is touched."""
+    M, K, whole = 300, 320, 520
+    a, b, _, _ = operands(g, M, whole, K, "mx")
+    options = g.Fp4Options(tile=256)
+    want = g.gemm_fp4_nt(a, b, dtype=dtype, options=options)[:, :N]
+    part = g.quantize_fp4(g.dequantize_fp4(b)[:N].contiguous(), "mx")
+    for shift in range(8):
+        buf = torch.full((M * N + 64,), -7.0, dtype=dtype, device="cuda")
+        d = g.gemm_fp4_nt(a, part, buf[32 + shift:32 + shift + M * N].view(M, N), options=options)
+        assert torch.equal(d, want), shift
+        assert bool((buf[:32 + shift] == -7).all()) and bool((buf[32 + shift + M * N:] == -7).all()), shift
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_products_of_one_term_are_exact(g, fmt):
     """One element a row that is not zero: D holds the products of values, each exact."""

@@ -80,6 +80,18 @@ def test_forward_and_gradient(g, cols, dtype, wdtype):
         check_backward(g, rows_of(7 * cols + rows, rows, cols, dtype, offset=0.0), x, w, mean, rstd)
 
 
+@pytest.mark.parametrize("cols", [8193, 9001, 12280, 12288, 12289, 12296, 16376, 16383])
+@pytest.mark.parametrize("dtype,wdtype", TYPES, ids=lambda t: str(t).split(".")[-1])
+def test_wide_rows(g, cols, dtype, wdtype):
+    """Each side of the widths at which 384 and 512 threads take a row, aligned and not; more rows
+    than CTAs fit at once."""
+    for rows in (2, 309):
+        x = rows_of(cols + rows, rows, cols, dtype)
+        w, b = weights_of(cols, cols, wdtype)
+        _, mean, rstd = check_forward(g, x, w, b, 1e-5)
+        check_backward(g, rows_of(7 * cols + rows, rows, cols, dtype, offset=0.0), x, w, mean, rstd)
+
+
 @pytest.mark.parametrize("rows", [303, 304, 305, 1000, 4001])
 @pytest.mark.parametrize("cols", [48, 1024, 4096])
 def test_many_rows(g, rows, cols):

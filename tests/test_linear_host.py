@@ -68,6 +68,7 @@ def test_layer_norm_refusals():
     assert norm(ys=63) == norm(xs=-1) == norm(y=P) == norm(y=P + 256) == norm(w=2 * P) == INVALID
     assert norm(rows=1 << 31) == norm(cols=1 << 31) == UNSUPPORTED
     assert norm(x=P + 1) == norm(y=2 * P + 1) == norm(w=8 * P + 2, wt=2) == norm(mean=3 * P + 2) == MISALIGNED
+    assert norm(mean=P + 64) == norm(rstd=3 * P + 12) == norm(mean=2 * P) == norm(w=8 * P, rstd=8 * P) == INVALID
     assert norm(rows=0, x=None, y=None) == OK
     assert grad(dw=None) == grad(db=None) == grad(dx=None) == grad(ws=None) == grad(dxs=63) == grad(nb=-1) == INVALID
     assert grad(dx=P) == grad(dw=2 * P) == grad(db=6 * P + 2) == grad(ws=5 * P) == INVALID

@@ -31,20 +31,22 @@ struct GradArgs {
 // work on an SM, and a row's time is the latency of its sums.  8192 x 4096 bf16
 // (the memory takes 29.6 us at the copy rate): 36.4 us, with them held 40.1; 31.8
 // without the weights' gradient, the rest is the parts' way to the join.  4096 x
-// 8192 fp16 42 us (parts twice as long), 4096 x 4096 fp32 34.7.  Of rows past 8192
+// 8192 fp16 41.9 us (parts twice as long), 4096 x 4096 fp32 34.7.  Of rows past 8192
 // columns one is at work on an SM: 2048 x 12288 bf16 33.4 us, and past 12288 of 16
 // bits the weights are read again with each row and the ring has two stages: 2048 x
 // 16384 53.7.  Whole rows in a second pass over memory (norm_backward_long_kernel)
 // took 84 and 93; fp32 rows past 12288 still do, their ring has no room.
 // The second pass of a row behind the first pass of the next, with one barrier a
-// row, gained nothing (8192 x 4096 36.9, 4096 x 8192 42.0, 8192 x 1024 16.4, 14.8
-// as it is).
+// row, gained nothing (8192 x 4096 36.9, 4096 x 8192 42.0, 8192 x 1024 16.4; 14.0 as
+// it is).
 template <typename T, int E, bool WIDE, int TPR>
 struct GradShape {
     static constexpr int BUDGET = 200 * 1024;
     static constexpr int ROW = RowRing<T, E, WIDE, TPR, 2, 1>::BYTES;  // of dy and x
     static constexpr bool HELD = TPR <= 384;  // the weights, in registers
-    static constexpr int STAGES = 3 * ROW <= BUDGET && HELD ? 3 : 2;
+    // Two stages or three: 8192 x 512 fp16 8.8 and 9.4 us, 8192 x 1024 14.0 and 14.7, but
+    // 4096 x 8192 42.6 and 41.9, and rows that start anywhere, 8192 x 1021, 20.7 and 18.4.
+    static constexpr int STAGES = (WIDE && TPR <= 64) || !HELD || 3 * ROW > BUDGET ? 2 : 3;
     static constexpr int ROW_BYTES = STAGES * ROW;
     static constexpr int BY_SMEM = BUDGET / ROW_BYTES, BY_THREADS = E <= 16 ? 512 / TPR : (TPR < 384 ? 384 / TPR : 1);
     static constexpr int ROWS = BY_SMEM < BY_THREADS ? BY_SMEM : BY_THREADS;  // at most; 0: no room for a row

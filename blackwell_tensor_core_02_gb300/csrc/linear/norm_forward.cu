@@ -15,6 +15,8 @@ struct NormArgs {
     float eps, inv_cols;
 };
 
+// Of the ring.  8192 x 4096 bf16: two 23.3 us, three 21.9, four 22.1; 20000 x 256
+// fp16: 9.2, 6.3, 6.3; 8192 x 1024 fp16: 7.7, 7.4, 8.1.
 constexpr int kStages = 3;
 
 // Rows of a CTA: 128 threads' worth; CTAs of an SM: 512 threads (32 elements, their

@@ -32,7 +32,7 @@ struct RowShare {
     int cols;
     // Columns of the narrowest row of this shape, less one (LINEAR_ROW_SHAPES); for
     // WIDE rows of one warp it is not used: the gradient of 8192 x 1024 took 18.3 us
-    // with it and takes 14.8 with the comparisons.
+    // with it and 14.8 with the comparisons.
     static constexpr int kFewest = TPR > 256 ? (TPR - 128) * E : (TPR > 32 ? (TPR - 32) * E : (WIDE ? 0 : (E - 8) * 32));
     // the column of element e (a constant after unrolling), and whether it is one of
     // the row's: known without a comparison for what the narrowest row has

@@ -241,12 +241,20 @@ __device__ __forceinline__ float4 load_sums(uint32_t addr) {
 // of BN < 128 are for a Q of at most BN rows (see Fp4Stage::multiply).  KS
 // CTAs of a cluster share a tile's K; their fp32 sums meet through distributed
 // shared memory, added in slice order, rounded once.
+//
+// For few rows of Q the time is P's bytes: 1 x 8192 x 8192 mx 7.8 us, 4.6 TB/s (5.3
+// us at the copy rate; launch, first loads, the cluster's sums and the end take the
+// rest), 64 x 28672 x 4096 nv 13.8 us, 5.1 TB/s.  D's rows of whole units of four go
+// in one store for each; others element by element: 64 x 4096 x 4096 mx 5.6 us, 64 x
+// 4097 x 4096 6.0.
 template <int BN, int KS, bool NV>
 struct Fp4Single {
     using S = Fp4Stage<1, BN, NV>;
-    // two CTAs an SM, so that one's start and end pass under the other's loads
-    static constexpr int BUDGET = 112 * 1024;
-    static constexpr int STAGES = (BUDGET - 2048) / S::BYTES < 8 ? (BUDGET - 2048) / S::BYTES : 8;
+    // two CTAs an SM, so that one's start and end pass under the other's loads: half of
+    // 228 KiB, less 1 KiB that each takes beside its own
+    static constexpr int BUDGET = 113 * 1024;
+    static constexpr int REST = 8 + 16 + 896;  // barrier, flags, from a multiple of 128 bytes to one of 1024
+    static constexpr int STAGES = (BUDGET - REST) / (S::BYTES + 16);
     static constexpr int SF_BUFS = 2;
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * S::A_BYTES;
@@ -261,12 +269,12 @@ struct Fp4Single {
     static constexpr int SUMS = 4 * (128 * LD > BN * LD_SWAP ? 128 * LD : BN * LD_SWAP);
     static constexpr int OFF_BAR = RING > SUMS ? RING : (SUMS + 15) / 16 * 16;
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 1) * 8;
-    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
+    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 896;
     static constexpr int TMEM_USED = BN + SF_BUFS * S::SF_COLS;
     static constexpr int TMEM_COLS = TMEM_USED <= 64 ? 64 : (TMEM_USED <= 128 ? 128 : 256);
     static constexpr int SF_COL = BN;
     static constexpr int THREADS = 192;
-    static_assert(TMEM_USED <= 256 && STAGES >= 3 && SMEM_ALLOC <= 114 * 1024, "two CTAs an SM");
+    static_assert(TMEM_USED <= 256 && STAGES >= 3 && SMEM_ALLOC <= BUDGET, "two CTAs an SM");
     static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128, "tile width");
 };
 
@@ -460,6 +468,13 @@ __global__ void __launch_bounds__(192, 2)
 // shares first and hands them over; all others of that accumulator it has read
 // by then, with the tile before.  So the next tile's MMAs wait for OVER columns
 // only, and run while the epilogue reads the rest.
+//
+// Bound by the MMAs, 512 cycles a stage (520 measured, and some 2000 a tile between
+// tiles): 8192 x 8192 x 8192 mx 148 us, 7.4 PFLOP/s; 8192 x 28672 x 4096 mx 269 us,
+// 7.15.  One tile a pair is bound by the start, the first loads and the epilogue:
+// 1000 x 1528 x 256 4.5 us, 512 x 4096 x 4096 8.65.  Eight epilogue warps of 128
+// columns, as one warp's way through TMEM, registers and staging is latency: with
+// four of 256 columns these took 5.0 and 9.2 us.
 template <bool NV>
 struct Fp4Pair {
     using S = Fp4Stage<2, 256, NV>;
@@ -500,7 +515,9 @@ __device__ __forceinline__ void move_edge(uint16_t *to, const uint8_t *from) {
 // warps share is moved by the left one, which reads the next eight columns too
 // (`after`).  What the tile's first and last unit hold of the row goes in aligned
 // words of 8, 4 and 2 bytes.  Two warps run on each scheduler here and little hides
-// their latencies, so the index arithmetic counts.
+// their latencies, so the index arithmetic counts: 1000 x 1529 x 256 takes 5.9 us (4.5
+// at 1528 columns, by TMA); with each warp's edges element by element, also in the
+// middle of the tile, 7.1.
 template <int HALF, int PITCH>
 __device__ __forceinline__ void store_unaligned(const Fp4Params &p, uint8_t *staging, const uint32_t (&w)[32],
                                                 uint32_t before, const uint32_t (&after)[4], bool left, int lane,

@@ -199,7 +199,9 @@ __device__ __forceinline__ void load_shifted(const T *p, int left, int64_t all, 
 // the row's, to `p`, anywhere.  w: the four words before the run, then the run.
 // The 16-byte unit that the run shares with the one before belongs to this thread
 // if `before` (w then has that run's end), and the one it shares with the next run
-// to that one's thread if `after`; else each stores its own elements of it.
+// to that one's thread if `after`; else each stores its own elements of it, in
+// aligned words of 8, 4 and 2 bytes (4096 x 4099 to bf16: @@NEW@@ us, element by
+// element 12.8).
 template <typename T, int N>
 __device__ __forceinline__ void store_shifted(T *p, int valid, bool before, bool after, const uint32_t (&w)[N]) {
     constexpr int W = N - 4, U = kUnit<T>;
@@ -219,17 +221,50 @@ __device__ __forceinline__ void store_shifted(T *p, int valid, bool before, bool
         const int at = i / 4 * U;
         if (at >= start && at + U <= end) {
             *reinterpret_cast<uint4 *>(to + at) = make_uint4(out[i], out[i + 1], out[i + 2], out[i + 3]);
-        } else if (at < end && !(after && at + U > end)) {
+        }
+    }
+    const int tail = end / U * U;  // of the last unit, if it is not whole
+    if (start > 0 && end < U) {
+        // the first unit and the last: [start, end) of it
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                if (at + j >= start && at + j < end) {
-                    if constexpr (sizeof(T) == 4) {
-                        reinterpret_cast<uint32_t *>(to)[at + j] = out[i + j];
-                    } else {
-                        reinterpret_cast<uint16_t *>(to)[at + j] = static_cast<uint16_t>(out[i + j / 2] >> (j % 2 * 16));
-                    }
-                }
+        for (int j = 0; j < U; ++j) {
+            if (j < start || j >= end) continue;
+            if constexpr (sizeof(T) == 4) {
+                reinterpret_cast<uint32_t *>(to)[j] = out[j];
+            } else {
+                reinterpret_cast<uint16_t *>(to)[j] = static_cast<uint16_t>(out[j / 2] >> (j % 2 * 16));
             }
+        }
+        return;
+    }
+    if (start > 0) {
+        if constexpr (sizeof(T) == 4) {
+            if (start & 1) reinterpret_cast<uint32_t *>(to)[start] = start == 1 ? out[1] : out[3];
+            if (start <= 2) *reinterpret_cast<uint2 *>(to + 2) = make_uint2(out[2], out[3]);
+        } else {
+            const int even = start + (start & 1);
+            const uint32_t low = start & 2 ? out[1] : out[0], high = start & 2 ? out[3] : out[2];
+            if (start & 1) reinterpret_cast<uint16_t *>(to)[start] = static_cast<uint16_t>((start & 4 ? high : low) >> 16);
+            if (even & 2) *reinterpret_cast<uint32_t *>(to + even) = even & 4 ? out[3] : out[1];
+            if (start <= 4) *reinterpret_cast<uint2 *>(to + 4) = make_uint2(out[2], out[3]);
+        }
+    }
+    if (tail < end && !after) {
+        uint32_t t[4] = {out[0], out[1], out[2], out[3]};
+#pragma unroll
+        for (int i = 4; i < W + 4; i += 4) {
+            if (tail == i / 4 * U) t[0] = out[i], t[1] = out[i + 1], t[2] = out[i + 2], t[3] = out[i + 3];
+        }
+        const int n = end - tail;
+        T *d = to + tail;
+        if constexpr (sizeof(T) == 4) {
+            if (n & 2) *reinterpret_cast<uint2 *>(d) = make_uint2(t[0], t[1]);
+            if (n & 1) *reinterpret_cast<uint32_t *>(d + (n & 2)) = n & 2 ? t[2] : t[0];
+        } else {
+            const uint32_t low = n & 2 ? t[1] : t[0], high = n & 2 ? t[3] : t[2];
+            if (n & 4) *reinterpret_cast<uint2 *>(d) = make_uint2(t[0], t[1]);
+            if (n & 2) *reinterpret_cast<uint32_t *>(d + (n & 4)) = n & 4 ? t[2] : t[0];
+            if (n & 1) *reinterpret_cast<uint16_t *>(d + (n & 6)) = static_cast<uint16_t>(n & 4 ? high : low);
         }
     }
 }

@@ -106,6 +106,24 @@ def test_strided_and_unaligned_rows(g, gap, shift):
         assert torch.equal(out[:, :200].double(), ref.values(codes, scales, fmt)[:, :200]) and bool((out[:, 200:] == -7).all())
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, F32], ids=["f16", "bf16", "f32"])
+@pytest.mark.parametrize("cols", [1, 2, 5, 7, 8, 9, 15, 17, 23, 25, 31, 40, 130, 500, 509, 512, 515, 525, 1037])
+def test_values_into_rows_that_start_anywhere(g, cols, dtype):
+    """Each offset of the first row within 16 bytes; nothing beside the rows is touched."""
+    rows = 11
+    q, codes, scales = check_quantize(g, normal(cols, rows, cols), "nv")
+    want = ref.values(codes, scales, "nv")[:, :cols].to(dtype)
+    for shift in range(8):
+        for gap in (0, 3):
+            buf = torch.full((rows * (cols + gap) + 64,), -7.0, dtype=dtype, device="cuda")
+            inside = torch.zeros_like(buf, dtype=torch.bool)
+            view = lambda t: t[32 + shift:32 + shift + rows * (cols + gap)].view(rows, cols + gap)[:, :cols]
+            view(inside).fill_(True)
+            g.dequantize_fp4(q, dtype, out=view(buf))
+            assert torch.equal(view(buf), want), (shift, gap)
+            assert bool((buf[~inside] == -7).all()), (shift, gap)
+
+
 def test_empty_matrices(g):
     for rows, cols in ((0, 64), (5, 0), (0, 0)):
         q = g.quantize_fp4(torch.empty(rows, cols, dtype=F16, device="cuda"))

@@ -9,8 +9,8 @@
 //
 // 8192 x 4096 (share of the copy rate): fp16 to mx 15.7 us (80 %, with two thirds of
 // the issue slots taken), bf16 to nv 17.4 (73 %), fp32 to mx 23.1 (97 %), back to bf16
-// 13.7 (91 %).  Rows that start anywhere: 4096 x 4099 fp16 to mx 12.3 us (51 %), back
-// 12.8.  One row of 8192: 2.0 us and 1.1.
+// 13.7 (91 %).  Rows that start anywhere: 4096 x 4099 fp16 to mx 11.2 us (56 %), back
+// 11.5.  One row of 8192: 2.0 us and 1.1.
 #include "common.cuh"
 #include "fp4.cuh"
 

@@ -500,12 +500,6 @@ struct Fp4Pair {
     static_assert(ACC1 + 256 <= SF_COL && SMEM_ALLOC <= 232448, "TMEM columns, 227 KiB");
 };
 
-// An aligned word of a row of D from its place in the staging.
-template <typename U>
-__device__ __forceinline__ void move_edge(uint16_t *to, const uint8_t *from) {
-    *reinterpret_cast<U *>(to) = *reinterpret_cast<const U *>(from);
-}
-
 // Half HALF (64 columns) of a warp's 32 rows x 128 16-bit elements, a row a lane
 // (packed in w; `before`: the row's two elements before them), to rows of D that
 // start anywhere; the two halves one after the other.  A lane stages its row with
@@ -514,10 +508,14 @@ __device__ __forceinline__ void move_edge(uint16_t *to, const uint8_t *from) {
 // the halves share stays in the staging between them; the one that the tile's two
 // warps share is moved by the left one, which reads the next eight columns too
 // (`after`).  What the tile's first and last unit hold of the row goes in aligned
-// words of 8, 4 and 2 bytes.  Two warps run on each scheduler here and little hides
-// their latencies, so the index arithmetic counts: 1000 x 1529 x 256 takes 5.9 us (4.5
-// at 1528 columns, by TMA); with each warp's edges element by element, also in the
-// middle of the tile, 7.1.
+// words of 8, 4 and 2 bytes.
+//
+// Rows 8 apart have one shift and, at a pitch of 9 units, the same banks; so the words
+// of a unit are rotated by row / 8 in the staging, which who reads whole units undoes
+// at compile time.  Two warps run on each scheduler here and little hides their
+// latencies, so index arithmetic and accesses count: 1000 x 1529 x 256 takes 5.4 us
+// (4.5 at 1528 columns, by TMA), 7252 x 2575 x 405 16.4 (12.4 at 2576); without the
+// rotation 5.9 and 17.7, in words of 4 bytes row by row 5.5 and 19.5.
 template <int HALF, int PITCH>
 __device__ __forceinline__ void store_unaligned(const Fp4Params &p, uint8_t *staging, const uint32_t (&w)[32],
                                                 uint32_t before, const uint32_t (&after)[4], bool left, int lane,
@@ -525,22 +523,27 @@ __device__ __forceinline__ void store_unaligned(const Fp4Params &p, uint8_t *sta
     uint16_t *first = static_cast<uint16_t *>(p.D) + static_cast<int64_t>(row0) * p.N + col0;  // row 0, the slice's start
     const int cols = p.N - col0 > HALF * 64 ? p.N - col0 - HALF * 64 : 0;  // of the row from this half on
     uint8_t *own = staging + lane * PITCH;
+    const int turn = lane / 8;
+    auto place = [&](int word) {  // in the lane's row
+        return reinterpret_cast<uint32_t *>(own) + (word / 4 * 4 + ((word + turn) & 3));
+    };
     const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(first + static_cast<int64_t>(lane) * p.N) / 2) & 7);
     if (HALF == 1) {  // the shared unit: last of the first half, first of this one
         *reinterpret_cast<uint4 *>(own) = *reinterpret_cast<const uint4 *>(own + 128);
     }
-    uint32_t *at = reinterpret_cast<uint32_t *>(own) + shift / 2;
     const uint32_t odd = static_cast<uint32_t>(shift & 1) * 16u;
-    at[0] = __funnelshift_l(before, w[0], odd);
+    uint32_t *at[4];  // of words 0 to 3; those four further on are a unit further
 #pragma unroll
-    for (int k = 1; k < 32; ++k) at[k] = __funnelshift_l(w[k - 1], w[k], odd);
+    for (int j = 0; j < 4; ++j) at[j] = place(shift / 2 + j);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) at[k % 4][k / 4 * 4] = __funnelshift_l(k ? w[k - 1] : before, w[k], odd);
     if (HALF == 1 && left) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // up to the end of the unit
-            if (k + shift / 2 < 4) at[32 + k] = __funnelshift_l(k ? after[k - 1] : w[31], after[k], odd);
+            if (k + shift / 2 < 4) at[k][32] = __funnelshift_l(k ? after[k - 1] : w[31], after[k], odd);
         }
     } else {
-        at[32] = __funnelshift_l(w[31], 0u, odd);
+        at[0][32] = __funnelshift_l(w[31], 0u, odd);
     }
     __syncwarp();
     {
@@ -555,7 +558,11 @@ __device__ __forceinline__ void store_unaligned(const Fp4Params &p, uint8_t *sta
             const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row) / 2 & 7);
             // the first half's first unit is whole without a shift, the second's always
             if (4 * i < rows && unit * 8 + 8 <= s + cols && (HALF == 1 || s == 0 || unit > 0)) {
-                *reinterpret_cast<uint4 *>(row + (unit * 8 - s)) = *reinterpret_cast<const uint4 *>(from + i * 4 * PITCH);
+                const uint4 v = *reinterpret_cast<const uint4 *>(from + i * 4 * PITCH);
+                const uint32_t t[4] = {v.x, v.y, v.z, v.w};
+                const int g = i / 2;  // the row's turn
+                *reinterpret_cast<uint4 *>(row + (unit * 8 - s)) =
+                    make_uint4(t[g], t[(1 + g) & 3], t[(2 + g) & 3], t[(3 + g) & 3]);
             }
         }
     }
@@ -567,25 +574,24 @@ __device__ __forceinline__ void store_unaligned(const Fp4Params &p, uint8_t *sta
         const int end = shift + cols < past ? shift + cols : past;
         const int tail = end / 8 * 8;
         if (HALF == 0 && left && shift > 0) {
+            const int even = shift + (shift & 1);
             if (end >= 8) {
-                if (shift & 1) move_edge<uint16_t>(to + shift, own + shift * 2);
-                const int even = shift + (shift & 1);
-                if (even & 2) move_edge<uint32_t>(to + even, own + even * 2);
-                if (shift <= 4) move_edge<uint2>(to + 4, own + 8);
+                if (shift & 1) to[shift] = static_cast<uint16_t>(*place(shift / 2) >> 16);
+                if (even & 2) *reinterpret_cast<uint32_t *>(to + even) = *place(even / 2);
+                if (shift <= 4) *reinterpret_cast<uint2 *>(to + 4) = make_uint2(*place(2), *place(3));
             } else {
-                for (int e = shift; e < end; ++e) move_edge<uint16_t>(to + e, own + e * 2);
+                for (int e = shift; e < end; ++e) to[e] = static_cast<uint16_t>(*place(e / 2) >> (e % 2 * 16));
             }
         }
         if (HALF == 1 && end == 72) {
-            move_edge<uint4>(to + 64, own + 128);
+            *reinterpret_cast<uint4 *>(to + 64) = make_uint4(*place(32), *place(33), *place(34), *place(35));
         } else if (cols > 0 && (HALF == 1 || (cols <= 64 && (tail > 0 || shift == 0)))) {
             // not where the next half continues the unit, nor the first unit (above, or the left warp's)
             uint16_t *d = to + tail;
-            const uint8_t *from = own + tail * 2;
-            const int n = end - tail;
-            if (n & 4) move_edge<uint2>(d, from);
-            if (n & 2) move_edge<uint32_t>(d + (n & 4), from + (n & 4) * 2);
-            if (n & 1) move_edge<uint16_t>(d + (n & 6), from + (n & 6) * 2);
+            const int n = end - tail, word = tail / 2;
+            if (n & 4) *reinterpret_cast<uint2 *>(d) = make_uint2(*place(word), *place(word + 1));
+            if (n & 2) *reinterpret_cast<uint32_t *>(d + (n & 4)) = *place(word + (n & 4) / 2);
+            if (n & 1) d[n & 6] = static_cast<uint16_t>(*place(word + (n & 6) / 2));
         }
     }
     __syncwarp();

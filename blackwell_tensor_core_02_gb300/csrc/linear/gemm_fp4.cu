@@ -252,9 +252,9 @@ int split_of(int64_t tiles, int64_t k_tiles, int tile, int sms) {
 // tiles leave enough SMs free for a split of a long K.  Microseconds, FP4_MX, pairs
 // and then 128 x 128 tiles with their best split:
 //   512 x 2048 x 1024 5.1, 5.7     512 x 1024 x 2048 6.2, 6.2     256 x 512 x 2048  6.1, 4.9
-//   500 x 1529 x 256  5.8, 7.0     500 x 1529 x 2048 7.7, 7.6     500 x 1529 x 4096 9.9, 8.5
+//   500 x 1529 x 256  5.4, 7.0     500 x 1529 x 2048 7.2, 7.7     500 x 1529 x 4096 9.4, 8.5
 //   512 x 2048 x 4096 8.3, 8.3     512 x 2048 x 8192 13.0, 10.2
-//   384 x 4096 x 4096 8.5, 9.0     384 x 4096 x 8192 13.5, 12.8   2048 x 4096 x 4096 14.8, 21.4
+//   384 x 4096 x 4096 8.5, 9.0     384 x 4096 x 8192 13.5, 12.8   2048 x 4096 x 4096 14.9, 21.4
 bool resolve(int64_t M, int64_t N, int64_t K, int sms, gemm_fp4_options *o) {
     const int64_t k_tiles = (K + 255) / 256;
     if (o->tile == 0 && o->swap == 0 && o->cluster_k == 0 && M > 128 && N > 128) {

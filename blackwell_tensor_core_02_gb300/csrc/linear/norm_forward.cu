@@ -24,8 +24,8 @@ constexpr int kStages = 3;
 //
 // 8192 x 4096 bf16: 21.9 us, 6.1 TB/s, 90 % of the copy rate; 8192 x 8192 fp32 86.8
 // (91 %); 2048 x 16384 fp16 24.4 (81 %).  Rows that start anywhere, 1023 x 5003 fp32:
-// 10.9 us (55 %; the first rows' latency, 7 rows an SM); 8192 x 1021 fp16 10.3, where
-// 2-byte accesses to shared and global memory bound it (8192 x 1024: 7.4).  One row
+// 10.9 us (55 %; the first rows' latency, 7 rows an SM); 8192 x 1021 fp16 10.3, element
+// by element (8192 x 1024: 7.4).  One row
 // of 4096: 1.9 us, a launch and one trip to memory.
 template <typename T, int E, bool WIDE, int TPR>
 struct NormShape {

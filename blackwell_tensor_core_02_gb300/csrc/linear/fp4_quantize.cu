@@ -197,28 +197,33 @@ __global__ void __launch_bounds__(kThreads, kQuantizePerSm<T, NV, LAYOUT>) quant
             // remainder x - q * s leaves an error far below half an ulp before its rounding.
             // That gives a quotient that is a tie of E2M1 (or E4M3; they have few bits)
             // exactly, and no other quotient of fp32 numbers lies within half an ulp of one.
+            // It is formed with its sign turned, which the codes then undo: for x = -0 every
+            // step leaves the +0 that stands for -0 (x - q * s = +0, and +0 * -i + +0 = +0;
+            // unturned the last step is +0 + -0, which loses the sign).
             const float m = __uint_as_float(amax);
             constexpr float sixth = 1.f / 6.f;
             const float t0 = m * sixth, t = fmaf(fmaf(-t0, 6.f, m), sixth, t0) * pow2(-a.exponent);
             code = to_e4m3(fminf(fmaxf(t, 0x1p-9f), 448.f));
             const float s = from_e4m3(code) * pow2(a.exponent);
-            float inv;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+            float inv;  // -i
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(-s));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float2 q0 = mul2(v[i], both(inv));
-                q[i] = fma2(fma2(q0, both(-s), v[i]), both(inv), q0);
+                q[i] = fma2(fma2(q0, both(s), v[i]), both(inv), q0);
             }
-            if (m > 8.f * s) {
+            if (!(m <= 8.f * s)) {
                 // the scale ended at its largest: quotients may overflow, and their
-                // remainders with them, but past 8 the code is 6 either way
+                // remainders with them, but past 8 the code is 6 either way; an infinity or
+                // NaN comes here too
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (fabsf(v[i].x * inv) >= 8.f) q[i].x = copysignf(8.f, v[i].x);
-                    if (fabsf(v[i].y * inv) >= 8.f) q[i].y = copysignf(8.f, v[i].y);
+                    if (fabsf(v[i].x * inv) >= 8.f) q[i].x = copysignf(8.f, -v[i].x);
+                    if (fabsf(v[i].y * inv) >= 8.f) q[i].y = copysignf(8.f, -v[i].y);
+                    if (bad) q[i] = both(-0.f);
                 }
+                if (bad) code = 0x7fu;
             }
-            if (bad) code = 0x7fu;
         } else {
             const uint32_t e = amax >> 23;  // floor(log2(amax)) + 127; 0 for zeros and subnormal values
             code = e > 2u ? e - 2u : 0u;
@@ -228,7 +233,11 @@ __global__ void __launch_bounds__(kThreads, kQuantizePerSm<T, NV, LAYOUT>) quant
             if (bad) code = 0xffu;
         }
         uint2 packed = to_e2m1(q);
-        if (bad) packed = make_uint2(0u, 0u);
+        if constexpr (NV) {
+            packed.x ^= 0x88888888u, packed.y ^= 0x88888888u;  // the signs turned back
+        } else if (bad) {
+            packed = make_uint2(0u, 0u);
+        }
         if (inside && unit < a.data_units) {
             *reinterpret_cast<uint2 *>(a.data + (row * a.data_units + unit) * 8) = packed;
         }

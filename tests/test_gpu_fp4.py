@@ -69,6 +69,23 @@ def test_ties_and_every_scale(g, fmt):
     check_quantize(g, torch.stack(rows).float(), fmt)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, F32], ids=["f16", "bf16", "f32"])
+@pytest.mark.parametrize("fmt,exponent", [("mx", 0), ("nv", 0), ("nv", -8)])
+def test_sign_of_zeros(g, fmt, exponent, dtype):
+    """A zero of either sign, and a value too small for its block, keep their sign: in blocks of
+    ordinary values, of zeros alone, at the end of a row, and where the scale is at its largest."""
+    x = normal(12, 7, 100, dtype)
+    x[0, ::3], x[1, 1::3], x[2], x[3] = -0.0, 0.0, -0.0, 0.0
+    x[4, ::2], x[4, 1::2], x[6, 1:] = -6e-8, 6e-8, -0.0
+    x[5, ::4], x[6, 0] = -0.0, 65504.0
+    q, codes, scales = check_quantize(g, x, fmt, exponent)
+    assert bool((q.data[2, :48] == 0x88).all()) and not q.data[2, 50:].any() and not q.data[3].any()
+    want = ref.values(codes, scales, fmt, exponent)[:, :100]
+    for out in (F32, BF16):
+        v = g.dequantize_fp4(q, out)
+        assert torch.equal(v.double(), want) and torch.equal(torch.signbit(v), torch.signbit(x))
+
+
 @pytest.mark.parametrize("exponent", [-100, 100])
 def test_extreme_exponents(g, exponent):
     x = normal(4, 8, 64) * 2.0 ** exponent

@@ -17,6 +17,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 
@@ -363,9 +364,22 @@ PyObject *product(PyObject *const *args, Py_ssize_t n) {  // A, B, D, dtype, alp
     if (a.data->device() != b.data->device()) refuse(PyExc_ValueError, "A and B must be on one device");
     double alpha = PyFloat_AsDouble(args[4]);
     if (alpha == -1.0 && PyErr_Occurred()) throw Refused{};
-    alpha = std::ldexp(alpha, a.format.exponent + b.format.exponent);
     const void *options = PyLong_AsVoidPtr(args[5]);
     if (!options && PyErr_Occurred()) throw Refused{};
+    gemm_fp4_options o = {};
+    if (options) o = *static_cast<const gemm_fp4_options *>(options);
+    if (a.format.code == FP4_NV) {
+        // 24 bits of alpha, and its power of two with the matrices' (past 700 either way the
+        // result is an infinity or 0; an exponent of the options' own that is out of range
+        // stays so)
+        int e = 0;
+        alpha = std::frexp(alpha, &e);
+        const int64_t sum = static_cast<int64_t>(o.exponent) + std::max(-700, std::min(700, e)) + a.format.exponent +
+                            b.format.exponent;
+        o.exponent = static_cast<int32_t>(std::max<int64_t>(-2000, std::min<int64_t>(2000, sum)));
+    } else if (std::isfinite(alpha) && !std::isfinite(static_cast<float>(alpha))) {
+        refuse(PyExc_ValueError, "alpha must be in float32's range");
+    }
     const c10::cuda::CUDAGuard guard(a.data->device());
     at::Tensor d;
     if (given(args[2])) {
@@ -380,7 +394,7 @@ PyObject *product(PyObject *const *args, Py_ssize_t n) {  // A, B, D, dtype, alp
     }
     check_status(gemm_fp4_nt(a.data->data_ptr(), a.scales->data_ptr(), b.data->data_ptr(), b.scales->data_ptr(),
                              d.data_ptr(), a.rows, b.rows, a.cols, a.format.code, dtype_of(d, "D"),
-                             static_cast<float>(alpha), stream_of(d), static_cast<const gemm_fp4_options *>(options)),
+                             static_cast<float>(alpha), stream_of(d), &o),
                  "gemm_fp4_nt");
     return THPVariable_Wrap(d);
 }

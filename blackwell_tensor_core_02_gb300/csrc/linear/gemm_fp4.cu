@@ -89,7 +89,7 @@ struct Call {
     void *D;
     int64_t M, N, K;
     int32_t d_type;
-    float alpha;
+    float first, alpha;  // of split_factor()
     cudaStream_t stream;
     gemm_fp4_options o;  // resolved: tile, cluster_k and swap set
 };
@@ -119,6 +119,7 @@ int launch_single(const Call &c) {
     p.wide_store = c.N % 4 == 0 && aligned(c.D, 4 * type_size(c.d_type));
     p.debug_flags = static_cast<uint32_t>(c.o.debug_flags);
     p.timeout_ns = static_cast<uint64_t>(c.o.timeout_ns);
+    p.first = c.first;
     p.alpha = c.alpha;
     p.D = c.D;
     const int64_t ctas = static_cast<int64_t>(p.m_tiles) * p.n_tiles * KS;
@@ -169,6 +170,7 @@ int launch_pair(const Call &c) {
     p.tma_store = c.d_type != LINEAR_F32 && c.N % 8 == 0 && aligned(c.D, 16);
     p.debug_flags = static_cast<uint32_t>(c.o.debug_flags);
     p.timeout_ns = static_cast<uint64_t>(c.o.timeout_ns);
+    p.first = c.first;
     p.alpha = c.alpha;
     p.D = c.D;
     CUtensorMap tmA, tmB, tmSA, tmSB, tmD;
@@ -214,12 +216,28 @@ int check_options(const gemm_fp4_options *opts, gemm_fp4_options *o) {
     *o = opts ? *opts : gemm_fp4_options{};
     if ((o->tile != 0 && o->tile != 16 && o->tile != 32 && o->tile != 64 && o->tile != 128 && o->tile != 256) ||
         (o->cluster_k != 0 && o->cluster_k != 1 && o->cluster_k != 2 && o->cluster_k != 4 && o->cluster_k != 8) ||
-        o->swap < 0 || o->swap > 2 || o->max_clusters < 0 || (o->debug_flags & ~1) != 0 || o->timeout_ns < 0 ||
+        o->swap < 0 || o->swap > 2 || o->max_clusters < 0 || o->exponent < -1000 || o->exponent > 1000 || (o->debug_flags & ~1) != 0 || o->timeout_ns < 0 ||
         (o->tile == 256 && (o->cluster_k > 1 || o->swap != 0))) {
         return GEMM_ERR_INVALID_ARG;
     }
     if (o->timeout_ns == 0) o->timeout_ns = kDefaultTimeoutNs;
     return GEMM_OK;
+}
+
+// The result's factor f = alpha * 2^exponent as the kernels take it: the sum times
+// `first`, a power of two, times `alpha`.  first is 1 where f is a normal fp32
+// number, a zero or not finite.  Beyond, a sum of FP4_NV codes times scales is 0 or in
+// [2^-20, 2^51] (K < 2^28), so the sum times first stays exact and the one rounding is
+// the second product's; where alpha ends at its largest, or with fewer bits, the
+// result is an infinity or 0 whatever the sum.
+void split_factor(double f, float *first, float *alpha) {
+    constexpr double kLeast = 0x1p-126, kMost = 0x1.fffffep127;
+    const double size = std::fabs(f);
+    int shift = 0;
+    if (std::isfinite(f) && size > kMost) shift = 64;
+    if (size < kLeast && size > 0.0) shift = -100;
+    *first = std::ldexp(1.f, shift);
+    *alpha = static_cast<float>(shift ? std::copysign(std::fmin(std::ldexp(size, -shift), kMost), f) : f);
 }
 
 // CTAs that share a single-CTA tile's K: the most of 8, 4 and 2 that keep two CTAs
@@ -292,12 +310,14 @@ extern "C" {
 
 int gemm_fp4_nt(const void *A, const void *A_scales, const void *B, const void *B_scales, void *D, int64_t M, int64_t N,
                 int64_t K, int32_t format, int32_t d_type, float alpha, void *stream, const gemm_fp4_options *opts) {
-    Call c = {A, A_scales, B, B_scales, D, M, N, K, d_type, alpha, static_cast<cudaStream_t>(stream), {}};
+    Call c = {A, A_scales, B, B_scales, D, M, N, K, d_type, 1.f, alpha, static_cast<cudaStream_t>(stream), {}};
     int st = check_options(opts, &c.o);
     if (st != GEMM_OK) return st;
-    if (M < 0 || N < 0 || K < 0 || (format != FP4_MX && format != FP4_NV) || !type_ok(d_type)) {
+    if (M < 0 || N < 0 || K < 0 || (format != FP4_MX && format != FP4_NV) || !type_ok(d_type) ||
+        (format == FP4_MX && c.o.exponent != 0)) {
         return GEMM_ERR_INVALID_ARG;
     }
+    if (format == FP4_NV) split_factor(std::ldexp(static_cast<double>(alpha), c.o.exponent), &c.first, &c.alpha);
     if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
     if (M == 0 || N == 0) return GEMM_OK;
     if (!D || (K > 0 && (!A || !A_scales || !B || !B_scales))) return GEMM_ERR_INVALID_ARG;

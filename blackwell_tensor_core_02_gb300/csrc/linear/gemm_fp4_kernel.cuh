@@ -5,7 +5,8 @@
 // scale tiles (512 bytes: 128 rows x 4 blocks, stored in global memory in the
 // order the tensor cores take them) -TMA-> SMEM -tcgen05.cp-> TMEM, where the
 // MMA reads them.  The products and their scales are exact in fp32; the sum is
-// fp32, multiplied by alpha and rounded once.
+// fp32, multiplied by alpha (and before it, exactly, by a power of two where alpha
+// alone would leave fp32's range) and rounded once.
 //
 // A stage is a K tile of 256 elements: 128 bytes of each row, four MMAs of
 // K = 64.  Scale tiles of a stage: two (FP4_MX: 8 blocks of 32, 2 scales per
@@ -165,7 +166,7 @@ struct Fp4Params {
     int32_t wide_store;            // single-CTA tiles: D's rows are aligned units of four elements
     uint32_t debug_flags;
     uint64_t timeout_ns;
-    float alpha;
+    float first, alpha;            // D = (sum * first) * alpha; first is a power of two
     void *D;
 };
 
@@ -212,6 +213,17 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
     } else {
         ptx::tmem_ld_32x32b_x16(taddr, v);
     }
+}
+
+// Two sums times first, exactly, and alpha.  Packed, the two multiplications take as
+// many instructions as one by itself did (1000 x 1529 x 2088 8.3 us either way; with a
+// branch around the first one 8.4).
+__device__ __forceinline__ float2 scaled(const Fp4Params &p, uint32_t a, uint32_t b) {
+    return mul2(mul2(make_float2(__uint_as_float(a), __uint_as_float(b)), both(p.first)), both(p.alpha));
+}
+__device__ __forceinline__ uint32_t scaled16(const Fp4Params &p, uint32_t a, uint32_t b) {
+    const float2 v = scaled(p, a, b);
+    return pack16(p.d_type, v.x, v.y);
 }
 
 // Four sums of a CTA of the cluster (of this CTA without a K split).
@@ -398,6 +410,10 @@ __global__ void __launch_bounds__(192, 2)
                 uint32_t v[kCols];
                 tmem_ld<kCols>(taddr + c, v);
                 ptx::tmem_wait_ld();
+                if (p.first != 1.f) {  // here, not with alpha below, where it costs 64 x 28672 x 4096 nv 0.3 us
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * p.first);
+                }
                 if (p.swap) {
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) {
@@ -770,10 +786,8 @@ __global__ void __launch_bounds__(Fp4Pair<NV>::THREADS, 1)
                     if (shares && i == kShared - 1) hand_over();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        h[i][j] = pack16(p.d_type, __uint_as_float(lo[2 * j]) * p.alpha,
-                                         __uint_as_float(lo[2 * j + 1]) * p.alpha);
-                        h[i][16 + j] = pack16(p.d_type, __uint_as_float(hi[2 * j]) * p.alpha,
-                                              __uint_as_float(hi[2 * j + 1]) * p.alpha);
+                        h[i][j] = scaled16(p, lo[2 * j], lo[2 * j + 1]);
+                        h[i][16 + j] = scaled16(p, hi[2 * j], hi[2 * j + 1]);
                     }
                 }
                 if (!p.tma_store) {
@@ -783,10 +797,7 @@ __global__ void __launch_bounds__(Fp4Pair<NV>::THREADS, 1)
                         ptx::tmem_ld_32x32b_x16(taddr + 128, v);
                         ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            after[j] = pack16(p.d_type, __uint_as_float(v[2 * j]) * p.alpha,
-                                              __uint_as_float(v[2 * j + 1]) * p.alpha);
-                        }
+                        for (int j = 0; j < 4; ++j) after[j] = scaled16(p, v[2 * j], v[2 * j + 1]);
                     }
                     uint8_t *rows = smem + (rows_base - base);
                     uint32_t w[32];  // the low 64 columns, then the high ones
@@ -830,7 +841,11 @@ __global__ void __launch_bounds__(Fp4Pair<NV>::THREADS, 1)
                     ptx::tmem_wait_ld();
                     if (shares && i == 2 * kShared - 1) hand_over();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) stage[lane * 32 + (j ^ lane)] = __uint_as_float(v[j]) * p.alpha;
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 d = scaled(p, v[j], v[j + 1]);
+                        stage[lane * 32 + (j ^ lane)] = d.x;
+                        stage[lane * 32 + ((j + 1) ^ lane)] = d.y;
+                    }
                     __syncwarp();
                     const int32_t col = col0 + c32 * 32 + lane;
                     if (col < p.N) {

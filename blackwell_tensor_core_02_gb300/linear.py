@@ -35,7 +35,8 @@ _FORMATS = {"mx": 0, "nv": 1}
 class Fp4Options(ctypes.Structure):
     """Mirror of ``gemm_fp4_options`` (zero fields mean defaults)."""
     _fields_ = [("tile", ctypes.c_int32), ("cluster_k", ctypes.c_int32), ("swap", ctypes.c_int32),
-                ("max_clusters", ctypes.c_int32), ("debug_flags", ctypes.c_int32), ("timeout_ns", ctypes.c_int64)]
+                ("max_clusters", ctypes.c_int32), ("debug_flags", ctypes.c_int32), ("timeout_ns", ctypes.c_int64),
+                ("exponent", ctypes.c_int32)]
 
 
 class Fp4LaunchInfo(ctypes.Structure):
@@ -179,7 +180,9 @@ def gemm_fp4_nt(A: Fp4Tensor, B: Fp4Tensor, D=None, *, dtype=torch.float16, alph
                 options: Fp4Options | None = None):
     """D = alpha * A·Bᵀ of the values of A (M×K) and B (N×K), both of one format; returns D (M×N).
 
-    The sum is fp32 on the tensor cores, D (float16, bfloat16 or float32) is rounded once.
+    The sum is fp32 on the tensor cores, D (float16, bfloat16 or float32) is rounded once.  "nv"
+    matrices' exponents are brought in whatever their sum; alpha and they together may leave fp32's
+    range.
     """
     address = 0 if options is None else ctypes.addressof(options)
     if stream is not None:

@@ -116,6 +116,8 @@ int fp4_dequantize(const void *data, const void *scales, int64_t rows, int64_t c
  *   max_clusters  cap on the persistent grid of CTA pairs; 0: as many as fit.
  *   debug_flags   test hook: 1 makes every wait run out (see gemm_f16.h).
  *   timeout_ns    limit of every wait inside the kernel; 0: 4 s.
+ *   exponent      FP4_NV: the result's power of two beside alpha, in [-1000,
+ *                 1000] (0 for FP4_MX).
  */
 typedef struct gemm_fp4_options {
     int32_t tile;
@@ -124,13 +126,16 @@ typedef struct gemm_fp4_options {
     int32_t max_clusters;
     int32_t debug_flags;
     int64_t timeout_ns;
+    int32_t exponent;
 } gemm_fp4_options;
 
 /*
- * D = alpha * A * B^T for quantised A (M x K) and B (N x K) of one format, K
- * their number of columns; D (M x N, row-major, `d_type`) is rounded once from
- * the fp32 sum times alpha.  The exponents of FP4_NV matrices belong into
- * alpha (2^(exponent of A + exponent of B)).  A, B and their scales are
+ * D = alpha * 2^exponent * A * B^T for quantised A (M x K) and B (N x K) of one
+ * format, K their number of columns; D (M x N, row-major, `d_type`) is rounded
+ * once from the fp32 sum of codes times scales, times alpha * 2^exponent.  The
+ * exponents of FP4_NV matrices, which the kernel does not see, belong there: into
+ * the option (exponent of A + exponent of B), as their sum may leave fp32's range,
+ * or into alpha where it does not.  A, B and their scales are
  * 16-byte aligned; D is aligned to its elements (16-byte aligned rows are
  * faster) and overlaps none of them.  M or N 0: nothing is launched; K 0:
  * D = 0.  M, N <= 2^31 - 1024, K as the columns of a quantised matrix.

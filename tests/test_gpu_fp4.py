@@ -249,6 +249,79 @@ def test_alpha_and_exponents(g):
     check_product(g, 300, 600, 512, "mx", F16, alpha=3.0, options=g.Fp4Options(tile=256))
 
 
+# exponents of A and B and alpha whose product leaves fp32's range, at its edges and inside it
+FACTORS = [(64, 64, 1.0), (64, 63, 1.9), (100, 100, 1.0), (100, -100, 0.3), (-100, 100, -1.0), (-100, -50, 1.0),
+           (-60, -70, 1 / 3), (-63, -63, 0.7), (-100, -100, 1.0), (90, 90, 1e-40), (-90, -90, 3e39), (0, 3, -1e-41), (-3, 0, 1e300),
+           (0, 0, float("inf"))]
+
+
+def one_term(exponent, seed, n=192, K=512):
+    """Rows of one element that is not zero, near 2**exponent; the first and the last row zeros."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.zeros(n, K, dtype=torch.float64, device="cuda")
+    at = torch.randint(0, K, (n,), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    v = torch.randn(n, generator=gen, device="cuda").double() * torch.exp2(torch.randint(-6, 9, (n,), generator=gen, device="cuda").double())
+    x[torch.arange(n), at] = v * 2.0 ** exponent
+    x[0] = x[-1] = 0
+    return x.float()
+
+
+def same(d, want):
+    return torch.equal(d.isnan(), want.isnan()) and torch.equal(torch.where(d.isnan(), 0, d), torch.where(want.isnan(), 0, want))
+
+
+@pytest.mark.parametrize("options", [{}, dict(tile=256), dict(tile=128, cluster_k=2), dict(tile=128, swap=2)], ids=str)
+@pytest.mark.parametrize("ea,eb,alpha", FACTORS)
+def test_exponents_whose_sum_leaves_fp32(g, ea, eb, alpha, options):
+    """One term a row: the sum is exact in fp32, so D is the one rounding of the exact value, and 0
+    (NaN for an infinite alpha) where the sum is 0."""
+    x, w = one_term(ea, 1), one_term(eb, 2)
+    a, b = g.quantize_fp4(x, "nv", exponent=ea), g.quantize_fp4(w, "nv", exponent=eb)
+    exact = ref.values(*ref.quantize(x, "nv", ea), "nv", ea) @ ref.values(*ref.quantize(w, "nv", eb), "nv", eb).T
+    m, e = torch.frexp(torch.tensor(alpha, dtype=torch.float64))
+    exact = exact * (float(m.float()) * 2.0 ** min(int(e), 900) if alpha != float("inf") else alpha)
+    for dtype in (F32, BF16, F16):
+        d = g.gemm_fp4_nt(a, b, dtype=dtype, alpha=alpha, options=g.Fp4Options(**options))
+        assert same(d, exact.float().to(dtype)), dtype
+        # the last row of B left out: rows of D that start anywhere
+        d = g.gemm_fp4_nt(a, b._replace(data=b.data[:191]), dtype=dtype, alpha=alpha, options=g.Fp4Options(**options))
+        assert same(d, exact[:, :191].float().to(dtype)), dtype
+
+
+@pytest.mark.parametrize("ea,eb", [(64, 64), (100, -100), (-100, -50), (-80, -48), (-100, -100)])
+def test_sums_with_extreme_exponents(g, ea, eb):
+    """Values near 2**(exponent - 8) and 2**(exponent + 8), a padding row of zeros on each side."""
+    for shift in (-8, 8):
+        x, w = (normal(20, 90, 700).double() * 2.0 ** (ea + shift)).float(), (normal(21, 300, 700).double() * 2.0 ** (eb + shift)).float()
+        x[7] = w[5] = 0
+        a, b = g.quantize_fp4(x, "nv", exponent=ea), g.quantize_fp4(w, "nv", exponent=eb)
+        va, vb = ref.values(*ref.quantize(x, "nv", ea), "nv", ea), ref.values(*ref.quantize(w, "nv", eb), "nv", eb)
+        for options in (None, g.Fp4Options(tile=256)):
+            for dtype in (F32, BF16, F16):
+                d = g.gemm_fp4_nt(a, b, dtype=dtype, options=options)
+                want, bound = ref.product_bound(va, vb, dtype)
+                over = d.isinf() & (want.abs() + bound >= torch.finfo(dtype).max) & (torch.sign(d) == torch.sign(want))
+                assert bool(((d.double() - want).abs() <= bound).logical_or(over).all())
+                assert not d[7].any() and not d[:, 5].any()
+
+
+def test_the_products_factor(g):
+    """alpha and the option's exponent are one factor; out-of-range ones are refused."""
+    a, b, va, vb = operands(g, 40, 72, 320, "nv", exponents=(0, 0))
+    want = g.gemm_fp4_nt(a, b, dtype=F32, alpha=0.375)
+    for alpha, exponent in ((3.0, -3), (0.375 * 2.0 ** -90, 90), (1.5 * 2.0 ** 100, -102)):
+        assert torch.equal(g.gemm_fp4_nt(a, b, dtype=F32, alpha=alpha, options=g.Fp4Options(exponent=exponent)), want)
+    m = g.quantize_fp4(normal(1, 40, 320), "mx")
+    for bad in (lambda: g.gemm_fp4_nt(a, b, options=g.Fp4Options(exponent=2 ** 31 - 1)),
+                lambda: g.gemm_fp4_nt(a, b, options=g.Fp4Options(exponent=-(2 ** 31))),
+                lambda: g.gemm_fp4_nt(a, b, alpha=0.5, options=g.Fp4Options(exponent=1001)),
+                lambda: g.gemm_fp4_nt(m, m, options=g.Fp4Options(exponent=1))):
+        with pytest.raises(g.GemmError):
+            bad()
+    with pytest.raises(ValueError):
+        g.gemm_fp4_nt(m, m, alpha=1e39)
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_large_product_in_its_default_tile(g, fmt):
     check_product(g, 2304, 3840, 1056, fmt)

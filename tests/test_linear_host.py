@@ -105,6 +105,13 @@ def test_fp4_sizes_and_refusals():
     assert gemm(M=0, a=None, dd=None) == OK
 
 
+def test_product_exponent_refusals():
+    def gemm(fmt, exponent):
+        return g.load_linear().gemm_fp4_nt(P, 2 * P, 3 * P, 4 * P, 5 * P, 8, 8, 64, fmt, 0, 1.0, None, g.Fp4Options(exponent=exponent))
+
+    assert gemm(1, 1001) == gemm(1, -1001) == gemm(0, 1) == gemm(0, -1) == INVALID
+
+
 def test_choice_of_tile():
     for (M, N, K), tile, ks, swap, ctas in (
             ((1, 8192, 8192), 16, 4, 2, 256),        # a token: the weights' rows on the 128-row side

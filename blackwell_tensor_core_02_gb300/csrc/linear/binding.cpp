@@ -63,6 +63,13 @@ int dtype_of(const at::Tensor &t, const char *name) {
     return code;
 }
 
+at::ScalarType dtype_arg(PyObject *o, const char *name) {
+    if (!THPDtype_Check(o) || dtype_code(reinterpret_cast<THPDtype *>(o)->scalar_type) < 0) {
+        refuse(PyExc_TypeError, "%s must be float16, bfloat16 or float32", name);
+    }
+    return reinterpret_cast<THPDtype *>(o)->scalar_type;
+}
+
 struct Rows {
     int64_t rows, cols, step;
 };
@@ -179,8 +186,8 @@ const float *statistic(const at::Tensor &t, const at::Tensor &x, int64_t rows, c
     return t.data_ptr<float>();
 }
 
-PyObject *norm_backward(PyObject *const *args, Py_ssize_t n) {  // dy, x, weight, mean, rstd, dx
-    count(n, 6);
+PyObject *norm_backward(PyObject *const *args, Py_ssize_t n) {  // dy, x, weight, mean, rstd, dx, grad_dtype
+    count(n, 7);
     const at::Tensor &dy = tensor(args[0], "dy"), &x = tensor(args[1], "x");
     const int code = dtype_of(x, "x");
     const Rows r = rows_of(x, "x");
@@ -196,6 +203,14 @@ PyObject *norm_backward(PyObject *const *args, Py_ssize_t n) {  // dy, x, weight
         w = weights(t, x, r.cols, "weight");
         wtype = t.scalar_type();
     }
+    const bool parameters = w || given(args[6]);  // their gradients are wanted
+    if (given(args[6])) {
+        const at::ScalarType want = dtype_arg(args[6], "grad_dtype");
+        if (w ? want != wtype : (want != wtype && want != at::kFloat)) {
+            refuse(PyExc_TypeError, "grad_dtype must be weight's dtype or, without a weight, x's or float32");
+        }
+        wtype = want;
+    }
     const c10::cuda::CUDAGuard guard(x.device());
     Rows gr{r.rows, r.cols, r.cols};
     at::Tensor dx, dweight, dbias, space;
@@ -207,7 +222,7 @@ PyObject *norm_backward(PyObject *const *args, Py_ssize_t n) {  // dy, x, weight
         dx = empty(x.sizes(), x.scalar_type(), x);
     }
     int64_t need = 0;
-    if (w) {
+    if (parameters) {
         dweight = empty({r.cols}, wtype, x);
         dbias = empty({r.cols}, wtype, x);
         need = layer_norm_backward_workspace_size(r.rows, r.cols);
@@ -215,8 +230,9 @@ PyObject *norm_backward(PyObject *const *args, Py_ssize_t n) {  // dy, x, weight
         space = empty({need}, at::kByte, x);
     }
     check_status(layer_norm_backward(dy.data_ptr(), dr.step, x.data_ptr(), r.step, w, mean, rstd, dx.data_ptr(), gr.step,
-                                     w ? dweight.data_ptr() : nullptr, w ? dbias.data_ptr() : nullptr, r.rows, r.cols,
-                                     code, dtype_code(wtype), w ? space.data_ptr() : nullptr, need, stream_of(x)),
+                                     parameters ? dweight.data_ptr() : nullptr, parameters ? dbias.data_ptr() : nullptr,
+                                     r.rows, r.cols, code, dtype_code(wtype), parameters ? space.data_ptr() : nullptr, need,
+                                     stream_of(x)),
                  "layer_norm_backward");
     return tuple_of({dx, dweight, dbias});
 }
@@ -322,13 +338,6 @@ PyObject *quantize(PyObject *const *args, Py_ssize_t n) {  // x, format, exponen
                               scales.data_ptr(), stream_of(x)),
                  "quantize_fp4");
     return tuple_of({data, scales});
-}
-
-at::ScalarType dtype_arg(PyObject *o, const char *name) {
-    if (!THPDtype_Check(o) || dtype_code(reinterpret_cast<THPDtype *>(o)->scalar_type) < 0) {
-        refuse(PyExc_TypeError, "%s must be float16, bfloat16 or float32", name);
-    }
-    return reinterpret_cast<THPDtype *>(o)->scalar_type;
 }
 
 PyObject *dequantize(PyObject *const *args, Py_ssize_t n) {  // q, dtype, out

@@ -140,16 +140,17 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, out=None, stream
     return _native.layer_norm(x, weight, bias, eps, out)
 
 
-def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, stream=None):
+def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, grad_dtype=None, stream=None):
     """(dx, dweight, dbias): the gradient of ``layer_norm`` at x, from its mean and rstd.
 
-    dx has x's dtype and shape; dweight and dbias have weight's dtype, and are None where weight is
-    None.  Sums over rows are fp32 in a fixed order: the same inputs give the same bits.  ``dx``:
+    dx has x's dtype and shape; dweight and dbias have weight's dtype.  Without a weight they are
+    None unless ``grad_dtype`` (x's or float32) asks for them, as a norm with a bias alone does.  Sums over rows are fp32 in a fixed order: the same inputs give the same bits.  ``dx``:
     the memory for dx, which must not overlap the inputs.
     """
     if stream is not None:
-        return _on(stream, _native.layer_norm_backward, (dy, x, weight, mean, rstd, dx), (dy, x, weight, mean, rstd, dx))
-    return _native.layer_norm_backward(dy, x, weight, mean, rstd, dx)
+        return _on(stream, _native.layer_norm_backward, (dy, x, weight, mean, rstd, dx, grad_dtype),
+                   (dy, x, weight, mean, rstd, dx))
+    return _native.layer_norm_backward(dy, x, weight, mean, rstd, dx, grad_dtype)
 
 
 def quantize_fp4(x, format: str = "mx", *, exponent: int = 0, out: Fp4Tensor | None = None, stream=None) -> Fp4Tensor:

@@ -141,6 +141,38 @@ def test_without_weight_or_bias(g, w_on, b_on):
     check_backward(g, rows_of(6, 9, 1000, BF16), x, w, mean, rstd)
 
 
+@pytest.mark.parametrize("dtype,wdtype", TYPES, ids=lambda t: str(t).split(".")[-1])
+@pytest.mark.parametrize("cols", [1, 1000, 1021, 16385, 20480])
+def test_gradient_of_a_bias_alone(g, cols, dtype, wdtype):
+    """Without a weight dbias (and dweight, that of a weight of ones) comes when it is asked for."""
+    x, dy = rows_of(5, 200, cols, dtype), rows_of(6, 200, cols, dtype)
+    b = weights_of(6, cols, wdtype)[1]
+    _, mean, rstd = check_forward(g, x, None, b, 1e-5)
+    want = ref.norm_grad(dy, x, None, mean, rstd)
+    bound = ref.norm_grad_bounds(dy, x, None, mean, rstd, dtype, wdtype)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        got = g.layer_norm_backward(dy, x, None, mean, rstd, grad_dtype=wdtype, stream=stream)
+        side.synchronize()
+        assert got[0].dtype == dtype and got[1].dtype == got[2].dtype == wdtype
+        for t, w, e, what in zip(got, want, bound, ("dx", "dweight", "dbias")):
+            within(t, w, e, what)
+    assert torch.equal(got[0], g.layer_norm_backward(dy, x, None, mean, rstd)[0])
+    none = g.layer_norm_backward(dy[:0], x[:0], None, mean[:0], rstd[:0], grad_dtype=wdtype)
+    assert none[2].shape == (cols,) and not none[2].any()
+
+
+def test_gradient_dtype_refusals(g):
+    x = rows_of(5, 9, 64, BF16)
+    w, _ = weights_of(6, 64, BF16)
+    _, mean, rstd = g.layer_norm(x, w)
+    for weight, dtype in ((w, F32), (None, F16), (None, torch.float64), (None, 3)):
+        with pytest.raises(TypeError):
+            g.layer_norm_backward(x, x, weight, mean, rstd, grad_dtype=dtype)
+    assert g.layer_norm_backward(x, x, w, mean, rstd, grad_dtype=BF16)[1].dtype == BF16
+
+
 def test_leading_axes(g):
     x = rows_of(5, 24, 512, F16).view(2, 3, 4, 512)
     w, b = weights_of(6, 512, F16)

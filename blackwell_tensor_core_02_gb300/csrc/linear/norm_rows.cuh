@@ -128,9 +128,9 @@ struct RowRing : RowShare<T, E, WIDE, TPR> {
             }
         }
     }
-    // U of this thread's elements (the i-th U of its E) of the current slot; zeros past
-    // the row's end
-    __device__ __forceinline__ void read_some(int op, const T *row, int i, float2 *v) const {
+    // U of this thread's elements (the i-th U of its E) of the current slot; past the
+    // row's end `fill`, of WIDE rows 0
+    __device__ __forceinline__ void read_some(int op, const T *row, int i, float2 *v, float fill = 0.f) const {
         const uint32_t src = base + static_cast<uint32_t>(slot * OPS + op) * SLOT;
         if constexpr (WIDE) {
             uint4 raw = make_uint4(0, 0, 0, 0);
@@ -145,7 +145,7 @@ struct RowRing : RowShare<T, E, WIDE, TPR> {
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const int e = i * U + j;
-                f[j] = 0.f;
+                f[j] = fill;
                 if (this->holds(e)) {
                     if constexpr (sizeof(T) == 4) {
                         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[j]) : "r"(at + e * TPR * 4u) : "memory");

@@ -173,6 +173,27 @@ def test_gradient_dtype_refusals(g):
     assert g.layer_norm_backward(x, x, w, mean, rstd, grad_dtype=BF16)[1].dtype == BF16
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("cols", [3, 8, 255, 1000, 1021, 2056, 5003, 12304, 16385, 20479, 20480])
+def test_gradient_where_mean_times_rstd_leaves_fp32(g, cols, dtype):
+    """Constant rows of 2**110 (h = 0) with rstd = 2**22 among ordinary ones and one of NaN: threads
+    that hold columns past the row's end see mean * rstd there, which is no number of fp32."""
+    x, dy = rows_of(5, 300, cols, dtype), rows_of(6, 300, cols, dtype)
+    w, b = weights_of(6, cols, F32)
+    x[::3] = 2.0 ** 110
+    x[4, cols // 2] = float("nan")
+    _, mean, rstd = g.layer_norm(x, w, b, 1e-5)
+    mean[::3], rstd[::3] = 2.0 ** 110, 2.0 ** 22
+    for weight in (w, None):
+        dx = g.layer_norm_backward(dy, x, weight, mean, rstd)[0]
+        assert dx[4].isnan().all()
+        keep = torch.arange(300, device="cuda") != 4
+        within(dx[keep], ref.norm_grad(dy, x, weight, mean, rstd)[0][keep],
+               ref.norm_grad_bounds(dy, x, weight, mean, rstd, dtype, F32)[0][keep], "dx")
+    x[4], mean[4], rstd[4] = 0, 0, 1
+    check_backward(g, dy, x, w, mean, rstd)
+
+
 def test_leading_axes(g):
     x = rows_of(5, 24, 512, F16).view(2, 3, 4, 512)
     w, b = weights_of(6, 512, F16)

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import argparse
 import json
+import math
 import os
 import sys
 
@@ -52,8 +53,10 @@ class PreNormLinear:
 
     def quantize(self, format: str = "mx") -> None:
         # "nv" scales reach from 2^-9 to 448: one exponent brings a layer's weights, some
-        # 1 / sqrt(width) in size, into their middle
-        exponent = 0 if format == "mx" else round(float(torch.log2(self.weight.float().abs().amax() / 6))) - 3
+        # 1 / sqrt(width) in size, into their middle (0 for weights that have none: zeros, or
+        # with an infinity or NaN)
+        size = 0.0 if format == "mx" else float(torch.log2(self.weight.float().abs().amax() / 6))
+        exponent = round(size) - 3 if format != "mx" and math.isfinite(size) else 0
         self.weight4 = g.quantize_fp4(self.weight, format, exponent=max(-100, min(100, exponent)))
 
     def serve(self, x):

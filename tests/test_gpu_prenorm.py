@@ -60,6 +60,26 @@ def test_served_result_is_the_quantised_product(gpu_lib, layer, fmt, tokens):
     assert gpu_lib.fp4_device_status()[0] == 0
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("value", [0.0, float("inf"), float("nan")])
+def test_weights_without_a_size(gpu_lib, fmt, value):
+    """A layer whose weights are zeros gives zeros; one infinity or NaN among them gives its output."""
+    from blackwell_tensor_core_02_gb300 import prenorm
+
+    layer = prenorm.make_layer(128, 48, seed=2)
+    if value == 0.0:
+        layer.weight.zero_()
+    else:
+        layer.weight[5, 7] = value
+    layer.quantize(fmt)
+    assert layer.weight4.exponent == 0
+    served = layer.serve(_x(9, 3)[:, :128].contiguous())
+    want = torch.zeros(9, 48, dtype=torch.bool, device="cuda")
+    want[:, 5] = value != 0.0
+    assert torch.equal(served.isnan(), want)
+    assert bool((served != 0).any()) == (value != 0.0) and gpu_lib.fp4_device_status()[0] == 0
+
+
 def test_command(capsys, gpu_lib):
     from blackwell_tensor_core_02_gb300 import prenorm
 

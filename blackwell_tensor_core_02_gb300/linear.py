@@ -111,8 +111,8 @@ _native = _load_binding()
 
 def _on(stream, call, args, tensors):
     """call(*args) on `stream` (a torch stream or a handle), the tensors' memory kept until it has run."""
-    device = next(t.device for t in tensors if isinstance(t, torch.Tensor))
-    if device.type != "cuda":
+    device = next((t.device for t in tensors if isinstance(t, torch.Tensor)), None)
+    if device is None or device.type != "cuda":
         return call(*args)  # refused there
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
@@ -124,6 +124,11 @@ def _on(stream, call, args, tensors):
         if isinstance(t, torch.Tensor):
             t.record_stream(stream)
     return result
+
+
+def _parts(q) -> tuple:
+    """The tensors of an Fp4Tensor; of anything else, which the call refuses, itself."""
+    return q[:2] if isinstance(q, tuple) else (q,)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, out=None, stream=None):
@@ -163,7 +168,7 @@ def quantize_fp4(x, format: str = "mx", *, exponent: int = 0, out: Fp4Tensor | N
     """
     if stream is not None:
         data, scales = _on(stream, _native.quantize_fp4, (x, format, exponent, out),
-                           (x,) if out is None else (x, out.data, out.scales))
+                           (x, *_parts(out)))
     else:
         data, scales = _native.quantize_fp4(x, format, exponent, out)
     return Fp4Tensor(data, scales, x.shape[1], format, exponent) if out is None else out
@@ -173,7 +178,7 @@ def dequantize_fp4(q: Fp4Tensor, dtype=torch.float32, *, out=None, stream=None):
     """The values of q as a rows x cols matrix of `dtype` (float32 and, short of its range, bfloat16
     hold every one exactly)."""
     if stream is not None:
-        return _on(stream, _native.dequantize_fp4, (q, dtype, out), (q.data, q.scales, out))
+        return _on(stream, _native.dequantize_fp4, (q, dtype, out), (*_parts(q), out))
     return _native.dequantize_fp4(q, dtype, out)
 
 
@@ -187,7 +192,7 @@ def gemm_fp4_nt(A: Fp4Tensor, B: Fp4Tensor, D=None, *, dtype=torch.float16, alph
     """
     address = 0 if options is None else ctypes.addressof(options)
     if stream is not None:
-        return _on(stream, _native.gemm_fp4_nt, (A, B, D, dtype, alpha, address), (A.data, A.scales, B.data, B.scales, D))
+        return _on(stream, _native.gemm_fp4_nt, (A, B, D, dtype, alpha, address), (*_parts(A), *_parts(B), D))
     return _native.gemm_fp4_nt(A, B, D, dtype, alpha, address)
 
 

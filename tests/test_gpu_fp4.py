@@ -367,6 +367,19 @@ def test_streams_and_graphs(g):
     assert torch.equal(d3, g.gemm_fp4_nt(q, b))
 
 
+def test_refusals_on_a_stream(g):
+    """What a call refuses it refuses with stream= as well, by the same error."""
+    x, side = normal(1, 8, 64, F16), torch.cuda.Stream()
+    q = g.quantize_fp4(x, "mx")
+    for bad in (lambda: g.dequantize_fp4(x, stream=side), lambda: g.gemm_fp4_nt(x, x, stream=side), lambda: g.gemm_fp4_nt(q, x, stream=side),
+                lambda: g.gemm_fp4_nt(3, q, stream=side), lambda: g.quantize_fp4(x, out=x, stream=side)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(ValueError):
+        g.quantize_fp4(x, "nv", out=q, stream=side)
+    assert torch.equal(g.dequantize_fp4(q, stream=side), g.dequantize_fp4(q))
+
+
 def test_chain_of_dependent_calls(g):
     """Each call reads what the one before wrote, with overlapped launches between them."""
     w = g.quantize_fp4(normal(1, 512, 512, scale=0.06), "mx")

@@ -149,6 +149,21 @@ def test_cpu_tensors_and_wrong_types_are_refused():
             bad()
 
 
+@pytest.mark.parametrize("kwargs", [{}, dict(stream=0)], ids=["here", "stream"])
+def test_refusals_are_the_same_on_a_stream(kwargs):
+    x, q = torch.zeros(4, 64), g.Fp4Tensor(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(1, 1, 32, 4, 4, dtype=torch.uint8), 64)
+    for bad in (lambda: g.layer_norm(3, **kwargs), lambda: g.layer_norm(None, **kwargs), lambda: g.layer_norm_backward(1, 2, 3, 4, 5, **kwargs),
+                lambda: g.quantize_fp4("x", **kwargs), lambda: g.dequantize_fp4(x, **kwargs), lambda: g.dequantize_fp4(None, **kwargs),
+                lambda: g.gemm_fp4_nt(x, q, **kwargs), lambda: g.gemm_fp4_nt(3, 4, **kwargs),
+                lambda: g.gemm_fp4_nt((), (), **kwargs), lambda: g.quantize_fp4(3, out=4, **kwargs)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: g.layer_norm(x, **kwargs), lambda: g.quantize_fp4(x, **kwargs), lambda: g.dequantize_fp4(q, **kwargs),
+                lambda: g.gemm_fp4_nt(q, q, **kwargs)):
+        with pytest.raises(ValueError):
+            bad()
+
+
 # ------------------------------------------------------------ the reference --
 
 def test_reference_formats_by_hand():

@@ -190,6 +190,8 @@ def gemm_fp4_nt(A: Fp4Tensor, B: Fp4Tensor, D=None, *, dtype=torch.float16, alph
     matrices' exponents are brought in whatever their sum; alpha and they together may leave fp32's
     range.
     """
+    if options is not None and not isinstance(options, Fp4Options):
+        raise TypeError("options must be an Fp4Options")
     address = 0 if options is None else ctypes.addressof(options)
     if stream is not None:
         return _on(stream, _native.gemm_fp4_nt, (A, B, D, dtype, alpha, address), (*_parts(A), *_parts(B), D))

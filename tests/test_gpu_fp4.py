@@ -372,7 +372,8 @@ def test_refusals_on_a_stream(g):
     x, side = normal(1, 8, 64, F16), torch.cuda.Stream()
     q = g.quantize_fp4(x, "mx")
     for bad in (lambda: g.dequantize_fp4(x, stream=side), lambda: g.gemm_fp4_nt(x, x, stream=side), lambda: g.gemm_fp4_nt(q, x, stream=side),
-                lambda: g.gemm_fp4_nt(3, q, stream=side), lambda: g.quantize_fp4(x, out=x, stream=side)):
+                lambda: g.gemm_fp4_nt(3, q, stream=side), lambda: g.quantize_fp4(x, out=x, stream=side),
+                lambda: g.gemm_fp4_nt(q, q, options=g.Options(), stream=side)):
         with pytest.raises(TypeError):
             bad()
     with pytest.raises(ValueError):

@@ -164,6 +164,13 @@ def test_refusals_are_the_same_on_a_stream(kwargs):
             bad()
 
 
+@pytest.mark.parametrize("options", [g.Options(), 0, {}, (16, 0, 0, 0, 0, 0, 0)], ids=["f16", "int", "dict", "tuple"])
+def test_options_of_another_type_are_refused(options):
+    q = g.Fp4Tensor(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(1, 1, 32, 4, 4, dtype=torch.uint8), 64)
+    with pytest.raises(TypeError):
+        g.gemm_fp4_nt(q, q, options=options)
+
+
 # ------------------------------------------------------------ the reference --
 
 def test_reference_formats_by_hand():

@@ -353,7 +353,7 @@ PyObject *dequantize(PyObject *const *args, Py_ssize_t n) {  // q, dtype, out
         }
         step = rows_of(y, "out").step;
     } else {
-        y = empty({q.rows, q.cols}, dtype_arg(args[1], "dtype"), *q.data);
+        y = empty({q.rows, q.cols}, given(args[1]) ? dtype_arg(args[1], "dtype") : at::kFloat, *q.data);
     }
     check_status(fp4_dequantize(q.data->data_ptr(), q.scales->data_ptr(), q.rows, q.cols, q.format.code,
                                 q.format.exponent, y.data_ptr(), step, dtype_of(y, "out"), stream_of(y)),
@@ -399,7 +399,7 @@ PyObject *product(PyObject *const *args, Py_ssize_t n) {  // A, B, D, dtype, alp
                    static_cast<long long>(a.rows), static_cast<long long>(b.rows));
         }
     } else {
-        d = empty({a.rows, b.rows}, dtype_arg(args[3], "dtype"), *a.data);
+        d = empty({a.rows, b.rows}, given(args[3]) ? dtype_arg(args[3], "dtype") : at::kHalf, *a.data);
     }
     check_status(gemm_fp4_nt(a.data->data_ptr(), a.scales->data_ptr(), b.data->data_ptr(), b.scales->data_ptr(),
                              d.data_ptr(), a.rows, b.rows, a.cols, a.format.code, dtype_of(d, "D"),

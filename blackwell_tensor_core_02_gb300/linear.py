@@ -4,7 +4,7 @@ microscaled 4-bit floats, and the product of two such matrices.
 Argument marshalling over the C ABI of ``include/linear_ops.h`` (library ``_build/liblinear_ops.so``),
 as the package's ``gemm_f16_nt`` is over its own, here by a compiled binding (``csrc/linear/binding.cpp``):
 PyTorch supplies memory and streams, every step of the computation runs in the library, and there is
-no fallback.
+no fallback.  The first call builds what is stale and loads it (importing this module does neither).
 
     y, mean, rstd = g.layer_norm(x, weight, bias)
     dx, dweight, dbias = g.layer_norm_backward(dy, x, weight, mean, rstd)
@@ -20,11 +20,12 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import threading
-from typing import NamedTuple
-
-import torch
+from typing import TYPE_CHECKING, NamedTuple
 
 from . import build as _build
+
+if TYPE_CHECKING:
+    import torch
 
 __all__ = ["layer_norm", "layer_norm_backward", "Fp4Tensor", "quantize_fp4", "dequantize_fp4", "gemm_fp4_nt",
            "Fp4Options", "describe_fp4", "fp4_device_status"]
@@ -69,8 +70,9 @@ _lib: ctypes.CDLL | None = None
 
 
 def load_linear() -> ctypes.CDLL:
-    """Build (if stale) and load the library; raise if that is impossible."""
+    """Build (if stale) and load the library and its binding; raise if that is impossible."""
     global _lib
+    _native.layer_norm  # loads the binding
     if _lib is None:
         with _lock:
             if _lib is None:
@@ -106,11 +108,24 @@ def _load_binding():
     return module
 
 
-_native = _load_binding()
+class _Unloaded:
+    """The binding before its first use, which puts the loaded one in its place."""
+
+    def __getattr__(self, name):
+        global _native
+        with _lock:
+            if _native is self:
+                _native = _load_binding()
+        return getattr(_native, name)
+
+
+_native = _Unloaded()
 
 
 def _on(stream, call, args, tensors):
     """call(*args) on `stream` (a torch stream or a handle), the tensors' memory kept until it has run."""
+    import torch
+
     device = next((t.device for t in tensors if isinstance(t, torch.Tensor)), None)
     if device is None or device.type != "cuda":
         return call(*args)  # refused there
@@ -174,17 +189,18 @@ def quantize_fp4(x, format: str = "mx", *, exponent: int = 0, out: Fp4Tensor | N
     return Fp4Tensor(data, scales, x.shape[1], format, exponent) if out is None else out
 
 
-def dequantize_fp4(q: Fp4Tensor, dtype=torch.float32, *, out=None, stream=None):
-    """The values of q as a rows x cols matrix of `dtype` (float32 and, short of its range, bfloat16
-    hold every one exactly)."""
+def dequantize_fp4(q: Fp4Tensor, dtype=None, *, out=None, stream=None):
+    """The values of q as a rows x cols matrix of `dtype` (None: torch.float32; it and, short of its
+    range, bfloat16 hold every one exactly)."""
     if stream is not None:
         return _on(stream, _native.dequantize_fp4, (q, dtype, out), (*_parts(q), out))
     return _native.dequantize_fp4(q, dtype, out)
 
 
-def gemm_fp4_nt(A: Fp4Tensor, B: Fp4Tensor, D=None, *, dtype=torch.float16, alpha: float = 1.0, stream=None,
+def gemm_fp4_nt(A: Fp4Tensor, B: Fp4Tensor, D=None, *, dtype=None, alpha: float = 1.0, stream=None,
                 options: Fp4Options | None = None):
-    """D = alpha * A·Bᵀ of the values of A (M×K) and B (N×K), both of one format; returns D (M×N).
+    """D = alpha * A·Bᵀ of the values of A (M×K) and B (N×K), both of one format; returns D (M×N; of
+    `dtype` if none is given, None: torch.float16).
 
     The sum is fp32 on the tensor cores, D (float16, bfloat16 or float32) is rounded once.  "nv"
     matrices' exponents are brought in whatever their sum; alpha and they together may leave fp32's
@@ -213,6 +229,8 @@ def describe_fp4(M: int, N: int, K: int, format: str = "mx", options: Fp4Options
 
 def fp4_device_status(stream=None) -> tuple[int, int]:
     """(status, info) of the products' device status word, after synchronising `stream`; clears it."""
+    import torch
+
     handle = torch.cuda.current_stream().cuda_stream if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
     info = ctypes.c_uint64(0)
     rc = load_linear().gemm_fp4_last_device_status(handle, ctypes.byref(info))

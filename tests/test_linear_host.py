@@ -137,6 +137,52 @@ def test_choice_of_tile():
         g.describe_fp4(1, 1, 1, "int4")
 
 
+def test_import_builds_nothing():
+    """`import *` brings the operators' names without torch, a build or a compiler; the first call
+    builds."""
+    code = """
+import sys
+sys.modules["torch"] = None
+import blackwell_tensor_core_02_gb300.build as build
+def refuse(*args, **kwargs):
+    raise SystemExit("built")
+build.build_many = build.build_binding = refuse
+from blackwell_tensor_core_02_gb300 import *
+q = Fp4Tensor(None, None, 64, "nv", 3)
+assert q.exponent == 3 and gemm_fp4_nt and Fp4Options(tile=16).tile == 16
+print("imported")
+layer_norm(3)
+"""
+    import sys
+
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.stdout == "imported\n" and r.returncode == 1 and "built" in r.stderr, r.stderr
+
+
+def test_first_calls_from_several_threads():
+    """The binding is loaded once, whoever calls first."""
+    code = """
+import threading
+import torch
+import blackwell_tensor_core_02_gb300 as g
+from blackwell_tensor_core_02_gb300 import linear
+loads, load, errors = [], linear._load_binding, []
+linear._load_binding = lambda: loads.append(0) or load()
+def call():
+    try:
+        g.layer_norm(torch.zeros(2, 8))
+    except ValueError as e:
+        errors.append(e)
+threads = [threading.Thread(target=call) for _ in range(8)]
+[t.start() for t in threads], [t.join() for t in threads]
+assert len(loads) == 1 and len(errors) == 8, (len(loads), len(errors))
+"""
+    import sys
+
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
 def test_cpu_tensors_and_wrong_types_are_refused():
     x = torch.zeros(4, 64)
     for bad in (lambda: g.layer_norm(x), lambda: g.layer_norm(x, stream=0), lambda: g.quantize_fp4(x),

@@ -102,6 +102,18 @@ def test_many_rows(g, rows, cols):
     check_backward(g, dy, x, w, mean, rstd)
 
 
+# one row a CTA on 152 SMs, and as many as a CTA takes: 16, 12 and 3 of these widths
+@pytest.mark.parametrize("cols,rows", [(cols, rows + d) for cols, most in ((48, 16), (1024, 12), (4096, 3), (4099, 1))
+                                       for rows in sorted({152, 152 * 2, 152 * most}) for d in (-1, 0, 1)])
+def test_rows_around_the_parts(g, cols, rows):
+    """Each side of the row counts at which a CTA of the gradient takes a second row, or a row of its
+    threads does."""
+    x, dy = rows_of(rows, rows, cols, F16), rows_of(rows + 1, rows, cols, F16)
+    w, b = weights_of(3, cols, F32)
+    _, mean, rstd = check_forward(g, x, w, b, 1e-5)
+    check_backward(g, dy, x, w, mean, rstd)
+
+
 @pytest.mark.parametrize("gap,shift", [(8, 0), (6, 0), (0, 1), (8, 8), (3, 5)])
 @pytest.mark.parametrize("dtype", [F16, F32], ids=["f16", "f32"])
 def test_strides_and_alignment(g, gap, shift, dtype):

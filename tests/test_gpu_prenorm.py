@@ -80,6 +80,44 @@ def test_weights_without_a_size(gpu_lib, fmt, value):
     assert bool((served != 0).any()) == (value != 0.0) and gpu_lib.fp4_device_status()[0] == 0
 
 
+def test_calls_from_several_threads(gpu_lib, layer):
+    """Threads with streams of their own, each the first to launch some shape: the results are those
+    of one thread alone."""
+    import threading
+
+    g = gpu_lib
+    layer.quantize("nv")
+    inputs = [(_x(tokens, tokens), _x(tokens, tokens + 1)) for tokens in (3, 40, 129, 700)]
+
+    def work(x, dy, stream=None):
+        y, mean, rstd = g.layer_norm(x, layer.scale, layer.shift, stream=stream)
+        grads = g.layer_norm_backward(dy, x, layer.scale, mean, rstd, stream=stream)
+        q = g.quantize_fp4(y, "nv", stream=stream)
+        return (y, *grads, g.gemm_fp4_nt(q, layer.weight4, stream=stream), g.dequantize_fp4(q, stream=stream))
+
+    results, failures = {}, []
+
+    def run(i):
+        try:
+            side = torch.cuda.Stream()
+            for _ in range(20):
+                results[i] = work(*inputs[i % len(inputs)], stream=side)
+            side.synchronize()
+        except Exception as e:  # seen by the test below
+            failures.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures and len(results) == 8, failures
+    for i, got in results.items():
+        assert all(torch.equal(a, b) for a, b in zip(got, work(*inputs[i % len(inputs)])))
+    assert g.fp4_device_status()[0] == 0
+
+
 def test_command(capsys, gpu_lib):
     from blackwell_tensor_core_02_gb300 import prenorm
 

@@ -408,8 +408,12 @@ int layer_norm_backward(const void *dy, int64_t dy_stride, const void *x, int64_
                  {workspace, need}},
       ins[5] = {{dy, span_bytes(rows, cols, dy_stride, size)}, {x, span_bytes(rows, cols, x_stride, size)},
                 {weight, cols * wsize}, {mean, rows * 4}, {rstd, rows * 4}};
+    if (rows_overlap(dx, dy, rows, cols * size, dx_stride * size, dy_stride * size) ||
+        rows_overlap(dx, x, rows, cols * size, dx_stride * size, x_stride * size)) {
+        return GEMM_ERR_INVALID_ARG;
+    }
     for (int i = 0; i < 4; ++i) {
-        for (int j = 0; j < 5; ++j) {
+        for (int j = i == 0 ? 2 : 0; j < 5; ++j) {  // dx with dy and x above
             if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return GEMM_ERR_INVALID_ARG;
         }
         for (int j = 0; j < i; ++j) {

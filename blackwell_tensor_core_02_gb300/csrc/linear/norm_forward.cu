@@ -283,8 +283,9 @@ int layer_norm_forward(const void *x, int64_t x_stride, const void *weight, cons
         int64_t bytes;
     } outs[3] = {{y, span_bytes(rows, cols, y_stride, size)}, {mean, rows * 4}, {rstd, rows * 4}},
       ins[3] = {{x, span_bytes(rows, cols, x_stride, size)}, {weight, cols * wsize}, {bias, cols * wsize}};
+    if (rows_overlap(y, x, rows, cols * size, y_stride * size, x_stride * size)) return GEMM_ERR_INVALID_ARG;
     for (int i = 0; i < 3; ++i) {
-        for (int j = 0; j < 3; ++j) {
+        for (int j = i == 0 ? 1 : 0; j < 3; ++j) {  // y and x above
             if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return GEMM_ERR_INVALID_ARG;
         }
         for (int j = 0; j < i; ++j) {

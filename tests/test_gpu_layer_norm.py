@@ -135,6 +135,29 @@ def test_strides_and_alignment(g, gap, shift, dtype):
                ref.norm_grad_bounds(dy, x, wv, mean, rstd, dtype, F32)[0], "dx with a gap")
 
 
+@pytest.mark.parametrize("dtype", [F16, F32], ids=["f16", "f32"])
+@pytest.mark.parametrize("cols,gap", [(1000, 0), (1024, 0), (333, 0), (1021, 3), (16400, 0)])
+def test_slices_of_one_matrix(g, cols, gap, dtype):
+    """Input and output beside each other in the rows of one buffer: the bits of separate tensors,
+    and the rest of the buffer as it was."""
+    rows, width = 200, cols + gap
+    buf = rows_of(1, rows, 4 * width, dtype).contiguous()
+    x, dy, y, dx = (buf[:, i * width:i * width + cols] for i in range(4))
+    w, b = weights_of(3, cols, F32)
+    kept = buf.clone()
+    xs, dys = (kept[:, i * width:i * width + cols] for i in range(2))
+    # the same rows elsewhere, so that the kernels are the same
+    want = g.layer_norm(xs, w, b, out=torch.empty_like(kept)[:, 2 * width:2 * width + cols])
+    grads = g.layer_norm_backward(dys, xs, w, *want[1:], dx=torch.empty_like(kept)[:, 3 * width:3 * width + cols])
+    got = g.layer_norm(x, w, b, out=y)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert all(torch.equal(p, q) for p, q in zip(g.layer_norm_backward(dy, x, w, *got[1:], dx=dx), grads))
+    kept[:, 2 * width:2 * width + cols], kept[:, 3 * width:3 * width + cols] = want[0], grads[0]
+    assert torch.equal(buf, kept)
+    with pytest.raises(g.GemmError):
+        g.layer_norm(x, w, b, out=buf[:, 1:1 + cols])
+
+
 def test_one_row_read_many_times(g):
     """An expanded row (stride 0): every output row is its norm, the gradients sum over all."""
     x = rows_of(5, 1, 768, F16).expand(50, 768)

@@ -79,6 +79,23 @@ def test_layer_norm_refusals():
     assert g.load_linear().layer_norm_backward_workspace_size(-1, 64) == INVALID
 
 
+def test_layer_norm_rows_between_each_others():
+    """Slices of one wider matrix share no memory unless their columns do; 4 rows of 64 halves, 256
+    bytes apart.  (Where nothing is refused the calls end at the missing device.)"""
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real")
+    for y, refused in ((P + 128, False), (P + 126, True), (P + 2, True), (P + 130, True), (P - 128, False), (P - 126, True),
+                       (P + 3 * 256 + 128, False), (P + 2 * 256, True), (P + 4 * 256, False), (P - 3 * 256 - 128, False)):
+        assert (norm(x=P, xs=128, y=y, ys=128) == INVALID) == refused, y - P
+        assert (grad(dy=P, ds=128, dx=y, dxs=128) == INVALID) == refused, y - P
+        assert (grad(x=P, xs=128, dy=9 * P, dx=y, dxs=128) == INVALID) == refused, y - P
+    assert norm(x=P, xs=128, y=P + 128, ys=136) == norm(x=P, xs=0, y=P - 128, ys=128) == INVALID
+    assert norm(x=P, xs=64, y=P + 128, ys=64) == norm(rows=1, xs=128, y=P + 64, ys=128) == INVALID
+    assert norm(x=P, xs=128, y=P + 128, ys=128, mean=P + 128) == grad(dy=P, ds=128, dx=P + 128, dxs=128, dw=P) == INVALID
+
+
 def test_fp4_sizes_and_refusals():
     lib = g.load_linear()
     for rows, cols, data, mx, nv in ((1, 1, 16, 512, 512), (128, 128, 128 * 64, 512, 1024), (129, 129, 129 * 80, 2 * 1024, 2 * 1536),

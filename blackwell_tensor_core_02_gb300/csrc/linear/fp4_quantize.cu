@@ -8,7 +8,7 @@
 // of a row) is gathered from 4 or 8 lanes and stored once.
 //
 // 8192 x 4096 (share of the copy rate): fp16 to mx 15.7 us (80 %, with two thirds of
-// the issue slots taken), bf16 to nv 17.4 (73 %), fp32 to mx 23.1 (97 %), back to bf16
+// the issue slots taken), bf16 to nv 17.5 (72 %), fp32 to mx 23.1 (97 %), back to bf16
 // 13.7 (91 %).  Rows that start anywhere: 4096 x 4099 fp16 to mx 11.2 us (56 %), back
 // 11.5.  One row of 8192: 2.0 us and 1.1.
 #include "common.cuh"
@@ -127,7 +127,7 @@ __device__ __forceinline__ uint32_t largest(const uint32_t (&w)[N]) {
 
 // FP4_NV, with the longer arithmetic, runs on a grid of the CTAs that fit at once: a
 // thread takes rows a grid apart and loads its unit of the next row while it works
-// on this one (8192 x 4096 bf16: 17.4 us, a CTA for each row 18.7; FP4_MX 15.6 and
+// on this one (8192 x 4096 bf16: 17.5 us, a CTA for each row 18.7; FP4_MX 15.6 and
 // 15.4, so it takes a CTA for each row, and so do rows that start anywhere, whose
 // loads take more registers).
 template <typename T, bool NV, int LAYOUT>

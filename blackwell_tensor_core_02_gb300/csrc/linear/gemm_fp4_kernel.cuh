@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(192, 2)
 //
 // Bound by the MMAs, 512 cycles a stage (520 measured, and some 2000 a tile between
 // tiles): 8192 x 8192 x 8192 mx 148 us, 7.4 PFLOP/s; 8192 x 28672 x 4096 mx 270 us,
-// 7.1.  One tile a pair is bound by the start, the first loads and the epilogue:
+// 7.1, in a short run (300 in a stream of calls under the power cap; nv 300 to 319).  One tile a pair is bound by the start, the first loads and the epilogue:
 // 1000 x 1528 x 256 4.5 us, 512 x 4096 x 4096 8.65.  Eight epilogue warps of 128
 // columns, as one warp's way through TMEM, registers and staging is latency: with
 // four of 256 columns these took 5.0 and 9.2 us.

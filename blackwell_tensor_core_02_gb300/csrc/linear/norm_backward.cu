@@ -29,12 +29,12 @@ struct GradArgs {
 // A row is read from the ring twice, once for its sums and once for dx: holding
 // h and g in between takes 64 registers more a thread, which halves the rows at
 // work on an SM, and a row's time is the latency of its sums.  8192 x 4096 bf16
-// (the memory takes 29.6 us at the copy rate): 36.4 us, with them held 40.1; 31.8
+// (the memory takes 29.6 us at the copy rate): 36.2 us, with them held 40.1; 32.1
 // without the weights' gradient, the rest is the parts' way to the join.  4096 x
 // 8192 fp16 41.9 us (parts twice as long), 4096 x 4096 fp32 34.7.  Of rows past 8192
 // columns one is at work on an SM: 2048 x 12288 bf16 33.4 us, and past 12288 of 16
 // bits the weights are read again with each row and the ring has two stages: 2048 x
-// 16384 53.7.  Whole rows in a second pass over memory (norm_backward_long_kernel)
+// 16384 50.2.  Whole rows in a second pass over memory (norm_backward_long_kernel)
 // took 84 and 93; fp32 rows past 12288 still do, their ring has no room.
 // The second pass of a row behind the first pass of the next, with one barrier a
 // row, gained nothing (8192 x 4096 36.9, 4096 x 8192 42.0, 8192 x 1024 16.4; 14.0 as

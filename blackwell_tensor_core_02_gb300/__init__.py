@@ -13,6 +13,7 @@ cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import threading
 
 from . import build as _build
@@ -398,13 +399,15 @@ def pipeline_trace(depth: int, initial_phase: int, steps: int) -> list[tuple[int
 # The operators around the product of a linear layer (they need torch, as every call above does).
 _LINEAR = ("layer_norm", "layer_norm_backward", "Fp4Tensor", "quantize_fp4", "dequantize_fp4", "gemm_fp4_nt", "Fp4Options",
            "describe_fp4", "fp4_device_status", "load_linear")
-__all__ += list(_LINEAR)
+# Products grouped by rows, likewise.
+_GROUPED = ("grouped_gemm_nt", "grouped_gemm_nn", "grouped_gemm_tn", "GroupedOptions", "grouped_device_status")
+__all__ += [*_LINEAR, *_GROUPED]
 
 
 def __getattr__(name):
-    if name in _LINEAR:
-        from . import linear
-
-        globals().update({n: getattr(linear, n) for n in _LINEAR})
-        return globals()[name]
+    for names, module in ((_LINEAR, "linear"), (_GROUPED, "grouped")):
+        if name in names:
+            module = importlib.import_module(f".{module}", __name__)
+            globals().update({n: getattr(module, n) for n in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -89,7 +89,7 @@ def build_binding(force: bool = False) -> str:
     the operators' library, which is built first.)"""
     build_linear()
     path = binding_path()
-    sources = [os.path.join(LINEAR_CSRC, "binding.cpp"), os.path.join(INCLUDE, "linear_ops.h"), os.path.join(INCLUDE, "gemm_f16.h")]
+    sources = [os.path.join(LINEAR_CSRC, "binding.cpp"), *glob.glob(os.path.join(INCLUDE, "*.h"))]
     if force or not os.path.exists(path) or any(os.path.getmtime(s) > os.path.getmtime(path) for s in sources):
         tmp = f"{path}.{os.getpid()}.tmp"
         r = subprocess.run(_binding_command(tmp), capture_output=True, text=True)

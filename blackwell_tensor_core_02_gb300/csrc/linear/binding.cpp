@@ -1,6 +1,6 @@
-// binding.cpp -- the calls of linear.py below their keyword handling: checks of the
-// tensors, outputs and workspaces from torch's allocator, the current stream, and
-// the C entry points of linear_ops.h.
+// binding.cpp -- the calls of linear.py and grouped.py below their keyword handling:
+// checks of the tensors, outputs and workspaces from torch's allocator, the current
+// stream, and the C entry points of linear_ops.h and grouped_ops.h.
 //
 // The smallest calls (one token) run for two to four microseconds on the GPU, far
 // less than the same checks, allocations and conversions take in Python (a layer
@@ -21,6 +21,7 @@
 #include <cmath>
 #include <initializer_list>
 
+#include "grouped_ops.h"
 #include "linear_ops.h"
 
 namespace {
@@ -408,6 +409,110 @@ PyObject *product(PyObject *const *args, Py_ssize_t n) {  // A, B, D, dtype, alp
     return THPVariable_Wrap(d);
 }
 
+// ---------------------------------------------------------------- grouped --
+
+int half_type(const at::Tensor &t, const char *name) {
+    const int code = dtype_code(t.scalar_type());
+    if (code != LINEAR_F16 && code != LINEAR_BF16) refuse(PyExc_TypeError, "%s must be float16 or bfloat16", name);
+    return code;
+}
+
+// A tensor of `dims` axes, the last contiguous, of like's type on its device.
+void operand(const at::Tensor &t, const char *name, int64_t dims, const at::Tensor &like) {
+    if (t.scalar_type() != like.scalar_type()) refuse(PyExc_TypeError, "%s must have the first operand's dtype", name);
+    if (!t.is_cuda() || t.device() != like.device()) {
+        refuse(PyExc_ValueError, "%s must be a CUDA tensor, all on one device", name);
+    }
+    if (t.dim() != dims) refuse(PyExc_ValueError, "%s must have %lld axes", name, static_cast<long long>(dims));
+    if (t.size(dims - 1) > 1 && t.stride(dims - 1) != 1) {
+        refuse(PyExc_ValueError, "%s: its last axis must be contiguous", name);
+    }
+}
+
+// Whole numbers in device memory; whether they are 64-bit.
+int whole_numbers(const at::Tensor &t, const char *name, int64_t count, const at::Tensor &like) {
+    if (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong) refuse(PyExc_TypeError, "%s must be int32 or int64", name);
+    if (t.device() != like.device() || t.dim() != 1 || t.size(0) != count || !t.is_contiguous()) {
+        refuse(PyExc_ValueError, "%s must be a contiguous vector of %lld on the operands' device", name,
+               static_cast<long long>(count));
+    }
+    return t.scalar_type() == at::kLong;
+}
+
+const grouped_options *grouped_opts(PyObject *o) {
+    const void *p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw Refused{};
+    return static_cast<const grouped_options *>(p);
+}
+
+// The rows of a result, `like`'s or given, and whether they are new.
+at::Tensor grouped_rows(PyObject *o, const char *name, int64_t rows, int64_t cols, const at::Tensor &like, bool *made) {
+    *made = !given(o);
+    if (*made) return empty({rows, cols}, like.scalar_type(), like);
+    const at::Tensor &t = tensor(o, name);
+    operand(t, name, 2, like);
+    if (t.size(0) != rows || t.size(1) != cols) {
+        refuse(PyExc_ValueError, "%s must be %lld x %lld", name, static_cast<long long>(rows), static_cast<long long>(cols));
+    }
+    return t;
+}
+
+// The two products whose results have the ragged rows: NT (x is A, the result D) and NN (x is dD, the result dA).
+template <bool NT>
+PyObject *grouped_rows_product(PyObject *const *args, Py_ssize_t n) {  // x, B, offsets, out, address of the options or 0
+    count(n, 5);
+    const at::Tensor &x = tensor(args[0], NT ? "A" : "dD"), &B = tensor(args[1], "B"), &offsets = tensor(args[2], "offsets");
+    const int code = half_type(x, NT ? "A" : "dD");
+    operand(x, NT ? "A" : "dD", 2, x);
+    operand(B, "B", 3, x);
+    const int64_t rows = x.size(0), groups = B.size(0), N = B.size(1), K = B.size(2);
+    if (x.size(1) != (NT ? K : N)) {
+        refuse(PyExc_ValueError, NT ? "expected A (rows x K) and B (groups x N x K), got rows of %lld and of %lld"
+                                    : "expected dD (rows x N) and B (groups x N x K), got rows of %lld and N %lld",
+               static_cast<long long>(x.size(1)), static_cast<long long>(NT ? K : N));
+    }
+    const int wide = whole_numbers(offsets, "offsets", groups + 1, x);
+    const grouped_options *opts = grouped_opts(args[4]);
+    const c10::cuda::CUDAGuard guard(x.device());
+    bool made = false;
+    at::Tensor out = grouped_rows(args[3], NT ? "D" : "dA", rows, NT ? N : K, x, &made);
+    const auto call = NT ? grouped_gemm_nt : grouped_gemm_nn;
+    check_status(call(x.data_ptr(), x.stride(0), B.data_ptr(), B.stride(1), B.stride(0), offsets.data_ptr(), wide,
+                      out.data_ptr(), out.stride(0), rows, groups, N, K, code, made, stream_of(x), opts),
+                 NT ? "grouped_gemm_nt" : "grouped_gemm_nn");
+    return THPVariable_Wrap(out);
+}
+
+PyObject *grouped_matrices(PyObject *const *args, Py_ssize_t n) {  // dD, A, offsets, dB, address of the options or 0
+    count(n, 5);
+    const at::Tensor &dD = tensor(args[0], "dD"), &A = tensor(args[1], "A"), &offsets = tensor(args[2], "offsets");
+    const int code = half_type(dD, "dD");
+    operand(dD, "dD", 2, dD);
+    operand(A, "A", 2, dD);
+    const int64_t rows = dD.size(0), N = dD.size(1), K = A.size(1);
+    if (A.size(0) != rows) refuse(PyExc_ValueError, "expected dD (rows x N) and A (rows x K) of the same rows");
+    const int64_t groups = offsets.numel() - 1;
+    if (groups < 0) refuse(PyExc_ValueError, "offsets must be a vector of at least one");
+    const int wide = whole_numbers(offsets, "offsets", groups + 1, dD);
+    const grouped_options *opts = grouped_opts(args[4]);
+    const c10::cuda::CUDAGuard guard(dD.device());
+    at::Tensor dB;
+    if (given(args[3])) {
+        dB = tensor(args[3], "dB");
+        operand(dB, "dB", 3, dD);
+        if (dB.size(0) != groups || dB.size(1) != N || dB.size(2) != K) {
+            refuse(PyExc_ValueError, "dB must be %lld x %lld x %lld", static_cast<long long>(groups),
+                   static_cast<long long>(N), static_cast<long long>(K));
+        }
+    } else {
+        dB = empty({groups, N, K}, dD.scalar_type(), dD);
+    }
+    check_status(grouped_gemm_tn(dD.data_ptr(), dD.stride(0), A.data_ptr(), A.stride(0), offsets.data_ptr(), wide,
+                                 dB.data_ptr(), dB.stride(1), dB.stride(0), rows, groups, N, K, code, stream_of(dD), opts),
+                 "grouped_gemm_tn");
+    return THPVariable_Wrap(dB);
+}
+
 template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -432,6 +537,9 @@ PyMethodDef g_methods[] = {LINEAR_METHOD("layer_norm", norm),
                            LINEAR_METHOD("quantize_fp4", quantize),
                            LINEAR_METHOD("dequantize_fp4", dequantize),
                            LINEAR_METHOD("gemm_fp4_nt", product),
+                           LINEAR_METHOD("grouped_gemm_nt", grouped_rows_product<true>),
+                           LINEAR_METHOD("grouped_gemm_nn", grouped_rows_product<false>),
+                           LINEAR_METHOD("grouped_gemm_tn", grouped_matrices),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_linear_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

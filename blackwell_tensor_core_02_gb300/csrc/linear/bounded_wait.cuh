@@ -1,0 +1,44 @@
+// bounded_wait.cuh -- waits with a limit and the status word of the kernels that
+// include this: after `timeout_ns` a wait records where it gave up, raises its CTA's
+// abort flag and returns, so a protocol error ends a kernel instead of hanging the
+// GPU.  (The GEMM's own are in gemm_kernel.cuh, with its kernels; one translation
+// unit has one status word.)
+#pragma once
+
+#include <stdint.h>
+
+#include "../ptx.cuh"
+
+namespace linear_ops {
+
+__device__ int g_group_status;               // GEMM_ERR_DEVICE_TIMEOUT of the first wait that ran out (0: none)
+__device__ unsigned long long g_group_info;  // its role, CTA and tile
+
+enum : uint32_t { kWaitProducer = 1, kWaitMma = 2, kWaitEpilogue = 3, kWaitClear = 4 };
+
+// By one thread.  False if the wait ran out or, when `honor_abort`, as soon as another
+// role of this CTA has given up.  kCluster: the arrivals come from other CTAs of the
+// cluster, and what they wrote before is wanted.
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint64_t timeout_ns,
+                                             uint32_t role, uint32_t seq, bool honor_abort = true) {
+    namespace ptx = gemm_f16::ptx;
+    auto arrived = [&] { return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+    if (arrived()) return true;
+    const uint64_t begun = ptx::globaltimer_ns();
+    for (uint32_t turn = 1; !arrived(); ++turn) {
+        if (turn % 16 != 0) continue;
+        if (honor_abort && *abort_flag) return false;
+        if (ptx::globaltimer_ns() - begun > timeout_ns) {
+            *abort_flag = 1;
+            if (atomicCAS(&g_group_status, 0, -7) == 0) {
+                g_group_info = static_cast<unsigned long long>(role) << 56 |
+                               static_cast<unsigned long long>(blockIdx.x & 0xFFFFFFu) << 32 | seq;
+            }
+            return false;
+        }
+    }
+    return true;
+}
+
+}  // namespace linear_ops

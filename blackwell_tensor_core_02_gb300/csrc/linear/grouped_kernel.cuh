@@ -1,0 +1,609 @@
+// grouped_kernel.cuh -- products grouped by rows on the tensor cores
+// (tcgen05.mma kind::f16): each group of rows has a matrix of its own.
+//
+// All three directions are one sum, with the contiguous axis of the result, i,
+// on the 128-row side of the MMA (P) and the other, j, on its N side (Q):
+//
+//     out[j][i] = sum_r P[i][r] * Q[j][r]
+//
+//          i               j               r            P             Q
+//     NT   columns of B_e  rows (ragged)   K            B_e           A
+//     NN   K               rows (ragged)   columns      B_e, MN-major dD
+//     TN   K               columns of dD   rows (ragged) A, MN-major  dD, MN-major
+//
+// So the ragged axis of NT and NN is N of the MMA, which takes any multiple of 16:
+// a group's last tile costs what its rows cost, and few rows (decoding) leave the
+// matrices' bytes to stream through the 128-row side.  Results of other groups' rows
+// that a tile loaded with its own are other columns of the accumulator and are not
+// stored.
+//
+// The ragged axis of TN is summed over: rows of the next group that came with a
+// group's last K tile must not count, whatever they hold (zeros by mask times an
+// infinity would be NaN), so a warp of its own overwrites them with zeros in shared
+// memory, between the load's arrival and the MMA.  At most 15 rows: the MMAs go in
+// steps of 16.
+//
+// Persistent CTAs (or pairs, cta_group::2, 256 x 256 tiles) walk one list of tiles
+// over all groups; each CTA reads the offsets once and keeps the groups' first rows
+// and first tiles in shared memory, so the host needs to know no offset.
+//
+// Warps: 0 TMA producer, 1 MMA issuer and TMEM allocator, 2 reads the offsets and
+// clears the rows behind a group's end (TN), 4-7 epilogue.
+#pragma once
+
+#include "../schedule.h"
+#include "bounded_wait.cuh"
+#include "common.cuh"
+#include "grouped_ops.h"
+
+namespace linear_ops {
+
+using gemm_f16::PipelineState;
+
+namespace ptxg {
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
+                                                 int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// An arrival, possibly on the peer's barrier, that publishes no memory writes.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Makes this thread's ordinary shared-memory writes visible to the async proxy, the
+// peer CTA's MMAs among it.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// 16 TMEM lanes x 32 columns of 32 bits: thread t gets of lane t / 4 and columns 8 n + 2 (t % 4),
+// + 1 registers 4 n and 4 n + 1, of lane t / 4 + 8 registers 4 n + 2 and 4 n + 3.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements, transposed on the way: thread t holds of
+// matrix m elements (t / 4, 2 (t % 4)) and (t / 4, 2 (t % 4) + 1) in a word; threads
+// 8 m to 8 m + 7 give the addresses of the 16 bytes that its columns 0 to 7 become.
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: rows of
+// 64 elements along M/N (128 bytes), one for each k; 8 such rows are an atom of 1024
+// bytes (the stride offset, along K), blocks of 64 elements along M/N lie
+// `block_bytes` apart (the leading offset).  Other fields as in ptx::smem_desc_k_sw128.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_addr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// True in every thread if it is true in any of the 128 that share the barrier.
+__device__ __forceinline__ bool any_of_128(uint32_t barrier, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u), "r"(barrier)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void sync_128(uint32_t barrier) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(barrier) : "memory");
+}
+
+}  // namespace ptxg
+
+enum GroupMode { kGroupNT = 0, kGroupNN = 1, kGroupTN = 2 };
+
+// CG: CTAs of a tile; TN: its columns j.  A CTA holds 128 rows of P and TN / CG of Q.
+template <int CG, int TN, int MODE>
+struct GroupShape {
+    static constexpr int BLOCK_R = 64;  // 128 bytes of a K-major row, 64 rows of an MN-major tile
+    static constexpr int Q_ROWS = TN / CG;
+    static constexpr int P_BYTES = 128 * 128;
+    static constexpr int Q_BYTES = Q_ROWS * 128;
+    static constexpr int STAGE = P_BYTES + Q_BYTES;
+    static constexpr uint32_t TX = STAGE * CG;
+    static constexpr int STAGES = 196608 / STAGE < 9 ? 196608 / STAGE : 9;
+    static constexpr int TMEM_COLS = 2 * TN;
+    // The epilogue's staging: buffers of 32 rows j of 128 elements, as two boxes of 64 with
+    // the 128-byte swizzle.
+    static constexpr int BOX = 32 * 128;
+    static constexpr int BUF = 2 * BOX;
+    static constexpr int BUFS = 3;
+    static constexpr int OFF_P = 0;
+    static constexpr int OFF_Q = OFF_P + STAGES * P_BYTES;
+    static constexpr int OFF_D = OFF_Q + STAGES * Q_BYTES;
+    static constexpr int OFF_START = OFF_D + BUFS * BUF;                     // int32 [groups + 1]
+    static constexpr int OFF_TILES = OFF_START + 4 * (GROUPED_MAX_GROUPS + 4);  // int32 [groups + 1]
+    static constexpr int OFF_BAR = OFF_TILES + 4 * (GROUPED_MAX_GROUPS + 4);
+    // full, empty, land, peer [STAGES]; accumulator full, empty [2]; drain
+    static constexpr int OFF_MISC = OFF_BAR + (4 * STAGES + 5) * 8;
+    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 896;                 // from a multiple of 128 bytes to one of 1024
+    static constexpr int THREADS = 256;
+    static_assert(OFF_BAR % 8 == 0 && SMEM_ALLOC <= 232448, "227 KiB");
+    static_assert((CG == 2 && TN == 256) || (CG == 1 && (TN == 32 || TN == 64 || TN == 128)), "tile");
+    static_assert(MODE != kGroupTN || Q_ROWS % 64 == 0, "MN-major blocks of 64");
+};
+
+struct GroupParams {
+    const void *offsets;
+    void *out;
+    int64_t out_row, out_group;  // elements between rows j of the result, and between groups' matrices (TN)
+    int32_t offsets_64;
+    int32_t groups, rows;
+    int32_t I, J, R;             // sizes; the ragged one is `rows`
+    int32_t i_tiles, j_tiles;    // of a group; j_tiles for TN
+    int32_t bf16;
+    int32_t zero_rest;
+    uint32_t debug_flags;
+    uint64_t timeout_ns;
+};
+
+// A tile: its group, first i and j (of the result's row 0, or of the group's matrix),
+// the j that count, and the length of its sum from row r0 on.
+struct GroupTile {
+    int32_t group, i0, j0, n, r0, r;
+};
+
+// Tiles of a band of j tiles share their P tiles, one after the other; a group's P is
+// read again for each band.
+constexpr int kGroupBand = 8;
+
+template <int CG, int TN, int MODE>
+__device__ __forceinline__ GroupTile group_tile(const GroupParams &p, const int32_t *start, const int32_t *tiles, int t) {
+    int lo = 0, hi = p.groups;  // tiles[lo] <= t < tiles[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (tiles[mid] <= t) {
+            lo = mid;
+        } else {
+            hi = mid;
+        }
+    }
+    const int32_t first = start[lo], count = start[lo + 1] - first;
+    const int32_t J = MODE == kGroupTN ? p.J : count;
+    const int j_tiles = (J + TN - 1) / TN;
+    int l = t - tiles[lo];
+    const int band = l / (kGroupBand * p.i_tiles);
+    const int width = j_tiles - band * kGroupBand < kGroupBand ? j_tiles - band * kGroupBand : kGroupBand;
+    l -= band * kGroupBand * p.i_tiles;
+    GroupTile w;
+    w.group = lo;
+    w.i0 = l / width * (128 * CG);
+    const int32_t j = (band * kGroupBand + l % width) * TN;
+    w.n = J - j < TN ? J - j : TN;
+    w.j0 = MODE == kGroupTN ? j : first + j;
+    w.r0 = MODE == kGroupTN ? first : 0;
+    w.r = MODE == kGroupTN ? count : p.R;
+    return w;
+}
+
+// The groups' first rows (all threads), then from them, by one warp, their first tiles.
+__device__ __forceinline__ void group_starts(const GroupParams &p, int32_t *start, int thread, int threads) {
+    for (int e = thread; e <= p.groups; e += threads) {
+        const int64_t o = p.offsets_64 ? static_cast<const int64_t *>(p.offsets)[e]
+                                       : static_cast<int64_t>(static_cast<const int32_t *>(p.offsets)[e]);
+        start[e] = static_cast<int32_t>(o < 0 ? 0 : (o > p.rows ? p.rows : o));
+    }
+}
+template <int TN, int MODE>
+__device__ __forceinline__ void group_tiles(const GroupParams &p, int32_t *start, int32_t *tiles, int lane) {
+    int32_t most = 0, sum = 0;
+    for (int base = 0; base <= p.groups; base += 32) {
+        const int e = base + lane;
+        int32_t v = e <= p.groups ? start[e] : 0;
+        v = v > most ? v : most;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {  // none lies before its predecessor
+            const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o && u > v) v = u;
+        }
+        int32_t before = __shfl_up_sync(0xffffffffu, v, 1);
+        if (lane == 0) before = most;
+        // the tiles of group e - 1
+        int32_t n = e == 0 || e > p.groups ? 0 : (MODE == kGroupTN ? p.j_tiles : (v - before + TN - 1) / TN) * p.i_tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += u;
+        }
+        if (e <= p.groups) {
+            start[e] = v;
+            tiles[e] = sum + n;
+        }
+        most = __shfl_sync(0xffffffffu, v, 31);
+        sum += __shfl_sync(0xffffffffu, n, 31);
+    }
+}
+
+// Instruction descriptor of tcgen05.mma kind::f16 (PTX ISA): D fp32 [4,6)=1, A and B
+// fp16 [7,10)=[10,13)=0 or bf16 1, MN-major ones marked [15], [16], N>>3 at [17,23),
+// M>>4 at [24,29).
+template <int CG, int MODE>
+__device__ __forceinline__ uint32_t group_idesc(int n, bool bf16) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 * CG >> 4) << 24) | (bf16 ? (1u << 7) | (1u << 10) : 0u) |
+           (MODE != kGroupNT ? 1u << 15 : 0u) | (MODE == kGroupTN ? 1u << 16 : 0u);
+}
+
+__device__ __forceinline__ uint32_t pack_pair(bool bf16, uint32_t lo, uint32_t hi) {
+    const float2 v = make_float2(__uint_as_float(lo), __uint_as_float(hi));
+    uint32_t w;
+    if (bf16) {
+        Pair<__nv_bfloat16>::narrow(v, &w);
+    } else {
+        Pair<__half>::narrow(v, &w);
+    }
+    return w;
+}
+
+template <int CG, int TN, int MODE>
+__global__ void __launch_bounds__(256, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                   const __grid_constant__ CUtensorMap tmD, const GroupParams p) {
+    using C = GroupShape<CG, TN, MODE>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    const int rank = CG == 2 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+    const bool leader = rank == 0;
+    const int cluster = static_cast<int>(blockIdx.x) / CG, clusters = static_cast<int>(gridDim.x) / CG;
+
+    const uint32_t bar_full = base + C::OFF_BAR, bar_empty = bar_full + 8 * C::STAGES;
+    const uint32_t bar_land = bar_empty + 8 * C::STAGES;  // TN: a group's last K tile, in this CTA
+    const uint32_t bar_peer = bar_land + 8 * C::STAGES;   // TN: the same, cleared, in the peer
+    const uint32_t bar_tfull = bar_peer + 8 * C::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    int32_t *start = reinterpret_cast<int32_t *>(smem + C::OFF_START);
+    int32_t *tiles = reinterpret_cast<int32_t *>(smem + C::OFF_TILES);
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_empty + 8 * s, 1);
+            ptx::mbar_init(bar_land + 8 * s, 1);
+            ptx::mbar_init(bar_peer + 8 * s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(bar_tfull + 8 * a, 1);
+            ptx::mbar_init(bar_tempty + 8 * a, 4 * CG);  // the epilogue warps of all the tile's CTAs
+        }
+        ptx::mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        ptx::fence_mbarrier_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<CG>(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
+        ptx::tmem_relinquish<CG>();
+    }
+    if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    group_starts(p, start, static_cast<int>(threadIdx.x), C::THREADS);
+    __syncthreads();
+    if (warp == 2) group_tiles<TN, MODE>(p, start, tiles, lane);
+    ptx::tcgen05_fence_before();
+    if constexpr (CG == 2) {
+        ptx::cluster_sync();
+    } else {
+        __syncthreads();
+    }
+    ptx::tcgen05_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    const int total = tiles[p.groups];
+    auto tile_of = [&](int t) { return group_tile<CG, TN, MODE>(p, start, tiles, t); };
+    // N of a tile's MMAs; a pair's CTAs hold half of these rows of Q each
+    auto columns_of = [](const GroupTile &w) { return (w.n + 16 * CG - 1) / (16 * CG) * (16 * CG); };
+
+    if (warp == 0) {
+        if (ptx::elect_one()) {
+            PipelineState ring(C::STAGES, (p.debug_flags & 1u) ? 0u : 1u);
+            bool ok = true;
+            uint32_t seq = 0;
+            for (int t = cluster; ok && t < total; t += clusters, ++seq) {
+                const GroupTile w = tile_of(t);
+                const int k_tiles = (w.r + 63) / 64;
+                const int32_t i0 = w.i0 + rank * 128, j0 = w.j0 + rank * (columns_of(w) / 2);
+                for (int kt = 0; kt < k_tiles; ++kt) {
+                    if (!wait_bounded(bar_empty + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns,
+                                      kWaitProducer, seq)) {
+                        ok = false;
+                        break;
+                    }
+                    const int s = ring.stage, r = kt * 64;
+                    const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, sq = base + C::OFF_Q + s * C::Q_BYTES;
+                    uint32_t full = bar_full + 8 * s;
+                    if (MODE == kGroupTN && kt == k_tiles - 1 && w.r % 16 != 0) {
+                        // through the warp that clears the rows behind the group's end
+                        const uint32_t land = bar_land + 8 * s;
+                        ptx::mbar_arrive_expect_tx(land, C::STAGE);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) ptx::tma_load_2d(sp + b * 8192, &tmP, land, i0 + 64 * b, w.r0 + r);
+#pragma unroll
+                        for (int b = 0; b < C::Q_ROWS / 64; ++b) {
+                            ptx::tma_load_2d(sq + b * 8192, &tmQ, land, j0 + 64 * b, w.r0 + r);
+                        }
+                        ring.advance();
+                        continue;
+                    }
+                    if (leader) ptx::mbar_arrive_expect_tx(full, C::TX);
+                    if constexpr (CG == 2) full = ptx::mapa(full, 0);
+                    auto load_2d = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y) {
+                        if constexpr (CG == 2) {
+                            ptx::tma_load_2d_pair(dst, map, full, x, y);
+                        } else {
+                            ptx::tma_load_2d(dst, map, full, x, y);
+                        }
+                    };
+                    auto load_3d = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
+                        if constexpr (CG == 2) {
+                            ptxg::tma_load_3d_pair(dst, map, full, x, y, z);
+                        } else {
+                            ptxg::tma_load_3d(dst, map, full, x, y, z);
+                        }
+                    };
+                    if constexpr (MODE == kGroupNT) {
+                        load_3d(sp, &tmP, r, i0, w.group);
+                    } else if constexpr (MODE == kGroupNN) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) load_3d(sp + b * 8192, &tmP, i0 + 64 * b, r, w.group);
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) load_2d(sp + b * 8192, &tmP, i0 + 64 * b, w.r0 + r);
+                    }
+                    if constexpr (MODE != kGroupTN) {
+                        load_2d(sq, &tmQ, r, j0);
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < C::Q_ROWS / 64; ++b) load_2d(sq + b * 8192, &tmQ, j0 + 64 * b, w.r0 + r);
+                    }
+                    ring.advance();
+                }
+            }
+            if (!ok) {  // time for loads in flight to land before the shared memory goes
+                const uint64_t t0 = ptx::globaltimer_ns();
+                while (ptx::globaltimer_ns() - t0 < 20000) ptx::nanosleep(1000);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader && ptx::elect_one()) {
+            PipelineState ring(C::STAGES, 0u);
+            PipelineState acc(2, 1u);
+            bool ok = true;
+            uint32_t seq = 0;
+            for (int t = cluster; ok && t < total; t += clusters, ++seq) {
+                const GroupTile w = tile_of(t);
+                const int k_tiles = (w.r + 63) / 64;
+                if (k_tiles == 0) continue;
+                const uint32_t idesc = group_idesc<CG, MODE>(columns_of(w), p.bf16);
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc.stage * TN);
+                if (!wait_bounded(bar_tempty + 8 * acc.stage, acc.phase, abort_flag, p.timeout_ns, kWaitMma,
+                                  seq)) {
+                    break;
+                }
+                ptx::tcgen05_fence_after();
+                for (int kt = 0; kt < k_tiles; ++kt) {
+                    if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns,
+                                      kWaitMma, seq)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tcgen05_fence_after();
+                    const int s = ring.stage;
+                    const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, sq = base + C::OFF_Q + s * C::Q_BYTES;
+                    const uint64_t pd = MODE == kGroupNT ? ptx::smem_desc_k_sw128(sp) : ptxg::smem_desc_mn_sw128(sp, 8192);
+                    const uint64_t qd = MODE == kGroupTN ? ptxg::smem_desc_mn_sw128(sq, 8192) : ptx::smem_desc_k_sw128(sq);
+                    // 16 elements of the sum: 32 bytes of a K-major row, 16 rows of an MN-major tile
+                    constexpr uint64_t kP = MODE == kGroupNT ? 2 : 128, kQ = MODE == kGroupTN ? 128 : 2;
+                    const int steps = w.r - kt * 64 >= 64 ? 4 : (w.r - kt * 64 + 15) / 16;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k < steps) ptx::mma_f16<CG>(d, pd + k * kP, qd + k * kQ, idesc, kt > 0 || k > 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit<CG>(bar_empty + 8 * s, 0x3);
+                    ring.advance();
+                }
+                if (!ok) break;
+                ptx::mma_commit<CG>(bar_tfull + 8 * acc.stage, 0x3);
+                acc.advance();
+            }
+            ptx::mma_commit<CG>(bar_drain, 0x1);
+            wait_bounded(bar_drain, 0, abort_flag, p.timeout_ns, kWaitMma, 0xFFFFFFFFu, false);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        if constexpr (MODE == kGroupTN) {
+            int stage = 0;
+            uint32_t phases = 0, seq = 0;  // of the landing barriers, a bit a stage
+            for (int t = cluster; t < total; t += clusters, ++seq) {
+                const GroupTile w = tile_of(t);
+                const int k_tiles = (w.r + 63) / 64;
+                if (k_tiles == 0) continue;
+                const int s = (stage + k_tiles - 1) % C::STAGES;
+                stage = (s + 1) % C::STAGES;
+                if (w.r % 16 == 0) continue;
+                bool ok = true;
+                if (lane == 0) {
+                    ok = wait_bounded(bar_land + 8 * s, phases >> s & 1u, abort_flag, p.timeout_ns,
+                                      kWaitProducer, seq);
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                const int first = w.r - (k_tiles - 1) * 64, last = (first + 15) / 16 * 16;
+                const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, sq = base + C::OFF_Q + s * C::Q_BYTES;
+                for (int row = first; row < last; ++row) {  // 128 bytes of each block of 64
+                    for (int u = lane; u < 16; u += 32) {
+                        ptx::st_shared_v4(sp + (u / 8) * 8192 + row * 128 + u % 8 * 16, 0, 0, 0, 0);
+                    }
+                    for (int u = lane; u < C::Q_ROWS / 8; u += 32) {
+                        ptx::st_shared_v4(sq + (u / 8) * 8192 + row * 128 + u % 8 * 16, 0, 0, 0, 0);
+                    }
+                }
+                ptxg::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2 && !leader) {
+                        ptx::mbar_arrive_cluster(ptx::mapa(bar_peer + 8 * s, 0));
+                    } else {
+                        if constexpr (CG == 2) {
+                            ok = wait_bounded<true>(bar_peer + 8 * s, phases >> s & 1u, abort_flag, p.timeout_ns,
+                                                    kWaitProducer, seq);
+                        }
+                        if (ok) ptx::mbar_arrive(bar_full + 8 * s);
+                    }
+                }
+                phases ^= 1u << s;
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp - 4;
+        const uint32_t tempty = CG == 2 ? ptx::mapa(bar_tempty, 0) : bar_tempty;
+        const int tid = static_cast<int>(threadIdx.x) - 128;
+        uint16_t *out = static_cast<uint16_t *>(p.out);
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        if (MODE != kGroupTN && p.zero_rest) {  // rows without a group: 16-byte units, a warp a row
+            const int32_t head = start[0], rest = head + p.rows - start[p.groups];
+            for (int32_t k = static_cast<int32_t>(blockIdx.x) * 4 + quarter; k < rest; k += static_cast<int32_t>(gridDim.x) * 4) {
+                uint16_t *row = out + static_cast<int64_t>(k < head ? k : start[p.groups] + (k - head)) * p.out_row;
+                for (int32_t u = lane * 8; u < p.I; u += 256) *reinterpret_cast<uint4 *>(row + u) = none;
+            }
+        }
+        PipelineState acc(2, 0u);
+        uint32_t seq = 0, turn = 0;  // tiles, chunks
+        for (int t = cluster; t < total; t += clusters, ++seq) {
+            const GroupTile w = tile_of(t);
+            const int32_t i0 = w.i0 + rank * 128;
+            const int32_t width = p.I - i0 < 128 ? p.I - i0 : 128;  // of this CTA's columns
+            uint16_t *at = out + (MODE == kGroupTN ? w.group * p.out_group : 0) + static_cast<int64_t>(w.j0) * p.out_row + i0;
+            if (w.r == 0) {  // a sum of nothing
+                for (int32_t j = tid / 16; j < w.n; j += 8) {
+                    if (tid % 16 * 8 < width) *reinterpret_cast<uint4 *>(at + j * p.out_row + tid % 16 * 8) = none;
+                }
+                continue;
+            }
+            bool failed = false;
+            if (lane == 0) {
+                failed = !wait_bounded(bar_tfull + 8 * acc.stage, acc.phase, abort_flag, p.timeout_ns,
+                                       kWaitEpilogue, seq);
+            }
+            if (ptxg::any_of_128(1, failed)) break;  // all four warps or none
+            ptx::tcgen05_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc.stage * TN);
+            const int chunks = (w.n + 31) / 32;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c, ++turn) {
+                uint32_t lo[16], hi[16];
+                ptxg::tmem_ld_16x256b_x4(taddr + c * 32, lo);
+                ptxg::tmem_ld_16x256b_x4(taddr + (16u << 16) + c * 32, hi);
+                ptx::tmem_wait_ld();
+                if (c == chunks - 1) {  // the accumulator is read: the next tile but one may have it
+                    ptx::tcgen05_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2) {
+                            ptxg::mbar_arrive_cluster_relaxed(tempty + 8 * acc.stage);
+                        } else {
+                            ptx::mbar_arrive(tempty + 8 * acc.stage);
+                        }
+                    }
+                }
+                const uint32_t buf = base + C::OFF_D + turn % C::BUFS * C::BUF;
+                if (tid == 0) ptx::bulk_wait_group_read<C::BUFS - 1>();  // what was in the buffer has left it
+                ptxg::sync_128(1);
+                // lane l: row l % 8 of matrix l / 8 (columns 8 (n + l / 16) on, lanes 8 (l / 8 % 2) on);
+                // 16-byte unit u of row j lies at u ^ j % 8
+                const uint32_t own = buf + static_cast<uint32_t>(quarter >> 1) * C::BOX +
+                                     static_cast<uint32_t>((lane & 7) + (lane >> 4) * 8) * 128u;
+                const uint32_t unit = static_cast<uint32_t>((quarter & 1) * 4 + (lane >> 3 & 1));
+                const uint32_t low = own + ((unit ^ (lane & 7u)) * 16u), high = own + (((unit + 2) ^ (lane & 7u)) * 16u);
+#pragma unroll
+                for (int n = 0; n < 4; n += 2) {
+                    ptxg::stmatrix_trans(low + n * 8 * 128, pack_pair(p.bf16, lo[4 * n], lo[4 * n + 1]),
+                                         pack_pair(p.bf16, lo[4 * n + 2], lo[4 * n + 3]),
+                                         pack_pair(p.bf16, lo[4 * n + 4], lo[4 * n + 5]),
+                                         pack_pair(p.bf16, lo[4 * n + 6], lo[4 * n + 7]));
+                    ptxg::stmatrix_trans(high + n * 8 * 128, pack_pair(p.bf16, hi[4 * n], hi[4 * n + 1]),
+                                         pack_pair(p.bf16, hi[4 * n + 2], hi[4 * n + 3]),
+                                         pack_pair(p.bf16, hi[4 * n + 4], hi[4 * n + 5]),
+                                         pack_pair(p.bf16, hi[4 * n + 6], hi[4 * n + 7]));
+                }
+                const int32_t rows = w.n - c * 32;  // of the chunk that count
+                if (MODE == kGroupTN || rows >= 32) {
+                    ptx::fence_proxy_async_smem();
+                    ptxg::sync_128(1);
+                    if (tid == 0) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            if (width <= b * 64) continue;
+                            if constexpr (MODE == kGroupTN) {
+                                ptx::tma_store_3d(&tmD, buf + b * C::BOX, i0 + b * 64, w.j0 + c * 32, w.group);
+                            } else {
+                                ptx::tma_store_2d(&tmD, buf + b * C::BOX, i0 + b * 64, w.j0 + c * 32);
+                            }
+                        }
+                    }
+                } else {
+                    // the rows behind a group's end belong to the next
+                    ptxg::sync_128(1);
+                    for (int32_t u = tid; u < rows * 16; u += 128) {
+                        const int32_t j = u / 16, x = u % 16;
+                        if (x * 8 >= width) continue;
+                        const uint4 v = ptx::ld_shared_v4(buf + static_cast<uint32_t>((x >> 3) * C::BOX + j * 128) +
+                                                          ((static_cast<uint32_t>(x & 7) ^ (j & 7u)) * 16u));
+                        *reinterpret_cast<uint4 *>(at + (c * 32 + j) * p.out_row + x * 8) = v;
+                    }
+                }
+                if (tid == 0) ptx::bulk_commit_group();
+            }
+            acc.advance();
+        }
+        if (tid == 0) ptx::bulk_wait_group_read<0>();
+        __syncwarp();
+    }
+    ptx::tcgen05_fence_before();
+    if constexpr (CG == 2) {
+        ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) {
+        ptx::tcgen05_fence_after();
+        ptx::tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);
+    }
+}
+
+}  // namespace linear_ops

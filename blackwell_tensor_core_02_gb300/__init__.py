@@ -400,7 +400,7 @@ def pipeline_trace(depth: int, initial_phase: int, steps: int) -> list[tuple[int
 _LINEAR = ("layer_norm", "layer_norm_backward", "Fp4Tensor", "quantize_fp4", "dequantize_fp4", "gemm_fp4_nt", "Fp4Options",
            "describe_fp4", "fp4_device_status", "load_linear")
 # Products grouped by rows, likewise.
-_GROUPED = ("grouped_gemm_nt", "grouped_gemm_nn", "grouped_gemm_tn", "GroupedOptions", "grouped_device_status")
+_GROUPED = ("grouped_gemm_nt", "grouped_gemm_nn", "grouped_gemm_tn", "gemm_lora_nt", "GroupedOptions", "grouped_device_status")
 __all__ += [*_LINEAR, *_GROUPED]
 
 

@@ -513,6 +513,48 @@ PyObject *grouped_matrices(PyObject *const *args, Py_ssize_t n) {  // dD, A, off
     return THPVariable_Wrap(dB);
 }
 
+PyObject *lora(PyObject *const *args, Py_ssize_t n) {  // x, W, down, up, offsets, adapters, D, scales, options or 0
+    count(n, 9);
+    const at::Tensor &x = tensor(args[0], "x"), &W = tensor(args[1], "W"), &down = tensor(args[2], "down"),
+                     &up = tensor(args[3], "up"), &offsets = tensor(args[4], "offsets"), &adapters = tensor(args[5], "adapters");
+    const int code = half_type(x, "x");
+    operand(x, "x", 2, x);
+    operand(W, "W", 2, x);
+    operand(down, "down", 3, x);
+    operand(up, "up", 3, x);
+    const int64_t rows = x.size(0), K = x.size(1), N = W.size(0), many = down.size(0), rank = down.size(1);
+    if (W.size(1) != K || down.size(2) != K || up.size(0) != many || up.size(1) != N || up.size(2) != rank) {
+        refuse(PyExc_ValueError,
+               "expected x (rows x K), W (N x K), down (adapters x rank x K) and up (adapters x N x rank)");
+    }
+    if (adapters.scalar_type() != at::kInt) refuse(PyExc_TypeError, "adapters must be int32");
+    const int64_t requests = adapters.numel();
+    whole_numbers(adapters, "adapters", requests, x);
+    const int wide = whole_numbers(offsets, "offsets", requests + 1, x);
+    const float *scales = nullptr;
+    if (given(args[7])) {
+        const at::Tensor &t = tensor(args[7], "scales");
+        if (t.scalar_type() != at::kFloat) refuse(PyExc_TypeError, "scales must be float32");
+        if (t.device() != x.device() || t.dim() != 1 || t.size(0) != many || !t.is_contiguous()) {
+            refuse(PyExc_ValueError, "scales must be a contiguous vector of one for each adapter, on x's device");
+        }
+        scales = t.data_ptr<float>();
+    }
+    const grouped_options *opts = grouped_opts(args[8]);
+    const c10::cuda::CUDAGuard guard(x.device());
+    bool made = false;
+    at::Tensor D = grouped_rows(args[6], "D", rows, N, x, &made);
+    const int64_t need = gemm_lora_workspace_size(rows, rank);
+    check_status(need, "gemm_lora_nt");
+    at::Tensor space = empty({need}, at::kByte, x);
+    check_status(gemm_lora_nt(x.data_ptr(), x.stride(0), W.data_ptr(), W.stride(0), down.data_ptr(), down.stride(1),
+                              down.stride(0), up.data_ptr(), up.stride(1), up.stride(0), scales, offsets.data_ptr(), wide,
+                              adapters.data_ptr<int32_t>(), D.data_ptr(), D.stride(0), rows, requests, many, N, K, rank, code,
+                              need ? space.data_ptr() : nullptr, need, stream_of(x), opts),
+                 "gemm_lora_nt");
+    return THPVariable_Wrap(D);
+}
+
 template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -540,6 +582,7 @@ PyMethodDef g_methods[] = {LINEAR_METHOD("layer_norm", norm),
                            LINEAR_METHOD("grouped_gemm_nt", grouped_rows_product<true>),
                            LINEAR_METHOD("grouped_gemm_nn", grouped_rows_product<false>),
                            LINEAR_METHOD("grouped_gemm_tn", grouped_matrices),
+                           LINEAR_METHOD("gemm_lora_nt", lora),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_linear_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

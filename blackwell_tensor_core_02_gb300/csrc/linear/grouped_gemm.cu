@@ -1,11 +1,13 @@
-// grouped_gemm.cu -- host side of the products grouped by rows: checks, tensor maps,
-// the choice of a tile, launches (see grouped_ops.h).
+// grouped_gemm.cu -- host side of the products grouped by rows and of low-rank adapters
+// beside a shared product: checks, tensor maps, the choice of a tile, launches (see
+// grouped_ops.h).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <atomic>
 #include <mutex>
 
+#include "grouped_few_kernel.cuh"
 #include "grouped_kernel.cuh"
 
 namespace linear_ops {
@@ -51,11 +53,35 @@ bool encode(CUtensorMap *map, const Matrix &m, uint32_t box_rows) {
 
 struct Call {
     Matrix P, Q, D;
+    Matrix U, H;           // LORA: up, and h as 16-bit numbers
     GroupParams p;
     int max_clusters;
     int sms;
     cudaStream_t stream;
 };
+
+template <typename... P>
+int launch_cluster(void (*kernel)(P...), int64_t ctas, unsigned threads, unsigned cluster, size_t smem, cudaStream_t stream,
+                   const P &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
 
 template <int CG, int TN, int MODE>
 int launch_tile(const Call &c) {
@@ -67,15 +93,20 @@ int launch_tile(const Call &c) {
     const int64_t i_tiles = (static_cast<int64_t>(p.I) + 128 * CG - 1) / (128 * CG);
     const int64_t j_tiles = MODE == kGroupTN ? (static_cast<int64_t>(p.J) + TN - 1) / TN : 0;
     // every group's tiles, at most: each group may end in a part of a tile
-    const int64_t some = p.groups < p.rows ? p.groups : p.rows;
+    const int64_t groups = MODE == kGroupLora ? int64_t(p.groups) + 2 : p.groups;
+    const int64_t some = groups < p.rows ? groups : p.rows;
     const int64_t most = MODE == kGroupTN ? p.groups * i_tiles * j_tiles : (static_cast<int64_t>(p.rows) / TN + some) * i_tiles;
     if (most > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
     p.i_tiles = static_cast<int32_t>(i_tiles);
     p.j_tiles = static_cast<int32_t>(j_tiles);
-    CUtensorMap tmP = {}, tmQ = {}, tmD = {};  // P's and Q's are not used by sums of nothing
-    if (!encode(&tmD, c.D, 32)) return GEMM_ERR_CUDA;
-    if (p.groups > 0 && c.P.rows > 0 && c.P.cols > 0 && c.Q.rows > 0 && c.Q.cols > 0) {
-        if (!encode(&tmP, c.P, MODE == kGroupNT ? 128 : 64) || !encode(&tmQ, c.Q, MODE == kGroupTN ? 64 : TN / CG)) {
+    CUtensorMap tmP = {}, tmQ = {}, tmD = {}, tmU = {}, tmH = {};  // P's and Q's are not used by sums of nothing
+    if (MODE != kGroupDown && !encode(&tmD, c.D, 32)) return GEMM_ERR_CUDA;
+    if (MODE == kGroupLora && p.groups > 0) {
+        if (!encode(&tmU, c.U, 128) || !encode(&tmH, c.H, TN / CG)) return GEMM_ERR_CUDA;
+    }
+    if (groups > 0 && c.P.rows > 0 && c.P.cols > 0 && c.Q.rows > 0 && c.Q.cols > 0) {
+        const uint32_t p_rows = MODE == kGroupDown ? static_cast<uint32_t>(p.rank) : (MODE == kGroupNN || MODE == kGroupTN ? 64 : 128);
+        if (!encode(&tmP, c.P, p_rows) || !encode(&tmQ, c.Q, MODE == kGroupTN ? 64 : TN / CG)) {
             return GEMM_ERR_CUDA;
         }
     }
@@ -104,44 +135,93 @@ int launch_tile(const Call &c) {
         }
         grid = clusters;
     }
-    if (!(MODE != kGroupTN && p.zero_rest) && most < grid) grid = most;
+    if (!p.zero_rest && most < grid) grid = most;
     if (c.max_clusters > 0 && c.max_clusters < grid) grid = c.max_clusters;
     if (grid == 0) return GEMM_OK;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(CG * grid));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM_ALLOC;
-    cfg.stream = c.stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, tmP, tmQ, tmD, static_cast<const GroupParams &>(p)) != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_LAUNCH;
-    }
-    return GEMM_OK;
+    return launch_cluster(kernel, CG * grid, C::THREADS, CG, C::SMEM_ALLOC, c.stream, tmP, tmQ, tmD, tmU, tmH, p);
 }
 
-// The tile's columns: of the ragged axis by the rows that a group has on average, of
-// TN's by the columns.
-int choose_tile(int mode, const GroupParams &p) {
-    if (mode == kGroupTN) return p.J <= 64 ? 64 : (p.J <= 128 || p.I <= 128 ? 128 : 256);
+template <int TN, int KS, int MODE>
+int launch_few(const Call &c, const LoraParams &l) {
+    using C = FewShape<TN>;
+    auto *kernel = grouped_few_kernel<TN, KS, MODE>;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(kernel, C::SMEM_ALLOC, done)) return GEMM_ERR_CUDA;
+    GroupParams p = c.p;
+    const int64_t i_tiles = (static_cast<int64_t>(p.I) + 127) / 128;
     const int64_t some = p.groups < p.rows ? p.groups : p.rows;
-    const int64_t each = some > 0 ? (p.rows + some - 1) / some : 0;
-    return each <= 16 ? 32 : (each <= 32 ? 64 : (each <= 112 || p.I <= 128 ? 128 : 256));
+    const int64_t most = MODE == kGroupLora ? (static_cast<int64_t>(p.rows) + TN - 1) / TN * i_tiles
+                                            : (static_cast<int64_t>(p.rows) / TN + some) * i_tiles;
+    if (most * KS > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    p.i_tiles = static_cast<int32_t>(i_tiles);
+    CUtensorMap tmP = {}, tmQ = {};  // not used by sums of nothing
+    if (c.P.rows > 0 && c.P.cols > 0 && c.Q.rows > 0 && c.Q.cols > 0) {
+        if (!encode(&tmP, c.P, MODE == kGroupNN ? 64 : 128) || !encode(&tmQ, c.Q, TN)) return GEMM_ERR_CUDA;
+    }
+    const int64_t tiles = most > 0 ? most : 1;  // one for the rows without a group
+    return launch_cluster(kernel, KS * tiles, C::THREADS, KS, C::SMEM_ALLOC, c.stream, tmP, tmQ, p, l);
+}
+
+template <int TN, int MODE>
+int launch_split(const Call &c, const LoraParams &l, int split) {
+    switch (split) {
+        case 8: return launch_few<TN, 8, MODE>(c, l);
+        case 4: return launch_few<TN, 4, MODE>(c, l);
+        case 2: return launch_few<TN, 2, MODE>(c, l);
+        default: return launch_few<TN, 1, MODE>(c, l);
+    }
 }
 
 template <int MODE>
-int launch_mode(const Call &c, int tile) {
+int launch_few_mode(const Call &c, const LoraParams &l, int tile, int split) {
     switch (tile) {
-        case 32:
-            if constexpr (MODE != kGroupTN) return launch_tile<1, 32, MODE>(c);
-            return GEMM_ERR_INVALID_ARG;
+        case 16: return launch_split<16, MODE>(c, l, split);
+        case 32: return launch_split<32, MODE>(c, l, split);
+        case 64: return launch_split<64, MODE>(c, l, split);
+        default: return launch_split<128, MODE>(c, l, split);
+    }
+}
+
+// How a call runs: its tile, and the CTAs that share a tile's sum, or 0 for a persistent grid.
+struct Choice {
+    int tile, split;
+};
+
+// CTAs that share a tile's sum: the most of 8, 4 and 2 that keep two CTAs an SM and leave
+// each four K tiles.
+int split_of(int64_t tiles, int64_t k_tiles, int sms) {
+    for (int ks = 8; ks > 1; ks /= 2) {
+        if (tiles * ks <= 2 * sms && k_tiles >= 4 * ks) return ks;
+    }
+    return 1;
+}
+
+// The tile's columns: of the ragged axis by the rows that a group has on average, of
+// TN's by the columns.  Tiles for less than half of the SMs share their sums.
+Choice choose(int mode, const GroupParams &p, int sms, const grouped_options &o) {
+    if (mode == kGroupTN) return {o.tile ? o.tile : (p.J <= 64 ? 64 : (p.J <= 128 || p.I <= 128 ? 128 : 256)), 0};
+    const int64_t some = p.groups < p.rows ? p.groups : p.rows;
+    const int64_t each = some > 0 ? (p.rows + some - 1) / some : 0;
+    const int64_t k_tiles = (static_cast<int64_t>(p.R) + 63) / 64, i_tiles = (static_cast<int64_t>(p.I) + 127) / 128;
+    Choice c = {o.tile, o.split > 0 ? o.split : 0};
+    if (c.tile == 0) {
+        c.tile = each <= 16 ? (c.split > 0 ? 16 : 32) : (each <= 32 ? 64 : (each <= 112 || p.I <= 128 || c.split > 0 ? 128 : 256));
+    }
+    if (o.split == 0 && c.tile <= 128) {
+        const int64_t tiles = (static_cast<int64_t>(p.rows) / c.tile + some) * i_tiles;
+        if (c.tile == 16 || tiles * 2 <= sms) c.split = split_of(tiles, k_tiles, sms);
+    }
+    while (c.split > 1 && c.split > k_tiles) c.split /= 2;
+    return c;
+}
+
+template <int MODE>
+int launch_mode(const Call &c, const Choice &how) {
+    if constexpr (MODE != kGroupTN) {
+        if (how.split > 0) return launch_few_mode<MODE>(c, {}, how.tile, how.split);
+        if (how.tile == 32) return launch_tile<1, 32, MODE>(c);
+    }
+    switch (how.tile) {
         case 64: return launch_tile<1, 64, MODE>(c);
         case 128: return launch_tile<1, 128, MODE>(c);
         default: return launch_tile<2, 256, MODE>(c);
@@ -150,8 +230,9 @@ int launch_mode(const Call &c, int tile) {
 
 int check_options(const grouped_options *opts, grouped_options *o) {
     *o = opts ? *opts : grouped_options{};
-    if ((o->tile != 0 && o->tile != 32 && o->tile != 64 && o->tile != 128 && o->tile != 256) || o->max_clusters < 0 ||
-        (o->debug_flags & ~1) != 0 || o->timeout_ns < 0) {
+    if ((o->tile != 0 && o->tile != 16 && o->tile != 32 && o->tile != 64 && o->tile != 128 && o->tile != 256) ||
+        (o->split != 0 && o->split != -1 && o->split != 1 && o->split != 2 && o->split != 4 && o->split != 8) ||
+        o->max_clusters < 0 || (o->debug_flags & ~1) != 0 || o->timeout_ns < 0) {
         return GEMM_ERR_INVALID_ARG;
     }
     if (o->timeout_ns == 0) o->timeout_ns = kDefaultTimeoutNs;
@@ -183,7 +264,8 @@ int grouped(int mode, Matrix ragged, Matrix other, Matrix out, const void *offse
     int st = check_options(opts, &o);
     if (st != GEMM_OK) return st;
     if (rows < 0 || groups < 0 || N < 0 || K < 0 || (type != LINEAR_F16 && type != LINEAR_BF16) ||
-        (offsets_type != 0 && offsets_type != 1) || (mode == kGroupTN && o.tile == 32)) {
+        (offsets_type != 0 && offsets_type != 1) || (o.tile == 256 && o.split > 0) || (o.tile == 16 && o.split < 0) ||
+        (mode == kGroupTN && (o.split > 0 || (o.tile != 0 && o.tile < 64)))) {
         return GEMM_ERR_INVALID_ARG;
     }
     if (N % 8 != 0 || K % 8 != 0 || rows > kMaxDim || N > kMaxDim || K > kMaxDim || groups > GROUPED_MAX_GROUPS) {
@@ -227,12 +309,69 @@ int grouped(int mode, Matrix ragged, Matrix other, Matrix out, const void *offse
     p.zero_rest = zero_rest != 0;
     p.debug_flags = static_cast<uint32_t>(o.debug_flags);
     p.timeout_ns = static_cast<uint64_t>(o.timeout_ns);
-    const int tile = o.tile ? o.tile : choose_tile(mode, p);
+    const Choice how = choose(mode, p, c.sms, o);
     switch (mode) {
-        case kGroupNT: return launch_mode<kGroupNT>(c, tile);
-        case kGroupNN: return launch_mode<kGroupNN>(c, tile);
-        default: return launch_mode<kGroupTN>(c, tile);
+        case kGroupNT: return launch_mode<kGroupNT>(c, how);
+        case kGroupNN: return launch_mode<kGroupNN>(c, how);
+        default: return launch_mode<kGroupTN>(c, how);
     }
+}
+
+// ------------------------------------------------------------- adapters --
+
+constexpr int64_t kMaxRank = 128;
+
+struct Lora {
+    Matrix x, W, down, up, D;
+    const float *scales;
+    const void *offsets;
+    const int32_t *adapters;
+    int64_t rows, requests, adapter_count, N, K, rank;
+    void *workspace;
+};
+
+// Requests of many rows: tiles of one request each, the adapter as more of the sum.
+int lora_long(Call &c, const Lora &l) {
+    GroupParams &p = c.p;
+    p.rank_pad = static_cast<int32_t>((l.rank + 63) / 64 * 64);
+    if (p.groups > 0) {
+        Call d = c;
+        d.P = l.down;
+        d.Q = l.x;
+        d.p.I = p.rank;
+        d.p.out = l.workspace;
+        d.p.out_row = 2 * p.rank_pad;
+        d.max_clusters = 0;
+        const int st = launch_tile<1, 32, kGroupDown>(d);
+        if (st != GEMM_OK) return st;
+        p.follows = 1;
+    }
+    c.P = l.W;
+    c.Q = l.x;
+    c.D = l.D;
+    c.U = l.up;
+    c.H = {l.workspace, l.rows, 2 * p.rank_pad, 2 * p.rank_pad, 0, 0};
+    return launch_tile<2, 256, kGroupLora>(c);
+}
+
+// Requests of few rows: tiles of any rows, each row's adapter added behind the sum.
+int lora_short(Call &c, const Lora &l, const Choice &how) {
+    GroupParams &p = c.p;
+    if (p.groups > 0) {
+        const DownParams d = {static_cast<const uint16_t *>(l.x.ptr), static_cast<const uint16_t *>(l.down.ptr), l.x.stride,
+                              l.down.stride, l.down.depth_stride, static_cast<float *>(l.workspace)};
+        const unsigned ranks = static_cast<unsigned>((l.rank + 7) / 8);
+        const int st = l.rows <= 256
+                           ? launch(lora_down_kernel<1>, dim3(static_cast<unsigned>(l.rows), ranks), dim3(256), 0, c.stream, p, d)
+                           : launch(lora_down_kernel<8>, dim3(static_cast<unsigned>((l.rows + 7) / 8), ranks), dim3(256), 0, c.stream, p, d);
+        if (st != GEMM_OK) return st;
+        p.follows = 1;
+    }
+    c.P = l.W;
+    c.Q = l.x;
+    const LoraParams lp = {static_cast<const float *>(l.workspace), static_cast<const uint16_t *>(l.up.ptr), l.up.stride,
+                           l.up.depth_stride};
+    return launch_few_mode<kGroupLora>(c, lp, how.tile, how.split);
 }
 
 }  // namespace
@@ -261,6 +400,103 @@ int grouped_gemm_tn(const void *dD, int64_t ldd, const void *A, int64_t lda, con
                     int32_t type, void *stream, const grouped_options *opts) {
     return grouped(kGroupTN, {dD, rows, N, ldd, 0, 0}, {A, rows, K, lda, 0, 0}, {dB, N, K, ldb, groups, b_stride},
                    offsets, offsets_type, rows, groups, N, K, type, 0, stream, opts);
+}
+
+int64_t gemm_lora_workspace_size(int64_t rows, int64_t rank) {
+    if (rows < 0 || rank < 0) return GEMM_ERR_INVALID_ARG;
+    if (rows > kMaxDim || rank > kMaxRank || rank % 8 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
+    return rows * ((rank + 63) / 64 * 64) * 4;  // fp32, or two 16-bit numbers
+}
+
+int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const void *down, int64_t ld_down,
+                 int64_t down_stride, const void *up, int64_t ld_up, int64_t up_stride, const float *scales,
+                 const void *offsets, int32_t offsets_type, const int32_t *adapters, void *D, int64_t ldd, int64_t rows,
+                 int64_t requests, int64_t adapter_count, int64_t N, int64_t K, int64_t rank, int32_t type,
+                 void *workspace, int64_t workspace_bytes, void *stream, const grouped_options *opts) {
+    grouped_options o;
+    int st = check_options(opts, &o);
+    if (st != GEMM_OK) return st;
+    if (rows < 0 || requests < 0 || adapter_count < 0 || N < 0 || K < 0 || rank < 0 || workspace_bytes < 0 ||
+        (type != LINEAR_F16 && type != LINEAR_BF16) || (offsets_type != 0 && offsets_type != 1) ||
+        (o.tile == 256 && o.split > 0) || (o.tile != 0 && o.tile < 256 && o.split < 0)) {
+        return GEMM_ERR_INVALID_ARG;
+    }
+    if (N % 8 != 0 || K % 8 != 0 || rank % 8 != 0 || rank > kMaxRank || rows > kMaxDim || N > kMaxDim || K > kMaxDim ||
+        adapter_count > kMaxDim || requests > GROUPED_MAX_GROUPS) {
+        return GEMM_ERR_UNSUPPORTED_SHAPE;
+    }
+    if (rows == 0 || N == 0) return GEMM_OK;
+    const bool some = requests > 0 && adapter_count > 0 && rank > 0 && K > 0;  // adapters at all
+    Lora l = {{x, rows, K, ldx, 0, 0}, {W, N, K, ldw, 1, 0}, {down, rank, K, ld_down, adapter_count, down_stride},
+              {up, N, rank, ld_up, adapter_count, up_stride}, {D, rows, N, ldd, 0, 0}, scales, offsets, adapters,
+              rows, requests, adapter_count, N, K, rank, workspace};
+    if (!D || (requests > 0 && (!offsets || !adapters))) return GEMM_ERR_INVALID_ARG;
+    for (const Matrix *m : {&l.x, &l.W, &l.D}) {
+        st = check_matrix(*m);
+        if (st != GEMM_OK) return st;
+    }
+    if (some) {
+        for (const Matrix *m : {&l.down, &l.up}) {
+            st = check_matrix(*m);
+            if (st != GEMM_OK) return st;
+        }
+        if (!workspace) return GEMM_ERR_INVALID_ARG;
+        if (workspace_bytes < gemm_lora_workspace_size(rows, rank)) return GEMM_ERR_SCRATCH_LIMIT;
+    }
+    if (!aligned(offsets, offsets_type ? 8 : 4) || !aligned(adapters, 4) || !aligned(scales, 4) || !aligned(workspace, 16)) {
+        return GEMM_ERR_MISALIGNED;
+    }
+    const struct {
+        const void *p;
+        int64_t bytes;
+    } outs[2] = {{D, matrix_bytes(l.D)}, {workspace, some ? gemm_lora_workspace_size(rows, rank) : 0}},
+      ins[7] = {{x, matrix_bytes(l.x)}, {W, matrix_bytes(l.W)}, {down, some ? matrix_bytes(l.down) : 0},
+                {up, some ? matrix_bytes(l.up) : 0}, {offsets, (requests + 1) * (offsets_type ? 8 : 4)},
+                {adapters, requests * 4}, {scales, adapter_count * 4}};
+    for (const auto &out : outs) {
+        for (const auto &in : ins) {
+            if (overlap(out.p, out.bytes, in.p, in.bytes)) return GEMM_ERR_INVALID_ARG;
+        }
+    }
+    if (overlap(outs[0].p, outs[0].bytes, outs[1].p, outs[1].bytes)) return GEMM_ERR_INVALID_ARG;
+    Call c = {};
+    st = gb300_sms(&c.sms);
+    if (st != GEMM_OK) return st;
+    if (!encoder()) return GEMM_ERR_CUDA;
+    c.stream = static_cast<cudaStream_t>(stream);
+    if (K == 0) {
+        const cudaError_t e = cudaMemset2DAsync(D, static_cast<size_t>(rows > 1 ? ldd : N) * 2, 0, static_cast<size_t>(N) * 2,
+                                                static_cast<size_t>(rows), c.stream);
+        return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    }
+    c.max_clusters = o.max_clusters;
+    GroupParams &p = c.p;
+    p.offsets = some ? offsets : nullptr;
+    p.offsets_64 = offsets_type;
+    p.out = D;
+    p.out_row = rows > 1 ? ldd : 0;
+    p.groups = some ? static_cast<int32_t>(requests) : 0;
+    p.rows = static_cast<int32_t>(rows);
+    p.I = static_cast<int32_t>(N);
+    p.R = static_cast<int32_t>(K);
+    p.bf16 = type == LINEAR_BF16;
+    p.adapters = adapters;
+    p.scales = scales;
+    p.adapter_count = static_cast<int32_t>(adapter_count);
+    p.rank = static_cast<int32_t>(rank);
+    p.debug_flags = static_cast<uint32_t>(o.debug_flags);
+    p.timeout_ns = static_cast<uint64_t>(o.timeout_ns);
+    if (rows == 1) l.x.stride = 0;
+    Choice how = {o.tile, o.split};
+    if (how.tile == 0) {
+        const int64_t each = p.groups > 0 ? rows / p.groups : rows;
+        how.tile = o.split < 0 || (o.split == 0 && each >= 128) ? 256 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)));
+    }
+    if (how.tile == 256) return lora_long(c, l);
+    const int64_t k_tiles = (K + 63) / 64;
+    if (how.split <= 0) how.split = split_of((rows + how.tile - 1) / how.tile * ((N + 127) / 128), k_tiles, c.sms);
+    while (how.split > 1 && how.split > k_tiles) how.split /= 2;
+    return lora_short(c, l, how);
 }
 
 int grouped_last_device_status(void *stream, uint64_t *info) {

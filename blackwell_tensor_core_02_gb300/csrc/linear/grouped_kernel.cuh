@@ -11,6 +11,9 @@
 //     NN   K               rows (ragged)   columns      B_e, MN-major dD
 //     TN   K               columns of dD   rows (ragged) A, MN-major  dD, MN-major
 //
+//     LORA columns of W    rows (ragged)   K, ranks      W, up_a       x, x * down_a^T
+//     DOWN ranks           rows (ragged)   K             down_a        x
+//
 // So the ragged axis of NT and NN is N of the MMA, which takes any multiple of 16:
 // a group's last tile costs what its rows cost, and few rows (decoding) leave the
 // matrices' bytes to stream through the 128-row side.  Results of other groups' rows
@@ -22,6 +25,14 @@
 // infinity would be NaN), so a warp of its own overwrites them with zeros in shared
 // memory, between the load's arrival and the MMA.  At most 15 rows: the MMAs go in
 // steps of 16.
+//
+// LORA and DOWN are the two launches of low-rank adapters beside a shared product, with
+// the rows of a request as a group.  DOWN leaves h = scale_a * x * down_a^T as two
+// 16-bit numbers, h rounded and what that rounding left, which hold 16 (bf16) or 22 bits
+// of it; LORA's sum goes on over the ranks, once for each, so the result is rounded once.
+// Rows without a request are a group without an adapter, before the first and behind the
+// last.  A request's tile holds its own rows only: what another request's adapter holds
+// cannot reach them.
 //
 // Persistent CTAs (or pairs, cta_group::2, 256 x 256 tiles) walk one list of tiles
 // over all groups; each CTA reads the offsets once and keeps the groups' first rows
@@ -121,7 +132,7 @@ __device__ __forceinline__ void sync_128(uint32_t barrier) {
 
 }  // namespace ptxg
 
-enum GroupMode { kGroupNT = 0, kGroupNN = 1, kGroupTN = 2 };
+enum GroupMode { kGroupNT = 0, kGroupNN = 1, kGroupTN = 2, kGroupLora = 3, kGroupDown = 4 };
 
 // CG: CTAs of a tile; TN: its columns j.  A CTA holds 128 rows of P and TN / CG of Q.
 template <int CG, int TN, int MODE>
@@ -138,13 +149,15 @@ struct GroupShape {
     // the 128-byte swizzle.
     static constexpr int BOX = 32 * 128;
     static constexpr int BUF = 2 * BOX;
-    static constexpr int BUFS = 3;
+    static constexpr bool ADAPTERS = MODE == kGroupLora || MODE == kGroupDown;
+    static constexpr int BUFS = ADAPTERS ? 2 : 3;
     static constexpr int OFF_P = 0;
     static constexpr int OFF_Q = OFF_P + STAGES * P_BYTES;
     static constexpr int OFF_D = OFF_Q + STAGES * Q_BYTES;
     static constexpr int OFF_START = OFF_D + BUFS * BUF;                     // int32 [groups + 1]
     static constexpr int OFF_TILES = OFF_START + 4 * (GROUPED_MAX_GROUPS + 4);  // int32 [groups + 1]
-    static constexpr int OFF_BAR = OFF_TILES + 4 * (GROUPED_MAX_GROUPS + 4);
+    static constexpr int OFF_CHOSEN = OFF_TILES + 4 * (GROUPED_MAX_GROUPS + 4);  // the groups' adapters, -1 without
+    static constexpr int OFF_BAR = OFF_CHOSEN + (ADAPTERS ? 4 * (GROUPED_MAX_GROUPS + 4) : 0);
     // full, empty, land, peer [STAGES]; accumulator full, empty [2]; drain
     static constexpr int OFF_MISC = OFF_BAR + (4 * STAGES + 5) * 8;
     static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 896;                 // from a multiple of 128 bytes to one of 1024
@@ -164,6 +177,12 @@ struct GroupParams {
     int32_t i_tiles, j_tiles;    // of a group; j_tiles for TN
     int32_t bf16;
     int32_t zero_rest;
+    // adapters
+    const int32_t *adapters;     // of each request
+    const float *scales;         // of each adapter (NULL: 1)
+    int32_t adapter_count, rank;
+    int32_t rank_pad;            // rank in whole 64s: h has 2 * rank_pad elements a row
+    int32_t follows;             // LORA: behind a launch that leaves h
     uint32_t debug_flags;
     uint64_t timeout_ns;
 };
@@ -179,8 +198,9 @@ struct GroupTile {
 constexpr int kGroupBand = 8;
 
 template <int CG, int TN, int MODE>
-__device__ __forceinline__ GroupTile group_tile(const GroupParams &p, const int32_t *start, const int32_t *tiles, int t) {
-    int lo = 0, hi = p.groups;  // tiles[lo] <= t < tiles[hi]
+__device__ __forceinline__ GroupTile group_tile(const GroupParams &p, int groups, const int32_t *start,
+                                                const int32_t *tiles, int t) {
+    int lo = 0, hi = groups;  // tiles[lo] <= t < tiles[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (tiles[mid] <= t) {
@@ -207,20 +227,43 @@ __device__ __forceinline__ GroupTile group_tile(const GroupParams &p, const int3
     return w;
 }
 
+// The adapter of request e, -1 if it has none.
+__device__ __forceinline__ int32_t adapter_of(const GroupParams &p, int e) {
+    const int32_t a = p.adapters[e];
+    return a >= 0 && a < p.adapter_count ? a : -1;
+}
+
+__device__ __forceinline__ int64_t offset_of(const GroupParams &p, int e) {
+    if (!p.offsets) return 0;  // no requests
+    return p.offsets_64 ? static_cast<const int64_t *>(p.offsets)[e]
+                        : static_cast<int64_t>(static_cast<const int32_t *>(p.offsets)[e]);
+}
+
 // The groups' first rows (all threads), then from them, by one warp, their first tiles.
-__device__ __forceinline__ void group_starts(const GroupParams &p, int32_t *start, int thread, int threads) {
+// With `rest` the rows without a group are groups too, the first and the last; `chosen`
+// gets the groups' adapters.  Returns the number of groups.
+__device__ __forceinline__ int group_starts(const GroupParams &p, int32_t *start, bool rest, int32_t *chosen, int thread,
+                                            int threads) {
+    const int shift = rest ? 1 : 0, groups = p.groups + 2 * shift;
     for (int e = thread; e <= p.groups; e += threads) {
-        const int64_t o = p.offsets_64 ? static_cast<const int64_t *>(p.offsets)[e]
-                                       : static_cast<int64_t>(static_cast<const int32_t *>(p.offsets)[e]);
-        start[e] = static_cast<int32_t>(o < 0 ? 0 : (o > p.rows ? p.rows : o));
+        const int64_t o = offset_of(p, e);
+        start[e + shift] = static_cast<int32_t>(o < 0 ? 0 : (o > p.rows ? p.rows : o));
+        if (chosen && e < p.groups) chosen[e + shift] = adapter_of(p, e);
     }
+    if (rest && thread == 0) {
+        start[0] = 0;
+        start[groups] = p.rows;
+        if (chosen) chosen[0] = chosen[groups - 1] = -1;
+    }
+    return groups;
 }
 template <int TN, int MODE>
-__device__ __forceinline__ void group_tiles(const GroupParams &p, int32_t *start, int32_t *tiles, int lane) {
+__device__ __forceinline__ void group_tiles(const GroupParams &p, int groups, int32_t *start, int32_t *tiles,
+                                            const int32_t *chosen, int lane) {
     int32_t most = 0, sum = 0;
-    for (int base = 0; base <= p.groups; base += 32) {
+    for (int base = 0; base <= groups; base += 32) {
         const int e = base + lane;
-        int32_t v = e <= p.groups ? start[e] : 0;
+        int32_t v = e <= groups ? start[e] : 0;
         v = v > most ? v : most;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {  // none lies before its predecessor
@@ -230,13 +273,14 @@ __device__ __forceinline__ void group_tiles(const GroupParams &p, int32_t *start
         int32_t before = __shfl_up_sync(0xffffffffu, v, 1);
         if (lane == 0) before = most;
         // the tiles of group e - 1
-        int32_t n = e == 0 || e > p.groups ? 0 : (MODE == kGroupTN ? p.j_tiles : (v - before + TN - 1) / TN) * p.i_tiles;
+        int32_t n = e == 0 || e > groups ? 0 : (MODE == kGroupTN ? p.j_tiles : (v - before + TN - 1) / TN) * p.i_tiles;
+        if (MODE == kGroupDown && n > 0 && chosen[e - 1] < 0) n = 0;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
             const int32_t u = __shfl_up_sync(0xffffffffu, n, o);
             if (lane >= o) n += u;
         }
-        if (e <= p.groups) {
+        if (e <= groups) {
             start[e] = v;
             tiles[e] = sum + n;
         }
@@ -251,7 +295,7 @@ __device__ __forceinline__ void group_tiles(const GroupParams &p, int32_t *start
 template <int CG, int MODE>
 __device__ __forceinline__ uint32_t group_idesc(int n, bool bf16) {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 * CG >> 4) << 24) | (bf16 ? (1u << 7) | (1u << 10) : 0u) |
-           (MODE != kGroupNT ? 1u << 15 : 0u) | (MODE == kGroupTN ? 1u << 16 : 0u);
+           (MODE == kGroupNN || MODE == kGroupTN ? 1u << 15 : 0u) | (MODE == kGroupTN ? 1u << 16 : 0u);
 }
 
 __device__ __forceinline__ uint32_t pack_pair(bool bf16, uint32_t lo, uint32_t hi) {
@@ -265,10 +309,28 @@ __device__ __forceinline__ uint32_t pack_pair(bool bf16, uint32_t lo, uint32_t h
     return w;
 }
 
+// h as a 16-bit number and the rest of it as another (0 where h, or its rounding, is not
+// finite: an infinity less itself would be NaN).
+__device__ __forceinline__ void split_16(bool bf16, float h, uint16_t *high, uint16_t *low) {
+    uint32_t a, b;
+    if (bf16) {
+        Pair<__nv_bfloat16>::narrow(make_float2(h, 0.f), &a);
+        const float rest = h - Pair<__nv_bfloat16>::widen(&a).x;
+        Pair<__nv_bfloat16>::narrow(make_float2(fabsf(rest) < INFINITY ? rest : 0.f, 0.f), &b);
+    } else {
+        Pair<__half>::narrow(make_float2(h, 0.f), &a);
+        const float rest = h - Pair<__half>::widen(&a).x;
+        Pair<__half>::narrow(make_float2(fabsf(rest) < INFINITY ? rest : 0.f, 0.f), &b);
+    }
+    *high = static_cast<uint16_t>(a);
+    *low = static_cast<uint16_t>(b);
+}
+
 template <int CG, int TN, int MODE>
 __global__ void __launch_bounds__(256, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                   const __grid_constant__ CUtensorMap tmD, const GroupParams p) {
+                   const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmU,
+                   const __grid_constant__ CUtensorMap tmH, const GroupParams p) {
     using C = GroupShape<CG, TN, MODE>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -308,11 +370,15 @@ __global__ void __launch_bounds__(256, 1)
         ptx::tmem_alloc<CG>(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
         ptx::tmem_relinquish<CG>();
     }
-    if (threadIdx.x == 0) ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    group_starts(p, start, static_cast<int>(threadIdx.x), C::THREADS);
+    // LORA follows DOWN, which lets it start only once the kernels before both have
+    // completed: it waits for h alone, in the producer.
+    if (MODE != kGroupDown && threadIdx.x == 0) ptx::griddep_launch_dependents();
+    if (MODE != kGroupLora || !p.follows) ptx::griddep_wait();
+    if (MODE == kGroupDown && threadIdx.x == 0) ptx::griddep_launch_dependents();
+    int32_t *chosen = C::ADAPTERS ? reinterpret_cast<int32_t *>(smem + C::OFF_CHOSEN) : nullptr;
+    const int groups = group_starts(p, start, MODE == kGroupLora, chosen, static_cast<int>(threadIdx.x), C::THREADS);
     __syncthreads();
-    if (warp == 2) group_tiles<TN, MODE>(p, start, tiles, lane);
+    if (warp == 2) group_tiles<TN, MODE>(p, groups, start, tiles, chosen, lane);
     ptx::tcgen05_fence_before();
     if constexpr (CG == 2) {
         ptx::cluster_sync();
@@ -321,21 +387,25 @@ __global__ void __launch_bounds__(256, 1)
     }
     ptx::tcgen05_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
-    const int total = tiles[p.groups];
-    auto tile_of = [&](int t) { return group_tile<CG, TN, MODE>(p, start, tiles, t); };
+    const int total = tiles[groups];
+    auto tile_of = [&](int t) { return group_tile<CG, TN, MODE>(p, groups, start, tiles, t); };
+    // K tiles over the ranks, two of each 64: with h rounded and with the rest of it
+    auto rank_tiles = [&](const GroupTile &w) {
+        return MODE == kGroupLora && chosen[w.group] >= 0 ? p.rank_pad / 64 * 2 : 0;
+    };
     // N of a tile's MMAs; a pair's CTAs hold half of these rows of Q each
     auto columns_of = [](const GroupTile &w) { return (w.n + 16 * CG - 1) / (16 * CG) * (16 * CG); };
 
     if (warp == 0) {
         if (ptx::elect_one()) {
             PipelineState ring(C::STAGES, (p.debug_flags & 1u) ? 0u : 1u);
-            bool ok = true;
+            bool ok = true, waited = false;
             uint32_t seq = 0;
             for (int t = cluster; ok && t < total; t += clusters, ++seq) {
                 const GroupTile w = tile_of(t);
-                const int k_tiles = (w.r + 63) / 64;
+                const int k_tiles = (w.r + 63) / 64, all_tiles = k_tiles + rank_tiles(w);
                 const int32_t i0 = w.i0 + rank * 128, j0 = w.j0 + rank * (columns_of(w) / 2);
-                for (int kt = 0; kt < k_tiles; ++kt) {
+                for (int kt = 0; kt < all_tiles; ++kt) {
                     if (!wait_bounded(bar_empty + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns,
                                       kWaitProducer, seq)) {
                         ok = false;
@@ -357,7 +427,8 @@ __global__ void __launch_bounds__(256, 1)
                         ring.advance();
                         continue;
                     }
-                    if (leader) ptx::mbar_arrive_expect_tx(full, C::TX);
+                    // of DOWN's P only the ranks that there are
+                    if (leader) ptx::mbar_arrive_expect_tx(full, MODE == kGroupDown ? p.rank * 128u + C::Q_BYTES : C::TX);
                     if constexpr (CG == 2) full = ptx::mapa(full, 0);
                     auto load_2d = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y) {
                         if constexpr (CG == 2) {
@@ -373,7 +444,20 @@ __global__ void __launch_bounds__(256, 1)
                             ptxg::tma_load_3d(dst, map, full, x, y, z);
                         }
                     };
-                    if constexpr (MODE == kGroupNT) {
+                    if constexpr (MODE == kGroupLora) {
+                        if (kt >= k_tiles) {
+                            if (!waited) ptx::griddep_wait();
+                            waited = true;
+                            const int32_t c = (kt - k_tiles) / 2 * 64, rest = (kt - k_tiles) % 2 * p.rank_pad;
+                            load_3d(sp, &tmU, c, i0, chosen[w.group]);
+                            load_2d(sq, &tmH, rest + c, j0);
+                            ring.advance();
+                            continue;
+                        }
+                        load_3d(sp, &tmP, r, i0, 0);
+                    } else if constexpr (MODE == kGroupDown) {
+                        load_3d(sp, &tmP, r, 0, chosen[w.group]);
+                    } else if constexpr (MODE == kGroupNT) {
                         load_3d(sp, &tmP, r, i0, w.group);
                     } else if constexpr (MODE == kGroupNN) {
 #pragma unroll
@@ -405,8 +489,8 @@ __global__ void __launch_bounds__(256, 1)
             uint32_t seq = 0;
             for (int t = cluster; ok && t < total; t += clusters, ++seq) {
                 const GroupTile w = tile_of(t);
-                const int k_tiles = (w.r + 63) / 64;
-                if (k_tiles == 0) continue;
+                const int k_tiles = (w.r + 63) / 64, all_tiles = k_tiles + rank_tiles(w);
+                if (all_tiles == 0) continue;
                 const uint32_t idesc = group_idesc<CG, MODE>(columns_of(w), p.bf16);
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc.stage * TN);
                 if (!wait_bounded(bar_tempty + 8 * acc.stage, acc.phase, abort_flag, p.timeout_ns, kWaitMma,
@@ -414,7 +498,7 @@ __global__ void __launch_bounds__(256, 1)
                     break;
                 }
                 ptx::tcgen05_fence_after();
-                for (int kt = 0; kt < k_tiles; ++kt) {
+                for (int kt = 0; kt < all_tiles; ++kt) {
                     if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns,
                                       kWaitMma, seq)) {
                         ok = false;
@@ -423,11 +507,13 @@ __global__ void __launch_bounds__(256, 1)
                     ptx::tcgen05_fence_after();
                     const int s = ring.stage;
                     const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, sq = base + C::OFF_Q + s * C::Q_BYTES;
-                    const uint64_t pd = MODE == kGroupNT ? ptx::smem_desc_k_sw128(sp) : ptxg::smem_desc_mn_sw128(sp, 8192);
+                    constexpr bool kMn = MODE == kGroupNN || MODE == kGroupTN;  // P is MN-major
+                    const uint64_t pd = kMn ? ptxg::smem_desc_mn_sw128(sp, 8192) : ptx::smem_desc_k_sw128(sp);
                     const uint64_t qd = MODE == kGroupTN ? ptxg::smem_desc_mn_sw128(sq, 8192) : ptx::smem_desc_k_sw128(sq);
                     // 16 elements of the sum: 32 bytes of a K-major row, 16 rows of an MN-major tile
-                    constexpr uint64_t kP = MODE == kGroupNT ? 2 : 128, kQ = MODE == kGroupTN ? 128 : 2;
-                    const int steps = w.r - kt * 64 >= 64 ? 4 : (w.r - kt * 64 + 15) / 16;
+                    constexpr uint64_t kP = kMn ? 128 : 2, kQ = MODE == kGroupTN ? 128 : 2;
+                    const int left = kt < k_tiles ? w.r - kt * 64 : p.rank - (kt - k_tiles) / 2 * 64;
+                    const int steps = left >= 64 ? 4 : (left + 15) / 16;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (k < steps) ptx::mma_f16<CG>(d, pd + k * kP, qd + k * kQ, idesc, kt > 0 || k > 0 ? 1u : 0u);
@@ -494,7 +580,7 @@ __global__ void __launch_bounds__(256, 1)
         const int tid = static_cast<int>(threadIdx.x) - 128;
         uint16_t *out = static_cast<uint16_t *>(p.out);
         const uint4 none = make_uint4(0, 0, 0, 0);
-        if (MODE != kGroupTN && p.zero_rest) {  // rows without a group: 16-byte units, a warp a row
+        if ((MODE == kGroupNT || MODE == kGroupNN) && p.zero_rest) {  // rows without a group: 16-byte units, a warp a row
             const int32_t head = start[0], rest = head + p.rows - start[p.groups];
             for (int32_t k = static_cast<int32_t>(blockIdx.x) * 4 + quarter; k < rest; k += static_cast<int32_t>(gridDim.x) * 4) {
                 uint16_t *row = out + static_cast<int64_t>(k < head ? k : start[p.groups] + (k - head)) * p.out_row;
@@ -523,6 +609,31 @@ __global__ void __launch_bounds__(256, 1)
             ptx::tcgen05_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc.stage * TN);
             const int chunks = (w.n + 31) / 32;
+            if constexpr (MODE == kGroupDown) {
+                // a lane a rank: h and what its rounding left, zeros up to a whole 16
+                const int32_t padded = (p.rank + 15) / 16 * 16, i = quarter * 32 + lane;
+                const float scale = p.scales ? p.scales[chosen[w.group]] : 1.f;
+                uint16_t *to = out + static_cast<int64_t>(w.j0) * p.out_row + i;
+#pragma unroll 1
+                for (int c = 0; c < chunks && quarter * 32 < padded; ++c) {
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(taddr + c * 32, v);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (c * 32 + j >= w.n || i >= padded) continue;
+                        const float h = i < p.rank ? __uint_as_float(v[j]) * scale : 0.f;
+                        uint16_t high, low;
+                        split_16(p.bf16, h, &high, &low);
+                        to[(c * 32 + j) * p.out_row] = high;
+                        to[(c * 32 + j) * p.out_row + p.rank_pad] = low;
+                    }
+                }
+                ptx::tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(tempty + 8 * acc.stage);
+                acc.advance();
+            } else {
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c, ++turn) {
                 uint32_t lo[16], hi[16];
@@ -589,10 +700,12 @@ __global__ void __launch_bounds__(256, 1)
                 if (tid == 0) ptx::bulk_commit_group();
             }
             acc.advance();
+            }
         }
         if (tid == 0) ptx::bulk_wait_group_read<0>();
         __syncwarp();
     }
+    if (MODE == kGroupLora) ptx::griddep_wait();  // the next kernel waits for this one alone: not before DOWN has ended
     ptx::tcgen05_fence_before();
     if constexpr (CG == 2) {
         ptx::cluster_arrive_relaxed();

@@ -1,4 +1,5 @@
-"""Products grouped by rows: each group (an expert's tokens) is multiplied with a matrix of its own.
+"""Products grouped by rows: each group (an expert's tokens) is multiplied with a matrix of its own,
+or (a request's tokens) goes through its own low-rank adapter beside a shared matrix.
 
 Over the C ABI of ``include/grouped_ops.h`` (library ``_build/liblinear_ops.so``), by the binding and
 in the manner of ``linear.py``: float16 and bfloat16, fp32 sums, one rounding; ``stream=`` as there.
@@ -6,6 +7,8 @@ in the manner of ``linear.py``: float16 and bfloat16, fp32 sums, one rounding; `
     D = g.grouped_gemm_nt(A, B, offsets)       # D[r] = A[r]·B[e]ᵀ for the rows r of group e
     dA = g.grouped_gemm_nn(dD, B, offsets)     # dA[r] = dD[r]·B[e]
     dB = g.grouped_gemm_tn(dD, A, offsets)     # dB[e] = dD_eᵀ·A_e
+    D = g.gemm_lora_nt(x, W, down, up, offsets, adapters, scales=scales)
+                                               # D[r] = x[r]·Wᵀ + scales[a]·(x[r]·down[a]ᵀ)·up[a]ᵀ, a = adapters[e]
 
 ``offsets`` (int32 or int64, groups + 1 of them on the device): group e has the rows offsets[e] to
 offsets[e + 1] - 1.  No call reads them on the host.  Values are taken as at least 0, at most the
@@ -19,12 +22,12 @@ import ctypes
 from . import build as _build
 from . import linear as _linear
 
-__all__ = ["grouped_gemm_nt", "grouped_gemm_nn", "grouped_gemm_tn", "GroupedOptions", "grouped_device_status"]
+__all__ = ["grouped_gemm_nt", "grouped_gemm_nn", "grouped_gemm_tn", "gemm_lora_nt", "GroupedOptions", "grouped_device_status"]
 
 
 class GroupedOptions(ctypes.Structure):
     """Mirror of ``grouped_options`` (zero fields mean defaults)."""
-    _fields_ = [("tile", ctypes.c_int32), ("max_clusters", ctypes.c_int32), ("debug_flags", ctypes.c_int32),
+    _fields_ = [("tile", ctypes.c_int32), ("split", ctypes.c_int32), ("max_clusters", ctypes.c_int32), ("debug_flags", ctypes.c_int32),
                 ("timeout_ns", ctypes.c_int64)]
 
 
@@ -40,9 +43,12 @@ def load_grouped() -> ctypes.CDLL:
         rows = [vp, i64, vp, i64, i64, vp, i32, vp, i64, i64, i64, i64, i64, i32, i32, vp, opts]
         for name, args in (("grouped_gemm_nt", rows), ("grouped_gemm_nn", rows),
                            ("grouped_gemm_tn", [vp, i64, vp, i64, vp, i32, vp, i64, i64, i64, i64, i64, i64, i32, vp, opts]),
+                           ("gemm_lora_nt", [vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, i32, vp, vp, i64, i64, i64, i64, i64,
+                                             i64, i64, i32, vp, i64, vp, opts]),
                            ("grouped_last_device_status", [vp, ctypes.POINTER(ctypes.c_uint64)])):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, ctypes.c_int
+        lib.gemm_lora_workspace_size.argtypes, lib.gemm_lora_workspace_size.restype = [i64, i64], i64
         _lib = lib
     return _lib
 
@@ -78,6 +84,18 @@ def grouped_gemm_tn(dD, A, offsets, dB=None, *, stream=None, options: GroupedOpt
     Rows without a group count for nothing, whatever they hold.
     """
     return _call("grouped_gemm_tn", (dD, A, offsets, dB), stream, options)
+
+
+def gemm_lora_nt(x, W, down, up, offsets, adapters, D=None, *, scales=None, stream=None,
+                 options: GroupedOptions | None = None):
+    """D[r] = x[r]·Wᵀ + scales[a]·(x[r]·down[a]ᵀ)·up[a]ᵀ for the rows r of request e, a = adapters[e].
+
+    x rows x K, W N x K, down adapters x rank x K, up adapters x N x rank, D rows x N; rank a multiple
+    of 8 up to 128; ``adapters`` int32, ``scales`` float32 (None: 1), both on the device, one for each
+    request and each adapter.  An adapter out of range (-1) and rows without a request have the
+    shared product alone.  No row's result depends on another row's adapter.
+    """
+    return _call("gemm_lora_nt", (x, W, down, up, offsets, adapters, D, scales), stream, options)
 
 
 def grouped_device_status(stream=None) -> tuple[int, int]:

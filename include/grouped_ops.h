@@ -1,6 +1,7 @@
 /*
  * grouped_ops.h -- C ABI of the products grouped by rows on GB300 (sm_103a):
- * a matrix of its own for each group of rows (experts), with both gradients.
+ * a matrix of its own for each group of rows (experts), with both gradients, and
+ * low-rank adapters of many requests beside a shared product.
  *
  * Conventions and element types as in linear_ops.h.  Groups are given by
  * `offsets`, groups + 1 whole numbers in DEVICE memory (int32, or int64 with
@@ -29,16 +30,20 @@ enum { GROUPED_MAX_GROUPS = 1024 };
 
 /*
  * Options; every zero field means "the default".
- *   tile          columns of a tile along the second operand's rows: 32, 64 or
- *                 128 (one CTA, by 128 of the first's), 256 (a CTA pair, by 256);
- *                 the gradient for the matrices takes 64 at least.  0: chosen
- *                 from the sizes.
+ *   tile          rows (of the gradient for the matrices: columns of dD) of a tile:
+ *                 16 to 128 (one CTA, by 128 of the other axis), 256 (a CTA pair,
+ *                 by 256).  0: chosen from the sizes.
+ *   split         1, 2, 4 or 8: a tile's sum is shared by a cluster of so many CTAs,
+ *                 one tile each (tiles of 16 to 128; not the gradient for the
+ *                 matrices); -1: a persistent grid (tiles of 32 to 256; the gradient
+ *                 for the matrices: 64 to 256).  0: chosen.
  *   max_clusters  cap on the persistent grid (CTAs, or pairs); 0: as many as fit.
  *   debug_flags   test hook: 1 makes every wait run out (see gemm_f16.h).
  *   timeout_ns    limit of every wait inside the kernel; 0: 4 s.
  */
 typedef struct grouped_options {
     int32_t tile;
+    int32_t split;
     int32_t max_clusters;
     int32_t debug_flags;
     int64_t timeout_ns;
@@ -68,6 +73,32 @@ int grouped_gemm_nn(const void *dD, int64_t ldd, const void *B, int64_t ldb, int
 int grouped_gemm_tn(const void *dD, int64_t ldd, const void *A, int64_t lda, const void *offsets, int32_t offsets_type,
                     void *dB, int64_t ldb, int64_t b_stride, int64_t rows, int64_t groups, int64_t N, int64_t K,
                     int32_t type, void *stream, const grouped_options *opts);
+
+/*
+ * A shared product and, beside it, each row's low-rank adapter:
+ *
+ *     D[r] = x[r] * W^T + scales[a] * (x[r] * down[a]^T) * up[a]^T
+ *
+ * for the rows r of request e (offsets as above), a = adapters[e] (int32, DEVICE
+ * memory); without the second term where a is not in [0, adapter_count) and for rows
+ * without a request.  x rows x K, W N x K, down adapter_count matrices of rank x K,
+ * up of N x rank, scales fp32 in DEVICE memory (NULL: 1).  x * down^T is fp32 or two
+ * 16-bit numbers (16 bits of it for LINEAR_BF16, 22 for LINEAR_F16, where it must
+ * be below 65520), the sum fp32, D rounded once.  rank is a multiple of 8 up to 128.
+ * No row's result depends on another row's adapter.  `workspace`
+ * (gemm_lora_workspace_size() bytes, 16-byte aligned, no initialisation, not shared
+ * by calls that may overlap on the GPU) holds x * down^T; GEMM_ERR_SCRATCH_LIMIT if it
+ * is smaller.  D overlaps no input.  opts: tiles of 16 to 128 take each row's
+ * adapter (split 1 to 8), 256 tiles of one request each (split -1).
+ */
+int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const void *down, int64_t ld_down,
+                 int64_t down_stride, const void *up, int64_t ld_up, int64_t up_stride, const float *scales,
+                 const void *offsets, int32_t offsets_type, const int32_t *adapters, void *D, int64_t ldd, int64_t rows,
+                 int64_t requests, int64_t adapter_count, int64_t N, int64_t K, int64_t rank, int32_t type,
+                 void *workspace, int64_t workspace_bytes, void *stream, const grouped_options *opts);
+
+/* Bytes of workspace for those sizes, or a negative gemm_status_t. */
+int64_t gemm_lora_workspace_size(int64_t rows, int64_t rank);
 
 /*
  * As gemm_f16_last_device_status(), for the calls above: synchronises `stream`,

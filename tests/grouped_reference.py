@@ -50,3 +50,27 @@ def matrices(dD, A, offsets):
             out[e] = d.t() @ a
             far[e] = bound(out[e], d.abs().t() @ a.abs(), j - i, A.dtype)
     return out, far
+
+
+def adapters(x, W, down, up, offsets, chosen, scales):
+    """(D, bound) of x·Wᵀ + scales[a]·(x·down[a]ᵀ)·up[a]ᵀ, a each row's adapter.
+
+    The shared sum and h = scales[a]·x·down[a]ᵀ are off as any fp32 sum here; h, where it is held as
+    two 16-bit numbers, by the second's rounding of what the first left, half a step of half a step
+    (and half the least subnormal); the sum over the ranks by what h is, and as another sum."""
+    rows, K = x.shape
+    a64, w64 = x.double(), W.double()
+    D = a64 @ w64.t()
+    far = (K / 64 + 64) * 2.0 ** -23 * (a64.abs() @ w64.abs().t())
+    for e, (i, j) in enumerate(spans(offsets, rows)):
+        a = int(chosen[e])
+        if j == i or not 0 <= a < down.shape[0]:
+            continue
+        s = 1.0 if scales is None else float(scales[a])
+        d64, u64, xs = down[a].double(), up[a].double(), a64[i:j]
+        h = s * (xs @ d64.t())
+        unit = UNIT[x.dtype]
+        eh = abs(s) * (K / 64 + 64) * 2.0 ** -23 * (xs.abs() @ d64.abs().t()) + (2.0 ** -23 + unit * unit) * h.abs() + TINY[x.dtype]
+        D[i:j] += h @ u64.t()
+        far[i:j] += eh @ u64.abs().t() + (x.shape[1] / 64 + 64) * 2.0 ** -23 * ((h.abs() + eh) @ u64.abs().t())
+    return D, far + UNIT[x.dtype] * (D.abs() + far) + TINY[x.dtype]

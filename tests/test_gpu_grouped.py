@@ -235,6 +235,27 @@ def test_a_wait_that_runs_out(g, tile, mode):
     check_all(g, A, B, dD, offsets, tile)
 
 
+@pytest.mark.parametrize("tile", [16, 32, 64, 128])
+@pytest.mark.parametrize("split", [1, 2, 4, 8])
+def test_sums_shared_by_a_cluster(g, tile, split):
+    """Tiles of 16 to 128 rows whose sum 1 to 8 CTAs share: odd groups, rows without one, given results."""
+    for counts, N, K, first, spare in (([1, 0, 2], 200, 1032, 0, 0), ([15, 33, 0, 130], 136, 520, 3, 4), ([5], 8, 8, 0, 1)):
+        A, B, dD, offsets = inputs(counts, N, K, BF16, spare, first)
+        o = g.GroupedOptions(tile=tile, split=split, timeout_ns=2_000_000_000)
+        for call, x, nt in ((g.grouped_gemm_nt, A, True), (g.grouped_gemm_nn, dD, False)):
+            want = ref.product(x, B, offsets.tolist(), nt)
+            near(call(x, B, offsets, options=o), want)
+            given = torch.full(want[0].shape, 7.0, dtype=BF16, device="cuda")
+            call(x, B, offsets, given, options=o)
+            last = first + sum(counts)
+            near(given[first:last], (want[0][first:last], want[1][first:last]))
+            assert bool((given[:first] == 7.0).all() and (given[last:] == 7.0).all())
+        bad = g.GroupedOptions(tile=tile, split=split, debug_flags=1, timeout_ns=50_000_000)
+        assert g.grouped_device_status()[0] == 0
+        g.grouped_gemm_nt(A, B, offsets, options=bad)
+        assert g.grouped_device_status()[0] == TIMEOUT
+
+
 def test_capped_grids(g):
     A, B, dD, offsets = inputs([300, 5, 77], 520, 136, BF16)
     want = g.grouped_gemm_nt(A, B, offsets), g.grouped_gemm_tn(dD, A, offsets)

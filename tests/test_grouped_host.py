@@ -63,7 +63,7 @@ def test_refusals(lib):
     assert nt(a=P + 8) == nt(b=2 * P + 2) == nt(d=4 * P + 8) == nt(lda=68) == nt(bs=32 * 64 + 4) == nt(off=3 * P + 2) == MISALIGNED
     assert nt(off=3 * P + 4, ot=1) == MISALIGNED
     assert nt(d=P) == nt(d=2 * P + 16) == nt(d=3 * P) == nt(d=P + 16 * 64 * 2 - 16) == INVALID
-    for bad in (dict(tile=16), dict(max_clusters=-1), dict(debug_flags=2), dict(timeout_ns=-1)):
+    for bad in (dict(tile=8), dict(split=3), dict(split=2, tile=256), dict(split=-1, tile=16), dict(max_clusters=-1), dict(debug_flags=2), dict(timeout_ns=-1)):
         assert nt(o=g.GroupedOptions(**bad)) == INVALID, bad
     assert nt(rows=0, a=None, d=None) == nt(N=0, b=None, d=None) == OK
 
@@ -71,7 +71,7 @@ def test_refusals(lib):
         return lib.grouped_gemm_tn(dd, ldd, a, lda, off, ot, db, ldb, bs, rows, groups, N, K, t, None, o)
 
     assert tn(t=2) == tn(dd=None) == tn(a=None) == tn(db=None) == tn(db=P) == tn(bs=31 * 64) == tn(ldb=56) == INVALID
-    assert tn(o=g.GroupedOptions(tile=32)) == INVALID
+    assert tn(o=g.GroupedOptions(tile=32)) == tn(o=g.GroupedOptions(split=2)) == INVALID
     assert tn(dd=P + 8) == tn(db=4 * P + 8) == tn(ldd=36) == MISALIGNED
     assert tn(groups=0) == tn(N=0) == tn(K=0) == OK
 

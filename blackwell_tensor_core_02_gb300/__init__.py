@@ -401,11 +401,13 @@ _LINEAR = ("layer_norm", "layer_norm_backward", "Fp4Tensor", "quantize_fp4", "de
            "describe_fp4", "fp4_device_status", "load_linear")
 # Products grouped by rows, likewise.
 _GROUPED = ("grouped_gemm_nt", "grouped_gemm_nn", "grouped_gemm_tn", "gemm_lora_nt", "GroupedOptions", "grouped_device_status")
-__all__ += [*_LINEAR, *_GROUPED]
+# Layer norm with 8-bit checkpoints, likewise.
+_CHECKPOINT = ("Fp8Rows", "layer_norm_checkpoint", "layer_norm_restore", "layer_norm_backward_checkpoint")
+__all__ += [*_LINEAR, *_GROUPED, *_CHECKPOINT]
 
 
 def __getattr__(name):
-    for names, module in ((_LINEAR, "linear"), (_GROUPED, "grouped")):
+    for names, module in ((_LINEAR, "linear"), (_GROUPED, "grouped"), (_CHECKPOINT, "checkpoint")):
         if name in names:
             module = importlib.import_module(f".{module}", __name__)
             globals().update({n: getattr(module, n) for n in names})

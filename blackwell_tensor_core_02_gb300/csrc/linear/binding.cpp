@@ -1,6 +1,7 @@
-// binding.cpp -- the calls of linear.py and grouped.py below their keyword handling:
-// checks of the tensors, outputs and workspaces from torch's allocator, the current
-// stream, and the C entry points of linear_ops.h and grouped_ops.h.
+// binding.cpp -- the calls of linear.py, grouped.py and checkpoint.py below their
+// keyword handling: checks of the tensors, outputs and workspaces from torch's
+// allocator, the current stream, and the C entry points of linear_ops.h, grouped_ops.h
+// and checkpoint_ops.h.
 //
 // The smallest calls (one token) run for two to four microseconds on the GPU, far
 // less than the same checks, allocations and conversions take in Python (a layer
@@ -21,6 +22,7 @@
 #include <cmath>
 #include <initializer_list>
 
+#include "checkpoint_ops.h"
 #include "grouped_ops.h"
 #include "linear_ops.h"
 
@@ -555,6 +557,184 @@ PyObject *lora(PyObject *const *args, Py_ssize_t n) {  // x, W, down, up, offset
     return THPVariable_Wrap(D);
 }
 
+// ------------------------------------------------------------ checkpoints --
+
+// The parts of an Fp8Rows (a tuple: codes, scales) that fit together.
+struct Fp8 {
+    const at::Tensor *codes, *scales;
+    int64_t rows, cols;
+};
+
+Fp8 fp8_of(PyObject *o, const char *name) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) refuse(PyExc_TypeError, "%s must be an Fp8Rows", name);
+    Fp8 q;
+    q.codes = &tensor(PyTuple_GET_ITEM(o, 0), "codes");
+    q.scales = &tensor(PyTuple_GET_ITEM(o, 1), "scales");
+    if (q.codes->scalar_type() != at::kFloat8_e4m3fn || q.scales->scalar_type() != at::kByte) {
+        refuse(PyExc_TypeError, "%s: codes must be float8_e4m3fn and scales uint8", name);
+    }
+    const int64_t dims = q.codes->dim();
+    if (dims == 0) refuse(PyExc_ValueError, "%s: codes must have at least one axis", name);
+    q.cols = q.codes->size(dims - 1);
+    q.rows = 1;
+    bool fits = q.scales->dim() == dims && q.scales->size(dims - 1) == (q.cols + 31) / 32;
+    for (int64_t i = 0; i < dims - 1; ++i) {
+        q.rows *= q.codes->size(i);
+        fits = fits && q.scales->size(i) == q.codes->size(i);
+    }
+    if (!fits) refuse(PyExc_ValueError, "%s: scales must be one for each 32 codes of a row", name);
+    if (!q.codes->is_cuda() || q.scales->device() != q.codes->device() || !q.codes->is_contiguous() ||
+        !q.scales->is_contiguous()) {
+        refuse(PyExc_ValueError, "%s: codes and scales must be contiguous tensors of one CUDA device", name);
+    }
+    if (q.cols == 0) refuse(PyExc_ValueError, "%s: rows of no elements have no norm", name);
+    return q;
+}
+
+at::DimVector blocks_of(at::IntArrayRef sizes) {
+    at::DimVector s(sizes.begin(), sizes.end());
+    s.back() = (s.back() + 31) / 32;
+    return s;
+}
+
+// weight and bias (either may be None), vectors of `cols` of one dtype, `type` or float32, on like's device.
+struct Affine {
+    const void *weight = nullptr, *bias = nullptr;
+    at::ScalarType type;
+};
+
+Affine affine_of(PyObject *weight, PyObject *bias, int64_t cols, at::ScalarType type, const at::Tensor &like) {
+    Affine a;
+    a.type = type;
+    bool first = true;
+    for (int i = 0; i < 2; ++i) {
+        PyObject *o = i == 0 ? weight : bias;
+        if (!given(o)) continue;
+        const char *name = i == 0 ? "weight" : "bias";
+        const at::Tensor &t = tensor(o, name);
+        if (t.dim() != 1 || t.size(0) != cols || (cols > 1 && t.stride(0) != 1) || t.device() != like.device()) {
+            refuse(PyExc_ValueError, "%s must be a contiguous vector of the last axis, on the rows' device", name);
+        }
+        if (t.scalar_type() != type && t.scalar_type() != at::kFloat) {
+            refuse(PyExc_TypeError, "%s must have the rows' dtype or float32", name);
+        }
+        if (!first && t.scalar_type() != a.type) refuse(PyExc_TypeError, "weight and bias must have one dtype");
+        a.type = t.scalar_type();
+        first = false;
+        (i == 0 ? a.weight : a.bias) = t.data_ptr();
+    }
+    return a;
+}
+
+PyObject *keep(PyObject *const *args, Py_ssize_t n) {  // x, weight, bias, eps, out -> (y, codes, scales, rstd)
+    count(n, 5);
+    const at::Tensor &x = tensor(args[0], "x");
+    const int code = dtype_of(x, "x");
+    const Rows r = rows_of(x, "x");
+    if (r.cols == 0) refuse(PyExc_ValueError, "x: rows of no elements have no norm");
+    const Affine a = affine_of(args[1], args[2], r.cols, x.scalar_type(), x);
+    const double eps = PyFloat_AsDouble(args[3]);
+    if (eps == -1.0 && PyErr_Occurred()) throw Refused{};
+    const c10::cuda::CUDAGuard guard(x.device());
+    Rows yr{r.rows, r.cols, r.cols};
+    at::Tensor y;
+    if (given(args[4])) {
+        y = tensor(args[4], "out");
+        same_kind(y, x, "out", "x");
+        yr = rows_of(y, "out");
+    } else {
+        y = empty(x.sizes(), x.scalar_type(), x);
+    }
+    at::Tensor codes = empty(x.sizes(), at::kFloat8_e4m3fn, x), scales = empty(blocks_of(x.sizes()), at::kByte, x);
+    at::Tensor rstd = empty(x.sizes().slice(0, static_cast<size_t>(x.dim() - 1)), at::kFloat, x);
+    check_status(norm_checkpoint_forward(x.data_ptr(), r.step, a.weight, a.bias, y.data_ptr(), yr.step, codes.data_ptr(),
+                                         scales.data_ptr(), rstd.data_ptr<float>(), r.rows, r.cols, static_cast<float>(eps),
+                                         code, dtype_code(a.type), stream_of(x)),
+                 "layer_norm_checkpoint");
+    return tuple_of({y, codes, scales, rstd});
+}
+
+PyObject *restore(PyObject *const *args, Py_ssize_t n) {  // kept, weight, bias, dtype, out
+    count(n, 5);
+    const Fp8 q = fp8_of(args[0], "kept");
+    const at::Tensor &codes = *q.codes;
+    const c10::cuda::CUDAGuard guard(codes.device());
+    at::Tensor y;
+    int64_t step = q.cols;
+    if (given(args[4])) {
+        y = tensor(args[4], "out");
+        dtype_of(y, "out");
+        if (y.sizes() != codes.sizes() || y.device() != codes.device()) {
+            refuse(PyExc_ValueError, "out must have the kept rows' shape and device");
+        }
+        if (given(args[3]) && dtype_arg(args[3], "dtype") != y.scalar_type()) {
+            refuse(PyExc_TypeError, "dtype must be out's");
+        }
+        step = rows_of(y, "out").step;
+    } else {
+        at::ScalarType type = at::kFloat;
+        if (given(args[3])) {
+            type = dtype_arg(args[3], "dtype");
+        } else if (given(args[1]) || given(args[2])) {  // the weights'
+            const at::Tensor &t = given(args[1]) ? tensor(args[1], "weight") : tensor(args[2], "bias");
+            dtype_of(t, given(args[1]) ? "weight" : "bias");
+            type = t.scalar_type();
+        }
+        y = empty(codes.sizes(), type, codes);
+    }
+    const Affine a = affine_of(args[1], args[2], q.cols, y.scalar_type(), codes);
+    check_status(norm_checkpoint_restore(codes.data_ptr(), q.scales->data_ptr(), a.weight, a.bias, y.data_ptr(), step, q.rows,
+                                         q.cols, dtype_code(y.scalar_type()), dtype_code(a.type), stream_of(y)),
+                 "layer_norm_restore");
+    return THPVariable_Wrap(y);
+}
+
+PyObject *keep_backward(PyObject *const *args, Py_ssize_t n) {  // dy, kept, weight, rstd, dx, grad_dtype
+    count(n, 6);
+    const at::Tensor &dy = tensor(args[0], "dy");
+    const int code = dtype_of(dy, "dy");
+    const Rows r = rows_of(dy, "dy");
+    const Fp8 q = fp8_of(args[1], "kept");
+    if (q.codes->sizes() != dy.sizes() || q.codes->device() != dy.device()) {
+        refuse(PyExc_ValueError, "kept must have dy's shape and device");
+    }
+    const float *rstd = statistic(tensor(args[3], "rstd"), dy, r.rows, "rstd");
+    const Affine a = affine_of(args[2], Py_None, r.cols, dy.scalar_type(), dy);
+    at::ScalarType wtype = a.type;
+    const bool parameters = a.weight || given(args[5]);  // their gradients are wanted
+    if (given(args[5])) {
+        const at::ScalarType want = dtype_arg(args[5], "grad_dtype");
+        if (a.weight ? want != wtype : (want != wtype && want != at::kFloat)) {
+            refuse(PyExc_TypeError, "grad_dtype must be weight's dtype or, without a weight, dy's or float32");
+        }
+        wtype = want;
+    }
+    const c10::cuda::CUDAGuard guard(dy.device());
+    Rows gr{r.rows, r.cols, r.cols};
+    at::Tensor dx, dweight, dbias, space;
+    if (given(args[4])) {
+        dx = tensor(args[4], "dx");
+        same_kind(dx, dy, "dx", "dy");
+        gr = rows_of(dx, "dx");
+    } else {
+        dx = empty(dy.sizes(), dy.scalar_type(), dy);
+    }
+    int64_t need = 0;
+    if (parameters) {
+        dweight = empty({r.cols}, wtype, dy);
+        dbias = empty({r.cols}, wtype, dy);
+        need = layer_norm_backward_workspace_size(r.rows, r.cols);
+        check_status(need, "layer_norm_backward_checkpoint");
+        space = empty({need}, at::kByte, dy);
+    }
+    check_status(norm_checkpoint_backward(dy.data_ptr(), r.step, q.codes->data_ptr(), q.scales->data_ptr(), a.weight, rstd,
+                                          dx.data_ptr(), gr.step, parameters ? dweight.data_ptr() : nullptr,
+                                          parameters ? dbias.data_ptr() : nullptr, r.rows, r.cols, code, dtype_code(wtype),
+                                          parameters ? space.data_ptr() : nullptr, need, stream_of(dy)),
+                 "layer_norm_backward_checkpoint");
+    return tuple_of({dx, dweight, dbias});
+}
+
 template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -583,6 +763,9 @@ PyMethodDef g_methods[] = {LINEAR_METHOD("layer_norm", norm),
                            LINEAR_METHOD("grouped_gemm_nn", grouped_rows_product<false>),
                            LINEAR_METHOD("grouped_gemm_tn", grouped_matrices),
                            LINEAR_METHOD("gemm_lora_nt", lora),
+                           LINEAR_METHOD("layer_norm_checkpoint", keep),
+                           LINEAR_METHOD("layer_norm_restore", restore),
+                           LINEAR_METHOD("layer_norm_backward_checkpoint", keep_backward),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_linear_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -14,7 +14,7 @@ namespace linear_ops {
 __device__ int g_group_status;               // GEMM_ERR_DEVICE_TIMEOUT of the first wait that ran out (0: none)
 __device__ unsigned long long g_group_info;  // its role, CTA and tile
 
-enum : uint32_t { kWaitProducer = 1, kWaitMma = 2, kWaitEpilogue = 3, kWaitClear = 4 };
+enum : uint32_t { kWaitProducer = 1, kWaitMma = 2, kWaitEpilogue = 3 };
 
 // By one thread.  False if the wait ran out or, when `honor_abort`, as soon as another
 // role of this CTA has given up.  kCluster: the arrivals come from other CTAs of the

@@ -7,48 +7,53 @@
 // the matrix's bytes on few SMs, and a start and end of its own; hence the split.
 //
 // LORA: all rows are one group, the shared product's, and each row's own adapter is
-// added in fp32 as the parts meet, after h = scale_a * x * down_a^T from a launch before
-// (lora_down_kernel, fp32):
+// added before the parts meet, after h = scale_a * x * down_a^T from a launch before
+// (lora_down_kernel, as two 16-bit numbers, see grouped_kernel.cuh):
 //
 //     D[j][i] = round(sum_r W[i][r] * x[j][r] + sum_c up_a(j)[i][c] * h[j][c])
 //
-// As one more stretch of the MMA's sum, with zeros for the rows of other adapters, that
-// would be 0 * up for those rows, NaN where an adapter holds an infinity.
+// As one more stretch of the shared sum, with zeros for the rows of other adapters, that
+// would be 0 * up for those rows, NaN where an adapter holds an infinity.  So up to 16
+// consecutive rows of one adapter are a piece, with 16 columns of TMEM of its own: the
+// MMA multiplies up_a with the 16 rows of h from the piece's first on, and the epilogue
+// adds the columns that are the piece's to its sums.  The cluster's CTAs have the pieces
+// of a share of the tile's rows each.
 #pragma once
 
 #include "grouped_kernel.cuh"
 
 namespace linear_ops {
 
-template <int TN>
+template <int TN, bool LORA>
 struct FewShape {
-    static constexpr int P_BYTES = 128 * 128, Q_BYTES = TN * 128, STAGE = P_BYTES + Q_BYTES;
-    static constexpr int LISTS = 2 * 4 * (GROUPED_MAX_GROUPS + 4);  // the groups' first rows and first tiles
-    // two CTAs an SM: half of 228 KiB, less 1 KiB that each takes beside its own
-    static constexpr int BUDGET = 113 * 1024;
-    static constexpr int REST = LISTS + TN * 4 + 256 + 896;
-    static constexpr int STAGES = (BUDGET - REST) / STAGE;
-    // the CTA's fp32 sums, in the ring once it is idle: row j at j * LD floats, 16 bytes
-    // off a multiple of 128 bytes
+    static constexpr int P_BYTES = 128 * 128, Q_BYTES = (LORA && TN < 32 ? 32 : TN) * 128, STAGE = P_BYTES + Q_BYTES;
+    static constexpr int LIST = 4 * (GROUPED_MAX_GROUPS + 4);  // the groups' first rows; their first tiles
+    static constexpr int PIECE = 16;                           // rows of a piece, and its columns of TMEM
+    static constexpr int SLOTS = (512 - TN) / PIECE < 16 ? (512 - TN) / PIECE : 16;  // pieces in TMEM at once
+    // the CTA's fp32 sums, row j at j * LD floats, 16 bytes off a multiple of 128 bytes: in
+    // the ring once it is idle, of LORA behind it
     static constexpr int LD = 128 + 4;
-    static constexpr int OFF_P = 0, OFF_Q = STAGES * P_BYTES;
-    static constexpr int OFF_START = STAGES * STAGE;
-    static constexpr int OFF_TILES = OFF_START + 4 * (GROUPED_MAX_GROUPS + 4);
-    static constexpr int OFF_ROWS = OFF_TILES + 4 * (GROUPED_MAX_GROUPS + 4);  // int32 [TN]: the rows' adapters
-    static constexpr int OFF_BAR = OFF_ROWS + TN * 4;
-    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 1) * 8;
-    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 896;
+    static constexpr int SUMS = 4 * TN * LD;
+    // the rest of the shared memory, behind the ring
+    static constexpr int OFF_START = LORA ? SUMS : 0, OFF_TILES = OFF_START + LIST;
+    static constexpr int OFF_ROWS = OFF_TILES + LIST;             // int32 [TN]: the rows' adapters
+    static constexpr int OFF_PIECES = OFF_ROWS + TN * 4;          // int32 [TN]: first row + 256 * rows; their number behind
+    static constexpr int OFF_BAR = OFF_PIECES + TN * 4 + 8;
+    static constexpr int MOST_STAGES = 12;
+    // full, empty [stages]; done, list, pieces full, pieces free, drain
+    static constexpr int OFF_MISC = OFF_BAR + (2 * MOST_STAGES + 5) * 8;
+    static constexpr int REST = OFF_MISC + 16 + 896;
+    // Stages of a CTA that shares its SM with another (half of 228 KiB, less 1 KiB that each
+    // takes beside its own), and of one that has it alone, where that is more memory than
+    // two could have.  64 x 4096 x 4096: 4 CTAs a tile with 4 stages 10.8 us, with 8 9.2.
+    static constexpr int PAIRED = LORA ? 0 : (113 * 1024 - REST) / STAGE;
+    static constexpr int ALONE = (232448 - REST) / STAGE < MOST_STAGES ? (232448 - REST) / STAGE : MOST_STAGES;
+    static constexpr int smem(int stages) { return stages * STAGE + REST; }
     static constexpr int THREADS = 192;
-    static constexpr int TMEM_COLS = TN < 32 ? 32 : TN;
+    static constexpr int TMEM_COLS = LORA ? 512 : (TN < 32 ? 32 : TN);
     static_assert(TN == 16 || TN == 32 || TN == 64 || TN == 128, "tile");
-    static_assert(STAGES >= 3 && STAGES * STAGE >= 4 * TN * LD && SMEM_ALLOC <= BUDGET, "two CTAs an SM");
-};
-
-// What LORA's rows take beside the shared product.
-struct LoraParams {
-    const float *h;          // [rows][rank]
-    const uint16_t *up;      // [adapters][N][rank]
-    int64_t up_row, up_matrix;
+    static_assert(OFF_BAR % 8 == 0 && ALONE >= 4 && ALONE * STAGE + REST > 114 * 1024, "an SM alone");
+    static_assert(LORA || (PAIRED >= 3 && PAIRED * STAGE >= SUMS), "two CTAs an SM");
 };
 
 __device__ __forceinline__ float2 widen16(bool bf16, uint32_t w) {
@@ -74,32 +79,44 @@ __device__ __forceinline__ float4 few_sums(uint32_t addr) {
 }
 
 template <int TN, int KS, int MODE>
-__global__ void __launch_bounds__(192, 2)
-    grouped_few_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const GroupParams p,
-                       const LoraParams l) {
-    using C = FewShape<TN>;
-    static_assert(MODE == kGroupNT || MODE == kGroupNN || MODE == kGroupLora, "the rows are the N side");
+__global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
+    grouped_few_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmH, const GroupParams p,
+                       const int stages) {
+    constexpr bool LORA = MODE == kGroupLora;
+    using C = FewShape<TN, LORA>;
+    static_assert(MODE == kGroupNT || MODE == kGroupNN || LORA, "the rows are the N side");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t *smem = smem_raw + (base - raw);
+    const uint32_t ring_bytes = static_cast<uint32_t>(stages) * C::STAGE, off_q = static_cast<uint32_t>(stages) * C::P_BYTES;
+    uint8_t *smem = smem_raw + (base - raw) + ring_bytes;  // what lies behind the ring
+    const uint32_t sums_at = LORA ? base + ring_bytes : base;
+    float *sums = reinterpret_cast<float *>(smem_raw + (sums_at - raw));
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
     const int lane = static_cast<int>(threadIdx.x) % 32;
     const int rank = KS > 1 ? static_cast<int>(blockIdx.x) % KS : 0;
     const int tile = static_cast<int>(blockIdx.x) / KS;
 
-    const uint32_t bar_full = base + C::OFF_BAR, bar_empty = bar_full + 8 * C::STAGES, bar_done = bar_empty + 8 * C::STAGES;
+    const uint32_t bar_full = base + ring_bytes + C::OFF_BAR, bar_empty = bar_full + 8 * stages;
+    const uint32_t bar_done = bar_empty + 8 * stages;                               // the shared sum is complete
+    const uint32_t bar_list = bar_done + 8, bar_pfull = bar_list + 8, bar_pfree = bar_pfull + 8, bar_drain = bar_pfree + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     int32_t *start = reinterpret_cast<int32_t *>(smem + C::OFF_START), *tiles = reinterpret_cast<int32_t *>(smem + C::OFF_TILES);
-    int32_t *chosen = reinterpret_cast<int32_t *>(smem + C::OFF_ROWS);
+    int32_t *chosen = reinterpret_cast<int32_t *>(smem + C::OFF_ROWS), *pieces = reinterpret_cast<int32_t *>(smem + C::OFF_PIECES);
+    int32_t *piece_count = pieces + TN;
 
     if (warp == 0 && lane == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             ptx::mbar_init(bar_full + 8 * s, 1);
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
         ptx::mbar_init(bar_done, 1);
+        ptx::mbar_init(bar_list, 1);
+        ptx::mbar_init(bar_pfull, 1);
+        ptx::mbar_init(bar_pfree, 4);
+        ptx::mbar_init(bar_drain, 1);
         *abort_flag = 0;
         ptx::fence_mbarrier_init();
     }
@@ -109,13 +126,17 @@ __global__ void __launch_bounds__(192, 2)
     }
     if (threadIdx.x == 0) ptx::griddep_launch_dependents();
     // LORA follows lora_down_kernel, which lets it start only once the kernels before both
-    // have completed: it waits for h alone, below
-    if (MODE != kGroupLora || !p.follows) ptx::griddep_wait();
+    // have completed: it waits for h alone, in the producer
+    if (!LORA || !p.follows) ptx::griddep_wait();
     const int groups = group_starts(p, start, false, nullptr, static_cast<int>(threadIdx.x), C::THREADS);
     __syncthreads();
+    if (warp == 2) group_tiles<TN, LORA ? kGroupNT : MODE>(p, groups, start, tiles, nullptr, lane);
+    ptx::tcgen05_fence_before();
+    __syncthreads();
+    ptx::tcgen05_fence_after();
     GroupTile w;
-    if constexpr (MODE == kGroupLora) {
-        if (warp == 2) group_tiles<TN, kGroupNT>(p, groups, start, tiles, nullptr, lane);  // the first rows in order
+    w.n = 0;
+    if constexpr (LORA) {
         const int32_t j_tiles = (p.rows + TN - 1) / TN;
         w.group = 0;
         w.i0 = tile / j_tiles * 128;
@@ -123,14 +144,7 @@ __global__ void __launch_bounds__(192, 2)
         w.n = p.rows - w.j0 < TN ? p.rows - w.j0 : TN;
         w.r0 = 0;
         w.r = p.R;
-        ptx::tcgen05_fence_before();
-        __syncthreads();
-        ptx::tcgen05_fence_after();
     } else {
-        if (warp == 2) group_tiles<TN, MODE>(p, groups, start, tiles, nullptr, lane);
-        ptx::tcgen05_fence_before();
-        __syncthreads();
-        ptx::tcgen05_fence_after();
         if (p.zero_rest) {  // rows without a group: 16-byte units, a warp a row
             const int32_t head = start[0], rest = head + p.rows - start[groups];
             uint16_t *out = static_cast<uint16_t *>(p.out);
@@ -139,7 +153,6 @@ __global__ void __launch_bounds__(192, 2)
                 for (int32_t u = lane * 8; u < p.I; u += 256) *reinterpret_cast<uint4 *>(row + u) = make_uint4(0, 0, 0, 0);
             }
         }
-        w.n = 0;
         if (tile < tiles[groups]) w = group_tile<1, TN, MODE>(p, groups, start, tiles, tile);
     }
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
@@ -147,10 +160,11 @@ __global__ void __launch_bounds__(192, 2)
     const int k_tiles = work ? (w.r + 63) / 64 : 0;
     const int kt_begin = static_cast<int>(static_cast<int64_t>(k_tiles) * rank / KS);
     const int kt_end = static_cast<int>(static_cast<int64_t>(k_tiles) * (rank + 1) / KS);
+    const int rank_tiles = LORA ? p.rank_pad / 64 : 0;  // stages of a piece
 
     if (warp == 0) {
         if (work && ptx::elect_one()) {
-            PipelineState ring(C::STAGES, (p.debug_flags & 1u) ? 0u : 1u);
+            PipelineState ring(stages, (p.debug_flags & 1u) ? 0u : 1u);
             bool ok = true;
             for (int kt = kt_begin; kt < kt_end; ++kt) {
                 if (!wait_bounded(bar_empty + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitProducer, kt)) {
@@ -158,16 +172,35 @@ __global__ void __launch_bounds__(192, 2)
                     break;
                 }
                 const int s = ring.stage;
-                const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, full = bar_full + 8 * s;
-                ptx::mbar_arrive_expect_tx(full, C::STAGE);
+                const uint32_t sp = base + s * C::P_BYTES, full = bar_full + 8 * s;
+                ptx::mbar_arrive_expect_tx(full, C::P_BYTES + TN * 128);
                 if constexpr (MODE == kGroupNN) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) ptxg::tma_load_3d(sp + b * 8192, &tmP, full, w.i0 + 64 * b, kt * 64, w.group);
                 } else {
                     ptxg::tma_load_3d(sp, &tmP, full, kt * 64, w.i0, w.group);
                 }
-                ptx::tma_load_2d(base + C::OFF_Q + s * C::Q_BYTES, &tmQ, full, kt * 64, w.j0);
+                ptx::tma_load_2d(base + off_q + s * C::Q_BYTES, &tmQ, full, kt * 64, w.j0);
                 ring.advance();
+            }
+            if constexpr (LORA) {
+                ok = ok && wait_bounded(bar_list, 0, abort_flag, p.timeout_ns, kWaitProducer, 0);
+                const int count = ok ? *piece_count : 0;
+                if (count > 0) ptx::griddep_wait();
+                for (int q = 0; ok && q < count * rank_tiles; ++q) {
+                    const int j = pieces[q / rank_tiles] & 0xff, c = q % rank_tiles * 64;
+                    if (!wait_bounded(bar_empty + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitProducer, q)) {
+                        ok = false;
+                        break;
+                    }
+                    const int s = ring.stage;
+                    const uint32_t sq = base + off_q + s * C::Q_BYTES, full = bar_full + 8 * s;
+                    ptx::mbar_arrive_expect_tx(full, C::P_BYTES + 2 * C::PIECE * 128);
+                    ptxg::tma_load_3d(base + s * C::P_BYTES, &tmU, full, c, w.i0, chosen[j]);
+                    ptx::tma_load_2d(sq, &tmH, full, c, w.j0 + j);
+                    ptx::tma_load_2d(sq + C::PIECE * 128, &tmH, full, p.rank_pad + c, w.j0 + j);
+                    ring.advance();
+                }
             }
             if (!ok) {  // time for loads in flight to land before the shared memory goes
                 const uint64_t t0 = ptx::globaltimer_ns();
@@ -177,13 +210,17 @@ __global__ void __launch_bounds__(192, 2)
         __syncwarp();
     } else if (warp == 1) {
         if (work && ptx::elect_one()) {
-            PipelineState ring(C::STAGES, 0u);
+            PipelineState ring(stages, 0u);
             const uint32_t idesc = group_idesc<1, MODE>((w.n + 15) / 16 * 16, p.bf16);
+            bool ok = true;
             for (int kt = kt_begin; kt < kt_end; ++kt) {
-                if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitMma, kt)) break;
+                if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitMma, kt)) {
+                    ok = false;
+                    break;
+                }
                 ptx::tcgen05_fence_after();
                 const int s = ring.stage;
-                const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, sq = base + C::OFF_Q + s * C::Q_BYTES;
+                const uint32_t sp = base + s * C::P_BYTES, sq = base + off_q + s * C::Q_BYTES;
                 constexpr bool kMn = MODE == kGroupNN;
                 const uint64_t pd = kMn ? ptxg::smem_desc_mn_sw128(sp, 8192) : ptx::smem_desc_k_sw128(sp);
                 const uint64_t qd = ptx::smem_desc_k_sw128(sq);
@@ -197,13 +234,48 @@ __global__ void __launch_bounds__(192, 2)
                 ptx::mma_commit<1>(bar_empty + 8 * s, 0x1);
                 ring.advance();
             }
+            if (ok) ptx::mma_commit<1>(bar_done, 0x1);
+            if constexpr (LORA) {
+                ok = ok && wait_bounded(bar_list, 0, abort_flag, p.timeout_ns, kWaitMma, 0);
+                const int count = ok ? *piece_count : 0;
+                const uint32_t piece_idesc = group_idesc<1, MODE>(C::PIECE, p.bf16);
+                for (int q = 0; ok && q < count; ++q) {
+                    if (q > 0 && q % C::SLOTS == 0) {  // the epilogue has read the pieces before
+                        if (!wait_bounded(bar_pfree, (q / C::SLOTS - 1) & 1, abort_flag, p.timeout_ns, kWaitMma, q)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tcgen05_fence_after();
+                    }
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(TN + q % C::SLOTS * C::PIECE);
+                    for (int c = 0; c < rank_tiles; ++c) {
+                        if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitMma, q)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tcgen05_fence_after();
+                        const int s = ring.stage;
+                        const uint32_t sq = base + off_q + s * C::Q_BYTES;
+                        const uint64_t pd = ptx::smem_desc_k_sw128(base + s * C::P_BYTES);
+                        const uint64_t high = ptx::smem_desc_k_sw128(sq), low = ptx::smem_desc_k_sw128(sq + C::PIECE * 128);
+                        const int steps = p.rank - c * 64 >= 64 ? 4 : (p.rank - c * 64 + 15) / 16;
+                        for (int k = 0; k < steps; ++k) {
+                            ptx::mma_f16<1>(d, pd + k * 2, high + k * 2, piece_idesc, c > 0 || k > 0 ? 1u : 0u);
+                            ptx::mma_f16<1>(d, pd + k * 2, low + k * 2, piece_idesc, 1u);
+                        }
+                        ptx::mma_commit<1>(bar_empty + 8 * s, 0x1);
+                        ring.advance();
+                    }
+                    if (ok && (q % C::SLOTS == C::SLOTS - 1 || q == count - 1)) ptx::mma_commit<1>(bar_pfull, 0x1);
+                }
+            }
             // every MMA issued so far (after an abort as well: TMEM is freed below)
-            ptx::mma_commit<1>(bar_done, 0x1);
-            wait_bounded(bar_done, 0, abort_flag, p.timeout_ns, kWaitMma, 0xFFFFFFFFu, false);
+            ptx::mma_commit<1>(bar_drain, 0x1);
+            wait_bounded(bar_drain, 0, abort_flag, p.timeout_ns, kWaitMma, 0xFFFFFFFFu, false);
         }
         __syncwarp();
     } else if (work) {
-        if constexpr (MODE == kGroupLora) {  // the rows' adapters: the last request that starts at or before a row
+        if constexpr (LORA) {  // the rows' adapters: that of the last request that starts at or before a row
             for (int32_t j = static_cast<int32_t>(threadIdx.x) - 64; j < w.n; j += 128) {
                 const int32_t row = w.j0 + j;
                 int lo = -1, hi = groups;  // start[lo] <= row < start[hi]
@@ -217,16 +289,29 @@ __global__ void __launch_bounds__(192, 2)
                 }
                 chosen[j] = lo >= 0 && row < start[groups] ? adapter_of(p, lo) : -1;
             }
+            ptxg::sync_128(1);
+            if (warp == 2 && lane == 0) {  // the pieces of this CTA's share of the rows
+                const int first = w.n * rank / KS, last = w.n * (rank + 1) / KS;
+                int count = 0;
+                for (int j = first; j < last;) {
+                    const int32_t a = chosen[j];
+                    int n = 1;
+                    while (n < C::PIECE && j + n < last && chosen[j + n] == a) ++n;
+                    if (a >= 0) pieces[count++] = j | n << 8;
+                    j += n;
+                }
+                *piece_count = count;
+                ptx::mbar_arrive(bar_list);
+            }
         }
-        // all MMAs done: the accumulator is complete and the ring idle
+        // the shared sum is complete (without LORA, the ring idle)
         bool ok = true;
         if (lane == 0) ok = wait_bounded(bar_done, 0, abort_flag, p.timeout_ns, kWaitEpilogue, 0);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        const int i = (warp & 3) * 32 + lane;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         if (ok && *abort_flag == 0) {
             ptx::tcgen05_fence_after();
-            const int i = (warp & 3) * 32 + lane;
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            float *sums = reinterpret_cast<float *>(smem);
 #pragma unroll
             for (int c = 0; c < TN; c += 16) {
                 uint32_t v[16];
@@ -237,6 +322,30 @@ __global__ void __launch_bounds__(192, 2)
                 for (int j = 0; j < 16; ++j) sums[(c + j) * C::LD + i] = kt_begin < kt_end ? __uint_as_float(v[j]) : 0.f;
             }
         }
+        if constexpr (LORA) {
+            if (lane == 0) ok = ok && wait_bounded(bar_list, 0, abort_flag, p.timeout_ns, kWaitEpilogue, 0);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            const int count = ok ? *piece_count : 0;
+            for (int q = 0; q < count; q += C::SLOTS) {
+                if (lane == 0) ok = wait_bounded(bar_pfull, (q / C::SLOTS) & 1, abort_flag, p.timeout_ns, kWaitEpilogue, q);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                ptx::tcgen05_fence_after();
+                for (int s = 0; s < C::SLOTS && q + s < count; ++s) {
+                    const int j = pieces[q + s] & 0xff, n = pieces[q + s] >> 8;
+                    uint32_t v[16];
+                    ptx::tmem_ld_32x32b_x16(taddr + TN + s * C::PIECE, v);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int t = 0; t < C::PIECE; ++t) {
+                        if (t < n) sums[(j + t) * C::LD + i] += __uint_as_float(v[t]);
+                    }
+                }
+                ptx::tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar_pfree);
+            }
+        }
     }
     // ---- the cluster's sums of this CTA's share of the tile, added and stored
     ptx::tcgen05_fence_before();
@@ -245,14 +354,14 @@ __global__ void __launch_bounds__(192, 2)
     } else {
         __syncthreads();
     }
-    if (MODE == kGroupLora) ptx::griddep_wait();  // all threads: no later kernel may start before lora_down_kernel has ended
+    if (LORA) ptx::griddep_wait();  // all threads: no later kernel may start before lora_down_kernel has ended
     if (work && *abort_flag == 0) {
         // four columns i a thread and step, 32 threads a row j
         const int units = w.n * 32;
         const int first = units * rank / KS, last = units * (rank + 1) / KS;
         uint32_t peer[KS];
 #pragma unroll
-        for (int s = 0; s < KS; ++s) peer[s] = KS > 1 ? ptx::mapa(base, static_cast<uint32_t>(s)) : base;
+        for (int s = 0; s < KS; ++s) peer[s] = KS > 1 ? ptx::mapa(sums_at, static_cast<uint32_t>(s)) : sums_at;
         for (int u = first + static_cast<int>(threadIdx.x); u < last; u += C::THREADS) {
             const int j = u / 32, i = u % 32 * 4;
             const int32_t col = w.i0 + i;
@@ -261,38 +370,12 @@ __global__ void __launch_bounds__(192, 2)
             float4 part[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s) part[s] = few_sums<KS>(peer[s] + at);
-            float v[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
+            float4 v = part[0];
 #pragma unroll
-            for (int s = 1; s < KS; ++s) v[0] += part[s].x, v[1] += part[s].y, v[2] += part[s].z, v[3] += part[s].w;
-            const int64_t row = w.j0 + j;
-            if constexpr (MODE == kGroupLora) {
-                const int32_t a = chosen[j];
-                if (a >= 0) {
-                    const uint16_t *up = l.up + a * l.up_matrix + col * l.up_row;
-                    const float *h = l.h + row * p.rank;
-#pragma unroll 2
-                    for (int c = 0; c < p.rank; c += 8) {
-                        const float4 h0 = *reinterpret_cast<const float4 *>(h + c), h1 = *reinterpret_cast<const float4 *>(h + c + 4);
-                        uint4 m[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) m[q] = *reinterpret_cast<const uint4 *>(up + q * l.up_row + c);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float2 t = widen16(p.bf16, m[q].x);
-                            v[q] = fmaf(h0.x, t.x, v[q]), v[q] = fmaf(h0.y, t.y, v[q]);
-                            t = widen16(p.bf16, m[q].y);
-                            v[q] = fmaf(h0.z, t.x, v[q]), v[q] = fmaf(h0.w, t.y, v[q]);
-                            t = widen16(p.bf16, m[q].z);
-                            v[q] = fmaf(h1.x, t.x, v[q]), v[q] = fmaf(h1.y, t.y, v[q]);
-                            t = widen16(p.bf16, m[q].w);
-                            v[q] = fmaf(h1.z, t.x, v[q]), v[q] = fmaf(h1.w, t.y, v[q]);
-                        }
-                    }
-                }
-            }
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * p.out_row + col) =
-                make_uint2(pack_pair(p.bf16, __float_as_uint(v[0]), __float_as_uint(v[1])),
-                           pack_pair(p.bf16, __float_as_uint(v[2]), __float_as_uint(v[3])));
+            for (int s = 1; s < KS; ++s) v.x += part[s].x, v.y += part[s].y, v.z += part[s].z, v.w += part[s].w;
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + static_cast<int64_t>(w.j0 + j) * p.out_row + col) =
+                make_uint2(pack_pair(p.bf16, __float_as_uint(v.x), __float_as_uint(v.y)),
+                           pack_pair(p.bf16, __float_as_uint(v.z), __float_as_uint(v.w)));
         }
     }
     if constexpr (KS > 1) {
@@ -308,12 +391,16 @@ __global__ void __launch_bounds__(192, 2)
     }
 }
 
-// h[row] = scale_a * x[row] * down_a^T in fp32 for the rows with an adapter: a warp a rank,
-// of ROWS consecutive rows, of which those of one adapter share what is read of it.
+// h[row] = scale_a * x[row] * down_a^T for the rows with an adapter, as two 16-bit numbers
+// (split_16; zeros up to a whole 16 ranks).  Of ROWS consecutive rows those of one adapter
+// share what is read of it.  256 threads: two warps a rank and half of K each, four ranks
+// at a time and `each` times four a CTA.  The chain of a single token is the launch, the
+// offsets and adapters, what down holds, and the sums; x is on its way from the start.
 struct DownParams {
     const uint16_t *x, *down;
     int64_t x_row, down_row, down_matrix;
-    float *h;
+    uint16_t *h;
+    int32_t each;
 };
 
 __device__ __forceinline__ float dot_8(bool bf16, uint4 a, uint4 b, float sum) {
@@ -327,83 +414,127 @@ __device__ __forceinline__ float dot_8(bool bf16, uint4 a, uint4 b, float sum) {
     return sum;
 }
 
+constexpr int kDownRanks = 4;
+
 template <int ROWS>
 __global__ void __launch_bounds__(256) lora_down_kernel(const GroupParams p, const DownParams d) {
-    __shared__ int32_t past[ROWS];  // the first request that starts behind a row
-    const int tid = static_cast<int>(threadIdx.x), lane = tid % 32;
+    // of each row the first request that starts behind it, and that request's predecessor's adapter
+    __shared__ unsigned long long past[ROWS];
+    __shared__ float halves[kDownRanks][ROWS];
+    const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS;
-    if (tid < ROWS) past[tid] = p.groups + 1;
+    if (tid < ROWS) past[tid] = ~0ull;
     ptx::griddep_wait();
     // what follows may start: all before this kernel has completed
     if (tid == 0) ptx::griddep_launch_dependents();
-    __syncthreads();
-    int32_t least[ROWS];
+    const int half = warp / kDownRanks;
+    const int k_half = (p.R / 8 + 1) / 2 * 8;  // whole units of eight
+    const int k_begin = half * k_half, k_end = half ? p.R : k_half;
+    const uint16_t *x = d.x + first * d.x_row;
+    constexpr int U = 8;  // loads on their way at once
+    uint4 v[U];
+    if constexpr (ROWS == 1) {
 #pragma unroll
-    for (int t = 0; t < ROWS; ++t) least[t] = p.groups + 1;
+        for (int i = 0; i < U; ++i) {
+            const int k = k_begin + lane * 8 + i * 256;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (k < k_end) v[i] = *reinterpret_cast<const uint4 *>(x + k);
+        }
+    }
+    __syncthreads();
+    unsigned long long least[ROWS];
+#pragma unroll
+    for (int t = 0; t < ROWS; ++t) least[t] = ~0ull;
     for (int e = p.groups - tid; e >= 0; e -= 256) {
         const int64_t o = offset_of(p, e);
+        const uint32_t a = e > 0 ? static_cast<uint32_t>(adapter_of(p, e - 1)) : ~0u;
 #pragma unroll
         for (int t = 0; t < ROWS; ++t) {
-            if (o > first + t) least[t] = e;
+            if (o > first + t) least[t] = static_cast<unsigned long long>(e) << 32 | a;
         }
     }
 #pragma unroll
     for (int t = 0; t < ROWS; ++t) {
-        const int32_t v = __reduce_min_sync(0xffffffffu, least[t]);
-        if (lane == 0) atomicMin(&past[t], v);
+        // few threads have found one; of them the lowest
+        const uint32_t e = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(least[t] >> 32));
+        if (static_cast<uint32_t>(least[t] >> 32) == e && e != ~0u) atomicMin(&past[t], least[t]);
     }
     __syncthreads();
-    const int j = static_cast<int>(blockIdx.y) * 8 + tid / 32;
-    if (j >= p.rank) return;
     int32_t a[ROWS];
+    bool any = false;
 #pragma unroll
     for (int t = 0; t < ROWS; ++t) {
-        const int e = past[t] - 1;
-        a[t] = first + t < p.rows && e >= 0 && e < p.groups ? adapter_of(p, e) : -1;
+        // none behind it: the row is behind the last request
+        a[t] = first + t < p.rows && past[t] != ~0ull ? static_cast<int32_t>(past[t] & 0xffffffffull) : -1;
+        any = any || a[t] >= 0;
     }
-    const uint16_t *x = d.x + first * d.x_row, *down = d.down + j * d.down_row;
-    float sum[ROWS];
+    if (!any) return;
+    const int padded = (p.rank + 15) / 16 * 16;
+    for (int q = 0; q < d.each; ++q) {
+        const int j = (static_cast<int>(blockIdx.y) * d.each + q) * kDownRanks + warp % kDownRanks;
+        const uint16_t *down = d.down + j * d.down_row;
+        float sum[ROWS];
 #pragma unroll
-    for (int t = 0; t < ROWS; ++t) sum[t] = 0.f;
-    if constexpr (ROWS == 1) {
-        if (a[0] < 0) return;
-        down += a[0] * d.down_matrix;
-        constexpr int U = 8;  // loads on their way at once
-        for (int k = lane * 8; k < p.R; k += 256 * U) {
-            uint4 u[U], v[U];
+        for (int t = 0; t < ROWS; ++t) sum[t] = 0.f;
+        if constexpr (ROWS == 1) {
+            if (j < p.rank) {
+                down += a[0] * d.down_matrix;
+                for (int k = k_begin + lane * 8; k < k_end; k += 256 * U) {
+                    uint4 u[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                u[i] = v[i] = make_uint4(0, 0, 0, 0);
-                if (k + i * 256 < p.R) {
-                    u[i] = load_unit(down + k + i * 256);
-                    v[i] = *reinterpret_cast<const uint4 *>(x + k + i * 256);
+                    for (int i = 0; i < U; ++i) {
+                        u[i] = make_uint4(0, 0, 0, 0);
+                        if (k + i * 256 < k_end) u[i] = load_unit(down + k + i * 256);
+                    }
+                    if (k_end - k_begin > 256 * U) {  // v holds the first 256 U of x only where there are no more
+#pragma unroll
+                        for (int i = 0; i < U; ++i) {
+                            v[i] = make_uint4(0, 0, 0, 0);
+                            if (k + i * 256 < k_end) v[i] = *reinterpret_cast<const uint4 *>(x + k + i * 256);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < U; ++i) sum[0] = dot_8(p.bf16, u[i], v[i], sum[0]);
                 }
             }
+        } else if (j < p.rank) {
+#pragma unroll 1
+            for (int k = k_begin + lane * 8; k < k_end; k += 256) {
+                uint4 m[ROWS], w[ROWS];
 #pragma unroll
-            for (int i = 0; i < U; ++i) sum[0] = dot_8(p.bf16, u[i], v[i], sum[0]);
-        }
-    } else {
-        for (int k = lane * 8; k < p.R; k += 256) {
-            uint4 m = make_uint4(0, 0, 0, 0), v[ROWS];
+                for (int t = 0; t < ROWS; ++t) {
+                    w[t] = m[t] = make_uint4(0, 0, 0, 0);
+                    if (a[t] < 0) continue;
+                    w[t] = *reinterpret_cast<const uint4 *>(x + t * d.x_row + k);
+                    if (t > 0 && a[t] == a[t - 1]) {
+                        m[t] = m[t - 1];
+                    } else {
+                        m[t] = *reinterpret_cast<const uint4 *>(down + a[t] * d.down_matrix + k);
+                    }
+                }
 #pragma unroll
-            for (int t = 0; t < ROWS; ++t) {
-                v[t] = make_uint4(0, 0, 0, 0);
-                if (a[t] >= 0) v[t] = *reinterpret_cast<const uint4 *>(x + t * d.x_row + k);
+                for (int t = 0; t < ROWS; ++t) {
+                    if (a[t] >= 0) sum[t] = dot_8(p.bf16, m[t], w[t], sum[t]);
+                }
             }
+        }
+#pragma unroll
+        for (int t = 0; t < ROWS; ++t) {
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
+            if (half && lane == 0) halves[warp % kDownRanks][t] = sum[t];
+        }
+        __syncthreads();
+        if (!half && lane == 0 && j < padded) {
 #pragma unroll
             for (int t = 0; t < ROWS; ++t) {
                 if (a[t] < 0) continue;
-                if (t == 0 || a[t] != a[t - 1]) m = *reinterpret_cast<const uint4 *>(down + a[t] * d.down_matrix + k);
-                sum[t] = dot_8(p.bf16, m, v[t], sum[t]);
+                const float h = j < p.rank ? (sum[t] + halves[warp][t]) * (p.scales ? p.scales[a[t]] : 1.f) : 0.f;
+                uint16_t *to = d.h + (first + t) * (2 * p.rank_pad) + j;
+                split_16(p.bf16, h, to, to + p.rank_pad);
             }
         }
-    }
-#pragma unroll
-    for (int t = 0; t < ROWS; ++t) {
-        float v = sum[t];
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0 && a[t] >= 0) d.h[(first + t) * p.rank + j] = v * (p.scales ? p.scales[a[t]] : 1.f);
+        __syncthreads();
     }
 }
 

@@ -102,12 +102,18 @@ int launch_tile(const Call &c) {
     CUtensorMap tmP = {}, tmQ = {}, tmD = {}, tmU = {}, tmH = {};  // P's and Q's are not used by sums of nothing
     if (MODE != kGroupDown && !encode(&tmD, c.D, 32)) return GEMM_ERR_CUDA;
     if (MODE == kGroupLora && p.groups > 0) {
-        if (!encode(&tmU, c.U, 128) || !encode(&tmH, c.H, TN / CG)) return GEMM_ERR_CUDA;
+        if (!encode(&tmU, c.U, 128) || !encode(&tmH, c.H, C::Q_BOX)) return GEMM_ERR_CUDA;
     }
     if (groups > 0 && c.P.rows > 0 && c.P.cols > 0 && c.Q.rows > 0 && c.Q.cols > 0) {
         const uint32_t p_rows = MODE == kGroupDown ? static_cast<uint32_t>(p.rank) : (MODE == kGroupNN || MODE == kGroupTN ? 64 : 128);
-        if (!encode(&tmP, c.P, p_rows) || !encode(&tmQ, c.Q, MODE == kGroupTN ? 64 : TN / CG)) {
+        if (!encode(&tmP, c.P, p_rows) || !encode(&tmQ, c.Q, C::Q_BOX)) {
             return GEMM_ERR_CUDA;
+        }
+    }
+    GroupTails<MODE> tails = {};
+    if constexpr (MODE == kGroupTN) {
+        for (uint32_t k = 0; k < 5 && p.rows > 0; ++k) {
+            if (!encode(&tails.P[k], c.P, 1u << k) || !encode(&tails.Q[k], c.Q, 1u << k)) return GEMM_ERR_CUDA;
         }
     }
     int64_t grid = c.sms / CG;
@@ -138,15 +144,15 @@ int launch_tile(const Call &c) {
     if (!p.zero_rest && most < grid) grid = most;
     if (c.max_clusters > 0 && c.max_clusters < grid) grid = c.max_clusters;
     if (grid == 0) return GEMM_OK;
-    return launch_cluster(kernel, CG * grid, C::THREADS, CG, C::SMEM_ALLOC, c.stream, tmP, tmQ, tmD, tmU, tmH, p);
+    return launch_cluster(kernel, CG * grid, C::THREADS, CG, C::SMEM_ALLOC, c.stream, tmP, tmQ, tmD, tmU, tmH, tails, p);
 }
 
 template <int TN, int KS, int MODE>
-int launch_few(const Call &c, const LoraParams &l) {
-    using C = FewShape<TN>;
+int launch_few(const Call &c) {
+    using C = FewShape<TN, MODE == kGroupLora>;
     auto *kernel = grouped_few_kernel<TN, KS, MODE>;
     static std::atomic<uint64_t> done{0};
-    if (!allow_smem(kernel, C::SMEM_ALLOC, done)) return GEMM_ERR_CUDA;
+    if (!allow_smem(kernel, C::smem(C::ALONE), done)) return GEMM_ERR_CUDA;
     GroupParams p = c.p;
     const int64_t i_tiles = (static_cast<int64_t>(p.I) + 127) / 128;
     const int64_t some = p.groups < p.rows ? p.groups : p.rows;
@@ -154,31 +160,36 @@ int launch_few(const Call &c, const LoraParams &l) {
                                             : (static_cast<int64_t>(p.rows) / TN + some) * i_tiles;
     if (most * KS > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
     p.i_tiles = static_cast<int32_t>(i_tiles);
-    CUtensorMap tmP = {}, tmQ = {};  // not used by sums of nothing
+    CUtensorMap tmP = {}, tmQ = {}, tmU = {}, tmH = {};  // not used by sums of nothing
     if (c.P.rows > 0 && c.P.cols > 0 && c.Q.rows > 0 && c.Q.cols > 0) {
         if (!encode(&tmP, c.P, MODE == kGroupNN ? 64 : 128) || !encode(&tmQ, c.Q, TN)) return GEMM_ERR_CUDA;
     }
+    if (MODE == kGroupLora && p.groups > 0) {
+        if (!encode(&tmU, c.U, 128) || !encode(&tmH, c.H, C::PIECE)) return GEMM_ERR_CUDA;
+    }
     const int64_t tiles = most > 0 ? most : 1;  // one for the rows without a group
-    return launch_cluster(kernel, KS * tiles, C::THREADS, KS, C::SMEM_ALLOC, c.stream, tmP, tmQ, p, l);
+    const int stages = MODE == kGroupLora || KS * tiles <= c.sms ? C::ALONE : C::PAIRED;
+    return launch_cluster(kernel, KS * tiles, C::THREADS, KS, static_cast<size_t>(C::smem(stages)), c.stream, tmP, tmQ, tmU, tmH, p,
+                          stages);
 }
 
 template <int TN, int MODE>
-int launch_split(const Call &c, const LoraParams &l, int split) {
+int launch_split(const Call &c, int split) {
     switch (split) {
-        case 8: return launch_few<TN, 8, MODE>(c, l);
-        case 4: return launch_few<TN, 4, MODE>(c, l);
-        case 2: return launch_few<TN, 2, MODE>(c, l);
-        default: return launch_few<TN, 1, MODE>(c, l);
+        case 8: return launch_few<TN, 8, MODE>(c);
+        case 4: return launch_few<TN, 4, MODE>(c);
+        case 2: return launch_few<TN, 2, MODE>(c);
+        default: return launch_few<TN, 1, MODE>(c);
     }
 }
 
 template <int MODE>
-int launch_few_mode(const Call &c, const LoraParams &l, int tile, int split) {
+int launch_few_mode(const Call &c, int tile, int split) {
     switch (tile) {
-        case 16: return launch_split<16, MODE>(c, l, split);
-        case 32: return launch_split<32, MODE>(c, l, split);
-        case 64: return launch_split<64, MODE>(c, l, split);
-        default: return launch_split<128, MODE>(c, l, split);
+        case 16: return launch_split<16, MODE>(c, split);
+        case 32: return launch_split<32, MODE>(c, split);
+        case 64: return launch_split<64, MODE>(c, split);
+        default: return launch_split<128, MODE>(c, split);
     }
 }
 
@@ -187,11 +198,11 @@ struct Choice {
     int tile, split;
 };
 
-// CTAs that share a tile's sum: the most of 8, 4 and 2 that keep two CTAs an SM and leave
-// each four K tiles.
+// CTAs that share a tile's sum: the most of 8, 4 and 2 that have an SM each and two K
+// tiles.
 int split_of(int64_t tiles, int64_t k_tiles, int sms) {
     for (int ks = 8; ks > 1; ks /= 2) {
-        if (tiles * ks <= 2 * sms && k_tiles >= 4 * ks) return ks;
+        if (tiles * ks <= sms && k_tiles >= 2 * ks) return ks;
     }
     return 1;
 }
@@ -218,7 +229,7 @@ Choice choose(int mode, const GroupParams &p, int sms, const grouped_options &o)
 template <int MODE>
 int launch_mode(const Call &c, const Choice &how) {
     if constexpr (MODE != kGroupTN) {
-        if (how.split > 0) return launch_few_mode<MODE>(c, {}, how.tile, how.split);
+        if (how.split > 0) return launch_few_mode<MODE>(c, how.tile, how.split);
         if (how.tile == 32) return launch_tile<1, 32, MODE>(c);
     }
     switch (how.tile) {
@@ -330,10 +341,18 @@ struct Lora {
     void *workspace;
 };
 
+// x, W, up and h as the product's launch takes them.
+void lora_operands(Call &c, const Lora &l) {
+    c.P = l.W;
+    c.Q = l.x;
+    c.D = l.D;
+    c.U = l.up;
+    c.H = {l.workspace, l.rows, 2 * c.p.rank_pad, 2 * c.p.rank_pad, 0, 0};
+}
+
 // Requests of many rows: tiles of one request each, the adapter as more of the sum.
 int lora_long(Call &c, const Lora &l) {
     GroupParams &p = c.p;
-    p.rank_pad = static_cast<int32_t>((l.rank + 63) / 64 * 64);
     if (p.groups > 0) {
         Call d = c;
         d.P = l.down;
@@ -346,32 +365,30 @@ int lora_long(Call &c, const Lora &l) {
         if (st != GEMM_OK) return st;
         p.follows = 1;
     }
-    c.P = l.W;
-    c.Q = l.x;
-    c.D = l.D;
-    c.U = l.up;
-    c.H = {l.workspace, l.rows, 2 * p.rank_pad, 2 * p.rank_pad, 0, 0};
+    lora_operands(c, l);
     return launch_tile<2, 256, kGroupLora>(c);
 }
 
-// Requests of few rows: tiles of any rows, each row's adapter added behind the sum.
+// Requests of few rows: tiles of any rows, the adapters piece by piece.
 int lora_short(Call &c, const Lora &l, const Choice &how) {
     GroupParams &p = c.p;
     if (p.groups > 0) {
+        const int64_t fours = (l.rank + 15) / 16 * 16 / kDownRanks;
+        const bool one = l.rows <= 256;
+        // a wave of CTAs, with as few ranks each as that allows
+        const int64_t ctas = one ? l.rows : (l.rows + 7) / 8;
+        int64_t each = 1;
+        while (each < fours && ctas * ((fours + each - 1) / each) > 2 * c.sms) each *= 2;
         const DownParams d = {static_cast<const uint16_t *>(l.x.ptr), static_cast<const uint16_t *>(l.down.ptr), l.x.stride,
-                              l.down.stride, l.down.depth_stride, static_cast<float *>(l.workspace)};
-        const unsigned ranks = static_cast<unsigned>((l.rank + 7) / 8);
-        const int st = l.rows <= 256
-                           ? launch(lora_down_kernel<1>, dim3(static_cast<unsigned>(l.rows), ranks), dim3(256), 0, c.stream, p, d)
-                           : launch(lora_down_kernel<8>, dim3(static_cast<unsigned>((l.rows + 7) / 8), ranks), dim3(256), 0, c.stream, p, d);
+                              l.down.stride, l.down.depth_stride, static_cast<uint16_t *>(l.workspace), static_cast<int32_t>(each)};
+        const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>((fours + each - 1) / each));
+        const int st = one ? launch(lora_down_kernel<1>, grid, dim3(256), 0, c.stream, p, d)
+                           : launch(lora_down_kernel<8>, grid, dim3(256), 0, c.stream, p, d);
         if (st != GEMM_OK) return st;
         p.follows = 1;
     }
-    c.P = l.W;
-    c.Q = l.x;
-    const LoraParams lp = {static_cast<const float *>(l.workspace), static_cast<const uint16_t *>(l.up.ptr), l.up.stride,
-                           l.up.depth_stride};
-    return launch_few_mode<kGroupLora>(c, lp, how.tile, how.split);
+    lora_operands(c, l);
+    return launch_few_mode<kGroupLora>(c, how.tile, how.split);
 }
 
 }  // namespace
@@ -405,7 +422,7 @@ int grouped_gemm_tn(const void *dD, int64_t ldd, const void *A, int64_t lda, con
 int64_t gemm_lora_workspace_size(int64_t rows, int64_t rank) {
     if (rows < 0 || rank < 0) return GEMM_ERR_INVALID_ARG;
     if (rows > kMaxDim || rank > kMaxRank || rank % 8 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
-    return rows * ((rank + 63) / 64 * 64) * 4;  // fp32, or two 16-bit numbers
+    return rows * ((rank + 63) / 64 * 64) * 4;  // two 16-bit numbers
 }
 
 int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const void *down, int64_t ld_down,
@@ -484,6 +501,7 @@ int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const v
     p.scales = scales;
     p.adapter_count = static_cast<int32_t>(adapter_count);
     p.rank = static_cast<int32_t>(rank);
+    p.rank_pad = static_cast<int32_t>((rank + 63) / 64 * 64);
     p.debug_flags = static_cast<uint32_t>(o.debug_flags);
     p.timeout_ns = static_cast<uint64_t>(o.timeout_ns);
     if (rows == 1) l.x.stride = 0;

@@ -20,11 +20,13 @@
 // that a tile loaded with its own are other columns of the accumulator and are not
 // stored.
 //
-// The ragged axis of TN is summed over: rows of the next group that came with a
-// group's last K tile must not count, whatever they hold (zeros by mask times an
-// infinity would be NaN), so a warp of its own overwrites them with zeros in shared
-// memory, between the load's arrival and the MMA.  At most 15 rows: the MMAs go in
-// steps of 16.
+// The ragged axis of TN is summed over: rows of the next group must not count with a
+// group's last ones, whatever they hold (zeros by mask times an infinity would be NaN).
+// The MMAs go in steps of 16 rows, so a last K tile that is no whole number of steps is
+// loaded in boxes of 16, 8, 4, 2 and 1 rows, and the rest of its last step, in such boxes
+// too, from behind the matrix, where the copy engine fills zeros.  (Cleared by a warp in
+// shared memory, between the load's arrival and the MMA, they came too late: 8 groups of
+// 1025 rows, 4096 x 4096, took 189 us, of 1024 153; so TAIL_US.)
 //
 // LORA and DOWN are the two launches of low-rank adapters beside a shared product, with
 // the rows of a request as a group.  DOWN leaves h = scale_a * x * down_a^T as two
@@ -38,8 +40,9 @@
 // over all groups; each CTA reads the offsets once and keeps the groups' first rows
 // and first tiles in shared memory, so the host needs to know no offset.
 //
-// Warps: 0 TMA producer, 1 MMA issuer and TMEM allocator, 2 reads the offsets and
-// clears the rows behind a group's end (TN), 4-7 epilogue.
+// Warps: 0 TMA producer, 1 MMA issuer and TMEM allocator, 2 lists the groups, 4-7 and
+// 8-11 epilogue: two teams that take turns at
+// 32 columns of the accumulator, as a team's way from TMEM to the store is latency.
 #pragma once
 
 #include "../schedule.h"
@@ -74,10 +77,6 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-
-// Makes this thread's ordinary shared-memory writes visible to the async proxy, the
-// peer CTA's MMAs among it.
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // 16 TMEM lanes x 32 columns of 32 bits: thread t gets of lane t / 4 and columns 8 n + 2 (t % 4),
 // + 1 registers 4 n and 4 n + 1, of lane t / 4 + 8 registers 4 n + 2 and 4 n + 3.
@@ -142,27 +141,29 @@ struct GroupShape {
     static constexpr int P_BYTES = 128 * 128;
     static constexpr int Q_BYTES = Q_ROWS * 128;
     static constexpr int STAGE = P_BYTES + Q_BYTES;
-    static constexpr uint32_t TX = STAGE * CG;
-    static constexpr int STAGES = 196608 / STAGE < 9 ? 196608 / STAGE : 9;
+    // Q comes in boxes of so many rows, as many as a tile's columns need
+    static constexpr int Q_BOX = MODE == kGroupTN ? 64 : (Q_ROWS < 32 ? Q_ROWS : 32);
     static constexpr int TMEM_COLS = 2 * TN;
-    // The epilogue's staging: buffers of 32 rows j of 128 elements, as two boxes of 64 with
-    // the 128-byte swizzle.
+    // The epilogue's staging: of each team a buffer of 32 rows j of 128 elements, as two
+    // boxes of 64 with the 128-byte swizzle.
     static constexpr int BOX = 32 * 128;
     static constexpr int BUF = 2 * BOX;
     static constexpr bool ADAPTERS = MODE == kGroupLora || MODE == kGroupDown;
-    static constexpr int BUFS = ADAPTERS ? 2 : 3;
+    static constexpr int LIST = 4 * (GROUPED_MAX_GROUPS + 4);  // int32 of each group, and its end
+    static constexpr int REST = 2 * BUF + (ADAPTERS ? 3 : 2) * LIST + 1024 + 512;
+    static constexpr int STAGES = (232448 - REST) / STAGE < 9 ? (232448 - REST) / STAGE : 9;
     static constexpr int OFF_P = 0;
     static constexpr int OFF_Q = OFF_P + STAGES * P_BYTES;
     static constexpr int OFF_D = OFF_Q + STAGES * Q_BYTES;
-    static constexpr int OFF_START = OFF_D + BUFS * BUF;                     // int32 [groups + 1]
-    static constexpr int OFF_TILES = OFF_START + 4 * (GROUPED_MAX_GROUPS + 4);  // int32 [groups + 1]
-    static constexpr int OFF_CHOSEN = OFF_TILES + 4 * (GROUPED_MAX_GROUPS + 4);  // the groups' adapters, -1 without
-    static constexpr int OFF_BAR = OFF_CHOSEN + (ADAPTERS ? 4 * (GROUPED_MAX_GROUPS + 4) : 0);
-    // full, empty, land, peer [STAGES]; accumulator full, empty [2]; drain
-    static constexpr int OFF_MISC = OFF_BAR + (4 * STAGES + 5) * 8;
-    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 896;                 // from a multiple of 128 bytes to one of 1024
-    static constexpr int THREADS = 256;
-    static_assert(OFF_BAR % 8 == 0 && SMEM_ALLOC <= 232448, "227 KiB");
+    static constexpr int OFF_START = OFF_D + 2 * BUF;
+    static constexpr int OFF_TILES = OFF_START + LIST;
+    static constexpr int OFF_CHOSEN = OFF_TILES + LIST;  // the groups' adapters, -1 without
+    static constexpr int OFF_BAR = OFF_CHOSEN + (ADAPTERS ? LIST : 0);
+    // full, empty [STAGES]; accumulator full, empty [2]; drain
+    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 5) * 8;
+    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 896;  // from a multiple of 128 bytes to one of 1024
+    static constexpr int THREADS = 384;
+    static_assert(STAGES >= 4 && OFF_BAR % 8 == 0 && SMEM_ALLOC <= 232448, "227 KiB");
     static_assert((CG == 2 && TN == 256) || (CG == 1 && (TN == 32 || TN == 64 || TN == 128)), "tile");
     static_assert(MODE != kGroupTN || Q_ROWS % 64 == 0, "MN-major blocks of 64");
 };
@@ -326,11 +327,19 @@ __device__ __forceinline__ void split_16(bool bf16, float h, uint16_t *high, uin
     *low = static_cast<uint16_t>(b);
 }
 
+// TN: P's and Q's maps with boxes of 2^k rows.
+template <int MODE>
+struct GroupTails {};
+template <>
+struct GroupTails<kGroupTN> {
+    CUtensorMap P[5], Q[5];
+};
+
 template <int CG, int TN, int MODE>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(384, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                    const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmU,
-                   const __grid_constant__ CUtensorMap tmH, const GroupParams p) {
+                   const __grid_constant__ CUtensorMap tmH, const __grid_constant__ GroupTails<MODE> tails, const GroupParams p) {
     using C = GroupShape<CG, TN, MODE>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -343,9 +352,7 @@ __global__ void __launch_bounds__(256, 1)
     const int cluster = static_cast<int>(blockIdx.x) / CG, clusters = static_cast<int>(gridDim.x) / CG;
 
     const uint32_t bar_full = base + C::OFF_BAR, bar_empty = bar_full + 8 * C::STAGES;
-    const uint32_t bar_land = bar_empty + 8 * C::STAGES;  // TN: a group's last K tile, in this CTA
-    const uint32_t bar_peer = bar_land + 8 * C::STAGES;   // TN: the same, cleared, in the peer
-    const uint32_t bar_tfull = bar_peer + 8 * C::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
+    const uint32_t bar_tfull = bar_empty + 8 * C::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     int32_t *start = reinterpret_cast<int32_t *>(smem + C::OFF_START);
@@ -355,12 +362,10 @@ __global__ void __launch_bounds__(256, 1)
         for (int s = 0; s < C::STAGES; ++s) {
             ptx::mbar_init(bar_full + 8 * s, 1);
             ptx::mbar_init(bar_empty + 8 * s, 1);
-            ptx::mbar_init(bar_land + 8 * s, 1);
-            ptx::mbar_init(bar_peer + 8 * s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(bar_tfull + 8 * a, 1);
-            ptx::mbar_init(bar_tempty + 8 * a, 4 * CG);  // the epilogue warps of all the tile's CTAs
+            ptx::mbar_init(bar_tempty + 8 * a, 8 * CG);  // the epilogue warps of all the tile's CTAs
         }
         ptx::mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -405,6 +410,9 @@ __global__ void __launch_bounds__(256, 1)
                 const GroupTile w = tile_of(t);
                 const int k_tiles = (w.r + 63) / 64, all_tiles = k_tiles + rank_tiles(w);
                 const int32_t i0 = w.i0 + rank * 128, j0 = w.j0 + rank * (columns_of(w) / 2);
+                const int boxes = (columns_of(w) / CG + C::Q_BOX - 1) / C::Q_BOX;  // of Q, in each CTA
+                // of DOWN's P only the ranks that there are
+                const uint32_t bytes = (MODE == kGroupDown ? p.rank * 128u : C::P_BYTES) + static_cast<uint32_t>(boxes * C::Q_BOX) * 128u;
                 for (int kt = 0; kt < all_tiles; ++kt) {
                     if (!wait_bounded(bar_empty + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns,
                                       kWaitProducer, seq)) {
@@ -414,21 +422,12 @@ __global__ void __launch_bounds__(256, 1)
                     const int s = ring.stage, r = kt * 64;
                     const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, sq = base + C::OFF_Q + s * C::Q_BYTES;
                     uint32_t full = bar_full + 8 * s;
-                    if (MODE == kGroupTN && kt == k_tiles - 1 && w.r % 16 != 0) {
-                        // through the warp that clears the rows behind the group's end
-                        const uint32_t land = bar_land + 8 * s;
-                        ptx::mbar_arrive_expect_tx(land, C::STAGE);
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) ptx::tma_load_2d(sp + b * 8192, &tmP, land, i0 + 64 * b, w.r0 + r);
-#pragma unroll
-                        for (int b = 0; b < C::Q_ROWS / 64; ++b) {
-                            ptx::tma_load_2d(sq + b * 8192, &tmQ, land, j0 + 64 * b, w.r0 + r);
-                        }
-                        ring.advance();
-                        continue;
+                    const int rows = w.r - r;  // of a last K tile (TN)
+                    const bool tail = MODE == kGroupTN && rows < 64 && rows % 16 != 0;
+                    const int steps = (rows + 15) / 16 * 16;
+                    if (leader) {
+                        ptx::mbar_arrive_expect_tx(full, CG * (tail ? static_cast<uint32_t>(steps * 128 * (2 + boxes)) : bytes));
                     }
-                    // of DOWN's P only the ranks that there are
-                    if (leader) ptx::mbar_arrive_expect_tx(full, MODE == kGroupDown ? p.rank * 128u + C::Q_BYTES : C::TX);
                     if constexpr (CG == 2) full = ptx::mapa(full, 0);
                     auto load_2d = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y) {
                         if constexpr (CG == 2) {
@@ -437,6 +436,24 @@ __global__ void __launch_bounds__(256, 1)
                             ptx::tma_load_2d(dst, map, full, x, y);
                         }
                     };
+                    if constexpr (MODE == kGroupTN) {
+                        if (tail) {
+                            auto load_rows = [&](int k, int row, int32_t y) {  // 2^k rows from `row` on
+                                for (int b = 0; b < 2; ++b) load_2d(sp + b * 8192 + row * 128, &tails.P[k], i0 + 64 * b, y);
+                                for (int b = 0; b < boxes; ++b) load_2d(sq + b * 8192 + row * 128, &tails.Q[k], j0 + 64 * b, y);
+                            };
+                            int row = 0;
+                            for (; rows - row >= 16; row += 16) load_rows(4, row, w.r0 + r + row);
+                            for (int k = 3, left = rows - row; k >= 0; --k) {
+                                if (left >> k & 1) load_rows(k, row, w.r0 + r + row), row += 1 << k;
+                            }
+                            for (int k = 0, left = steps - row; k < 4; ++k) {
+                                if (left >> k & 1) load_rows(k, row, p.rows), row += 1 << k;
+                            }
+                            ring.advance();
+                            continue;
+                        }
+                    }
                     auto load_3d = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
                         if constexpr (CG == 2) {
                             ptxg::tma_load_3d_pair(dst, map, full, x, y, z);
@@ -450,7 +467,7 @@ __global__ void __launch_bounds__(256, 1)
                             waited = true;
                             const int32_t c = (kt - k_tiles) / 2 * 64, rest = (kt - k_tiles) % 2 * p.rank_pad;
                             load_3d(sp, &tmU, c, i0, chosen[w.group]);
-                            load_2d(sq, &tmH, rest + c, j0);
+                            for (int b = 0; b < boxes; ++b) load_2d(sq + b * C::Q_BOX * 128, &tmH, rest + c, j0 + b * C::Q_BOX);
                             ring.advance();
                             continue;
                         }
@@ -466,11 +483,12 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
                         for (int b = 0; b < 2; ++b) load_2d(sp + b * 8192, &tmP, i0 + 64 * b, w.r0 + r);
                     }
-                    if constexpr (MODE != kGroupTN) {
-                        load_2d(sq, &tmQ, r, j0);
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < C::Q_ROWS / 64; ++b) load_2d(sq + b * 8192, &tmQ, j0 + 64 * b, w.r0 + r);
+                    for (int b = 0; b < boxes; ++b) {
+                        if constexpr (MODE != kGroupTN) {
+                            load_2d(sq + b * C::Q_BOX * 128, &tmQ, r, j0 + b * C::Q_BOX);
+                        } else {
+                            load_2d(sq + b * 8192, &tmQ, j0 + 64 * b, w.r0 + r);
+                        }
                     }
                     ring.advance();
                 }
@@ -529,73 +547,29 @@ __global__ void __launch_bounds__(256, 1)
             wait_bounded(bar_drain, 0, abort_flag, p.timeout_ns, kWaitMma, 0xFFFFFFFFu, false);
         }
         __syncwarp();
-    } else if (warp == 2) {
-        if constexpr (MODE == kGroupTN) {
-            int stage = 0;
-            uint32_t phases = 0, seq = 0;  // of the landing barriers, a bit a stage
-            for (int t = cluster; t < total; t += clusters, ++seq) {
-                const GroupTile w = tile_of(t);
-                const int k_tiles = (w.r + 63) / 64;
-                if (k_tiles == 0) continue;
-                const int s = (stage + k_tiles - 1) % C::STAGES;
-                stage = (s + 1) % C::STAGES;
-                if (w.r % 16 == 0) continue;
-                bool ok = true;
-                if (lane == 0) {
-                    ok = wait_bounded(bar_land + 8 * s, phases >> s & 1u, abort_flag, p.timeout_ns,
-                                      kWaitProducer, seq);
-                }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
-                const int first = w.r - (k_tiles - 1) * 64, last = (first + 15) / 16 * 16;
-                const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, sq = base + C::OFF_Q + s * C::Q_BYTES;
-                for (int row = first; row < last; ++row) {  // 128 bytes of each block of 64
-                    for (int u = lane; u < 16; u += 32) {
-                        ptx::st_shared_v4(sp + (u / 8) * 8192 + row * 128 + u % 8 * 16, 0, 0, 0, 0);
-                    }
-                    for (int u = lane; u < C::Q_ROWS / 8; u += 32) {
-                        ptx::st_shared_v4(sq + (u / 8) * 8192 + row * 128 + u % 8 * 16, 0, 0, 0, 0);
-                    }
-                }
-                ptxg::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2 && !leader) {
-                        ptx::mbar_arrive_cluster(ptx::mapa(bar_peer + 8 * s, 0));
-                    } else {
-                        if constexpr (CG == 2) {
-                            ok = wait_bounded<true>(bar_peer + 8 * s, phases >> s & 1u, abort_flag, p.timeout_ns,
-                                                    kWaitProducer, seq);
-                        }
-                        if (ok) ptx::mbar_arrive(bar_full + 8 * s);
-                    }
-                }
-                phases ^= 1u << s;
-            }
-            __syncwarp();
-        }
     } else if (warp >= 4) {
-        const int quarter = warp - 4;
+        const int quarter = warp % 4, team = (warp - 4) / 4;
         const uint32_t tempty = CG == 2 ? ptx::mapa(bar_tempty, 0) : bar_tempty;
-        const int tid = static_cast<int>(threadIdx.x) - 128;
+        const int tid = static_cast<int>(threadIdx.x) % 128;  // in the team
+        const uint32_t barrier = 1u + static_cast<uint32_t>(team);
         uint16_t *out = static_cast<uint16_t *>(p.out);
         const uint4 none = make_uint4(0, 0, 0, 0);
         if ((MODE == kGroupNT || MODE == kGroupNN) && p.zero_rest) {  // rows without a group: 16-byte units, a warp a row
             const int32_t head = start[0], rest = head + p.rows - start[p.groups];
-            for (int32_t k = static_cast<int32_t>(blockIdx.x) * 4 + quarter; k < rest; k += static_cast<int32_t>(gridDim.x) * 4) {
+            for (int32_t k = static_cast<int32_t>(blockIdx.x) * 8 + (warp - 4); k < rest; k += static_cast<int32_t>(gridDim.x) * 8) {
                 uint16_t *row = out + static_cast<int64_t>(k < head ? k : start[p.groups] + (k - head)) * p.out_row;
                 for (int32_t u = lane * 8; u < p.I; u += 256) *reinterpret_cast<uint4 *>(row + u) = none;
             }
         }
         PipelineState acc(2, 0u);
-        uint32_t seq = 0, turn = 0;  // tiles, chunks
+        uint32_t seq = 0;
         for (int t = cluster; t < total; t += clusters, ++seq) {
             const GroupTile w = tile_of(t);
             const int32_t i0 = w.i0 + rank * 128;
             const int32_t width = p.I - i0 < 128 ? p.I - i0 : 128;  // of this CTA's columns
             uint16_t *at = out + (MODE == kGroupTN ? w.group * p.out_group : 0) + static_cast<int64_t>(w.j0) * p.out_row + i0;
             if (w.r == 0) {  // a sum of nothing
-                for (int32_t j = tid / 16; j < w.n; j += 8) {
+                for (int32_t j = team * 8 + tid / 16; j < w.n; j += 16) {
                     if (tid % 16 * 8 < width) *reinterpret_cast<uint4 *>(at + j * p.out_row + tid % 16 * 8) = none;
                 }
                 continue;
@@ -605,7 +579,7 @@ __global__ void __launch_bounds__(256, 1)
                 failed = !wait_bounded(bar_tfull + 8 * acc.stage, acc.phase, abort_flag, p.timeout_ns,
                                        kWaitEpilogue, seq);
             }
-            if (ptxg::any_of_128(1, failed)) break;  // all four warps or none
+            if (ptxg::any_of_128(barrier, failed)) break;  // all four warps or none
             ptx::tcgen05_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc.stage * TN);
             const int chunks = (w.n + 31) / 32;
@@ -615,7 +589,7 @@ __global__ void __launch_bounds__(256, 1)
                 const float scale = p.scales ? p.scales[chosen[w.group]] : 1.f;
                 uint16_t *to = out + static_cast<int64_t>(w.j0) * p.out_row + i;
 #pragma unroll 1
-                for (int c = 0; c < chunks && quarter * 32 < padded; ++c) {
+                for (int c = team; c < chunks && quarter * 32 < padded; c += 2) {
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(taddr + c * 32, v);
                     ptx::tmem_wait_ld();
@@ -634,13 +608,7 @@ __global__ void __launch_bounds__(256, 1)
                 if (lane == 0) ptx::mbar_arrive(tempty + 8 * acc.stage);
                 acc.advance();
             } else {
-#pragma unroll 1
-            for (int c = 0; c < chunks; ++c, ++turn) {
-                uint32_t lo[16], hi[16];
-                ptxg::tmem_ld_16x256b_x4(taddr + c * 32, lo);
-                ptxg::tmem_ld_16x256b_x4(taddr + (16u << 16) + c * 32, hi);
-                ptx::tmem_wait_ld();
-                if (c == chunks - 1) {  // the accumulator is read: the next tile but one may have it
+                auto hand_over = [&] {  // the accumulator is read: the next tile but one may have it
                     ptx::tcgen05_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -650,10 +618,18 @@ __global__ void __launch_bounds__(256, 1)
                             ptx::mbar_arrive(tempty + 8 * acc.stage);
                         }
                     }
-                }
-                const uint32_t buf = base + C::OFF_D + turn % C::BUFS * C::BUF;
-                if (tid == 0) ptx::bulk_wait_group_read<C::BUFS - 1>();  // what was in the buffer has left it
-                ptxg::sync_128(1);
+                };
+                if (chunks <= team) hand_over();
+#pragma unroll 1
+            for (int c = team; c < chunks; c += 2) {
+                uint32_t lo[16], hi[16];
+                ptxg::tmem_ld_16x256b_x4(taddr + c * 32, lo);
+                ptxg::tmem_ld_16x256b_x4(taddr + (16u << 16) + c * 32, hi);
+                ptx::tmem_wait_ld();
+                if (c + 2 >= chunks) hand_over();
+                const uint32_t buf = base + C::OFF_D + team * C::BUF;
+                if (tid == 0) ptx::bulk_wait_group_read<0>();  // what was in the buffer has left it
+                ptxg::sync_128(barrier);
                 // lane l: row l % 8 of matrix l / 8 (columns 8 (n + l / 16) on, lanes 8 (l / 8 % 2) on);
                 // 16-byte unit u of row j lies at u ^ j % 8
                 const uint32_t own = buf + static_cast<uint32_t>(quarter >> 1) * C::BOX +
@@ -674,7 +650,7 @@ __global__ void __launch_bounds__(256, 1)
                 const int32_t rows = w.n - c * 32;  // of the chunk that count
                 if (MODE == kGroupTN || rows >= 32) {
                     ptx::fence_proxy_async_smem();
-                    ptxg::sync_128(1);
+                    ptxg::sync_128(barrier);
                     if (tid == 0) {
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
@@ -688,7 +664,7 @@ __global__ void __launch_bounds__(256, 1)
                     }
                 } else {
                     // the rows behind a group's end belong to the next
-                    ptxg::sync_128(1);
+                    ptxg::sync_128(barrier);
                     for (int32_t u = tid; u < rows * 16; u += 128) {
                         const int32_t j = u / 16, x = u % 16;
                         if (x * 8 >= width) continue;

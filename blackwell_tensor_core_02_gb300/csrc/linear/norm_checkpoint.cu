@@ -195,58 +195,61 @@ struct RestoreArgs {
     int32_t rows, cols, blocks;
 };
 
-// A thread has the same columns of every gridDim.y-th row (blockDim.y rows a CTA): 8 of
-// them in rows of whole units, else one.
-template <typename T, typename W, bool WIDE>
+// A thread has the same N columns of every gridDim.y-th row (blockDim.y rows a CTA), whose
+// weights it keeps, and R rows' codes and scales on their way: 16 columns in rows of whole
+// units, else one.
+template <typename T, typename W, int N, int R>
 __global__ void __launch_bounds__(256) norm_restore_kernel(const RestoreArgs a) {
-    constexpr int N = WIDE ? 8 : 2, STEP = WIDE ? 8 : 1;
+    constexpr int P = N > 1 ? N / 2 : 1;  // pairs
     if (threadIdx.x == 0 && threadIdx.y == 0) ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int64_t column = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * STEP;
+    const int64_t column = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * N;
     if (column >= a.cols) return;
-    float2 w[N / 2], b[N / 2];
+    float2 w[P], b[P];
 #pragma unroll
-    for (int j = 0; j < N / 2; ++j) w[j] = both(1.f), b[j] = both(0.f);
-    if constexpr (WIDE) {
-        if (a.weight) load_pairs<W, N / 2>(static_cast<const W *>(a.weight) + column, w);
-        if (a.bias) load_pairs<W, N / 2>(static_cast<const W *>(a.bias) + column, b);
+    for (int j = 0; j < P; ++j) w[j] = both(1.f), b[j] = both(0.f);
+    if constexpr (N > 1) {
+        if (a.weight) load_pairs<W, P>(static_cast<const W *>(a.weight) + column, w);
+        if (a.bias) load_pairs<W, P>(static_cast<const W *>(a.bias) + column, b);
     } else {
         if (a.weight) w[0].x = to_f32(static_cast<const W *>(a.weight)[column]);
         if (a.bias) b[0].x = to_f32(static_cast<const W *>(a.bias)[column]);
     }
     const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.y;
-    constexpr int R = 4;  // rows on their way at once
-    for (int64_t row = static_cast<int64_t>(blockIdx.y) * blockDim.y + threadIdx.y; row < a.rows; row += R * step) {
-        uint2 code[R];
-        float scale[R];
+    int64_t row = static_cast<int64_t>(blockIdx.y) * blockDim.y + threadIdx.y;
+    const uint8_t *codes = a.codes + row * a.cols + column, *scales = a.scales + row * a.blocks + column / kFp8Block;
+    T *y = static_cast<T *>(a.y) + row * a.y_stride + column;
+    const int64_t code_step = step * a.cols, scale_step = step * a.blocks, y_step = step * a.y_stride;
+    for (; row < a.rows; row += R * step, codes += R * code_step, scales += R * scale_step, y += R * y_step) {
+        uint32_t code[R][N > 1 ? N / 4 : 1], scale[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t at = row + r * step;
-            code[r] = make_uint2(0, 0);
-            scale[r] = 1.f;
-            if (at >= a.rows) continue;
-            if constexpr (WIDE) {
-                code[r] = *reinterpret_cast<const uint2 *>(a.codes + at * a.cols + column);
+            if (row + r * step >= a.rows) break;
+            if constexpr (N == 16) {
+                const uint4 u = load_unit(codes + r * code_step);
+                code[r][0] = u.x, code[r][1] = u.y, code[r][2] = u.z, code[r][3] = u.w;
+            } else if constexpr (N == 8) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(codes + r * code_step);
+                code[r][0] = u.x, code[r][1] = u.y;
             } else {
-                code[r].x = a.codes[at * a.cols + column];
+                code[r][0] = codes[r * code_step];
             }
-            scale[r] = scale_value(a.scales[at * a.blocks + column / kFp8Block]);
+            scale[r] = scales[r * scale_step];
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t at = row + r * step;
-            if (at >= a.rows) continue;
-            T *y = static_cast<T *>(a.y) + at * a.y_stride + column;
-            float2 v[N / 2];
+            if (row + r * step >= a.rows) break;
+            const float2 s = both(scale_value(scale[r]));
+            float2 v[P];
 #pragma unroll
-            for (int j = 0; j < N / 2; ++j) {
-                const uint32_t pair = from_e4m3x2((j < 2 ? code[r].x : code[r].y) >> (j % 2 * 16) & 0xffffu);
-                v[j] = fma2(mul2(__half22float2(*reinterpret_cast<const __half2 *>(&pair)), both(scale[r])), w[j], b[j]);
+            for (int j = 0; j < P; ++j) {
+                const uint32_t pair = from_e4m3x2(code[r][j / 2] >> (j % 2 * 16) & 0xffffu);
+                v[j] = fma2(mul2(__half22float2(*reinterpret_cast<const __half2 *>(&pair)), s), w[j], b[j]);
             }
-            if constexpr (WIDE) {
-                store_pairs<T, N / 2>(y, v);
+            if constexpr (N > 1) {
+                store_pairs<T, P>(y + r * y_step, v);
             } else {
-                *y = from_f32<T>(v[0].x);
+                y[r * y_step] = from_f32<T>(v[0].x);
             }
         }
     }
@@ -280,22 +283,28 @@ int keep_as(const KeepArgs &a, int sms, cudaStream_t stream) {
     return wide ? keep_rows<T, W, true>(a, sms, stream) : keep_rows<T, W, false>(a, sms, stream);
 }
 
-template <typename T, typename W>
-int restore_as(const RestoreArgs &a, int sms, cudaStream_t stream) {
-    const bool wide = a.cols % 8 == 0 && a.y_stride % 8 == 0 && aligned(a.y, 16) && aligned(a.codes, 8) &&
-                      (!a.weight || aligned(a.weight, 16)) && (!a.bias || aligned(a.bias, 16));
-    const int64_t units = wide ? a.cols / 8 : a.cols;
+template <typename T, typename W, int N, int R>
+int restore_rows(const RestoreArgs &a, int sms, cudaStream_t stream) {
+    const int64_t units = a.cols / N;
     unsigned x = 256;
     while (x > 8 && x / 2 >= units) x /= 2;
     const unsigned y = 256 / x;
     const int64_t across = (units + x - 1) / x;
-    // CTAs for some 8 an SM, each with a few rows of a thread's columns
-    int64_t down = (static_cast<int64_t>(a.rows) + 4 * y - 1) / (4 * y);
-    const int64_t most = (static_cast<int64_t>(sms) * 8 + across - 1) / across;
+    // CTAs of R rows a thread, as far as they run at once
+    int64_t down = (static_cast<int64_t>(a.rows) + R * y - 1) / (R * y);
+    const int64_t most = (static_cast<int64_t>(sms) * (N > 1 ? 3 : 6) + across - 1) / across;
     if (down > most) down = most;
     if (down > 65535) down = 65535;
-    auto *kernel = wide ? norm_restore_kernel<T, W, true> : norm_restore_kernel<T, W, false>;
-    return launch(kernel, dim3(static_cast<unsigned>(across), static_cast<unsigned>(down)), dim3(x, y), 0, stream, a);
+    return launch(norm_restore_kernel<T, W, N, R>, dim3(static_cast<unsigned>(across), static_cast<unsigned>(down)), dim3(x, y),
+                  0, stream, a);
+}
+
+template <typename T, typename W>
+int restore_as(const RestoreArgs &a, int sms, cudaStream_t stream) {
+    const bool wide = a.cols % 8 == 0 && a.y_stride % 8 == 0 && aligned(a.y, 16) && aligned(a.codes, 8) &&
+                      (!a.weight || aligned(a.weight, 16)) && (!a.bias || aligned(a.bias, 16));
+    if (wide && a.cols % 16 == 0 && aligned(a.codes, 16)) return restore_rows<T, W, 16, 4>(a, sms, stream);
+    return wide ? restore_rows<T, W, 8, 4>(a, sms, stream) : restore_rows<T, W, 1, 16>(a, sms, stream);
 }
 
 }  // namespace

@@ -16,15 +16,13 @@ __device__ unsigned long long g_group_info;  // its role, CTA and tile
 
 enum : uint32_t { kWaitProducer = 1, kWaitMma = 2, kWaitEpilogue = 3 };
 
-// By one thread.  False if the wait ran out or, when `honor_abort`, as soon as another
-// role of this CTA has given up.  kCluster: the arrivals come from other CTAs of the
-// cluster, and what they wrote before is wanted.
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint64_t timeout_ns,
-                                             uint32_t role, uint32_t seq, bool honor_abort = true) {
+// The wait of a thread that found nothing yet (out of line: the roles' loops are short, and
+// what bounds those of small tiles is a thread's instructions).
+template <bool kCluster>
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint64_t timeout_ns,
+                                     uint32_t role, uint32_t seq, bool honor_abort) {
     namespace ptx = gemm_f16::ptx;
     auto arrived = [&] { return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
-    if (arrived()) return true;
     const uint64_t begun = ptx::globaltimer_ns();
     for (uint32_t turn = 1; !arrived(); ++turn) {
         if (turn % 16 != 0) continue;
@@ -39,6 +37,17 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
         }
     }
     return true;
+}
+
+// By one thread.  False if the wait ran out or, when `honor_abort`, as soon as another
+// role of this CTA has given up.  kCluster: the arrivals come from other CTAs of the
+// cluster, and what they wrote before is wanted.
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint64_t timeout_ns,
+                                             uint32_t role, uint32_t seq, bool honor_abort = true) {
+    namespace ptx = gemm_f16::ptx;
+    if (kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+    return wait_on<kCluster>(bar, parity, abort_flag, timeout_ns, role, seq, honor_abort);
 }
 
 }  // namespace linear_ops

@@ -13,11 +13,11 @@
 //     D[j][i] = round(sum_r W[i][r] * x[j][r] + sum_c up_a(j)[i][c] * h[j][c])
 //
 // As one more stretch of the shared sum, with zeros for the rows of other adapters, that
-// would be 0 * up for those rows, NaN where an adapter holds an infinity.  So up to 16
-// consecutive rows of one adapter are a piece, with 16 columns of TMEM of its own: the
-// MMA multiplies up_a with the 16 rows of h from the piece's first on, and the epilogue
-// adds the columns that are the piece's to its sums.  The cluster's CTAs have the pieces
-// of a share of the tile's rows each.
+// would be 0 * up for those rows, NaN where an adapter holds an infinity.  So consecutive
+// rows of one adapter are a piece, with columns of TMEM of its own: the MMA multiplies
+// up_a with the rows of h from the piece's first on, and the epilogue adds the columns
+// that are the piece's to its sums.  The cluster's CTAs have the pieces of a share of the
+// tile's rows each, as many at once as TMEM has columns for.
 #pragma once
 
 #include "grouped_kernel.cuh"
@@ -28,8 +28,8 @@ template <int TN, bool LORA>
 struct FewShape {
     static constexpr int P_BYTES = 128 * 128, Q_BYTES = (LORA && TN < 32 ? 32 : TN) * 128, STAGE = P_BYTES + Q_BYTES;
     static constexpr int LIST = 4 * (GROUPED_MAX_GROUPS + 4);  // the groups' first rows; their first tiles
-    static constexpr int PIECE = 16;                           // rows of a piece, and its columns of TMEM
-    static constexpr int SLOTS = (512 - TN) / PIECE < 16 ? (512 - TN) / PIECE : 16;  // pieces in TMEM at once
+    static constexpr int PIECE = TN < 64 ? 16 : TN / 2;        // rows of a piece, at most: h, twice, lies where a stage has Q
+    static constexpr int PIECE_COLS = 512 - TN;                // columns of TMEM for pieces, each a multiple of 16
     // the CTA's fp32 sums, row j at j * LD floats, 16 bytes off a multiple of 128 bytes: in
     // the ring once it is idle, of LORA behind it
     static constexpr int LD = 128 + 4;
@@ -37,7 +37,7 @@ struct FewShape {
     // the rest of the shared memory, behind the ring
     static constexpr int OFF_START = LORA ? SUMS : 0, OFF_TILES = OFF_START + LIST;
     static constexpr int OFF_ROWS = OFF_TILES + LIST;             // int32 [TN]: the rows' adapters
-    static constexpr int OFF_PIECES = OFF_ROWS + TN * 4;          // int32 [TN]: first row + 256 * rows; their number behind
+    static constexpr int OFF_PIECES = OFF_ROWS + TN * 4;          // Piece [TN], behind it their number
     static constexpr int OFF_BAR = OFF_PIECES + TN * 4 + 8;
     static constexpr int MOST_STAGES = 12;
     // full, empty [stages]; done, list, pieces full, pieces free, drain
@@ -47,13 +47,21 @@ struct FewShape {
     // takes beside its own), and of one that has it alone, where that is more memory than
     // two could have.  64 x 4096 x 4096: 4 CTAs a tile with 4 stages 10.8 us, with 8 9.2.
     static constexpr int PAIRED = LORA ? 0 : (113 * 1024 - REST) / STAGE;
-    static constexpr int ALONE = (232448 - REST) / STAGE < MOST_STAGES ? (232448 - REST) / STAGE : MOST_STAGES;
+    static constexpr int MOST = LORA ? 220 * 1024 : 232448;  // LORA leaves room for the launch before it
+    static constexpr int ALONE = (MOST - REST) / STAGE < MOST_STAGES ? (MOST - REST) / STAGE : MOST_STAGES;
     static constexpr int smem(int stages) { return stages * STAGE + REST; }
     static constexpr int THREADS = 192;
     static constexpr int TMEM_COLS = LORA ? 512 : (TN < 32 ? 32 : TN);
     static_assert(TN == 16 || TN == 32 || TN == 64 || TN == 128, "tile");
     static_assert(OFF_BAR % 8 == 0 && ALONE >= 4 && ALONE * STAGE + REST > 114 * 1024, "an SM alone");
     static_assert(LORA || (PAIRED >= 3 && PAIRED * STAGE >= SUMS), "two CTAs an SM");
+};
+
+// Rows [first, first + rows) of the tile, at columns [column, column + rows in whole 16s) of
+// those for pieces; where the columns start again from 0, they are a turn's first.
+struct Piece {
+    uint8_t first, rows;
+    uint16_t column;
 };
 
 __device__ __forceinline__ float2 widen16(bool bf16, uint32_t w) {
@@ -104,8 +112,8 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     int32_t *start = reinterpret_cast<int32_t *>(smem + C::OFF_START), *tiles = reinterpret_cast<int32_t *>(smem + C::OFF_TILES);
-    int32_t *chosen = reinterpret_cast<int32_t *>(smem + C::OFF_ROWS), *pieces = reinterpret_cast<int32_t *>(smem + C::OFF_PIECES);
-    int32_t *piece_count = pieces + TN;
+    int32_t *chosen = reinterpret_cast<int32_t *>(smem + C::OFF_ROWS), *piece_count = reinterpret_cast<int32_t *>(smem + C::OFF_PIECES) + TN;
+    Piece *pieces = reinterpret_cast<Piece *>(smem + C::OFF_PIECES);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < stages; ++s) {
@@ -128,9 +136,12 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
     // LORA follows lora_down_kernel, which lets it start only once the kernels before both
     // have completed: it waits for h alone, in the producer
     if (!LORA || !p.follows) ptx::griddep_wait();
-    const int groups = group_starts(p, start, false, nullptr, static_cast<int>(threadIdx.x), C::THREADS);
-    __syncthreads();
-    if (warp == 2) group_tiles<TN, LORA ? kGroupNT : MODE>(p, groups, start, tiles, nullptr, lane);
+    const int groups = p.groups;
+    if constexpr (!LORA) {  // LORA's epilogue lists the requests, beside the shared sum
+        group_starts(p, start, false, nullptr, static_cast<int>(threadIdx.x), C::THREADS);
+        __syncthreads();
+        if (warp == 2) group_tiles<TN, MODE>(p, groups, start, tiles, nullptr, lane);
+    }
     ptx::tcgen05_fence_before();
     __syncthreads();
     ptx::tcgen05_fence_after();
@@ -187,19 +198,24 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                 ok = ok && wait_bounded(bar_list, 0, abort_flag, p.timeout_ns, kWaitProducer, 0);
                 const int count = ok ? *piece_count : 0;
                 if (count > 0) ptx::griddep_wait();
-                for (int q = 0; ok && q < count * rank_tiles; ++q) {
-                    const int j = pieces[q / rank_tiles] & 0xff, c = q % rank_tiles * 64;
+                for (int q = 0, c = 0; ok && q < count;) {
+                    const Piece piece = pieces[q];
+                    const int j = piece.first, boxes = (piece.rows + 15) / 16;  // of 16 rows of h
                     if (!wait_bounded(bar_empty + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitProducer, q)) {
                         ok = false;
                         break;
                     }
                     const int s = ring.stage;
                     const uint32_t sq = base + off_q + s * C::Q_BYTES, full = bar_full + 8 * s;
-                    ptx::mbar_arrive_expect_tx(full, C::P_BYTES + 2 * C::PIECE * 128);
+                    ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(C::P_BYTES + 2 * boxes * 2048));
                     ptxg::tma_load_3d(base + s * C::P_BYTES, &tmU, full, c, w.i0, chosen[j]);
-                    ptx::tma_load_2d(sq, &tmH, full, c, w.j0 + j);
-                    ptx::tma_load_2d(sq + C::PIECE * 128, &tmH, full, p.rank_pad + c, w.j0 + j);
+                    for (int b = 0; b < boxes; ++b) {
+                        ptx::tma_load_2d(sq + b * 2048, &tmH, full, c, w.j0 + j + 16 * b);
+                        ptx::tma_load_2d(sq + C::PIECE * 128 + b * 2048, &tmH, full, p.rank_pad + c, w.j0 + j + 16 * b);
+                    }
                     ring.advance();
+                    c += 64;
+                    if (c >= p.rank) c = 0, ++q;
                 }
             }
             if (!ok) {  // time for loads in flight to land before the shared memory goes
@@ -212,6 +228,8 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
         if (work && ptx::elect_one()) {
             PipelineState ring(stages, 0u);
             const uint32_t idesc = group_idesc<1, MODE>((w.n + 15) / 16 * 16, p.bf16);
+            const uint32_t p_low = MODE == kGroupNN ? ptxg::desc_mn_low(base) : ptxg::desc_k_low(base);
+            const uint32_t q_low = ptxg::desc_k_low(base + off_q);
             bool ok = true;
             for (int kt = kt_begin; kt < kt_end; ++kt) {
                 if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitMma, kt)) {
@@ -220,17 +238,10 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                 }
                 ptx::tcgen05_fence_after();
                 const int s = ring.stage;
-                const uint32_t sp = base + s * C::P_BYTES, sq = base + off_q + s * C::Q_BYTES;
-                constexpr bool kMn = MODE == kGroupNN;
-                const uint64_t pd = kMn ? ptxg::smem_desc_mn_sw128(sp, 8192) : ptx::smem_desc_k_sw128(sp);
-                const uint64_t qd = ptx::smem_desc_k_sw128(sq);
-                const int steps = w.r - kt * 64 >= 64 ? 4 : (w.r - kt * 64 + 15) / 16;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k < steps) {
-                        ptx::mma_f16<1>(tmem_base, pd + k * (kMn ? 128 : 2), qd + k * 2, idesc, kt > kt_begin || k > 0 ? 1u : 0u);
-                    }
-                }
+                const int left = w.r - kt * 64;
+                ptxg::mma_stage<1, MODE == kGroupNN ? 128 : 2, 2>(
+                    tmem_base, p_low + static_cast<uint32_t>(s * (C::P_BYTES >> 4)), q_low + static_cast<uint32_t>(s * (C::Q_BYTES >> 4)),
+                    idesc, left >= 64 ? 4 : (left + 15) / 16, kt == kt_begin);
                 ptx::mma_commit<1>(bar_empty + 8 * s, 0x1);
                 ring.advance();
             }
@@ -238,16 +249,20 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
             if constexpr (LORA) {
                 ok = ok && wait_bounded(bar_list, 0, abort_flag, p.timeout_ns, kWaitMma, 0);
                 const int count = ok ? *piece_count : 0;
-                const uint32_t piece_idesc = group_idesc<1, MODE>(C::PIECE, p.bf16);
+                uint32_t turn = 0;  // pieces that had their columns at once
                 for (int q = 0; ok && q < count; ++q) {
-                    if (q > 0 && q % C::SLOTS == 0) {  // the epilogue has read the pieces before
-                        if (!wait_bounded(bar_pfree, (q / C::SLOTS - 1) & 1, abort_flag, p.timeout_ns, kWaitMma, q)) {
+                    const Piece piece = pieces[q];
+                    if (q > 0 && piece.column == 0) {  // the epilogue has read the pieces before
+                        ptx::mma_commit<1>(bar_pfull, 0x1);
+                        if (!wait_bounded(bar_pfree, turn & 1u, abort_flag, p.timeout_ns, kWaitMma, q)) {
                             ok = false;
                             break;
                         }
+                        ++turn;
                         ptx::tcgen05_fence_after();
                     }
-                    const uint32_t d = tmem_base + static_cast<uint32_t>(TN + q % C::SLOTS * C::PIECE);
+                    const uint32_t d = tmem_base + TN + piece.column;
+                    const uint32_t piece_idesc = group_idesc<1, MODE>((piece.rows + 15) / 16 * 16, p.bf16);
                     for (int c = 0; c < rank_tiles; ++c) {
                         if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitMma, q)) {
                             ok = false;
@@ -255,19 +270,16 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                         }
                         ptx::tcgen05_fence_after();
                         const int s = ring.stage;
-                        const uint32_t sq = base + off_q + s * C::Q_BYTES;
-                        const uint64_t pd = ptx::smem_desc_k_sw128(base + s * C::P_BYTES);
-                        const uint64_t high = ptx::smem_desc_k_sw128(sq), low = ptx::smem_desc_k_sw128(sq + C::PIECE * 128);
+                        const uint32_t up = p_low + static_cast<uint32_t>(s * (C::P_BYTES >> 4));
+                        const uint32_t high = q_low + static_cast<uint32_t>(s * (C::Q_BYTES >> 4)), low = high + (C::PIECE * 128 >> 4);
                         const int steps = p.rank - c * 64 >= 64 ? 4 : (p.rank - c * 64 + 15) / 16;
-                        for (int k = 0; k < steps; ++k) {
-                            ptx::mma_f16<1>(d, pd + k * 2, high + k * 2, piece_idesc, c > 0 || k > 0 ? 1u : 0u);
-                            ptx::mma_f16<1>(d, pd + k * 2, low + k * 2, piece_idesc, 1u);
-                        }
+                        ptxg::mma_stage<1, 2, 2>(d, up, high, piece_idesc, steps, c == 0);
+                        ptxg::mma_stage<1, 2, 2>(d, up, low, piece_idesc, steps, false);
                         ptx::mma_commit<1>(bar_empty + 8 * s, 0x1);
                         ring.advance();
                     }
-                    if (ok && (q % C::SLOTS == C::SLOTS - 1 || q == count - 1)) ptx::mma_commit<1>(bar_pfull, 0x1);
                 }
+                if (ok && count > 0) ptx::mma_commit<1>(bar_pfull, 0x1);
             }
             // every MMA issued so far (after an abort as well: TMEM is freed below)
             ptx::mma_commit<1>(bar_drain, 0x1);
@@ -276,6 +288,10 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
         __syncwarp();
     } else if (work) {
         if constexpr (LORA) {  // the rows' adapters: that of the last request that starts at or before a row
+            group_starts(p, start, false, nullptr, static_cast<int>(threadIdx.x) - 64, 128);
+            ptxg::sync_128(1);
+            if (warp == 2) group_tiles<TN, kGroupNT>(p, groups, start, tiles, nullptr, lane);
+            ptxg::sync_128(1);
             for (int32_t j = static_cast<int32_t>(threadIdx.x) - 64; j < w.n; j += 128) {
                 const int32_t row = w.j0 + j;
                 int lo = -1, hi = groups;  // start[lo] <= row < start[hi]
@@ -292,12 +308,18 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
             ptxg::sync_128(1);
             if (warp == 2 && lane == 0) {  // the pieces of this CTA's share of the rows
                 const int first = w.n * rank / KS, last = w.n * (rank + 1) / KS;
-                int count = 0;
+                int count = 0, column = 0;
+                int32_t next = first < last ? chosen[first] : -1;
                 for (int j = first; j < last;) {
-                    const int32_t a = chosen[j];
+                    const int32_t a = next;
                     int n = 1;
-                    while (n < C::PIECE && j + n < last && chosen[j + n] == a) ++n;
-                    if (a >= 0) pieces[count++] = j | n << 8;
+                    while (j + n < last && (next = chosen[j + n]) == a && n < C::PIECE) ++n;
+                    if (a >= 0) {
+                        const int columns = (n + 15) / 16 * 16;
+                        if (column + columns > C::PIECE_COLS) column = 0;
+                        pieces[count++] = {static_cast<uint8_t>(j), static_cast<uint8_t>(n), static_cast<uint16_t>(column)};
+                        column += columns;
+                    }
                     j += n;
                 }
                 *piece_count = count;
@@ -319,28 +341,54 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                 ptx::tmem_wait_ld();
                 // without K tiles of its own a CTA adds nothing
 #pragma unroll
-                for (int j = 0; j < 16; ++j) sums[(c + j) * C::LD + i] = kt_begin < kt_end ? __uint_as_float(v[j]) : 0.f;
+                for (int j = 0; j < 16; ++j) {
+                    const float own = kt_begin < kt_end ? __uint_as_float(v[j]) : 0.f;
+                    sums[(c + j) * C::LD + i] = own;
+                }
             }
         }
         if constexpr (LORA) {
             if (lane == 0) ok = ok && wait_bounded(bar_list, 0, abort_flag, p.timeout_ns, kWaitEpilogue, 0);
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             const int count = ok ? *piece_count : 0;
-            for (int q = 0; q < count; q += C::SLOTS) {
-                if (lane == 0) ok = wait_bounded(bar_pfull, (q / C::SLOTS) & 1, abort_flag, p.timeout_ns, kWaitEpilogue, q);
+            uint32_t turn = 0;
+            for (int q = 0; q < count; ++turn) {
+                if (lane == 0) ok = wait_bounded(bar_pfull, turn & 1u, abort_flag, p.timeout_ns, kWaitEpilogue, q);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) break;
                 ptx::tcgen05_fence_after();
-                for (int s = 0; s < C::SLOTS && q + s < count; ++s) {
-                    const int j = pieces[q + s] & 0xff, n = pieces[q + s] >> 8;
+                do {
+                    // pieces of one row, up to eight at once
+                    constexpr int B = 8;
                     uint32_t v[16];
-                    ptx::tmem_ld_32x32b_x16(taddr + TN + s * C::PIECE, v);
-                    ptx::tmem_wait_ld();
+                    int some = 0;
 #pragma unroll
-                    for (int t = 0; t < C::PIECE; ++t) {
-                        if (t < n) sums[(j + t) * C::LD + i] += __uint_as_float(v[t]);
+                    for (int s = 0; s < B; ++s) {
+                        if (s == some && q + s < count && pieces[q + s].rows == 1 && (s == 0 || pieces[q + s].column != 0)) {
+                            ptxg::tmem_ld_32x32b_x1(taddr + TN + pieces[q + s].column, v[s]);
+                            ++some;
+                        }
                     }
-                }
+                    if (some > 0) {
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int s = 0; s < B; ++s) {
+                            if (s < some) sums[pieces[q + s].first * C::LD + i] += __uint_as_float(v[s]);
+                        }
+                        q += some;
+                        continue;
+                    }
+                    const Piece piece = pieces[q];
+                    for (int c = 0; c < piece.rows; c += 16) {
+                        ptx::tmem_ld_32x32b_x16(taddr + TN + piece.column + c, v);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) {
+                            if (c + t < piece.rows) sums[(piece.first + c + t) * C::LD + i] += __uint_as_float(v[t]);
+                        }
+                    }
+                    ++q;
+                } while (q < count && pieces[q].column != 0);
                 ptx::tcgen05_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar_pfree);
@@ -391,10 +439,9 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
     }
 }
 
-// h[row] = scale_a * x[row] * down_a^T for the rows with an adapter, as two 16-bit numbers
-// (split_16; zeros up to a whole 16 ranks).  Of ROWS consecutive rows those of one adapter
-// share what is read of it.  256 threads: two warps a rank and half of K each, four ranks
-// at a time and `each` times four a CTA.  The chain of a single token is the launch, the
+// h[row] = scale_a * x[row] * down_a^T for a row with an adapter, as two 16-bit numbers
+// (split_16; zeros up to a whole 16 ranks), for few rows.  256 threads: two warps a rank and
+// half of K each, four ranks at a time and `each` times four a CTA.  The chain of a single token is the launch, the
 // offsets and adapters, what down holds, and the sums; x is on its way from the start.
 struct DownParams {
     const uint16_t *x, *down;
@@ -416,123 +463,74 @@ __device__ __forceinline__ float dot_8(bool bf16, uint4 a, uint4 b, float sum) {
 
 constexpr int kDownRanks = 4;
 
-template <int ROWS>
 __global__ void __launch_bounds__(256) lora_down_kernel(const GroupParams p, const DownParams d) {
-    // of each row the first request that starts behind it, and that request's predecessor's adapter
-    __shared__ unsigned long long past[ROWS];
-    __shared__ float halves[kDownRanks][ROWS];
+    // the first request that starts behind the row, and its predecessor's adapter
+    __shared__ unsigned long long past;
+    __shared__ float halves[kDownRanks];
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS;
-    if (tid < ROWS) past[tid] = ~0ull;
+    const int64_t row = blockIdx.x;
+    if (tid == 0) past = ~0ull;
     ptx::griddep_wait();
     // what follows may start: all before this kernel has completed
     if (tid == 0) ptx::griddep_launch_dependents();
     const int half = warp / kDownRanks;
     const int k_half = (p.R / 8 + 1) / 2 * 8;  // whole units of eight
     const int k_begin = half * k_half, k_end = half ? p.R : k_half;
-    const uint16_t *x = d.x + first * d.x_row;
+    const uint16_t *x = d.x + row * d.x_row;
     constexpr int U = 8;  // loads on their way at once
     uint4 v[U];
-    if constexpr (ROWS == 1) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int k = k_begin + lane * 8 + i * 256;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (k < k_end) v[i] = *reinterpret_cast<const uint4 *>(x + k);
-        }
+    for (int i = 0; i < U; ++i) {
+        const int k = k_begin + lane * 8 + i * 256;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (k < k_end) v[i] = *reinterpret_cast<const uint4 *>(x + k);
     }
     __syncthreads();
-    unsigned long long least[ROWS];
-#pragma unroll
-    for (int t = 0; t < ROWS; ++t) least[t] = ~0ull;
+    unsigned long long least = ~0ull;
     for (int e = p.groups - tid; e >= 0; e -= 256) {
         const int64_t o = offset_of(p, e);
         const uint32_t a = e > 0 ? static_cast<uint32_t>(adapter_of(p, e - 1)) : ~0u;
-#pragma unroll
-        for (int t = 0; t < ROWS; ++t) {
-            if (o > first + t) least[t] = static_cast<unsigned long long>(e) << 32 | a;
-        }
+        if (o > row) least = static_cast<unsigned long long>(e) << 32 | a;
     }
-#pragma unroll
-    for (int t = 0; t < ROWS; ++t) {
-        // few threads have found one; of them the lowest
-        const uint32_t e = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(least[t] >> 32));
-        if (static_cast<uint32_t>(least[t] >> 32) == e && e != ~0u) atomicMin(&past[t], least[t]);
-    }
+    // few threads have found one; of them the lowest
+    const uint32_t first = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(least >> 32));
+    if (static_cast<uint32_t>(least >> 32) == first && first != ~0u) atomicMin(&past, least);
     __syncthreads();
-    int32_t a[ROWS];
-    bool any = false;
-#pragma unroll
-    for (int t = 0; t < ROWS; ++t) {
-        // none behind it: the row is behind the last request
-        a[t] = first + t < p.rows && past[t] != ~0ull ? static_cast<int32_t>(past[t] & 0xffffffffull) : -1;
-        any = any || a[t] >= 0;
-    }
-    if (!any) return;
+    // none behind it: the row is behind the last request
+    const int32_t a = past != ~0ull ? static_cast<int32_t>(past & 0xffffffffull) : -1;
+    if (a < 0) return;
     const int padded = (p.rank + 15) / 16 * 16;
     for (int q = 0; q < d.each; ++q) {
         const int j = (static_cast<int>(blockIdx.y) * d.each + q) * kDownRanks + warp % kDownRanks;
-        const uint16_t *down = d.down + j * d.down_row;
-        float sum[ROWS];
+        float sum = 0.f;
+        if (j < p.rank) {
+            const uint16_t *down = d.down + j * d.down_row + a * d.down_matrix;
+            for (int k = k_begin + lane * 8; k < k_end; k += 256 * U) {
+                uint4 u[U];
 #pragma unroll
-        for (int t = 0; t < ROWS; ++t) sum[t] = 0.f;
-        if constexpr (ROWS == 1) {
-            if (j < p.rank) {
-                down += a[0] * d.down_matrix;
-                for (int k = k_begin + lane * 8; k < k_end; k += 256 * U) {
-                    uint4 u[U];
+                for (int i = 0; i < U; ++i) {
+                    u[i] = make_uint4(0, 0, 0, 0);
+                    if (k + i * 256 < k_end) u[i] = load_unit(down + k + i * 256);
+                }
+                if (k_end - k_begin > 256 * U) {  // v holds all of x only where it is no longer
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
-                        u[i] = make_uint4(0, 0, 0, 0);
-                        if (k + i * 256 < k_end) u[i] = load_unit(down + k + i * 256);
-                    }
-                    if (k_end - k_begin > 256 * U) {  // v holds the first 256 U of x only where there are no more
-#pragma unroll
-                        for (int i = 0; i < U; ++i) {
-                            v[i] = make_uint4(0, 0, 0, 0);
-                            if (k + i * 256 < k_end) v[i] = *reinterpret_cast<const uint4 *>(x + k + i * 256);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < U; ++i) sum[0] = dot_8(p.bf16, u[i], v[i], sum[0]);
-                }
-            }
-        } else if (j < p.rank) {
-#pragma unroll 1
-            for (int k = k_begin + lane * 8; k < k_end; k += 256) {
-                uint4 m[ROWS], w[ROWS];
-#pragma unroll
-                for (int t = 0; t < ROWS; ++t) {
-                    w[t] = m[t] = make_uint4(0, 0, 0, 0);
-                    if (a[t] < 0) continue;
-                    w[t] = *reinterpret_cast<const uint4 *>(x + t * d.x_row + k);
-                    if (t > 0 && a[t] == a[t - 1]) {
-                        m[t] = m[t - 1];
-                    } else {
-                        m[t] = *reinterpret_cast<const uint4 *>(down + a[t] * d.down_matrix + k);
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (k + i * 256 < k_end) v[i] = *reinterpret_cast<const uint4 *>(x + k + i * 256);
                     }
                 }
 #pragma unroll
-                for (int t = 0; t < ROWS; ++t) {
-                    if (a[t] >= 0) sum[t] = dot_8(p.bf16, m[t], w[t], sum[t]);
-                }
+                for (int i = 0; i < U; ++i) sum = dot_8(p.bf16, u[i], v[i], sum);
             }
         }
 #pragma unroll
-        for (int t = 0; t < ROWS; ++t) {
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
-            if (half && lane == 0) halves[warp % kDownRanks][t] = sum[t];
-        }
+        for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (half && lane == 0) halves[warp % kDownRanks] = sum;
         __syncthreads();
         if (!half && lane == 0 && j < padded) {
-#pragma unroll
-            for (int t = 0; t < ROWS; ++t) {
-                if (a[t] < 0) continue;
-                const float h = j < p.rank ? (sum[t] + halves[warp][t]) * (p.scales ? p.scales[a[t]] : 1.f) : 0.f;
-                uint16_t *to = d.h + (first + t) * (2 * p.rank_pad) + j;
-                split_16(p.bf16, h, to, to + p.rank_pad);
-            }
+            const float h = j < p.rank ? (sum + halves[warp]) * (p.scales ? p.scales[a] : 1.f) : 0.f;
+            uint16_t *to = d.h + row * (2 * p.rank_pad) + j;
+            split_16(p.bf16, h, to, to + p.rank_pad);
         }
         __syncthreads();
     }

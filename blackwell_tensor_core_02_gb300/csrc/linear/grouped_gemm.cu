@@ -165,7 +165,7 @@ int launch_few(const Call &c) {
         if (!encode(&tmP, c.P, MODE == kGroupNN ? 64 : 128) || !encode(&tmQ, c.Q, TN)) return GEMM_ERR_CUDA;
     }
     if (MODE == kGroupLora && p.groups > 0) {
-        if (!encode(&tmU, c.U, 128) || !encode(&tmH, c.H, C::PIECE)) return GEMM_ERR_CUDA;
+        if (!encode(&tmU, c.U, 128) || !encode(&tmH, c.H, 16)) return GEMM_ERR_CUDA;
     }
     const int64_t tiles = most > 0 ? most : 1;  // one for the rows without a group
     const int stages = MODE == kGroupLora || KS * tiles <= c.sms ? C::ALONE : C::PAIRED;
@@ -341,54 +341,44 @@ struct Lora {
     void *workspace;
 };
 
-// x, W, up and h as the product's launch takes them.
-void lora_operands(Call &c, const Lora &l) {
+// h, by CUDA cores for a few rows, else by the tensor cores in tiles of one request each.
+int lora_down(Call &c, const Lora &l) {
+    if (c.p.groups == 0) return GEMM_OK;
+    int st;
+    if (l.rows <= 256) {
+        // three CTAs an SM, with as few ranks each as that allows
+        const int64_t fours = (l.rank + 15) / 16 * 16 / kDownRanks;
+        int64_t each = 1;
+        while (each < fours && l.rows * ((fours + each - 1) / each) > 3 * c.sms) ++each;
+        const DownParams d = {static_cast<const uint16_t *>(l.x.ptr), static_cast<const uint16_t *>(l.down.ptr), l.x.stride,
+                              l.down.stride, l.down.depth_stride, static_cast<uint16_t *>(l.workspace), static_cast<int32_t>(each)};
+        st = launch(lora_down_kernel, dim3(static_cast<unsigned>(l.rows), static_cast<unsigned>((fours + each - 1) / each)),
+                    dim3(256), 0, c.stream, c.p, d);
+    } else {
+        Call d = c;
+        d.P = l.down;
+        d.Q = l.x;
+        d.p.I = c.p.rank;
+        d.p.out = l.workspace;
+        d.p.out_row = 2 * c.p.rank_pad;
+        d.max_clusters = 0;
+        st = launch_tile<1, 32, kGroupDown>(d);
+    }
+    c.p.follows = 1;
+    return st;
+}
+
+// Requests of many rows: tiles of one request each, the adapter as more of the sum.
+// Requests of few: tiles of any rows, the adapters run by run.
+int lora(Call &c, const Lora &l, const Choice &how) {
+    const int st = lora_down(c, l);
+    if (st != GEMM_OK) return st;
     c.P = l.W;
     c.Q = l.x;
     c.D = l.D;
     c.U = l.up;
     c.H = {l.workspace, l.rows, 2 * c.p.rank_pad, 2 * c.p.rank_pad, 0, 0};
-}
-
-// Requests of many rows: tiles of one request each, the adapter as more of the sum.
-int lora_long(Call &c, const Lora &l) {
-    GroupParams &p = c.p;
-    if (p.groups > 0) {
-        Call d = c;
-        d.P = l.down;
-        d.Q = l.x;
-        d.p.I = p.rank;
-        d.p.out = l.workspace;
-        d.p.out_row = 2 * p.rank_pad;
-        d.max_clusters = 0;
-        const int st = launch_tile<1, 32, kGroupDown>(d);
-        if (st != GEMM_OK) return st;
-        p.follows = 1;
-    }
-    lora_operands(c, l);
-    return launch_tile<2, 256, kGroupLora>(c);
-}
-
-// Requests of few rows: tiles of any rows, the adapters piece by piece.
-int lora_short(Call &c, const Lora &l, const Choice &how) {
-    GroupParams &p = c.p;
-    if (p.groups > 0) {
-        const int64_t fours = (l.rank + 15) / 16 * 16 / kDownRanks;
-        const bool one = l.rows <= 256;
-        // a wave of CTAs, with as few ranks each as that allows
-        const int64_t ctas = one ? l.rows : (l.rows + 7) / 8;
-        int64_t each = 1;
-        while (each < fours && ctas * ((fours + each - 1) / each) > 2 * c.sms) each *= 2;
-        const DownParams d = {static_cast<const uint16_t *>(l.x.ptr), static_cast<const uint16_t *>(l.down.ptr), l.x.stride,
-                              l.down.stride, l.down.depth_stride, static_cast<uint16_t *>(l.workspace), static_cast<int32_t>(each)};
-        const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>((fours + each - 1) / each));
-        const int st = one ? launch(lora_down_kernel<1>, grid, dim3(256), 0, c.stream, p, d)
-                           : launch(lora_down_kernel<8>, grid, dim3(256), 0, c.stream, p, d);
-        if (st != GEMM_OK) return st;
-        p.follows = 1;
-    }
-    lora_operands(c, l);
-    return launch_few_mode<kGroupLora>(c, how.tile, how.split);
+    return how.tile == 256 ? launch_tile<2, 256, kGroupLora>(c) : launch_few_mode<kGroupLora>(c, how.tile, how.split);
 }
 
 }  // namespace
@@ -510,11 +500,11 @@ int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const v
         const int64_t each = p.groups > 0 ? rows / p.groups : rows;
         how.tile = o.split < 0 || (o.split == 0 && each >= 128) ? 256 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)));
     }
-    if (how.tile == 256) return lora_long(c, l);
+    if (how.tile == 256) return lora(c, l, how);
     const int64_t k_tiles = (K + 63) / 64;
     if (how.split <= 0) how.split = split_of((rows + how.tile - 1) / how.tile * ((N + 127) / 128), k_tiles, c.sms);
     while (how.split > 1 && how.split > k_tiles) how.split /= 2;
-    return lora_short(c, l, how);
+    return lora(c, l, how);
 }
 
 int grouped_last_device_status(void *stream, uint64_t *info) {

@@ -90,6 +90,11 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         : "memory");
 }
 
+// 32 TMEM lanes x one column.
+__device__ __forceinline__ void tmem_ld_32x32b_x1(uint32_t taddr, uint32_t &r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+}
+
 // Four 8 x 8 matrices of 16-bit elements, transposed on the way: thread t holds of
 // matrix m elements (t / 4, 2 (t % 4)) and (t / 4, 2 (t % 4) + 1) in a word; threads
 // 8 m to 8 m + 7 give the addresses of the 16 bytes that its columns 0 to 7 become.
@@ -99,18 +104,47 @@ __device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32
                  : "memory");
 }
 
-// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: rows of
-// 64 elements along M/N (128 bytes), one for each k; 8 such rows are an atom of 1024
-// bytes (the stride offset, along K), blocks of 64 elements along M/N lie
-// `block_bytes` apart (the leading offset).  Other fields as in ptx::smem_desc_k_sw128.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_addr, uint32_t block_bytes) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
+// Shared-memory descriptors of operands with the 128-byte swizzle, as words: the high one
+// (atoms of 8 rows, 1024 bytes, apart along M/N of a K-major operand, along K of an
+// MN-major one; fields as in ptx::smem_desc_k_sw128) is the same for both, the low one has
+// the address and, of an MN-major operand (rows of 64 elements along M/N, one for each k),
+// how far its blocks of 64 lie apart.  Addresses move by additions to the low word (14 bits
+// of it hold any offset in a CTA's shared memory; above them an address has the CTA's
+// number in its cluster).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k_low(uint32_t smem_addr) { return ((smem_addr >> 4) & 0x3FFFu) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn_low(uint32_t smem_addr) {
+    return ((smem_addr >> 4) & 0x3FFFu) | ((8192u >> 4) << 16);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
+#define GROUPED_MMA(GROUP)                                                                                         \
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"                           \
+                 "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"                                              \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),                   \
+                 "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(kDescHigh)                                \
+                 : "memory")
+    if constexpr (CG == 2) {
+        GROUPED_MMA("2");
+    } else {
+        GROUPED_MMA("1");
+    }
+#undef GROUPED_MMA
+}
+
+// The MMAs of a stage, 16 elements of the sum each: A and B move on by A_STEP and B_STEP (of
+// their low words; 32 bytes of a K-major row, 16 rows of 128 bytes of an MN-major tile).
+template <int CG, uint32_t A_STEP, uint32_t B_STEP>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, int steps, bool first) {
+    mma_f16<CG>(d, a_low, b_low, idesc, first ? 0u : 1u);
+    if (steps == 4) {
+        mma_f16<CG>(d, a_low + A_STEP, b_low + B_STEP, idesc, 1u);
+        mma_f16<CG>(d, a_low + 2 * A_STEP, b_low + 2 * B_STEP, idesc, 1u);
+        mma_f16<CG>(d, a_low + 3 * A_STEP, b_low + 3 * B_STEP, idesc, 1u);
+    } else {
+        for (int k = 1; k < steps; ++k) mma_f16<CG>(d, a_low + k * A_STEP, b_low + k * B_STEP, idesc, 1u);
+    }
 }
 
 // True in every thread if it is true in any of the 128 that share the barrier.
@@ -503,6 +537,9 @@ __global__ void __launch_bounds__(384, 1)
         if (leader && ptx::elect_one()) {
             PipelineState ring(C::STAGES, 0u);
             PipelineState acc(2, 1u);
+            const uint32_t sp = base + C::OFF_P, sq = base + C::OFF_Q;
+            const uint32_t p_low = MODE == kGroupNN || MODE == kGroupTN ? ptxg::desc_mn_low(sp) : ptxg::desc_k_low(sp);
+            const uint32_t q_low = MODE == kGroupTN ? ptxg::desc_mn_low(sq) : ptxg::desc_k_low(sq);
             bool ok = true;
             uint32_t seq = 0;
             for (int t = cluster; ok && t < total; t += clusters, ++seq) {
@@ -524,18 +561,11 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     ptx::tcgen05_fence_after();
                     const int s = ring.stage;
-                    const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, sq = base + C::OFF_Q + s * C::Q_BYTES;
-                    constexpr bool kMn = MODE == kGroupNN || MODE == kGroupTN;  // P is MN-major
-                    const uint64_t pd = kMn ? ptxg::smem_desc_mn_sw128(sp, 8192) : ptx::smem_desc_k_sw128(sp);
-                    const uint64_t qd = MODE == kGroupTN ? ptxg::smem_desc_mn_sw128(sq, 8192) : ptx::smem_desc_k_sw128(sq);
-                    // 16 elements of the sum: 32 bytes of a K-major row, 16 rows of an MN-major tile
-                    constexpr uint64_t kP = kMn ? 128 : 2, kQ = MODE == kGroupTN ? 128 : 2;
+                    constexpr bool kMnP = MODE == kGroupNN || MODE == kGroupTN, kMnQ = MODE == kGroupTN;
                     const int left = kt < k_tiles ? w.r - kt * 64 : p.rank - (kt - k_tiles) / 2 * 64;
-                    const int steps = left >= 64 ? 4 : (left + 15) / 16;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k < steps) ptx::mma_f16<CG>(d, pd + k * kP, qd + k * kQ, idesc, kt > 0 || k > 0 ? 1u : 0u);
-                    }
+                    ptxg::mma_stage<CG, kMnP ? 128 : 2, kMnQ ? 128 : 2>(
+                        d, p_low + static_cast<uint32_t>(s * (C::P_BYTES >> 4)), q_low + static_cast<uint32_t>(s * (C::Q_BYTES >> 4)),
+                        idesc, left >= 64 ? 4 : (left + 15) / 16, kt == 0);
                     ptx::mma_commit<CG>(bar_empty + 8 * s, 0x3);
                     ring.advance();
                 }

@@ -378,14 +378,26 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                         q += some;
                         continue;
                     }
+                    // 16 columns of two pieces at once, or of one of more
                     const Piece piece = pieces[q];
+                    const bool two = piece.rows <= 16 && q + 1 < count && pieces[q + 1].column != 0 && pieces[q + 1].rows <= 16;
+                    const Piece next = pieces[two ? q + 1 : q];
+                    uint32_t x[16];
                     for (int c = 0; c < piece.rows; c += 16) {
                         ptx::tmem_ld_32x32b_x16(taddr + TN + piece.column + c, v);
+                        if (two) ptx::tmem_ld_32x32b_x16(taddr + TN + next.column, x);
                         ptx::tmem_wait_ld();
 #pragma unroll
                         for (int t = 0; t < 16; ++t) {
                             if (c + t < piece.rows) sums[(piece.first + c + t) * C::LD + i] += __uint_as_float(v[t]);
                         }
+                    }
+                    if (two) {
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) {
+                            if (t < next.rows) sums[(next.first + t) * C::LD + i] += __uint_as_float(x[t]);
+                        }
+                        ++q;
                     }
                     ++q;
                 } while (q < count && pieces[q].column != 0);

@@ -60,6 +60,13 @@ struct Call {
     cudaStream_t stream;
 };
 
+// Tiles of `tile` rows that the groups have at most: each that has a row begins one, and
+// the other rows fill more.
+int64_t most_tiles(int64_t rows, int64_t groups, int64_t tile) {
+    const int64_t some = groups < rows ? groups : rows;
+    return some + (rows - some) / tile;
+}
+
 template <typename... P>
 int launch_cluster(void (*kernel)(P...), int64_t ctas, unsigned threads, unsigned cluster, size_t smem, cudaStream_t stream,
                    const P &...args) {
@@ -92,10 +99,8 @@ int launch_tile(const Call &c) {
     GroupParams p = c.p;
     const int64_t i_tiles = (static_cast<int64_t>(p.I) + 128 * CG - 1) / (128 * CG);
     const int64_t j_tiles = MODE == kGroupTN ? (static_cast<int64_t>(p.J) + TN - 1) / TN : 0;
-    // every group's tiles, at most: each group may end in a part of a tile
     const int64_t groups = MODE == kGroupLora ? int64_t(p.groups) + 2 : p.groups;
-    const int64_t some = groups < p.rows ? groups : p.rows;
-    const int64_t most = MODE == kGroupTN ? p.groups * i_tiles * j_tiles : (static_cast<int64_t>(p.rows) / TN + some) * i_tiles;
+    const int64_t most = MODE == kGroupTN ? p.groups * i_tiles * j_tiles : most_tiles(p.rows, groups, TN) * i_tiles;
     if (most > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
     p.i_tiles = static_cast<int32_t>(i_tiles);
     p.j_tiles = static_cast<int32_t>(j_tiles);
@@ -155,9 +160,7 @@ int launch_few(const Call &c) {
     if (!allow_smem(kernel, C::smem(C::ALONE), done)) return GEMM_ERR_CUDA;
     GroupParams p = c.p;
     const int64_t i_tiles = (static_cast<int64_t>(p.I) + 127) / 128;
-    const int64_t some = p.groups < p.rows ? p.groups : p.rows;
-    const int64_t most = MODE == kGroupLora ? (static_cast<int64_t>(p.rows) + TN - 1) / TN * i_tiles
-                                            : (static_cast<int64_t>(p.rows) / TN + some) * i_tiles;
+    const int64_t most = most_tiles(p.rows, MODE == kGroupLora ? 1 : p.groups, TN) * i_tiles;
     if (most * KS > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
     p.i_tiles = static_cast<int32_t>(i_tiles);
     CUtensorMap tmP = {}, tmQ = {}, tmU = {}, tmH = {};  // not used by sums of nothing
@@ -207,23 +210,56 @@ int split_of(int64_t tiles, int64_t k_tiles, int sms) {
     return 1;
 }
 
-// The tile's columns: of the ragged axis by the rows that a group has on average, of
-// TN's by the columns.  Tiles for less than half of the SMs share their sums.
+// Cycles that a choice takes, near enough to choose by: a stage (64 of the sum) of each
+// tile, set by the rows that the copy engine brings and, of pairs, by the MMAs; tiles by
+// the groups' average rows; whole waves of a persistent grid, but of clusters, two CTAs an
+// SM that share what it brings, a share of one; and what a tile and a launch take besides.
+// The numbers are fitted to the times of 85 shapes (1 to 8192 rows, 1 to 64 groups, 64 to
+// 14336 columns, sums of 64 to 4096) with each of the 20 choices: the chosen one is 4 % off
+// the best on average.  In microseconds, the choice and others:
+//   256 x 4096 x 4096, one group    128 rows, 2 CTAs a tile: 13.9   64, 1: 15.0   256, pairs: 23.5
+//   512 x 2048 x 2048, one group    64, 1: 9.1                      128, 2: 8.9   256, pairs: 14.2
+//   2000 x 2048 x 2048, 8 groups    128, 1: 20.7                    128, persistent: 21.5   256: 25.7
+//   8192 x 1024 x 1024, 8 groups    256, pairs: 16.9                128, persistent: 20.7   64: 28.4
+//   2 x 2048 x 1024, 64 groups      16, 4: 5.1                      32, 4: 5.4    32, persistent: 6.9
+double cost_of(const GroupParams &p, int sms, int tile, int split) {
+    const double rows = p.rows, some = p.groups < p.rows ? p.groups : p.rows, k_tiles = (p.R + 63) / 64;
+    double tiles = some;
+    if (rows > 0.7 * tile * some) tiles = rows / tile + 0.27 * some;
+    const double most = static_cast<double>(most_tiles(p.rows, p.groups, tile));
+    tiles = tiles < some ? some : (tiles > most ? most : tiles);
+    const double stage = tile == 16 ? 466 : (tile == 32 ? 368 : (tile == 64 ? 364 : (tile == 128 ? 480 : 602)));
+    const double slots = tile == 256 ? sms / 2 : sms;
+    const double n = tiles * ((p.I + (tile == 256 ? 255 : 127)) / (tile == 256 ? 256 : 128)) * (split > 0 ? split : 1);
+    if (split == 0) {
+        double waves = n / slots;
+        waves = waves < 3 ? static_cast<double>(static_cast<int64_t>(waves + 1 - 1e-6)) : waves + 0.5;
+        return waves * (k_tiles * stage + 1260) + 3470;
+    }
+    double load = n / sms;
+    const double turns = static_cast<double>(static_cast<int64_t>(load / 2 + 1 - 1e-6));
+    load = load < 1 ? 1 : (load > 2 ? 1.58 * (load + 0.5) : load);
+    return load * (k_tiles / split) * stage + turns * (3790 + 21 * tile + (split > 1 ? 590 + 20 * tile * split : 0));
+}
+
 Choice choose(int mode, const GroupParams &p, int sms, const grouped_options &o) {
     if (mode == kGroupTN) return {o.tile ? o.tile : (p.J <= 64 ? 64 : (p.J <= 128 || p.I <= 128 ? 128 : 256)), 0};
-    const int64_t some = p.groups < p.rows ? p.groups : p.rows;
-    const int64_t each = some > 0 ? (p.rows + some - 1) / some : 0;
-    const int64_t k_tiles = (static_cast<int64_t>(p.R) + 63) / 64, i_tiles = (static_cast<int64_t>(p.I) + 127) / 128;
-    Choice c = {o.tile, o.split > 0 ? o.split : 0};
-    if (c.tile == 0) {
-        c.tile = each <= 16 ? (c.split > 0 ? 16 : 32) : (each <= 32 ? 64 : (each <= 112 || p.I <= 128 || c.split > 0 ? 128 : 256));
+    const int64_t k_tiles = (static_cast<int64_t>(p.R) + 63) / 64;
+    Choice best = {o.tile ? o.tile : 32, o.split > 0 ? o.split : 0};
+    double least = -1;
+    for (int tile = 16; tile <= 256; tile *= 2) {
+        for (int split = 0; split <= 8; split = split ? 2 * split : 1) {
+            // split 0: a persistent grid, of tiles from 32 on; clusters of tiles up to 128
+            if ((o.tile && tile != o.tile) || (o.split && split != (o.split > 0 ? o.split : 0)) ||
+                (split == 0 ? tile == 16 : tile == 256) || (split > 1 && split > k_tiles && !o.split)) {
+                continue;
+            }
+            const double cost = cost_of(p, sms, tile, split);
+            if (least < 0 || cost < least) least = cost, best = {tile, split};
+        }
     }
-    if (o.split == 0 && c.tile <= 128) {
-        const int64_t tiles = (static_cast<int64_t>(p.rows) / c.tile + some) * i_tiles;
-        if (c.tile == 16 || tiles * 2 <= sms) c.split = split_of(tiles, k_tiles, sms);
-    }
-    while (c.split > 1 && c.split > k_tiles) c.split /= 2;
-    return c;
+    while (best.split > 1 && best.split > k_tiles) best.split /= 2;
+    return best;
 }
 
 template <int MODE>

@@ -223,23 +223,27 @@ int split_of(int64_t tiles, int64_t k_tiles, int sms) {
 //   8192 x 1024 x 1024, 8 groups    256, pairs: 16.9                128, persistent: 20.7   64: 28.4
 //   2 x 2048 x 1024, 64 groups      16, 4: 5.1                      32, 4: 5.4    32, persistent: 6.9
 double cost_of(const GroupParams &p, int sms, int tile, int split) {
-    const double rows = p.rows, some = p.groups < p.rows ? p.groups : p.rows, k_tiles = (p.R + 63) / 64;
-    double tiles = some;
-    if (rows > 0.7 * tile * some) tiles = rows / tile + 0.27 * some;
+    const double rows = p.rows, some = p.groups < p.rows ? p.groups : p.rows, each = rows / some, k_tiles = (p.R + 63) / 64;
+    const bool pair = tile == 256;
+    // a group's rows fill its last tile by half
+    double tiles = each > 0.5 * tile ? rows / tile + 0.5 * some : some;
     const double most = static_cast<double>(most_tiles(p.rows, p.groups, tile));
-    tiles = tiles < some ? some : (tiles > most ? most : tiles);
-    const double stage = tile == 16 ? 466 : (tile == 32 ? 368 : (tile == 64 ? 364 : (tile == 128 ? 480 : 602)));
-    const double slots = tile == 256 ? sms / 2 : sms;
-    const double n = tiles * ((p.I + (tile == 256 ? 255 : 127)) / (tile == 256 ? 256 : 128)) * (split > 0 ? split : 1);
+    if (tiles > most) tiles = most;
+    // rows of a stage in one CTA: 128 of P, and of Q boxes of 32 as far as a tile is filled
+    const int filled = tiles > some ? tile : (each < tile ? static_cast<int>(each + 31) / 32 * 32 : tile);
+    const int q = tile == 16 ? 16 : (filled / (pair ? 2 : 1) + 31) / 32 * 32;
+    double stage = 1.6 * (128 + q) * (pair ? 1.13 : 1.0);
+    if (stage < 450) stage = 450;
+    const double n = tiles * ((p.I + (pair ? 255 : 127)) / (pair ? 256 : 128)) * (split > 0 ? split : 1);
     if (split == 0) {
-        double waves = n / slots;
+        double waves = n / (pair ? sms / 2 : sms);
         waves = waves < 3 ? static_cast<double>(static_cast<int64_t>(waves + 1 - 1e-6)) : waves + 0.5;
-        return waves * (k_tiles * stage + 1260) + 3470;
+        return waves * (k_tiles * stage + 1330) + 3500;
     }
     double load = n / sms;
     const double turns = static_cast<double>(static_cast<int64_t>(load / 2 + 1 - 1e-6));
-    load = load < 1 ? 1 : (load > 2 ? 1.58 * (load + 0.5) : load);
-    return load * (k_tiles / split) * stage + turns * (3790 + 21 * tile + (split > 1 ? 590 + 20 * tile * split : 0));
+    load = load <= 1 ? 1 : (load <= 2 ? 1 + load / 2 : 1.5 * (load + 0.5));
+    return load * (k_tiles / split) * stage + turns * (3800 + 17 * tile + (split > 1 ? 600 + 20 * tile * split : 0));
 }
 
 Choice choose(int mode, const GroupParams &p, int sms, const grouped_options &o) {

@@ -37,11 +37,6 @@ def _parts(kept) -> tuple:
     return tuple(kept) if isinstance(kept, tuple) else (kept,)
 
 
-def _call(name, args, tensors, stream):
-    call = getattr(_linear._native, name)
-    return call(*args) if stream is None else _linear._on(stream, call, args, tensors)
-
-
 def layer_norm_checkpoint(x, weight=None, bias=None, eps: float = 1e-5, *, out=None, stream=None):
     """(y, kept, rstd): ``layer_norm`` of x, and what its backward pass needs.
 
@@ -50,7 +45,11 @@ def layer_norm_checkpoint(x, weight=None, bias=None, eps: float = 1e-5, *, out=N
     h / scale rounded to E4M3, ties to the even code, magnitudes past 448 to 448.  A block that holds an
     infinity or NaN becomes NaN.  x, weight, bias, eps and ``out`` are as ``layer_norm`` takes them.
     """
-    y, codes, scales, rstd = _call("layer_norm_checkpoint", (x, weight, bias, eps, out), (x, weight, bias, out), stream)
+    if stream is None:
+        y, codes, scales, rstd = _linear._native.layer_norm_checkpoint(x, weight, bias, eps, out)
+    else:
+        y, codes, scales, rstd = _linear._on(stream, _linear._native.layer_norm_checkpoint, (x, weight, bias, eps, out),
+                                             (x, weight, bias, out))
     return y, Fp8Rows(codes, scales), rstd
 
 
@@ -59,7 +58,10 @@ def layer_norm_restore(kept: Fp8Rows, weight=None, bias=None, dtype=None, *, out
 
     weight and bias have `dtype` or float32; without either y holds the kept values.
     """
-    return _call("layer_norm_restore", (kept, weight, bias, dtype, out), (*_parts(kept), weight, bias, out), stream)
+    if stream is None:
+        return _linear._native.layer_norm_restore(kept, weight, bias, dtype, out)
+    return _linear._on(stream, _linear._native.layer_norm_restore, (kept, weight, bias, dtype, out),
+                       (*_parts(kept), weight, bias, out))
 
 
 def layer_norm_backward_checkpoint(dy, kept: Fp8Rows, weight, rstd, *, dx=None, grad_dtype=None, stream=None):
@@ -68,5 +70,7 @@ def layer_norm_backward_checkpoint(dy, kept: Fp8Rows, weight, rstd, *, dx=None, 
     dx has dy's dtype and shape; weight, ``dx`` and ``grad_dtype`` are as ``layer_norm_backward`` takes
     them.  The same inputs give the same bits.
     """
-    return _call("layer_norm_backward_checkpoint", (dy, kept, weight, rstd, dx, grad_dtype),
-                 (dy, *_parts(kept), weight, rstd, dx), stream)
+    if stream is None:
+        return _linear._native.layer_norm_backward_checkpoint(dy, kept, weight, rstd, dx, grad_dtype)
+    return _linear._on(stream, _linear._native.layer_norm_backward_checkpoint, (dy, kept, weight, rstd, dx, grad_dtype),
+                       (dy, *_parts(kept), weight, rstd, dx))

@@ -164,7 +164,18 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                 for (int32_t u = lane * 8; u < p.I; u += 256) *reinterpret_cast<uint4 *>(row + u) = make_uint4(0, 0, 0, 0);
             }
         }
-        if (tile < tiles[groups]) w = group_tile<1, TN, MODE>(p, groups, start, tiles, tile);
+        if (tile < tiles[groups]) {
+            int lo = 0, hi = groups;  // tiles[lo] <= tile < tiles[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (tiles[mid] <= tile) {
+                    lo = mid;
+                } else {
+                    hi = mid;
+                }
+            }
+            w = group_tile<1, TN, MODE>(p, start, tiles, tile, lo);
+        }
     }
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     const bool work = w.n > 0;  // all CTAs of a cluster alike

@@ -67,6 +67,11 @@ int64_t most_tiles(int64_t rows, int64_t groups, int64_t tile) {
     return some + (rows - some) / tile;
 }
 
+uint32_t band_inverse(int64_t i_tiles) {
+    const uint64_t band = static_cast<uint64_t>(i_tiles) * kGroupBand;
+    return static_cast<uint32_t>(((uint64_t(1) << 32) + band - 1) / band);
+}
+
 template <typename... P>
 int launch_cluster(void (*kernel)(P...), int64_t ctas, unsigned threads, unsigned cluster, size_t smem, cudaStream_t stream,
                    const P &...args) {
@@ -103,6 +108,7 @@ int launch_tile(const Call &c) {
     const int64_t most = MODE == kGroupTN ? p.groups * i_tiles * j_tiles : most_tiles(p.rows, groups, TN) * i_tiles;
     if (most > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
     p.i_tiles = static_cast<int32_t>(i_tiles);
+    p.band_inverse = band_inverse(i_tiles);
     p.j_tiles = static_cast<int32_t>(j_tiles);
     CUtensorMap tmP = {}, tmQ = {}, tmD = {}, tmU = {}, tmH = {};  // P's and Q's are not used by sums of nothing
     if (MODE != kGroupDown && !encode(&tmD, c.D, 32)) return GEMM_ERR_CUDA;
@@ -163,6 +169,7 @@ int launch_few(const Call &c) {
     const int64_t most = most_tiles(p.rows, MODE == kGroupLora ? 1 : p.groups, TN) * i_tiles;
     if (most * KS > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
     p.i_tiles = static_cast<int32_t>(i_tiles);
+    p.band_inverse = band_inverse(i_tiles);
     CUtensorMap tmP = {}, tmQ = {}, tmU = {}, tmH = {};  // not used by sums of nothing
     if (c.P.rows > 0 && c.P.cols > 0 && c.Q.rows > 0 && c.Q.cols > 0) {
         if (!encode(&tmP, c.P, MODE == kGroupNN ? 64 : 128) || !encode(&tmQ, c.Q, TN)) return GEMM_ERR_CUDA;

@@ -210,6 +210,7 @@ struct GroupParams {
     int32_t groups, rows;
     int32_t I, J, R;             // sizes; the ragged one is `rows`
     int32_t i_tiles, j_tiles;    // of a group; j_tiles for TN
+    uint32_t band_inverse;       // 2^32 / (kGroupBand * i_tiles), rounded up
     int32_t bf16;
     int32_t zero_rest;
     // adapters
@@ -232,29 +233,37 @@ struct GroupTile {
 // read again for each band.
 constexpr int kGroupBand = 8;
 
+// n / d for d >= 1 by d's rounded-up 2^32 / d: one too many at most, which the product shows.
+__device__ __forceinline__ int div_by(int n, int d, uint32_t inverse) {
+    if (d == 1) return n;
+    const int q = static_cast<int>(__umulhi(static_cast<uint32_t>(n), inverse));
+    return q * d > n ? q - 1 : q;
+}
+
+// Tile t, t not before the one asked for last; `group` is that one's group (0 at first).
+// A role asks once a tile, and tiles of short sums take some 2000 cycles, so there is no
+// division here (band: kGroupBand * i_tiles, and its inverse).
 template <int CG, int TN, int MODE>
-__device__ __forceinline__ GroupTile group_tile(const GroupParams &p, int groups, const int32_t *start,
-                                                const int32_t *tiles, int t) {
-    int lo = 0, hi = groups;  // tiles[lo] <= t < tiles[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (tiles[mid] <= t) {
-            lo = mid;
-        } else {
-            hi = mid;
-        }
-    }
-    const int32_t first = start[lo], count = start[lo + 1] - first;
+__device__ __forceinline__ GroupTile group_tile(const GroupParams &p, const int32_t *start, const int32_t *tiles, int t,
+                                                int &group) {
+    while (tiles[group + 1] <= t) ++group;
+    const int32_t first = start[group], count = start[group + 1] - first;
     const int32_t J = MODE == kGroupTN ? p.J : count;
     const int j_tiles = (J + TN - 1) / TN;
-    int l = t - tiles[lo];
-    const int band = l / (kGroupBand * p.i_tiles);
+    int l = t - tiles[group];
+    const int band = div_by(l, kGroupBand * p.i_tiles, p.band_inverse);
     const int width = j_tiles - band * kGroupBand < kGroupBand ? j_tiles - band * kGroupBand : kGroupBand;
     l -= band * kGroupBand * p.i_tiles;
+    constexpr uint32_t kInverse[kGroupBand + 1] = {0,          0,          0x80000000, 0x55555556, 0x40000000,
+                                                   0x33333334, 0x2aaaaaab, 0x24924925, 0x20000000};
+    uint32_t inverse = kInverse[kGroupBand];
+#pragma unroll
+    for (int d = 2; d < kGroupBand; ++d) inverse = width == d ? kInverse[d] : inverse;
+    const int i = div_by(l, width, inverse);
     GroupTile w;
-    w.group = lo;
-    w.i0 = l / width * (128 * CG);
-    const int32_t j = (band * kGroupBand + l % width) * TN;
+    w.group = group;
+    w.i0 = i * (128 * CG);
+    const int32_t j = (band * kGroupBand + l - i * width) * TN;
     w.n = J - j < TN ? J - j : TN;
     w.j0 = MODE == kGroupTN ? j : first + j;
     w.r0 = MODE == kGroupTN ? first : 0;
@@ -427,7 +436,8 @@ __global__ void __launch_bounds__(384, 1)
     ptx::tcgen05_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     const int total = tiles[groups];
-    auto tile_of = [&](int t) { return group_tile<CG, TN, MODE>(p, groups, start, tiles, t); };
+    int group = 0;  // of a role's last tile
+    auto tile_of = [&](int t) { return group_tile<CG, TN, MODE>(p, start, tiles, t, group); };
     // K tiles over the ranks, two of each 64: with h rounded and with the rest of it
     auto rank_tiles = [&](const GroupTile &w) {
         return MODE == kGroupLora && chosen[w.group] >= 0 ? p.rank_pad / 64 * 2 : 0;

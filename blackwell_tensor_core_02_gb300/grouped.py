@@ -65,16 +65,24 @@ def _call(name, args, stream, options):
     return call(*args) if stream is None else _linear._on(stream, call, args, args[:-1])
 
 
+# The calls below go to the binding at once where neither a stream nor options are given: the
+# smallest take less time on the GPU than the way through _call.
+
+
 def grouped_gemm_nt(A, B, offsets, D=None, *, stream=None, options: GroupedOptions | None = None):
     """D[r] = A[r]·B[e]ᵀ for the rows r of group e; A rows x K, B groups x N x K, D rows x N.
 
     Rows without a group are 0 in a D that the call makes, and left as they are in a given one.
     """
+    if stream is None and options is None:
+        return _linear._native.grouped_gemm_nt(A, B, offsets, D, 0)
     return _call("grouped_gemm_nt", (A, B, offsets, D), stream, options)
 
 
 def grouped_gemm_nn(dD, B, offsets, dA=None, *, stream=None, options: GroupedOptions | None = None):
     """The gradient of ``grouped_gemm_nt`` for A: dA[r] = dD[r]·B[e]; rows without a group as there."""
+    if stream is None and options is None:
+        return _linear._native.grouped_gemm_nn(dD, B, offsets, dA, 0)
     return _call("grouped_gemm_nn", (dD, B, offsets, dA), stream, options)
 
 
@@ -83,6 +91,8 @@ def grouped_gemm_tn(dD, A, offsets, dB=None, *, stream=None, options: GroupedOpt
 
     Rows without a group count for nothing, whatever they hold.
     """
+    if stream is None and options is None:
+        return _linear._native.grouped_gemm_tn(dD, A, offsets, dB, 0)
     return _call("grouped_gemm_tn", (dD, A, offsets, dB), stream, options)
 
 
@@ -95,6 +105,8 @@ def gemm_lora_nt(x, W, down, up, offsets, adapters, D=None, *, scales=None, stre
     request and each adapter.  An adapter out of range (-1) and rows without a request have the
     shared product alone.  No row's result depends on another row's adapter.
     """
+    if stream is None and options is None:
+        return _linear._native.gemm_lora_nt(x, W, down, up, offsets, adapters, D, scales, 0)
     return _call("gemm_lora_nt", (x, W, down, up, offsets, adapters, D, scales), stream, options)
 
 

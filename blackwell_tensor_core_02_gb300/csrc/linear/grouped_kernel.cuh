@@ -233,6 +233,9 @@ struct GroupTile {
 // read again for each band.
 constexpr int kGroupBand = 8;
 
+// A sum from which on results leave by the copy engine.
+constexpr int kLongSum = 512;
+
 // n / d for d >= 1 by d's rounded-up 2^32 / d: one too many at most, which the product shows.
 __device__ __forceinline__ int div_by(int n, int d, uint32_t inverse) {
     if (d == 1) return n;
@@ -591,6 +594,7 @@ __global__ void __launch_bounds__(384, 1)
         const int quarter = warp % 4, team = (warp - 4) / 4;
         const uint32_t tempty = CG == 2 ? ptx::mapa(bar_tempty, 0) : bar_tempty;
         const int tid = static_cast<int>(threadIdx.x) % 128;  // in the team
+        const int x = tid % 16, y = tid / 16;
         const uint32_t barrier = 1u + static_cast<uint32_t>(team);
         uint16_t *out = static_cast<uint16_t *>(p.out);
         const uint4 none = make_uint4(0, 0, 0, 0);
@@ -609,8 +613,8 @@ __global__ void __launch_bounds__(384, 1)
             const int32_t width = p.I - i0 < 128 ? p.I - i0 : 128;  // of this CTA's columns
             uint16_t *at = out + (MODE == kGroupTN ? w.group * p.out_group : 0) + static_cast<int64_t>(w.j0) * p.out_row + i0;
             if (w.r == 0) {  // a sum of nothing
-                for (int32_t j = team * 8 + tid / 16; j < w.n; j += 16) {
-                    if (tid % 16 * 8 < width) *reinterpret_cast<uint4 *>(at + j * p.out_row + tid % 16 * 8) = none;
+                for (int32_t j = team * 8 + y; j < w.n; j += 16) {
+                    if (x * 8 < width) *reinterpret_cast<uint4 *>(at + j * p.out_row + x * 8) = none;
                 }
                 continue;
             }
@@ -687,8 +691,11 @@ __global__ void __launch_bounds__(384, 1)
                                          pack_pair(p.bf16, hi[4 * n + 4], hi[4 * n + 5]),
                                          pack_pair(p.bf16, hi[4 * n + 6], hi[4 * n + 7]));
                 }
-                const int32_t rows = w.n - c * 32;  // of the chunk that count
-                if (MODE == kGroupTN || rows >= 32) {
+                // By the copy engine, which needs no thread, where a tile's MMAs take longer than
+                // its epilogue: weights of 8 groups of 1024 rows, 4096 x 4096, 151 us, by threads
+                // 156.  By threads, which need not wait for it, where the epilogue is what takes
+                // the time: 32 groups of 16 rows, 1416 x 2040, 43 us, by the copy engine 51.
+                if ((MODE == kGroupTN || w.n - c * 32 >= 32) && w.r >= kLongSum) {
                     ptx::fence_proxy_async_smem();
                     ptxg::sync_128(barrier);
                     if (tid == 0) {
@@ -701,19 +708,23 @@ __global__ void __launch_bounds__(384, 1)
                                 ptx::tma_store_2d(&tmD, buf + b * C::BOX, i0 + b * 64, w.j0 + c * 32);
                             }
                         }
+                        ptx::bulk_commit_group();
                     }
-                } else {
-                    // the rows behind a group's end belong to the next
-                    ptxg::sync_128(barrier);
-                    for (int32_t u = tid; u < rows * 16; u += 128) {
-                        const int32_t j = u / 16, x = u % 16;
-                        if (x * 8 >= width) continue;
-                        const uint4 v = ptx::ld_shared_v4(buf + static_cast<uint32_t>((x >> 3) * C::BOX + j * 128) +
-                                                          ((static_cast<uint32_t>(x & 7) ^ (j & 7u)) * 16u));
-                        *reinterpret_cast<uint4 *>(at + (c * 32 + j) * p.out_row + x * 8) = v;
-                    }
+                    continue;
                 }
-                if (tid == 0) ptx::bulk_commit_group();
+                ptxg::sync_128(barrier);
+                // 16 threads a row, 16 bytes each; rows behind a group's end belong to the next
+                const uint32_t from = buf + static_cast<uint32_t>(x / 8) * C::BOX + static_cast<uint32_t>(y) * 128u +
+                                      ((static_cast<uint32_t>(x & 7) ^ (y & 7u)) * 16u);
+                uint16_t *to = at + (c * 32 + y) * p.out_row + x * 8;
+                const int32_t rows = x * 8 < width ? w.n - c * 32 - y : 0;
+                uint4 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = ptx::ld_shared_v4(from + k * 8 * 128);
+#pragma unroll
+                for (int k = 0; k < 4; ++k, to += 8 * p.out_row) {
+                    if (k * 8 < rows) *reinterpret_cast<uint4 *>(to) = v[k];
+                }
             }
             acc.advance();
             }

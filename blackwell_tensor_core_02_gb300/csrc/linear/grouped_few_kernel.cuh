@@ -38,7 +38,7 @@ struct FewShape {
     static constexpr int OFF_START = LORA ? SUMS : 0, OFF_TILES = OFF_START + LIST;
     static constexpr int OFF_ROWS = OFF_TILES + LIST;             // int32 [TN]: the rows' adapters
     static constexpr int OFF_PIECES = OFF_ROWS + TN * 4;          // Piece [TN], behind it their number
-    static constexpr int OFF_BAR = OFF_PIECES + TN * 4 + 8;
+    static constexpr int OFF_BAR = OFF_PIECES + (LORA ? TN * 16 : 0) + 16;
     static constexpr int MOST_STAGES = 12;
     // full, empty [stages]; done, list, pieces full, pieces free, drain
     static constexpr int OFF_MISC = OFF_BAR + (2 * MOST_STAGES + 5) * 8;
@@ -57,11 +57,16 @@ struct FewShape {
     static_assert(LORA || (PAIRED >= 3 && PAIRED * STAGE >= SUMS), "two CTAs an SM");
 };
 
-// Rows [first, first + rows) of the tile, at columns [column, column + rows in whole 16s) of
-// those for pieces; where the columns start again from 0, they are a turn's first.
-struct Piece {
-    uint8_t first, rows;
-    uint16_t column;
+// A piece as the producer and the MMA issuer take it, ready for use (a thread by itself
+// issues an instruction every few cycles: with these taken apart piece by piece, one cost
+// it 600 cycles, the MMAs' four times).
+struct alignas(16) Piece {
+    uint32_t idesc;
+    uint16_t column;  // of the TMEM columns for pieces: [column, column + rows in whole 16s)
+    uint8_t first;    // row of the tile
+    uint8_t rows;
+    int32_t adapter;
+    uint32_t turn;    // 1: the columns start again from 0, when the pieces before have been read
 };
 
 __device__ __forceinline__ float2 widen16(bool bf16, uint32_t w) {
@@ -112,7 +117,7 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     int32_t *start = reinterpret_cast<int32_t *>(smem + C::OFF_START), *tiles = reinterpret_cast<int32_t *>(smem + C::OFF_TILES);
-    int32_t *chosen = reinterpret_cast<int32_t *>(smem + C::OFF_ROWS), *piece_count = reinterpret_cast<int32_t *>(smem + C::OFF_PIECES) + TN;
+    int32_t *chosen = reinterpret_cast<int32_t *>(smem + C::OFF_ROWS), *piece_count = reinterpret_cast<int32_t *>(smem + C::OFF_BAR) - 4;
     Piece *pieces = reinterpret_cast<Piece *>(smem + C::OFF_PIECES);
 
     if (warp == 0 && lane == 0) {
@@ -182,7 +187,6 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
     const int k_tiles = work ? (w.r + 63) / 64 : 0;
     const int kt_begin = static_cast<int>(static_cast<int64_t>(k_tiles) * rank / KS);
     const int kt_end = static_cast<int>(static_cast<int64_t>(k_tiles) * (rank + 1) / KS);
-    const int rank_tiles = LORA ? p.rank_pad / 64 : 0;  // stages of a piece
 
     if (warp == 0) {
         if (work && ptx::elect_one()) {
@@ -209,9 +213,10 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                 ok = ok && wait_bounded(bar_list, 0, abort_flag, p.timeout_ns, kWaitProducer, 0);
                 const int count = ok ? *piece_count : 0;
                 if (count > 0) ptx::griddep_wait();
+                Piece piece = pieces[0];
                 for (int q = 0, c = 0; ok && q < count;) {
-                    const Piece piece = pieces[q];
-                    const int j = piece.first, boxes = (piece.rows + 15) / 16;  // of 16 rows of h
+                    const int32_t row = w.j0 + piece.first, a = piece.adapter;
+                    const int boxes = (piece.rows + 15) / 16;  // of 16 rows of h
                     if (!wait_bounded(bar_empty + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitProducer, q)) {
                         ok = false;
                         break;
@@ -219,14 +224,14 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                     const int s = ring.stage;
                     const uint32_t sq = base + off_q + s * C::Q_BYTES, full = bar_full + 8 * s;
                     ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(C::P_BYTES + 2 * boxes * 2048));
-                    ptxg::tma_load_3d(base + s * C::P_BYTES, &tmU, full, c, w.i0, chosen[j]);
+                    ptxg::tma_load_3d(base + s * C::P_BYTES, &tmU, full, c, w.i0, a);
                     for (int b = 0; b < boxes; ++b) {
-                        ptx::tma_load_2d(sq + b * 2048, &tmH, full, c, w.j0 + j + 16 * b);
-                        ptx::tma_load_2d(sq + C::PIECE * 128 + b * 2048, &tmH, full, p.rank_pad + c, w.j0 + j + 16 * b);
+                        ptx::tma_load_2d(sq + b * 2048, &tmH, full, c, row + 16 * b);
+                        ptx::tma_load_2d(sq + C::PIECE * 128 + b * 2048, &tmH, full, p.rank_pad + c, row + 16 * b);
                     }
                     ring.advance();
                     c += 64;
-                    if (c >= p.rank) c = 0, ++q;
+                    if (c >= p.rank) c = 0, piece = pieces[++q];
                 }
             }
             if (!ok) {  // time for loads in flight to land before the shared memory goes
@@ -261,9 +266,10 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                 ok = ok && wait_bounded(bar_list, 0, abort_flag, p.timeout_ns, kWaitMma, 0);
                 const int count = ok ? *piece_count : 0;
                 uint32_t turn = 0;  // pieces that had their columns at once
+                Piece piece = pieces[0];
                 for (int q = 0; ok && q < count; ++q) {
-                    const Piece piece = pieces[q];
-                    if (q > 0 && piece.column == 0) {  // the epilogue has read the pieces before
+                    const uint32_t d = tmem_base + TN + piece.column, piece_idesc = piece.idesc;
+                    if (piece.turn) {  // the epilogue has read the pieces before
                         ptx::mma_commit<1>(bar_pfull, 0x1);
                         if (!wait_bounded(bar_pfree, turn & 1u, abort_flag, p.timeout_ns, kWaitMma, q)) {
                             ok = false;
@@ -272,9 +278,8 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                         ++turn;
                         ptx::tcgen05_fence_after();
                     }
-                    const uint32_t d = tmem_base + TN + piece.column;
-                    const uint32_t piece_idesc = group_idesc<1, MODE>((piece.rows + 15) / 16 * 16, p.bf16);
-                    for (int c = 0; c < rank_tiles; ++c) {
+                    piece = pieces[q + 1];  // behind the last one: anything
+                    for (int c = 0; c < p.rank; c += 64) {
                         if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitMma, q)) {
                             ok = false;
                             break;
@@ -283,9 +288,15 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                         const int s = ring.stage;
                         const uint32_t up = p_low + static_cast<uint32_t>(s * (C::P_BYTES >> 4));
                         const uint32_t high = q_low + static_cast<uint32_t>(s * (C::Q_BYTES >> 4)), low = high + (C::PIECE * 128 >> 4);
-                        const int steps = p.rank - c * 64 >= 64 ? 4 : (p.rank - c * 64 + 15) / 16;
-                        ptxg::mma_stage<1, 2, 2>(d, up, high, piece_idesc, steps, c == 0);
-                        ptxg::mma_stage<1, 2, 2>(d, up, low, piece_idesc, steps, false);
+                        const int left = p.rank - c;
+                        if (left <= 16) {
+                            ptxg::mma_f16<1>(d, up, high, piece_idesc, c ? 1u : 0u);
+                            ptxg::mma_f16<1>(d, up, low, piece_idesc, 1u);
+                        } else {
+                            const int steps = left >= 64 ? 4 : (left + 15) / 16;
+                            ptxg::mma_stage<1, 2, 2>(d, up, high, piece_idesc, steps, c == 0);
+                            ptxg::mma_stage<1, 2, 2>(d, up, low, piece_idesc, steps, false);
+                        }
                         ptx::mma_commit<1>(bar_empty + 8 * s, 0x1);
                         ring.advance();
                     }
@@ -327,8 +338,10 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                     while (j + n < last && (next = chosen[j + n]) == a && n < C::PIECE) ++n;
                     if (a >= 0) {
                         const int columns = (n + 15) / 16 * 16;
-                        if (column + columns > C::PIECE_COLS) column = 0;
-                        pieces[count++] = {static_cast<uint8_t>(j), static_cast<uint8_t>(n), static_cast<uint16_t>(column)};
+                        const bool turn = column + columns > C::PIECE_COLS;
+                        if (turn) column = 0;
+                        pieces[count++] = {group_idesc<1, MODE>(columns, p.bf16), static_cast<uint16_t>(column),
+                                           static_cast<uint8_t>(j), static_cast<uint8_t>(n), a, turn ? 1u : 0u};
                         column += columns;
                     }
                     j += n;
@@ -375,7 +388,7 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                     int some = 0;
 #pragma unroll
                     for (int s = 0; s < B; ++s) {
-                        if (s == some && q + s < count && pieces[q + s].rows == 1 && (s == 0 || pieces[q + s].column != 0)) {
+                        if (s == some && q + s < count && pieces[q + s].rows == 1 && (s == 0 || !pieces[q + s].turn)) {
                             ptxg::tmem_ld_32x32b_x1(taddr + TN + pieces[q + s].column, v[s]);
                             ++some;
                         }
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                     }
                     // 16 columns of two pieces at once, or of one of more
                     const Piece piece = pieces[q];
-                    const bool two = piece.rows <= 16 && q + 1 < count && pieces[q + 1].column != 0 && pieces[q + 1].rows <= 16;
+                    const bool two = piece.rows <= 16 && q + 1 < count && !pieces[q + 1].turn && pieces[q + 1].rows <= 16;
                     const Piece next = pieces[two ? q + 1 : q];
                     uint32_t x[16];
                     for (int c = 0; c < piece.rows; c += 16) {
@@ -411,7 +424,7 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                         ++q;
                     }
                     ++q;
-                } while (q < count && pieces[q].column != 0);
+                } while (q < count && !pieces[q].turn);
                 ptx::tcgen05_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar_pfree);

@@ -279,27 +279,28 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                         ptx::tcgen05_fence_after();
                     }
                     piece = pieces[q + 1];  // behind the last one: anything
-                    for (int c = 0; c < p.rank; c += 64) {
+                    // little code: a thread by itself waits for each line of it that is not at hand
+                    uint32_t more = 0;
+                    int left = p.rank;
+#pragma unroll 1
+                    do {
                         if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitMma, q)) {
                             ok = false;
                             break;
                         }
                         ptx::tcgen05_fence_after();
-                        const int s = ring.stage;
-                        const uint32_t up = p_low + static_cast<uint32_t>(s * (C::P_BYTES >> 4));
-                        const uint32_t high = q_low + static_cast<uint32_t>(s * (C::Q_BYTES >> 4)), low = high + (C::PIECE * 128 >> 4);
-                        const int left = p.rank - c;
-                        if (left <= 16) {
-                            ptxg::mma_f16<1>(d, up, high, piece_idesc, c ? 1u : 0u);
-                            ptxg::mma_f16<1>(d, up, low, piece_idesc, 1u);
-                        } else {
-                            const int steps = left >= 64 ? 4 : (left + 15) / 16;
-                            ptxg::mma_stage<1, 2, 2>(d, up, high, piece_idesc, steps, c == 0);
-                            ptxg::mma_stage<1, 2, 2>(d, up, low, piece_idesc, steps, false);
+                        uint32_t up = p_low + static_cast<uint32_t>(ring.stage * (C::P_BYTES >> 4));
+                        uint32_t high = q_low + static_cast<uint32_t>(ring.stage * (C::Q_BYTES >> 4));
+                        const int end = left > 64 ? left - 64 : 0;
+#pragma unroll 1
+                        for (; left > end; left -= 16, up += 2, high += 2, more = 1) {
+                            ptxg::mma_f16<1>(d, up, high, piece_idesc, more);
+                            ptxg::mma_f16<1>(d, up, high + (C::PIECE * 128 >> 4), piece_idesc, 1u);
                         }
-                        ptx::mma_commit<1>(bar_empty + 8 * s, 0x1);
+                        left = end;
+                        ptx::mma_commit<1>(bar_empty + 8 * ring.stage, 0x1);
                         ring.advance();
-                    }
+                    } while (left > 0);
                 }
                 if (ok && count > 0) ptx::mma_commit<1>(bar_pfull, 0x1);
             }

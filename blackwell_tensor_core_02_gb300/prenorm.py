@@ -2,12 +2,19 @@
 
     python -m blackwell_tensor_core_02_gb300.prenorm --tokens 1 64 2048 --width 4096 --out 4096
     python -m blackwell_tensor_core_02_gb300.prenorm --tokens 8192 --width 4096 --out 28672 --format nv
+    python -m blackwell_tensor_core_02_gb300.prenorm --tokens 64 --adapters 8 --rank 16
+    python -m blackwell_tensor_core_02_gb300.prenorm --tokens 4096 --checkpoint --experts 16 --top 2
 
 Training runs in fp16: layer norm, the product, and their gradients (three products and the norm's
 gradient).  Serving quantises the weights once and each call's normalised tokens, and multiplies the
 4-bit matrices.  The command prints one JSON line per number of tokens: the time of a serving call,
 of the fp16 forward and of a training step (CUDA events over a run of calls), and how far the served
 result is from the fp16 one (2-norm, relative).
+
+``--checkpoint`` keeps the normalised rows in 8 bits between a training step's passes, in place of the
+layer's input and of the norm's result.  ``--adapters`` serves the tokens in as many requests, each with
+a low-rank adapter of its own beside the shared fp16 weights.  ``--experts`` runs the layer with a weight
+matrix for each expert, each token through ``--top`` of them.
 """
 from __future__ import annotations
 
@@ -31,24 +38,33 @@ class PreNormLinear:
 
     ``forward``/``backward`` are a training step's two passes; ``quantize`` makes the 4-bit copy of
     W that ``serve`` uses.  Widths, outputs and, in ``backward``, tokens are multiples of 8
-    (``gemm_f16_nt``'s shapes); ``serve`` takes any.
+    (``gemm_f16_nt``'s shapes); ``serve`` takes any.  With ``checkpoint`` the normalised rows stay between
+    the passes, in 8 bits (``layer_norm_checkpoint``), not x and the norm's result.
     """
 
-    def __init__(self, weight, scale, shift, eps: float = 1e-5):
-        self.weight, self.scale, self.shift, self.eps = weight, scale, shift, eps
+    def __init__(self, weight, scale, shift, eps: float = 1e-5, checkpoint: bool = False):
+        self.weight, self.scale, self.shift, self.eps, self.checkpoint = weight, scale, shift, eps, checkpoint
         self.weight4 = None
 
     def forward(self, x):
         """(y, what ``backward`` needs)."""
+        if self.checkpoint:
+            h, rows, rstd = g.layer_norm_checkpoint(x, self.scale, self.shift, self.eps)
+            return g.gemm_f16_nt(h, self.weight), (rows, rstd)
         h, mean, rstd = g.layer_norm(x, self.scale, self.shift, self.eps)
         return g.gemm_f16_nt(h, self.weight), (x, h, mean, rstd)
 
     def backward(self, dy, kept):
         """(dx, dweight, dscale, dshift) for the gradient dy of y."""
-        x, h, mean, rstd = kept
         dh = g.gemm_f16_nt(dy, self.weight.t().contiguous())                # dy·W
+        if self.checkpoint:
+            rows, rstd = kept
+            h = g.layer_norm_restore(rows, self.scale, self.shift)
+            dx, dscale, dshift = g.layer_norm_backward_checkpoint(dh, rows, self.scale, rstd)
+        else:
+            x, h, mean, rstd = kept
+            dx, dscale, dshift = g.layer_norm_backward(dh, x, self.scale, mean, rstd)
         dweight = g.gemm_f16_nt(dy.t().contiguous(), h.t().contiguous())    # dyᵀ·h
-        dx, dscale, dshift = g.layer_norm_backward(dh, x, self.scale, mean, rstd)
         return dx, dweight, dscale, dshift
 
     def quantize(self, format: str = "mx") -> None:
@@ -63,13 +79,83 @@ class PreNormLinear:
         h = g.layer_norm(x, self.scale, self.shift, self.eps)[0]
         return g.gemm_fp4_nt(g.quantize_fp4(h, self.weight4.format), self.weight4)
 
+    def serve_adapted(self, x, down, up, offsets, adapters, scales=None):
+        """The fp16 layer for tokens of many requests, each with its own adapter (``gemm_lora_nt``)."""
+        h = g.layer_norm(x, self.scale, self.shift, self.eps)[0]
+        return g.gemm_lora_nt(h, self.weight, down, up, offsets, adapters, scales=scales)
 
-def make_layer(width: int, out: int, seed: int = 0) -> PreNormLinear:
+
+class PreNormExperts:
+    """y[t] = Σ_j gates[t, j]·layer_norm(x[t]; scale, shift)·W[chosen[t, j]]ᵀ, W (experts × out × width).
+
+    x (tokens × width), scale, shift and W share float16 or bfloat16; ``chosen`` (tokens × top, integers)
+    names each token's experts, ``gates`` weighs them.  Widths and outputs are multiples of 8.  Between the
+    passes the normalised rows stay in 8 bits; each token's rows are gathered from them again.
+    """
+
+    def __init__(self, weights, scale, shift, eps: float = 1e-5):
+        self.weights, self.scale, self.shift, self.eps = weights, scale, shift, eps
+
+    def route(self, chosen):
+        """(token of each grouped row, place of each token's row among them, the groups' offsets); an
+        expert out of range counts as none: its rows stand before or behind the groups."""
+        experts = chosen.reshape(-1)
+        order = experts.argsort(stable=True)
+        place = torch.empty_like(order).scatter_(0, order, torch.arange(order.numel(), device=order.device))
+        bounds = torch.arange(self.weights.shape[0] + 1, device=chosen.device, dtype=experts.dtype)
+        offsets = torch.searchsorted(experts[order], bounds)
+        return order // chosen.shape[1], place, offsets
+
+    def forward(self, x, chosen, gates):
+        """(y, what ``backward`` needs)."""
+        h, rows, rstd = g.layer_norm_checkpoint(x, self.scale, self.shift, self.eps)
+        token, place, offsets = self.route(chosen)
+        out = g.grouped_gemm_nt(h[token], self.weights, offsets)
+        y = (out[place].view(*chosen.shape, -1).float() * gates.float()[..., None]).sum(1).to(x.dtype)
+        return y, (rows, rstd, token, place, offsets, gates)
+
+    def backward(self, dy, kept):
+        """(dx, dweights, dscale, dshift, dgates) for the gradient dy of y."""
+        rows, rstd, token, place, offsets, gates = kept
+        h = g.layer_norm_restore(rows, self.scale, self.shift)[token]
+        dout = dy[token]
+        dh = g.grouped_gemm_nn(dout, self.weights, offsets)                 # before the gates
+        dgates = (dh.float() * h.float()).sum(1)[place].view(gates.shape)
+        row_gates = torch.empty_like(gates).view(-1).scatter_(0, place, gates.reshape(-1))
+        dweights = g.grouped_gemm_tn((dout.float() * row_gates.float()[:, None]).to(dy.dtype), h, offsets)
+        dh = (dh[place].view(*gates.shape, -1).float() * gates.float()[..., None]).sum(1).to(dy.dtype)
+        dx, dscale, dshift = g.layer_norm_backward_checkpoint(dh, rows, self.scale, rstd)
+        return dx, dweights, dscale, dshift, dgates.to(gates.dtype)
+
+
+def make_layer(width: int, out: int, seed: int = 0, checkpoint: bool = False) -> PreNormLinear:
     gen = torch.Generator(device="cuda").manual_seed(seed)
     weight = (torch.randn(out, width, generator=gen, device="cuda") * width ** -0.5).half()
     scale = (1 + 0.1 * torch.randn(width, generator=gen, device="cuda")).half()
     shift = (0.1 * torch.randn(width, generator=gen, device="cuda")).half()
-    return PreNormLinear(weight, scale, shift)
+    return PreNormLinear(weight, scale, shift, checkpoint=checkpoint)
+
+
+def make_adapters(layer: PreNormLinear, adapters: int, rank: int, seed: int = 0):
+    """(down, up, scales) of as many random adapters for the layer, fp16 and fp32."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    out, width = layer.weight.shape
+    down = (torch.randn(adapters, rank, width, generator=gen, device="cuda") * width ** -0.5).half()
+    up = (torch.randn(adapters, out, rank, generator=gen, device="cuda") * rank ** -0.5).half()
+    return down, up, torch.rand(adapters, generator=gen, device="cuda") + 0.5
+
+
+def make_experts(width: int, out: int, experts: int, seed: int = 0, dtype=torch.bfloat16) -> PreNormExperts:
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    weights = (torch.randn(experts, out, width, generator=gen, device="cuda") * width ** -0.5).to(dtype)
+    scale = (1 + 0.1 * torch.randn(width, generator=gen, device="cuda")).to(dtype)
+    shift = (0.1 * torch.randn(width, generator=gen, device="cuda")).to(dtype)
+    return PreNormExperts(weights, scale, shift)
+
+
+def even_offsets(tokens: int, requests: int):
+    """Offsets of as many requests of nearly as many tokens each, on the device."""
+    return torch.tensor([tokens * i // requests for i in range(requests + 1)], device="cuda")
 
 
 def _time(call, steps: int) -> float:
@@ -93,9 +179,16 @@ def main(argv=None) -> None:
     ap.add_argument("--out", type=int, default=4096)
     ap.add_argument("--format", choices=["mx", "nv"], default="mx")
     ap.add_argument("--steps", type=int, default=50)
+    ap.add_argument("--checkpoint", action="store_true", help="keep 8 bits an element between a training step's passes")
+    ap.add_argument("--adapters", type=int, default=0, help="serve as many requests, each with its own adapter")
+    ap.add_argument("--rank", type=int, default=16, help="the adapters' rank")
+    ap.add_argument("--experts", type=int, default=0, help="run the layer with as many experts")
+    ap.add_argument("--top", type=int, default=2, help="experts of each token")
     args = ap.parse_args(argv)
-    layer = make_layer(args.width, args.out)
+    layer = make_layer(args.width, args.out, checkpoint=args.checkpoint)
     layer.quantize(args.format)
+    adapters = make_adapters(layer, args.adapters, args.rank) if args.adapters else None
+    experts = make_experts(args.width, args.out, args.experts) if args.experts else None
     for tokens in args.tokens:
         x = torch.randn(tokens, args.width, device="cuda").half()
         y, kept = layer.forward(x)
@@ -107,7 +200,19 @@ def main(argv=None) -> None:
         if tokens % 8 == 0:
             dy = torch.randn_like(y)
             line["step_us"] = round(_time(lambda: layer.backward(dy, layer.forward(x)[1]), args.steps), 2)
-        status = g.fp4_device_status()[0] or g.last_device_status()[0]
+        if adapters:
+            down, up, scales = adapters
+            offsets = even_offsets(tokens, args.adapters)
+            chosen = torch.arange(args.adapters, device="cuda", dtype=torch.int32)
+            line["adapted_us"] = round(_time(lambda: layer.serve_adapted(x, down, up, offsets, chosen, scales), args.steps), 2)
+        if experts:
+            xe = x.to(experts.weights.dtype)
+            chosen = torch.rand(tokens, args.experts, device="cuda").topk(args.top).indices
+            gates = torch.rand(tokens, args.top, device="cuda").softmax(1)
+            dy = torch.randn(tokens, args.out, device="cuda").to(xe.dtype)
+            line["experts_forward_us"] = round(_time(lambda: experts.forward(xe, chosen, gates), args.steps), 2)
+            line["experts_step_us"] = round(_time(lambda: experts.backward(dy, experts.forward(xe, chosen, gates)[1]), args.steps), 2)
+        status = g.fp4_device_status()[0] or g.last_device_status()[0] or g.grouped_device_status()[0]
         print(json.dumps({**line, "status": status}), flush=True)
 
 

@@ -72,6 +72,28 @@ uint32_t band_inverse(int64_t i_tiles) {
     return static_cast<uint32_t>(((uint64_t(1) << 32) + band - 1) / band);
 }
 
+// What TileWalk moves on by.  A group's last rows are a tile that costs less, and such come again
+// after as many tiles as a band has.  Where that number and `clusters` have a common factor, some
+// clusters would get only such tiles and others none: then a turn with which clusters + turn has
+// none of the widths' factors 2, 3, 5 and 7.  4096 x 4096, 76 pairs, with and without, us:
+//   16 groups of 300 rows (2 tiles)  130, 141      8 of 1400 (6)  213, 217   weights 32 of 16, 1416 x 2040 (6)  41.0, 42.3
+//   8 of 700 (3)                     119, 117      8 of 1030 (5)  170, 169   (no common factor: without)
+// Adapters share one matrix, which a turn spreads over more tiles at a time: 11 requests of 372 rows (2)
+// 109, 107; without.
+int32_t turn_of(int mode, const GroupParams &p, int tile, int64_t clusters) {
+    if (mode == kGroupLora || mode == kGroupDown || p.groups == 0) return 0;
+    const int64_t each = mode == kGroupTN ? p.J : (static_cast<int64_t>(p.rows) + p.groups - 1) / p.groups;
+    const int64_t j_tiles = (each + tile - 1) / tile, width = j_tiles < kGroupBand ? j_tiles : kGroupBand;
+    bool common = false;
+    for (int64_t d = 2; d <= width; ++d) common = common || (width % d == 0 && clusters % d == 0);
+    static_assert(kGroupBand <= 10, "the widths' factors");
+    for (int32_t turn = 0; common && turn < clusters; ++turn) {
+        const int64_t n = clusters + turn;
+        if (n % 2 != 0 && n % 3 != 0 && n % 5 != 0 && n % 7 != 0) return turn;
+    }
+    return 0;
+}
+
 template <typename... P>
 int launch_cluster(void (*kernel)(P...), int64_t ctas, unsigned threads, unsigned cluster, size_t smem, cudaStream_t stream,
                    const P &...args) {
@@ -155,6 +177,7 @@ int launch_tile(const Call &c) {
     if (!p.zero_rest && most < grid) grid = most;
     if (c.max_clusters > 0 && c.max_clusters < grid) grid = c.max_clusters;
     if (grid == 0) return GEMM_OK;
+    p.turn = turn_of(MODE, p, TN, grid);
     return launch_cluster(kernel, CG * grid, C::THREADS, CG, C::SMEM_ALLOC, c.stream, tmP, tmQ, tmD, tmU, tmH, tails, p);
 }
 

@@ -211,6 +211,7 @@ struct GroupParams {
     int32_t I, J, R;             // sizes; the ragged one is `rows`
     int32_t i_tiles, j_tiles;    // of a group; j_tiles for TN
     uint32_t band_inverse;       // 2^32 / (kGroupBand * i_tiles), rounded up
+    int32_t turn;                // places that a cluster moves on by with each turn (TileWalk)
     int32_t bf16;
     int32_t zero_rest;
     // adapters
@@ -235,6 +236,20 @@ constexpr int kGroupBand = 8;
 
 // A sum from which on results leave by the copy engine.
 constexpr int kLongSum = 512;
+
+// The tiles of a persistent cluster: one of each turn of `clusters`, `turn` places further on than in
+// the turn before (see turn_of() in grouped_gemm.cu).
+struct TileWalk {
+    int base, place, clusters, turn;
+    __device__ __forceinline__ TileWalk(int cluster, int clusters, int turn)
+        : base(0), place(cluster), clusters(clusters), turn(turn) {}
+    __device__ __forceinline__ int t() const { return base + place; }
+    __device__ __forceinline__ void next() {
+        base += clusters;
+        place += turn;
+        if (place >= clusters) place -= clusters;
+    }
+};
 
 // n / d for d >= 1 by d's rounded-up 2^32 / d: one too many at most, which the product shows.
 __device__ __forceinline__ int div_by(int n, int d, uint32_t inverse) {
@@ -453,8 +468,8 @@ __global__ void __launch_bounds__(384, 1)
             PipelineState ring(C::STAGES, (p.debug_flags & 1u) ? 0u : 1u);
             bool ok = true, waited = false;
             uint32_t seq = 0;
-            for (int t = cluster; ok && t < total; t += clusters, ++seq) {
-                const GroupTile w = tile_of(t);
+            for (TileWalk walk(cluster, clusters, p.turn); ok && walk.t() < total; walk.next(), ++seq) {
+                const GroupTile w = tile_of(walk.t());
                 const int k_tiles = (w.r + 63) / 64, all_tiles = k_tiles + rank_tiles(w);
                 const int32_t i0 = w.i0 + rank * 128, j0 = w.j0 + rank * (columns_of(w) / 2);
                 const int boxes = (columns_of(w) / CG + C::Q_BOX - 1) / C::Q_BOX;  // of Q, in each CTA
@@ -555,8 +570,8 @@ __global__ void __launch_bounds__(384, 1)
             const uint32_t q_low = MODE == kGroupTN ? ptxg::desc_mn_low(sq) : ptxg::desc_k_low(sq);
             bool ok = true;
             uint32_t seq = 0;
-            for (int t = cluster; ok && t < total; t += clusters, ++seq) {
-                const GroupTile w = tile_of(t);
+            for (TileWalk walk(cluster, clusters, p.turn); ok && walk.t() < total; walk.next(), ++seq) {
+                const GroupTile w = tile_of(walk.t());
                 const int k_tiles = (w.r + 63) / 64, all_tiles = k_tiles + rank_tiles(w);
                 if (all_tiles == 0) continue;
                 const uint32_t idesc = group_idesc<CG, MODE>(columns_of(w), p.bf16);
@@ -607,8 +622,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         PipelineState acc(2, 0u);
         uint32_t seq = 0;
-        for (int t = cluster; t < total; t += clusters, ++seq) {
-            const GroupTile w = tile_of(t);
+        for (TileWalk walk(cluster, clusters, p.turn); walk.t() < total; walk.next(), ++seq) {
+            const GroupTile w = tile_of(walk.t());
             const int32_t i0 = w.i0 + rank * 128;
             const int32_t width = p.I - i0 < 128 ? p.I - i0 : 128;  // of this CTA's columns
             uint16_t *at = out + (MODE == kGroupTN ? w.group * p.out_group : 0) + static_cast<int64_t>(w.j0) * p.out_row + i0;

@@ -26,7 +26,7 @@
 // loaded in boxes of 16, 8, 4, 2 and 1 rows, and the rest of its last step, in such boxes
 // too, from behind the matrix, where the copy engine fills zeros.  (Cleared by a warp in
 // shared memory, between the load's arrival and the MMA, they came too late: 8 groups of
-// 1025 rows, 4096 x 4096, took 189 us, of 1024 153; so TAIL_US.)
+// 1025 rows, 4096 x 4096, took 189 us, of 1024 153; so 157 to 163.)
 //
 // LORA and DOWN are the two launches of low-rank adapters beside a shared product, with
 // the rows of a request as a group.  DOWN leaves h = scale_a * x * down_a^T as two

@@ -212,7 +212,7 @@ struct RestoreArgs {
 // a CTA), whose weights it keeps.  Codes come ahead of time through shared memory, four
 // rows at a time and two such batches on their way (a thread copies and reads its own, so
 // there is no barrier); scales, bytes, a batch ahead in registers.  8192 x 4096 bf16
-// RESTORE_US; with a thread's codes in registers alone 21.8, 8 columns a thread 29.1.
+// 14.0 us; with a thread's codes in registers alone 21.8, 8 columns a thread 29.1.
 template <typename T, typename W>
 __global__ void __launch_bounds__(256) norm_restore_kernel(const RestoreArgs a) {
     constexpr int N = 16, R = 4, BATCHES = 3;
@@ -269,14 +269,16 @@ __global__ void __launch_bounds__(256) norm_restore_kernel(const RestoreArgs a) 
                 const uint32_t pair = from_e4m3x2(code[j / 2] >> (j % 2 * 16) & 0xffffu);
                 v[j] = fma2(mul2(__half22float2(*reinterpret_cast<const __half2 *>(&pair)), s), w[j], b[j]);
             }
-            if constexpr (sizeof(T) == 2) {
-                if (sectors) {  // a whole sector in one store, not two halves
+            if (sectors) {  // a whole sector in one store, not two halves (8192 x 4096 to fp32 27.4 us, else 41.4)
+                constexpr int kPairs = 8 / Pair<T>::WORDS;  // of a sector
+#pragma unroll
+                for (int i = 0; i < N / 2; i += kPairs) {
                     uint32_t t[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) Pair<T>::narrow(v[j], t + j);
-                    store_32(y, t);
-                    continue;
+                    for (int j = 0; j < kPairs; ++j) Pair<T>::narrow(v[i + j], t + j * Pair<T>::WORDS);
+                    store_32(y + 2 * i, t);
                 }
+                continue;
             }
             store_pairs<T, N / 2>(y, v);
         }
@@ -388,8 +390,15 @@ int restore_as(const RestoreArgs &a, int sms, cudaStream_t stream) {
     const bool wide = a.cols % 16 == 0 && a.y_stride % 8 == 0 && aligned(a.y, 16) && aligned(a.codes, 16) &&
                       (!a.weight || aligned(a.weight, 16)) && (!a.bias || aligned(a.bias, 16));
     const int64_t units = wide ? a.cols / 16 : (static_cast<int64_t>(a.cols) + 3) / 4;
+    // Threads of a row, of which an eighth at most has no unit: 4096 x 4099 fp16 18.2 us, 4096 x 4160 8.4;
+    // 256 at most, but for short rows, 19.9 and 10.5.  fp32 rows that start anywhere take those:
+    // 8192 x 333 4.3, 7.3 with the former.
     unsigned x = 256;
-    while (x > 8 && x / 2 >= units) x /= 2;
+    if (wide || sizeof(T) == 2) {
+        while (x > 8 && (units + x - 1) / x * x * 8 > units * 9) x /= 2;
+    } else {
+        while (x > 8 && x / 2 >= units) x /= 2;
+    }
     const unsigned y = 256 / x;
     const int64_t across = (units + x - 1) / x;
     // CTAs of four rows a thread, as far as they run at once

@@ -401,6 +401,7 @@ int grouped(int mode, Matrix ragged, Matrix other, Matrix out, const void *offse
 // ------------------------------------------------------------- adapters --
 
 constexpr int64_t kMaxRank = 128;
+constexpr int64_t kRowsOfOneRequest = 128;  // on average, from which on tiles have one request each (see lora())
 
 struct Lora {
     Matrix x, W, down, up, D;
@@ -411,11 +412,18 @@ struct Lora {
     void *workspace;
 };
 
-// h, by CUDA cores for a few rows, else by the tensor cores in tiles of one request each.
+// h, by CUDA cores, whose time goes with rows and ranks, or by the tensor cores in tiles of one
+// request each, whose time hardly does: about alike from 10 to 18 thousand rows x ranks on.  A whole
+// call of 4096 x 4096, by the former and the latter, us:
+//   64 requests of 1 row, rank 16   15.8, 30.2    64 of 4, 32   33.1, 40.6    128 of 4, 16   49.5, 59.6
+//   2 of 64, 64                     20.6, 22.6    64 of 4, 64   48.6, 42.1    128 of 4, 64   81.6, 62.9
+//   2 of 64, 128                    29.1, 23.0    1 of 256, 64  34.0, 24.3
+constexpr int64_t kDownByCores = 12288;
+
 int lora_down(Call &c, const Lora &l) {
     if (c.p.groups == 0) return GEMM_OK;
     int st;
-    if (l.rows <= 256) {
+    if (l.rows * l.rank <= kDownByCores) {
         // three CTAs an SM, with as few ranks each as that allows
         const int64_t fours = (l.rank + 15) / 16 * 16 / kDownRanks;
         int64_t each = 1;
@@ -439,7 +447,8 @@ int lora_down(Call &c, const Lora &l) {
 }
 
 // Requests of many rows: tiles of one request each, the adapter as more of the sum.
-// Requests of few: tiles of any rows, the adapters run by run.
+// Requests of few: tiles of any rows, the adapters run by run.  16 requests of 128 rows, rank 64,
+// 4096 x 4096, the former 65 us, the latter 95; 32 of 64 rows 144 and 92.
 int lora(Call &c, const Lora &l, const Choice &how) {
     const int st = lora_down(c, l);
     if (st != GEMM_OK) return st;
@@ -568,7 +577,7 @@ int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const v
     Choice how = {o.tile, o.split};
     if (how.tile == 0) {
         const int64_t each = p.groups > 0 ? rows / p.groups : rows;
-        how.tile = o.split < 0 || (o.split == 0 && each >= 128) ? 256 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)));
+        how.tile = o.split < 0 || (o.split == 0 && each >= kRowsOfOneRequest) ? 256 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)));
     }
     if (how.tile == 256) return lora(c, l, how);
     const int64_t k_tiles = (K + 63) / 64;

@@ -186,3 +186,11 @@ def test_a_wait_that_runs_out(g, path):
     g.gemm_lora_nt(*b.args(), scales=b.scales, options=bad)
     assert g.grouped_device_status()[0] == TIMEOUT
     check(g, b, **path)
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 40, 96])
+@pytest.mark.parametrize("path", PATHS, ids=lambda p: "-".join(f"{k}{v}" for k, v in p.items()) or "chosen")
+def test_both_ways_to_the_ranks(g, rank, path):
+    """x·downᵀ by either of its kernels: rows x rank below 12288, at it (rank 8, 16, 24, 96) and past it."""
+    for rows in (12288 // rank - 1, 12288 // rank, 12288 // rank + 8):
+        check(g, Batch([rows - 40, 3, 0, 30], [1, -1, 0, 2], 3, rank, 72, 136, F16, 2, 5), **path)

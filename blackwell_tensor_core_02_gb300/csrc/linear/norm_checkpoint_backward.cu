@@ -85,9 +85,9 @@ struct KeptRing {
         }
         return scale_value(t);
     }
-    // the values of unit i of this thread in slot s, 0 past the row's end; all of a warp's
-    // threads call it
-    template <typename S>
+    // the values of unit i of this thread in slot s, 0 past the row's end, without a WIDE unit's
+    // scale if not SCALED; all of a warp's threads call it
+    template <bool SCALED, typename S>
     __device__ __forceinline__ void read(const S &share, int s, int i, const uint8_t *codes, float scale_of_lane,
                                          const uint32_t (&code)[NV], float2 *h) const {
         const uint32_t src = base + static_cast<uint32_t>(s) * SLOT;
@@ -105,7 +105,8 @@ struct KeptRing {
 #pragma unroll
             for (int j = 0; j < U / 2; ++j) {
                 const uint32_t pair = from_e4m3x2(w[j / 2] >> (j % 2 * 16) & 0xffffu);
-                h[j] = mul2(__half22float2(*reinterpret_cast<const __half2 *>(&pair)), scale);
+                h[j] = __half22float2(*reinterpret_cast<const __half2 *>(&pair));
+                if constexpr (SCALED) h[j] = mul2(h[j], scale);
             }
         } else {
             const uint32_t at = src + static_cast<uint32_t>(reinterpret_cast<uintptr_t>(codes) % 16);
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(TPR *KeptGradShape<T, E, WIDE, TPR>::ROWS, 1)
 #pragma unroll
         for (int u = 0; u < Ring::NV; ++u) {
             float2 h[U / 2], g[U / 2];
-            kept.read(ring, ring.slot, u, codes, scale_of_lane, code, h);
+            kept.template read<true>(ring, ring.slot, u, codes, scale_of_lane, code, h);
             ring.read_some(0, dy, u, g);
             const float2 *wu = weights(u);
 #pragma unroll
@@ -230,14 +231,19 @@ __global__ void __launch_bounds__(TPR *KeptGradShape<T, E, WIDE, TPR>::ROWS, 1)
         row_sum<2, TPR, ROWS>(sums, slots[flip][threadIdx.y]);
         flip ^= 1;
         const float2 c1 = both(-sums[0] * a.inv_cols), c2 = both(-sums[1] * a.inv_cols);
+        auto c2_of = [&](int u) {  // with a unit's scale, a power of two, where h comes without
+            if constexpr (WIDE) return mul2(c2, both(scale_value(code[u])));
+            return c2;
+        };
 #pragma unroll
         for (int u = 0; u < Ring::NV; ++u) {
             float2 h[U / 2], g[U / 2];
-            kept.read(ring, ring.slot, u, codes, scale_of_lane, code, h);
+            kept.template read<false>(ring, ring.slot, u, codes, scale_of_lane, code, h);
             ring.read_some(0, dy, u, g);
             const float2 *wu = weights(u);
+            const float2 cu = c2_of(u);
 #pragma unroll
-            for (int i = 0; i < U / 2; ++i) g[i] = mul2(fma2(h[i], c2, fma2(g[i], wu[i], c1)), rs);
+            for (int i = 0; i < U / 2; ++i) g[i] = mul2(fma2(h[i], cu, fma2(g[i], wu[i], c1)), rs);
             ring.scatter_some(dx, u, g);
         }
         ring.next();

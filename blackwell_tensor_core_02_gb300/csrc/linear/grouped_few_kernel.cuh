@@ -4,7 +4,8 @@
 // One CTA of 6 warps per tile of 128 x TN and slice of the sum; KS CTAs of a cluster
 // share a tile's sum, and their fp32 parts meet through distributed shared memory,
 // added in slice order and rounded once.  Two CTAs an SM.  What bounds such a call is
-// the matrix's bytes on few SMs, and a start and end of its own; hence the split.
+// the matrix's bytes on few SMs (of sums over rows, TN: the rows'), and a start and end of
+// its own; hence the split.
 //
 // LORA: all rows are one group, the shared product's, and each row's own adapter is
 // added before the parts meet, after h = scale_a * x * down_a^T from a launch before
@@ -94,11 +95,11 @@ __device__ __forceinline__ float4 few_sums(uint32_t addr) {
 template <int TN, int KS, int MODE>
 __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
     grouped_few_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmH, const GroupParams p,
-                       const int stages) {
+                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmH,
+                       const __grid_constant__ GroupTails<MODE> tails, const GroupParams p, const int stages) {
     constexpr bool LORA = MODE == kGroupLora;
     using C = FewShape<TN, LORA>;
-    static_assert(MODE == kGroupNT || MODE == kGroupNN || LORA, "the rows are the N side");
+    static_assert(MODE != kGroupDown && (MODE != kGroupTN || TN % 64 == 0), "MN-major blocks of 64");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -199,6 +200,11 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                 }
                 const int s = ring.stage;
                 const uint32_t sp = base + s * C::P_BYTES, full = bar_full + 8 * s;
+                if constexpr (MODE == kGroupTN) {
+                    load_sum_rows<1>(p, tmP, tmQ, tails, w, kt * 64, w.i0, w.j0, (w.n + 63) / 64, true, sp, base + off_q + s * C::Q_BYTES, full);
+                    ring.advance();
+                    continue;
+                }
                 ptx::mbar_arrive_expect_tx(full, C::P_BYTES + TN * 128);
                 if constexpr (MODE == kGroupNN) {
 #pragma unroll
@@ -244,8 +250,9 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
         if (work && ptx::elect_one()) {
             PipelineState ring(stages, 0u);
             const uint32_t idesc = group_idesc<1, MODE>((w.n + 15) / 16 * 16, p.bf16);
-            const uint32_t p_low = MODE == kGroupNN ? ptxg::desc_mn_low(base) : ptxg::desc_k_low(base);
-            const uint32_t q_low = ptxg::desc_k_low(base + off_q);
+            constexpr bool kMnP = MODE == kGroupNN || MODE == kGroupTN, kMnQ = MODE == kGroupTN;
+            const uint32_t p_low = kMnP ? ptxg::desc_mn_low(base) : ptxg::desc_k_low(base);
+            const uint32_t q_low = kMnQ ? ptxg::desc_mn_low(base + off_q) : ptxg::desc_k_low(base + off_q);
             bool ok = true;
             for (int kt = kt_begin; kt < kt_end; ++kt) {
                 if (!wait_bounded(bar_full + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns, kWaitMma, kt)) {
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
                 ptx::tcgen05_fence_after();
                 const int s = ring.stage;
                 const int left = w.r - kt * 64;
-                ptxg::mma_stage<1, MODE == kGroupNN ? 128 : 2, 2>(
+                ptxg::mma_stage<1, kMnP ? 128 : 2, kMnQ ? 128 : 2>(
                     tmem_base, p_low + static_cast<uint32_t>(s * (C::P_BYTES >> 4)), q_low + static_cast<uint32_t>(s * (C::Q_BYTES >> 4)),
                     idesc, left >= 64 ? 4 : (left + 15) / 16, kt == kt_begin);
                 ptx::mma_commit<1>(bar_empty + 8 * s, 0x1);
@@ -458,7 +465,8 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
             float4 v = part[0];
 #pragma unroll
             for (int s = 1; s < KS; ++s) v.x += part[s].x, v.y += part[s].y, v.z += part[s].z, v.w += part[s].w;
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + static_cast<int64_t>(w.j0 + j) * p.out_row + col) =
+            uint16_t *out = static_cast<uint16_t *>(p.out) + (MODE == kGroupTN ? w.group * p.out_group : 0);
+            *reinterpret_cast<uint2 *>(out + static_cast<int64_t>(w.j0 + j) * p.out_row + col) =
                 make_uint2(pack_pair(p.bf16, __float_as_uint(v.x), __float_as_uint(v.y)),
                            pack_pair(p.bf16, __float_as_uint(v.z), __float_as_uint(v.w)));
         }

@@ -117,6 +117,17 @@ int launch_cluster(void (*kernel)(P...), int64_t ctas, unsigned threads, unsigne
     return GEMM_OK;
 }
 
+// Maps of sums over rows with boxes of 2^k rows.
+template <int MODE>
+bool encode_tails(const Call &c, GroupTails<MODE> *tails) {
+    if constexpr (MODE == kGroupTN) {
+        for (uint32_t k = 0; k < 5 && c.p.rows > 0; ++k) {
+            if (!encode(&tails->P[k], c.P, 1u << k) || !encode(&tails->Q[k], c.Q, 1u << k)) return false;
+        }
+    }
+    return true;
+}
+
 template <int CG, int TN, int MODE>
 int launch_tile(const Call &c) {
     using C = GroupShape<CG, TN, MODE>;
@@ -144,11 +155,7 @@ int launch_tile(const Call &c) {
         }
     }
     GroupTails<MODE> tails = {};
-    if constexpr (MODE == kGroupTN) {
-        for (uint32_t k = 0; k < 5 && p.rows > 0; ++k) {
-            if (!encode(&tails.P[k], c.P, 1u << k) || !encode(&tails.Q[k], c.Q, 1u << k)) return GEMM_ERR_CUDA;
-        }
-    }
+    if (!encode_tails(c, &tails)) return GEMM_ERR_CUDA;
     int64_t grid = c.sms / CG;
     if constexpr (CG == 2) {
         static std::atomic<int> fit[kMaxDevices];
@@ -189,21 +196,27 @@ int launch_few(const Call &c) {
     if (!allow_smem(kernel, C::smem(C::ALONE), done)) return GEMM_ERR_CUDA;
     GroupParams p = c.p;
     const int64_t i_tiles = (static_cast<int64_t>(p.I) + 127) / 128;
-    const int64_t most = most_tiles(p.rows, MODE == kGroupLora ? 1 : p.groups, TN) * i_tiles;
+    const int64_t j_tiles = MODE == kGroupTN ? (static_cast<int64_t>(p.J) + TN - 1) / TN : 0;
+    const int64_t most = MODE == kGroupTN ? p.groups * i_tiles * j_tiles : most_tiles(p.rows, MODE == kGroupLora ? 1 : p.groups, TN) * i_tiles;
     if (most * KS > kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
     p.i_tiles = static_cast<int32_t>(i_tiles);
+    p.j_tiles = static_cast<int32_t>(j_tiles);
     p.band_inverse = band_inverse(i_tiles);
     CUtensorMap tmP = {}, tmQ = {}, tmU = {}, tmH = {};  // not used by sums of nothing
     if (c.P.rows > 0 && c.P.cols > 0 && c.Q.rows > 0 && c.Q.cols > 0) {
-        if (!encode(&tmP, c.P, MODE == kGroupNN ? 64 : 128) || !encode(&tmQ, c.Q, TN)) return GEMM_ERR_CUDA;
+        if (!encode(&tmP, c.P, MODE == kGroupNN || MODE == kGroupTN ? 64 : 128) || !encode(&tmQ, c.Q, MODE == kGroupTN ? 64 : TN)) {
+            return GEMM_ERR_CUDA;
+        }
     }
+    GroupTails<MODE> tails = {};
+    if (!encode_tails(c, &tails)) return GEMM_ERR_CUDA;
     if (MODE == kGroupLora && p.groups > 0) {
         if (!encode(&tmU, c.U, 128) || !encode(&tmH, c.H, 16)) return GEMM_ERR_CUDA;
     }
     const int64_t tiles = most > 0 ? most : 1;  // one for the rows without a group
     const int stages = MODE == kGroupLora || KS * tiles <= c.sms ? C::ALONE : C::PAIRED;
-    return launch_cluster(kernel, KS * tiles, C::THREADS, KS, static_cast<size_t>(C::smem(stages)), c.stream, tmP, tmQ, tmU, tmH, p,
-                          stages);
+    return launch_cluster(kernel, KS * tiles, C::THREADS, KS, static_cast<size_t>(C::smem(stages)), c.stream, tmP, tmQ, tmU, tmH, tails,
+                          p, stages);
 }
 
 template <int TN, int MODE>
@@ -219,8 +232,10 @@ int launch_split(const Call &c, int split) {
 template <int MODE>
 int launch_few_mode(const Call &c, int tile, int split) {
     switch (tile) {
-        case 16: return launch_split<16, MODE>(c, split);
-        case 32: return launch_split<32, MODE>(c, split);
+        case 16:
+            if constexpr (MODE != kGroupTN) return launch_split<16, MODE>(c, split);
+        case 32:
+            if constexpr (MODE != kGroupTN) return launch_split<32, MODE>(c, split);
         case 64: return launch_split<64, MODE>(c, split);
         default: return launch_split<128, MODE>(c, split);
     }
@@ -252,13 +267,21 @@ int split_of(int64_t tiles, int64_t k_tiles, int sms) {
 //   2000 x 2048 x 2048, 8 groups    128, 1: 20.7                    128, persistent: 21.5   256: 25.7
 //   8192 x 1024 x 1024, 8 groups    256, pairs: 16.9                128, persistent: 20.7   64: 28.4
 //   2 x 2048 x 1024, 64 groups      16, 4: 5.1                      32, 4: 5.4    32, persistent: 6.9
-double cost_of(const GroupParams &p, int sms, int tile, int split) {
-    const double rows = p.rows, some = p.groups < p.rows ? p.groups : p.rows, each = rows / some, k_tiles = (p.R + 63) / 64;
+// Sums over rows, of which 60 shapes were timed with each choice and the chosen one is 2 % off:
+//   8192 rows, 1024 x 1024          128, 2: 22.4                    64, 2: 24.1   256, pairs: 40.3
+//   3855 rows, 208 x 208            64, 8: 6.6                      64, 4: 7.7    256, pairs: 21.4
+//   8192 rows, 8 groups, 1024 x 1024  256, pairs: 23.5              128, persistent: 26.4   128, 2: 37.2
+double cost_of(int mode, const GroupParams &p, int sms, int tile, int split) {
+    // of a sum over rows the groups have p.J columns each, and sums of as many rows as there are on average
+    const bool sum = mode == kGroupTN;
+    const double some = sum || p.groups < p.rows ? p.groups : p.rows, rows = sum ? some * p.J : p.rows, each = rows / some;
+    const double k_tiles = sum ? (p.rows / some + 63) / 64 : (p.R + 63) / 64;
     const bool pair = tile == 256;
     // a group's rows fill its last tile by half
     double tiles = each > 0.5 * tile ? rows / tile + 0.5 * some : some;
     const double most = static_cast<double>(most_tiles(p.rows, p.groups, tile));
-    if (tiles > most) tiles = most;
+    if (!sum && tiles > most) tiles = most;
+    if (sum) tiles = some * ((p.J + tile - 1) / tile);
     // rows of a stage in one CTA: 128 of P, and of Q boxes of 32 as far as a tile is filled
     const int filled = tiles > some ? tile : (each < tile ? static_cast<int>(each + 31) / 32 * 32 : tile);
     const int q = tile == 16 ? 16 : (filled / (pair ? 2 : 1) + 31) / 32 * 32;
@@ -277,18 +300,20 @@ double cost_of(const GroupParams &p, int sms, int tile, int split) {
 }
 
 Choice choose(int mode, const GroupParams &p, int sms, const grouped_options &o) {
-    if (mode == kGroupTN) return {o.tile ? o.tile : (p.J <= 64 ? 64 : (p.J <= 128 || p.I <= 128 ? 128 : 256)), 0};
-    const int64_t k_tiles = (static_cast<int64_t>(p.R) + 63) / 64;
+    const bool sum = mode == kGroupTN;
+    // K tiles of a sum: of rows, as many as the groups have on average
+    const int64_t k_tiles = sum ? (static_cast<int64_t>(p.rows) / p.groups + 63) / 64 : (static_cast<int64_t>(p.R) + 63) / 64;
     Choice best = {o.tile ? o.tile : 32, o.split > 0 ? o.split : 0};
     double least = -1;
-    for (int tile = 16; tile <= 256; tile *= 2) {
+    for (int tile = sum ? 64 : 16; tile <= 256; tile *= 2) {
         for (int split = 0; split <= 8; split = split ? 2 * split : 1) {
             // split 0: a persistent grid, of tiles from 32 on; clusters of tiles up to 128
             if ((o.tile && tile != o.tile) || (o.split && split != (o.split > 0 ? o.split : 0)) ||
-                (split == 0 ? tile == 16 : tile == 256) || (split > 1 && split > k_tiles && !o.split)) {
+                (split == 0 ? tile == 16 : tile == 256) || (split > 1 && split > k_tiles && !o.split) ||
+                (sum && split == 1 && !o.split)) {
                 continue;
             }
-            const double cost = cost_of(p, sms, tile, split);
+            const double cost = cost_of(mode, p, sms, tile, split);
             if (least < 0 || cost < least) least = cost, best = {tile, split};
         }
     }
@@ -298,8 +323,8 @@ Choice choose(int mode, const GroupParams &p, int sms, const grouped_options &o)
 
 template <int MODE>
 int launch_mode(const Call &c, const Choice &how) {
+    if (how.split > 0) return launch_few_mode<MODE>(c, how.tile, how.split);
     if constexpr (MODE != kGroupTN) {
-        if (how.split > 0) return launch_few_mode<MODE>(c, how.tile, how.split);
         if (how.tile == 32) return launch_tile<1, 32, MODE>(c);
     }
     switch (how.tile) {
@@ -346,7 +371,7 @@ int grouped(int mode, Matrix ragged, Matrix other, Matrix out, const void *offse
     if (st != GEMM_OK) return st;
     if (rows < 0 || groups < 0 || N < 0 || K < 0 || (type != LINEAR_F16 && type != LINEAR_BF16) ||
         (offsets_type != 0 && offsets_type != 1) || (o.tile == 256 && o.split > 0) || (o.tile == 16 && o.split < 0) ||
-        (mode == kGroupTN && (o.split > 0 || (o.tile != 0 && o.tile < 64)))) {
+        (mode == kGroupTN && o.tile != 0 && o.tile < 64)) {
         return GEMM_ERR_INVALID_ARG;
     }
     if (N % 8 != 0 || K % 8 != 0 || rows > kMaxDim || N > kMaxDim || K > kMaxDim || groups > GROUPED_MAX_GROUPS) {

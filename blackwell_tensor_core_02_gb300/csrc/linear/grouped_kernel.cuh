@@ -396,6 +396,44 @@ struct GroupTails<kGroupTN> {
     CUtensorMap P[5], Q[5];
 };
 
+// A K tile of a sum over rows, from the sum's row r on: P's columns from i0 on and `boxes` blocks of
+// Q's from j0 on.  A last tile that is no whole number of steps comes in boxes of 16 to 1 rows, and
+// zeros from behind the matrix up to the step's end.
+template <int CG>
+__device__ __forceinline__ void load_sum_rows(const GroupParams &p, const CUtensorMap &tmP, const CUtensorMap &tmQ,
+                                              const GroupTails<kGroupTN> &tails, const GroupTile &w, int r, int32_t i0, int32_t j0,
+                                              int boxes, bool leader, uint32_t sp, uint32_t sq, uint32_t full) {
+    const int rows = w.r - r;
+    const bool tail = rows < 64 && rows % 16 != 0;
+    const int steps = (rows + 15) / 16 * 16;
+    if (leader) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(CG * (tail ? steps : 64) * 128 * (2 + boxes)));
+    if constexpr (CG == 2) full = ptx::mapa(full, 0);
+    auto load = [&](const CUtensorMap &mapP, const CUtensorMap &mapQ, int row, int32_t y) {
+        auto one = [&](uint32_t dst, const CUtensorMap &map, int32_t x) {
+            if constexpr (CG == 2) {
+                ptx::tma_load_2d_pair(dst + row * 128, &map, full, x, y);
+            } else {
+                ptx::tma_load_2d(dst + row * 128, &map, full, x, y);
+            }
+        };
+#pragma unroll
+        for (int b = 0; b < 2; ++b) one(sp + b * 8192, mapP, i0 + 64 * b);
+        for (int b = 0; b < boxes; ++b) one(sq + b * 8192, mapQ, j0 + 64 * b);
+    };
+    if (!tail) {
+        load(tmP, tmQ, 0, w.r0 + r);
+        return;
+    }
+    int row = 0;
+    for (; rows - row >= 16; row += 16) load(tails.P[4], tails.Q[4], row, w.r0 + r + row);
+    for (int k = 3, left = rows - row; k >= 0; --k) {
+        if (left >> k & 1) load(tails.P[k], tails.Q[k], row, w.r0 + r + row), row += 1 << k;
+    }
+    for (int k = 0, left = steps - row; k < 4; ++k) {
+        if (left >> k & 1) load(tails.P[k], tails.Q[k], row, p.rows), row += 1 << k;
+    }
+}
+
 template <int CG, int TN, int MODE>
 __global__ void __launch_bounds__(384, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
@@ -484,12 +522,12 @@ __global__ void __launch_bounds__(384, 1)
                     const int s = ring.stage, r = kt * 64;
                     const uint32_t sp = base + C::OFF_P + s * C::P_BYTES, sq = base + C::OFF_Q + s * C::Q_BYTES;
                     uint32_t full = bar_full + 8 * s;
-                    const int rows = w.r - r;  // of a last K tile (TN)
-                    const bool tail = MODE == kGroupTN && rows < 64 && rows % 16 != 0;
-                    const int steps = (rows + 15) / 16 * 16;
-                    if (leader) {
-                        ptx::mbar_arrive_expect_tx(full, CG * (tail ? static_cast<uint32_t>(steps * 128 * (2 + boxes)) : bytes));
+                    if constexpr (MODE == kGroupTN) {
+                        load_sum_rows<CG>(p, tmP, tmQ, tails, w, r, i0, j0, boxes, leader, sp, sq, full);
+                        ring.advance();
+                        continue;
                     }
+                    if (leader) ptx::mbar_arrive_expect_tx(full, CG * bytes);
                     if constexpr (CG == 2) full = ptx::mapa(full, 0);
                     auto load_2d = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y) {
                         if constexpr (CG == 2) {
@@ -498,24 +536,6 @@ __global__ void __launch_bounds__(384, 1)
                             ptx::tma_load_2d(dst, map, full, x, y);
                         }
                     };
-                    if constexpr (MODE == kGroupTN) {
-                        if (tail) {
-                            auto load_rows = [&](int k, int row, int32_t y) {  // 2^k rows from `row` on
-                                for (int b = 0; b < 2; ++b) load_2d(sp + b * 8192 + row * 128, &tails.P[k], i0 + 64 * b, y);
-                                for (int b = 0; b < boxes; ++b) load_2d(sq + b * 8192 + row * 128, &tails.Q[k], j0 + 64 * b, y);
-                            };
-                            int row = 0;
-                            for (; rows - row >= 16; row += 16) load_rows(4, row, w.r0 + r + row);
-                            for (int k = 3, left = rows - row; k >= 0; --k) {
-                                if (left >> k & 1) load_rows(k, row, w.r0 + r + row), row += 1 << k;
-                            }
-                            for (int k = 0, left = steps - row; k < 4; ++k) {
-                                if (left >> k & 1) load_rows(k, row, p.rows), row += 1 << k;
-                            }
-                            ring.advance();
-                            continue;
-                        }
-                    }
                     auto load_3d = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
                         if constexpr (CG == 2) {
                             ptxg::tma_load_3d_pair(dst, map, full, x, y, z);
@@ -541,17 +561,8 @@ __global__ void __launch_bounds__(384, 1)
                     } else if constexpr (MODE == kGroupNN) {
 #pragma unroll
                         for (int b = 0; b < 2; ++b) load_3d(sp + b * 8192, &tmP, i0 + 64 * b, r, w.group);
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) load_2d(sp + b * 8192, &tmP, i0 + 64 * b, w.r0 + r);
                     }
-                    for (int b = 0; b < boxes; ++b) {
-                        if constexpr (MODE != kGroupTN) {
-                            load_2d(sq + b * C::Q_BOX * 128, &tmQ, r, j0 + b * C::Q_BOX);
-                        } else {
-                            load_2d(sq + b * 8192, &tmQ, j0 + 64 * b, w.r0 + r);
-                        }
-                    }
+                    for (int b = 0; b < boxes; ++b) load_2d(sq + b * C::Q_BOX * 128, &tmQ, r, j0 + b * C::Q_BOX);
                     ring.advance();
                 }
             }

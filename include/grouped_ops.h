@@ -34,9 +34,9 @@ enum { GROUPED_MAX_GROUPS = 1024 };
  *                 16 to 128 (one CTA, by 128 of the other axis), 256 (a CTA pair,
  *                 by 256).  0: chosen from the sizes.
  *   split         1, 2, 4 or 8: a tile's sum is shared by a cluster of so many CTAs,
- *                 one tile each (tiles of 16 to 128; not the gradient for the
- *                 matrices); -1: a persistent grid (tiles of 32 to 256; the gradient
- *                 for the matrices: 64 to 256).  0: chosen.
+ *                 one tile each (tiles of 16 to 128); -1: a persistent grid (tiles of
+ *                 32 to 256).  0: chosen.  The gradient for the matrices takes tiles
+ *                 from 64 on.
  *   max_clusters  cap on the persistent grid (CTAs, or pairs); 0: as many as fit.
  *   debug_flags   test hook: 1 makes every wait run out (see gemm_f16.h).
  *   timeout_ns    limit of every wait inside the kernel; 0: 4 s.

@@ -263,3 +263,42 @@ def test_capped_grids(g):
         o = g.GroupedOptions(max_clusters=n)
         assert torch.equal(g.grouped_gemm_nt(A, B, offsets, options=o), want[0])
         assert torch.equal(g.grouped_gemm_tn(dD, A, offsets, options=o), want[1])
+
+
+@pytest.mark.parametrize("tile", [64, 128])
+@pytest.mark.parametrize("split", [1, 2, 4, 8])
+@pytest.mark.parametrize("counts", [[1], [0, 5], [64], [130, 0, 17, 1], [1000], [512, 515, 3]], ids=lambda c: "-".join(map(str, c)))
+def test_sums_over_rows_shared_by_a_cluster(g, counts, tile, split):
+    """The matrices' gradient with its rows split over a cluster: sums shorter than the cluster's K tiles, of
+    no whole number of steps, of none; what rows of no group hold counts for nothing; a given result's other columns stay."""
+    for N, K, dtype in ((8, 8, F16), (136, 72, BF16), (264, 320, F16)):
+        A, B, dD, offsets = inputs(counts, N, K, dtype, 9, 3)
+        for t in (A, dD):
+            t[:3] = float("nan")
+            t[3 + sum(counts):] = float("inf")
+        o = g.GroupedOptions(tile=tile, split=split, timeout_ns=2_000_000_000)
+        whole = torch.full((len(counts), N + 8, K + 16), 7.0, dtype=dtype, device="cuda")
+        got = g.grouped_gemm_tn(dD, A, offsets, whole[:, :N, 8:8 + K], options=o)
+        near(got, ref.matrices(dD, A, offsets.tolist()))
+        whole[:, :N, 8:8 + K] = 7.0
+        assert bool((whole == 7.0).all())
+    assert g.grouped_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("rows,groups,N,K", [(3855, 1, 208, 208), (8192, 1, 64, 64), (3000, 2, 520, 136), (700, 1, 1032, 264), (5000, 12, 200, 104)])
+def test_long_sums_of_small_matrices(g, rows, groups, N, K):
+    """As the library chooses: few tiles and long sums, groups of unlike lengths, twice with the same bits."""
+    cuts = [rows * e * e // (groups * groups) for e in range(groups + 1)]
+    A, _, dD, _ = inputs([rows], N, K, BF16)
+    offsets = torch.tensor(cuts, device="cuda")
+    got = g.grouped_gemm_tn(dD, A, offsets)
+    near(got, ref.matrices(dD, A, cuts))
+    assert torch.equal(got, g.grouped_gemm_tn(dD, A, offsets)) and g.grouped_device_status()[0] == 0
+
+
+def test_shared_sums_over_rows_that_time_out(g):
+    A, B, dD, offsets = inputs([300, 200], 136, 72, F16)
+    o = g.GroupedOptions(tile=64, split=4, debug_flags=1, timeout_ns=50_000_000)
+    g.grouped_gemm_tn(dD, A, offsets, options=o)
+    assert g.grouped_device_status()[0] == TIMEOUT
+    near(g.grouped_gemm_tn(dD, A, offsets), ref.matrices(dD, A, offsets.tolist()))

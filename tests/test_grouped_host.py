@@ -71,7 +71,7 @@ def test_refusals(lib):
         return lib.grouped_gemm_tn(dd, ldd, a, lda, off, ot, db, ldb, bs, rows, groups, N, K, t, None, o)
 
     assert tn(t=2) == tn(dd=None) == tn(a=None) == tn(db=None) == tn(db=P) == tn(bs=31 * 64) == tn(ldb=56) == INVALID
-    assert tn(o=g.GroupedOptions(tile=32)) == tn(o=g.GroupedOptions(split=2)) == INVALID
+    assert tn(o=g.GroupedOptions(tile=32)) == tn(o=g.GroupedOptions(tile=16, split=2)) == INVALID
     assert tn(dd=P + 8) == tn(db=4 * P + 8) == tn(ldd=36) == MISALIGNED
     assert tn(groups=0) == tn(N=0) == tn(K=0) == OK
 

@@ -246,15 +246,6 @@ struct Choice {
     int tile, split;
 };
 
-// CTAs that share a tile's sum: the most of 8, 4 and 2 that have an SM each and two K
-// tiles.
-int split_of(int64_t tiles, int64_t k_tiles, int sms) {
-    for (int ks = 8; ks > 1; ks /= 2) {
-        if (tiles * ks <= sms && k_tiles >= 2 * ks) return ks;
-    }
-    return 1;
-}
-
 // Cycles that a choice takes, near enough to choose by: a stage (64 of the sum) of each
 // tile, set by the rows that the copy engine brings and, of pairs, by the MMAs; tiles by
 // the groups' average rows; whole waves of a persistent grid, but of clusters, two CTAs an
@@ -426,7 +417,6 @@ int grouped(int mode, Matrix ragged, Matrix other, Matrix out, const void *offse
 // ------------------------------------------------------------- adapters --
 
 constexpr int64_t kMaxRank = 128;
-constexpr int64_t kRowsOfOneRequest = 128;  // on average, from which on tiles have one request each (see lora())
 
 struct Lora {
     Matrix x, W, down, up, D;
@@ -471,9 +461,59 @@ int lora_down(Call &c, const Lora &l) {
     return st;
 }
 
+// As cost_of(), of a call with adapters behind its first launch: tiles of 256 rows have one request
+// each and its ranks as more of the sum; others, of a CTA an SM, pieces, shared by the cluster.
+// Clusters of 8 and 4 with an SM each leave some of a GPC's SMs without one.  Fitted to 65 shapes (1
+// to 3600 rows, 1 to 128 requests, 512 to 8192 columns, sums of 704 to 4096) with each choice: 1 % off
+// the best on average.  In microseconds, the choice and others, of 4096 x 4096 but where said:
+//   64 requests of 1 row, rank 16   64 rows, 4 CTAs a tile: 16.5   128, 4: 17.1   32, 2: 17.9   16, 1: over 22
+//   8 of 100, 16                    256, pairs: 37.2               128, 1: 49.8   64, 1: 55.5
+//   32 of 64, 16                    128, 1: 93.8                   256, pairs: 113
+//   64 of 4, 32, 1024 x 1024        16, 1: 19.1                    32, 2: 19.4    128, 8: 28.5
+//   1 of 1, 32, 2048 x 2048         16, 4: 6.2                     16, 8: 11.0
+double lora_cost(const GroupParams &p, int sms, int tile, int split) {
+    const int requests = p.groups > 0 ? p.groups : 1;
+    const double rows = p.rows, each = rows / requests, k_tiles = (p.R + 63) / 64;
+    const int ranks = (p.rank + 63) / 64;
+    auto whole = [](double v) { return static_cast<double>(static_cast<int64_t>(v + 1 - 1e-6)); };
+    if (tile == 256) {
+        const double tiles = each > 128 ? rows / 256 + 0.5 * requests : requests;
+        const int filled = each >= 256 ? 256 : (static_cast<int>(each) + 31) / 32 * 32, q = (filled / 2 + 31) / 32 * 32;
+        const double stage = 1.6 * (128 + q) * 1.13, waves = tiles * ((p.I + 255) / 256) / (sms / 2);
+        return (waves < 3 ? whole(waves) : waves + 0.5) * ((k_tiles + 2 * ranks) * (stage < 450 ? 450 : stage) + 1330) + 3500;
+    }
+    const int filled = tile < p.rows ? tile : p.rows, q = tile == 16 ? 16 : (filled + 31) / 32 * 32;
+    const int at_once = split == 8 ? sms * 15 / 19 : (split == 4 ? sms * 18 / 19 : sms);
+    const double turns = whole(static_cast<double>((static_cast<int64_t>(p.rows) + tile - 1) / tile * ((p.I + 127) / 128) * split) / at_once);
+    const double stage = 1.6 * (128 + q);
+    double pieces = 0;
+    if (p.groups > 0) {
+        const int piece = tile < 64 ? 16 : tile / 2;  // FewShape::PIECE
+        pieces = filled / each + 1 < filled ? filled / each + 1 : filled;
+        if (pieces * piece < filled) pieces = static_cast<double>(filled) / piece;
+        pieces = whole(pieces / split);
+    }
+    return turns * (k_tiles / split * (stage < 400 ? 400 : stage) + pieces * (800 + 200 * (ranks - 1)) + 3800 + 30 * tile +
+                    (split > 1 ? 600 + 20.0 * filled * split : 0));
+}
+
+Choice choose_lora(const GroupParams &p, int sms, const grouped_options &o) {
+    const int64_t k_tiles = (static_cast<int64_t>(p.R) + 63) / 64;
+    Choice best = {o.tile ? o.tile : 16, o.split > 0 ? o.split : 0};
+    double least = -1;
+    for (int tile = 16; tile <= 256; tile *= 2) {
+        for (int split = tile == 256 ? 0 : 1; split <= (tile == 256 ? 0 : 8); split = split ? 2 * split : 1) {
+            if ((o.tile && tile != o.tile) || (o.split && split != (o.split > 0 ? o.split : 0)) || (split > 1 && split > k_tiles && !o.split)) continue;
+            const double cost = lora_cost(p, sms, tile, split);
+            if (least < 0 || cost < least) least = cost, best = {tile, split};
+        }
+    }
+    while (best.split > 1 && best.split > k_tiles) best.split /= 2;
+    return best;
+}
+
 // Requests of many rows: tiles of one request each, the adapter as more of the sum.
-// Requests of few: tiles of any rows, the adapters run by run.  16 requests of 128 rows, rank 64,
-// 4096 x 4096, the former 65 us, the latter 95; 32 of 64 rows 144 and 92.
+// Requests of few: tiles of any rows, the adapters run by run.
 int lora(Call &c, const Lora &l, const Choice &how) {
     const int st = lora_down(c, l);
     if (st != GEMM_OK) return st;
@@ -599,15 +639,7 @@ int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const v
     p.debug_flags = static_cast<uint32_t>(o.debug_flags);
     p.timeout_ns = static_cast<uint64_t>(o.timeout_ns);
     if (rows == 1) l.x.stride = 0;
-    Choice how = {o.tile, o.split};
-    if (how.tile == 0) {
-        const int64_t each = p.groups > 0 ? rows / p.groups : rows;
-        how.tile = o.split < 0 || (o.split == 0 && each >= kRowsOfOneRequest) ? 256 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)));
-    }
-    if (how.tile == 256) return lora(c, l, how);
-    const int64_t k_tiles = (K + 63) / 64;
-    if (how.split <= 0) how.split = split_of((rows + how.tile - 1) / how.tile * ((N + 127) / 128), k_tiles, c.sms);
-    while (how.split > 1 && how.split > k_tiles) how.split /= 2;
+    const Choice how = choose_lora(p, c.sms, o);
     return lora(c, l, how);
 }
 

@@ -12,6 +12,7 @@
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -123,6 +124,24 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor &l
 }
 
 void *stream_of(const at::Tensor &t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
+
+// Memory for the length of a call, from torch's allocator and in the stream's order, without the
+// tensor around it.
+struct Workspace {
+    void *p = nullptr;
+    Workspace() = default;
+    Workspace(const Workspace &) = delete;
+    Workspace &operator=(const Workspace &) = delete;
+    ~Workspace() {
+        if (p) c10::cuda::CUDACachingAllocator::raw_delete(p);
+    }
+    void *take(int64_t bytes, void *stream) {
+        if (bytes > 0) {
+            p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(static_cast<size_t>(bytes), static_cast<cudaStream_t>(stream));
+        }
+        return p;
+    }
+};
 
 PyObject *tuple_of(std::initializer_list<at::Tensor> ts) {
     PyObject *r = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
@@ -548,11 +567,12 @@ PyObject *lora(PyObject *const *args, Py_ssize_t n) {  // x, W, down, up, offset
     at::Tensor D = grouped_rows(args[6], "D", rows, N, x, &made);
     const int64_t need = gemm_lora_workspace_size(rows, rank);
     check_status(need, "gemm_lora_nt");
-    at::Tensor space = empty({need}, at::kByte, x);
+    Workspace space;
+    void *workspace = space.take(need, stream_of(x));
     check_status(gemm_lora_nt(x.data_ptr(), x.stride(0), W.data_ptr(), W.stride(0), down.data_ptr(), down.stride(1),
                               down.stride(0), up.data_ptr(), up.stride(1), up.stride(0), scales, offsets.data_ptr(), wide,
                               adapters.data_ptr<int32_t>(), D.data_ptr(), D.stride(0), rows, requests, many, N, K, rank, code,
-                              need ? space.data_ptr() : nullptr, need, stream_of(x), opts),
+                              workspace, need, stream_of(x), opts),
                  "gemm_lora_nt");
     return THPVariable_Wrap(D);
 }
@@ -711,7 +731,8 @@ PyObject *keep_backward(PyObject *const *args, Py_ssize_t n) {  // dy, kept, wei
     }
     const c10::cuda::CUDAGuard guard(dy.device());
     Rows gr{r.rows, r.cols, r.cols};
-    at::Tensor dx, dweight, dbias, space;
+    at::Tensor dx, dweight, dbias;
+    Workspace space;
     if (given(args[4])) {
         dx = tensor(args[4], "dx");
         same_kind(dx, dy, "dx", "dy");
@@ -725,12 +746,11 @@ PyObject *keep_backward(PyObject *const *args, Py_ssize_t n) {  // dy, kept, wei
         dbias = empty({r.cols}, wtype, dy);
         need = layer_norm_backward_workspace_size(r.rows, r.cols);
         check_status(need, "layer_norm_backward_checkpoint");
-        space = empty({need}, at::kByte, dy);
     }
     check_status(norm_checkpoint_backward(dy.data_ptr(), r.step, q.codes->data_ptr(), q.scales->data_ptr(), a.weight, rstd,
                                           dx.data_ptr(), gr.step, parameters ? dweight.data_ptr() : nullptr,
                                           parameters ? dbias.data_ptr() : nullptr, r.rows, r.cols, code, dtype_code(wtype),
-                                          parameters ? space.data_ptr() : nullptr, need, stream_of(dy)),
+                                          space.take(need, stream_of(dy)), need, stream_of(dy)),
                  "layer_norm_backward_checkpoint");
     return tuple_of({dx, dweight, dbias});
 }

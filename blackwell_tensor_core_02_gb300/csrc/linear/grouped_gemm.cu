@@ -188,6 +188,11 @@ int launch_tile(const Call &c) {
     return launch_cluster(kernel, CG * grid, C::THREADS, CG, C::SMEM_ALLOC, c.stream, tmP, tmQ, tmD, tmU, tmH, tails, p);
 }
 
+// CTAs with an SM each that run at once: a cluster lies within a GPC, and clusters of 8 and 4 leave
+// some SMs of one without.  Past that two share an SM: 1 x 2048 x 4096, 16 clusters of 8, 5.3 us, where
+// the last cluster waits for an SM alone 9.1.
+constexpr int alone_at_once(int cluster, int sms) { return cluster == 8 ? sms * 15 / 19 : (cluster == 4 ? sms * 18 / 19 : sms); }
+
 template <int TN, int KS, int MODE>
 int launch_few(const Call &c) {
     using C = FewShape<TN, MODE == kGroupLora>;
@@ -214,7 +219,7 @@ int launch_few(const Call &c) {
         if (!encode(&tmU, c.U, 128) || !encode(&tmH, c.H, 16)) return GEMM_ERR_CUDA;
     }
     const int64_t tiles = most > 0 ? most : 1;  // one for the rows without a group
-    const int stages = MODE == kGroupLora || KS * tiles <= c.sms ? C::ALONE : C::PAIRED;
+    const int stages = MODE == kGroupLora || KS * tiles <= alone_at_once(KS, c.sms) ? C::ALONE : C::PAIRED;
     return launch_cluster(kernel, KS * tiles, C::THREADS, KS, static_cast<size_t>(C::smem(stages)), c.stream, tmP, tmQ, tmU, tmH, tails,
                           p, stages);
 }
@@ -462,8 +467,7 @@ int lora_down(Call &c, const Lora &l) {
 }
 
 // As cost_of(), of a call with adapters behind its first launch: tiles of 256 rows have one request
-// each and its ranks as more of the sum; others, of a CTA an SM, pieces, shared by the cluster.
-// Clusters of 8 and 4 with an SM each leave some of a GPC's SMs without one.  Fitted to 65 shapes (1
+// each and its ranks as more of the sum; others, of a CTA an SM, pieces, shared by the cluster.  Fitted to 65 shapes (1
 // to 3600 rows, 1 to 128 requests, 512 to 8192 columns, sums of 704 to 4096) with each choice: 1 % off
 // the best on average.  In microseconds, the choice and others, of 4096 x 4096 but where said:
 //   64 requests of 1 row, rank 16   64 rows, 4 CTAs a tile: 16.5   128, 4: 17.1   32, 2: 17.9   16, 1: over 22
@@ -483,7 +487,7 @@ double lora_cost(const GroupParams &p, int sms, int tile, int split) {
         return (waves < 3 ? whole(waves) : waves + 0.5) * ((k_tiles + 2 * ranks) * (stage < 450 ? 450 : stage) + 1330) + 3500;
     }
     const int filled = tile < p.rows ? tile : p.rows, q = tile == 16 ? 16 : (filled + 31) / 32 * 32;
-    const int at_once = split == 8 ? sms * 15 / 19 : (split == 4 ? sms * 18 / 19 : sms);
+    const int at_once = alone_at_once(split, sms);
     const double turns = whole(static_cast<double>((static_cast<int64_t>(p.rows) + tile - 1) / tile * ((p.I + 127) / 128) * split) / at_once);
     const double stage = 1.6 * (128 + q);
     double pieces = 0;

@@ -21,6 +21,8 @@
 // tile's rows each, as many at once as TMEM has columns for.
 #pragma once
 
+#include <type_traits>
+
 #include "grouped_kernel.cuh"
 
 namespace linear_ops {
@@ -38,7 +40,8 @@ struct FewShape {
     // the rest of the shared memory, behind the ring
     static constexpr int OFF_START = LORA ? SUMS : 0, OFF_TILES = OFF_START + LIST;
     static constexpr int OFF_ROWS = OFF_TILES + LIST;             // int32 [TN]: the rows' adapters
-    static constexpr int OFF_PIECES = OFF_ROWS + TN * 4;          // Piece [TN], behind it their number
+    static constexpr int OFF_BACK = OFF_ROWS + TN * 4;            // float [TN]: what brings the rows' h back
+    static constexpr int OFF_PIECES = OFF_BACK + (LORA ? TN * 4 : 0);  // Piece [TN], behind it their number
     static constexpr int OFF_BAR = OFF_PIECES + (LORA ? TN * 16 : 0) + 16;
     static constexpr int MOST_STAGES = 12;
     // full, empty [stages]; done, list, pieces full, pieces free, drain
@@ -119,6 +122,7 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     int32_t *start = reinterpret_cast<int32_t *>(smem + C::OFF_START), *tiles = reinterpret_cast<int32_t *>(smem + C::OFF_TILES);
     int32_t *chosen = reinterpret_cast<int32_t *>(smem + C::OFF_ROWS), *piece_count = reinterpret_cast<int32_t *>(smem + C::OFF_BAR) - 4;
+    float *back = reinterpret_cast<float *>(smem + C::OFF_BACK);
     Piece *pieces = reinterpret_cast<Piece *>(smem + C::OFF_PIECES);
 
     if (warp == 0 && lane == 0) {
@@ -384,58 +388,92 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             const int count = ok ? *piece_count : 0;
             uint32_t turn = 0;
-            for (int q = 0; q < count; ++turn) {
-                if (lane == 0) ok = wait_bounded(bar_pfull, turn & 1u, abort_flag, p.timeout_ns, kWaitEpilogue, q);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
-                ptx::tcgen05_fence_after();
-                do {
-                    // pieces of one row, up to eight at once
-                    constexpr int B = 8;
-                    uint32_t v[16];
-                    int some = 0;
+            bool scaled = false;
+            if (!p.bf16 && p.follows) {  // the powers of two that h has been divided by, while the first pieces are multiplied
+                ptx::griddep_wait();
+                for (int32_t j = static_cast<int32_t>(threadIdx.x) - 64; j < w.n; j += 128) {
+                    back[j] = chosen[j] >= 0 ? p.row_scale[w.j0 + j] : 1.f;
+                    scaled = scaled || back[j] != 1.f;
+                }
+                scaled = ptxg::any_of_128(1, scaled);
+            }
+            // What the columns v are of tile's rows j on, times those rows' powers (apart from the sums, whose
+            // loads would wait for one another's stores; with the choice inside the loop 128 requests of 4 rows
+            // took 50.7 us, so 49.8).
+            auto bring_back = [&](uint32_t (&v)[16], int j) {
 #pragma unroll
-                    for (int s = 0; s < B; ++s) {
-                        if (s == some && q + s < count && pieces[q + s].rows == 1 && (s == 0 || !pieces[q + s].turn)) {
-                            ptxg::tmem_ld_32x32b_x1(taddr + TN + pieces[q + s].column, v[s]);
-                            ++some;
-                        }
-                    }
-                    if (some > 0) {
-                        ptx::tmem_wait_ld();
+                for (int t = 0; t < 16; ++t) {
+                    if (j + t < TN) v[t] = __float_as_uint(__uint_as_float(v[t]) * back[j + t]);
+                }
+            };
+            auto add_pieces = [&](auto scaled_type) {
+                constexpr bool SCALED = decltype(scaled_type)::value;
+                for (int q = 0; q < count; ++turn) {
+                    if (lane == 0) ok = wait_bounded(bar_pfull, turn & 1u, abort_flag, p.timeout_ns, kWaitEpilogue, q);
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    if (!ok) break;
+                    ptx::tcgen05_fence_after();
+                    do {
+                        // pieces of one row, up to eight at once
+                        constexpr int B = 8;
+                        uint32_t v[16];
+                        int some = 0;
 #pragma unroll
                         for (int s = 0; s < B; ++s) {
-                            if (s < some) sums[pieces[q + s].first * C::LD + i] += __uint_as_float(v[s]);
+                            if (s == some && q + s < count && pieces[q + s].rows == 1 && (s == 0 || !pieces[q + s].turn)) {
+                                ptxg::tmem_ld_32x32b_x1(taddr + TN + pieces[q + s].column, v[s]);
+                                ++some;
+                            }
                         }
-                        q += some;
-                        continue;
-                    }
-                    // 16 columns of two pieces at once, or of one of more
-                    const Piece piece = pieces[q];
-                    const bool two = piece.rows <= 16 && q + 1 < count && !pieces[q + 1].turn && pieces[q + 1].rows <= 16;
-                    const Piece next = pieces[two ? q + 1 : q];
-                    uint32_t x[16];
-                    for (int c = 0; c < piece.rows; c += 16) {
-                        ptx::tmem_ld_32x32b_x16(taddr + TN + piece.column + c, v);
-                        if (two) ptx::tmem_ld_32x32b_x16(taddr + TN + next.column, x);
-                        ptx::tmem_wait_ld();
+                        if (some > 0) {
+                            ptx::tmem_wait_ld();
+                            if constexpr (SCALED) {
 #pragma unroll
-                        for (int t = 0; t < 16; ++t) {
-                            if (c + t < piece.rows) sums[(piece.first + c + t) * C::LD + i] += __uint_as_float(v[t]);
+                                for (int s = 0; s < B; ++s) {
+                                    if (s < some) v[s] = __float_as_uint(__uint_as_float(v[s]) * back[pieces[q + s].first]);
+                                }
+                            }
+#pragma unroll
+                            for (int s = 0; s < B; ++s) {
+                                if (s < some) sums[pieces[q + s].first * C::LD + i] += __uint_as_float(v[s]);
+                            }
+                            q += some;
+                            continue;
                         }
-                    }
-                    if (two) {
+                        // 16 columns of two pieces at once, or of one of more
+                        const Piece piece = pieces[q];
+                        const bool two = piece.rows <= 16 && q + 1 < count && !pieces[q + 1].turn && pieces[q + 1].rows <= 16;
+                        const Piece next = pieces[two ? q + 1 : q];
+                        uint32_t x[16];
+                        for (int c = 0; c < piece.rows; c += 16) {
+                            ptx::tmem_ld_32x32b_x16(taddr + TN + piece.column + c, v);
+                            if (two) ptx::tmem_ld_32x32b_x16(taddr + TN + next.column, x);
+                            ptx::tmem_wait_ld();
+                            if constexpr (SCALED) bring_back(v, piece.first + c);
 #pragma unroll
-                        for (int t = 0; t < 16; ++t) {
-                            if (t < next.rows) sums[(next.first + t) * C::LD + i] += __uint_as_float(x[t]);
+                            for (int t = 0; t < 16; ++t) {
+                                if (c + t < piece.rows) sums[(piece.first + c + t) * C::LD + i] += __uint_as_float(v[t]);
+                            }
+                        }
+                        if (two) {
+                            if constexpr (SCALED) bring_back(x, next.first);
+#pragma unroll
+                            for (int t = 0; t < 16; ++t) {
+                                if (t < next.rows) sums[(next.first + t) * C::LD + i] += __uint_as_float(x[t]);
+                            }
+                            ++q;
                         }
                         ++q;
-                    }
-                    ++q;
-                } while (q < count && !pieces[q].turn);
-                ptx::tcgen05_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar_pfree);
+                    } while (q < count && !pieces[q].turn);
+                    ptx::tcgen05_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar_pfree);
+                }
+            };
+            if (scaled) {
+                add_pieces(std::true_type{});
+            } else {
+                add_pieces(std::false_type{});
             }
         }
     }
@@ -488,6 +526,8 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
 // (split_16; zeros up to a whole 16 ranks), for few rows.  256 threads: two warps a rank and
 // half of K each, four ranks at a time and `each` times four a CTA.  The chain of a single token is the launch, the
 // offsets and adapters, what down holds, and the sums; x is on its way from the start.
+// SCALED (fp16): the row's CTAs are a cluster, which agrees on the row's power of two (row_exponent()); of up
+// to 8, so RANKS, those at a time, may be 8 or 16 there, with 64 threads each.
 struct DownParams {
     const uint16_t *x, *down;
     int64_t x_row, down_row, down_matrix;
@@ -506,23 +546,24 @@ __device__ __forceinline__ float dot_8(bool bf16, uint4 a, uint4 b, float sum) {
     return sum;
 }
 
-constexpr int kDownRanks = 4;
-
-__global__ void __launch_bounds__(256) lora_down_kernel(const GroupParams p, const DownParams d) {
+template <bool SCALED, int RANKS>
+__global__ void __launch_bounds__(64 * RANKS) lora_down_kernel(const GroupParams p, const DownParams d) {
     // the first request that starts behind the row, and its predecessor's adapter
     __shared__ unsigned long long past;
-    __shared__ float halves[kDownRanks];
+    __shared__ float halves[RANKS];
+    __shared__ float held[SCALED ? 128 : 1];  // this CTA's ranks of h
+    __shared__ uint32_t top_here;
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
     const int64_t row = blockIdx.x;
     if (tid == 0) past = ~0ull;
     ptx::griddep_wait();
     // what follows may start: all before this kernel has completed
     if (tid == 0) ptx::griddep_launch_dependents();
-    const int half = warp / kDownRanks;
+    const int half = warp / RANKS;
     const int k_half = (p.R / 8 + 1) / 2 * 8;  // whole units of eight
     const int k_begin = half * k_half, k_end = half ? p.R : k_half;
     const uint16_t *x = d.x + row * d.x_row;
-    constexpr int U = 8;  // loads on their way at once
+    constexpr int U = RANKS == 16 ? 4 : 8;  // loads on their way at once
     uint4 v[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -532,7 +573,7 @@ __global__ void __launch_bounds__(256) lora_down_kernel(const GroupParams p, con
     }
     __syncthreads();
     unsigned long long least = ~0ull;
-    for (int e = p.groups - tid; e >= 0; e -= 256) {
+    for (int e = p.groups - tid; e >= 0; e -= 64 * RANKS) {
         const int64_t o = offset_of(p, e);
         const uint32_t a = e > 0 ? static_cast<uint32_t>(adapter_of(p, e - 1)) : ~0u;
         if (o > row) least = static_cast<unsigned long long>(e) << 32 | a;
@@ -541,12 +582,12 @@ __global__ void __launch_bounds__(256) lora_down_kernel(const GroupParams p, con
     const uint32_t first = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(least >> 32));
     if (static_cast<uint32_t>(least >> 32) == first && first != ~0u) atomicMin(&past, least);
     __syncthreads();
-    // none behind it: the row is behind the last request
+    // none behind it: the row is behind the last request (all of a cluster return, or none)
     const int32_t a = past != ~0ull ? static_cast<int32_t>(past & 0xffffffffull) : -1;
     if (a < 0) return;
     const int padded = (p.rank + 15) / 16 * 16;
     for (int q = 0; q < d.each; ++q) {
-        const int j = (static_cast<int>(blockIdx.y) * d.each + q) * kDownRanks + warp % kDownRanks;
+        const int j = (static_cast<int>(blockIdx.y) * d.each + q) * RANKS + warp % RANKS;
         float sum = 0.f;
         if (j < p.rank) {
             const uint16_t *down = d.down + j * d.down_row + a * d.down_matrix;
@@ -570,14 +611,45 @@ __global__ void __launch_bounds__(256) lora_down_kernel(const GroupParams p, con
         }
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (half && lane == 0) halves[warp % kDownRanks] = sum;
+        if (half && lane == 0) halves[warp % RANKS] = sum;
         __syncthreads();
         if (!half && lane == 0 && j < padded) {
             const float h = j < p.rank ? (sum + halves[warp]) * (p.scales ? p.scales[a] : 1.f) : 0.f;
-            uint16_t *to = d.h + row * (2 * p.rank_pad) + j;
-            split_16(p.bf16, h, to, to + p.rank_pad);
+            if constexpr (SCALED) {
+                held[q * RANKS + warp] = h;
+            } else {
+                uint16_t *to = d.h + row * (2 * p.rank_pad) + j;
+                split_16(p.bf16, h, to, to + p.rank_pad);
+            }
         }
         __syncthreads();
+    }
+    if constexpr (SCALED) {
+        const int first = static_cast<int>(blockIdx.y) * d.each * RANKS;
+        const int count = padded - first < d.each * RANKS ? padded - first : d.each * RANKS;  // none: below 1
+        if (warp == 0) {
+            uint32_t top = 0;
+            for (int i = lane; i < count; i += 32) top = top > finite_bits(held[i]) ? top : finite_bits(held[i]);
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) top_here = top;
+            __syncwarp();
+        }
+        ptx::cluster_sync();
+        uint32_t top = 0;
+        for (uint32_t s = 0; s < gridDim.y; ++s) {
+            uint32_t t;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(t) : "r"(ptx::mapa(ptx::smem_u32(&top_here), s)) : "memory");
+            top = top > t ? top : t;
+        }
+        ptx::cluster_arrive();
+        const int e = row_exponent(top);
+        if (tid < count) {
+            uint16_t *to = d.h + row * (2 * p.rank_pad) + first + tid;
+            split_16(false, held[tid] * power_of_two(-e), to, to + p.rank_pad);
+        }
+        if (blockIdx.y == 0 && tid == 0) p.row_scale[row] = power_of_two(e);
+        __syncwarp();
+        ptx::cluster_wait();  // no CTA leaves while another reads its largest
     }
 }
 

@@ -95,10 +95,10 @@ int32_t turn_of(int mode, const GroupParams &p, int tile, int64_t clusters) {
 }
 
 template <typename... P>
-int launch_cluster(void (*kernel)(P...), int64_t ctas, unsigned threads, unsigned cluster, size_t smem, cudaStream_t stream,
-                   const P &...args) {
+int launch_clusters(void (*kernel)(P...), dim3 grid, unsigned threads, dim3 cluster, size_t smem, cudaStream_t stream,
+                    const P &...args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -106,15 +106,22 @@ int launch_cluster(void (*kernel)(P...), int64_t ctas, unsigned threads, unsigne
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.x = cluster.x;
+    attr[1].val.clusterDim.y = cluster.y;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = cluster.x * cluster.y > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }
     return GEMM_OK;
+}
+
+template <typename... P>
+int launch_cluster(void (*kernel)(P...), int64_t ctas, unsigned threads, unsigned cluster, size_t smem, cudaStream_t stream,
+                   const P &...args) {
+    return launch_clusters(kernel, dim3(static_cast<unsigned>(ctas)), threads, dim3(cluster), smem, stream, args...);
 }
 
 // Maps of sums over rows with boxes of 2^k rows.
@@ -440,18 +447,28 @@ struct Lora {
 //   2 of 64, 128                    29.1, 23.0    1 of 256, 64  34.0, 24.3
 constexpr int64_t kDownByCores = 12288;
 
-int lora_down(Call &c, const Lora &l) {
+// Of fp16 a row's CTAs agree on the power of two that its h is held in, so they are a cluster, of up to 8, with
+// 8 or 16 ranks at a time where 4 would take more (one row of rank 128 11.2 us, in bf16, of 32 CTAs, 8.7; 64 of rank
+// 16 18.5 and 16.7); and tiles of 256 rows take h from the tensor cores' launch, which leaves what they ask of each 32 rows.
+int lora_down(Call &c, const Lora &l, const Choice &how) {
     if (c.p.groups == 0) return GEMM_OK;
     int st;
-    if (l.rows * l.rank <= kDownByCores) {
-        // three CTAs an SM, with as few ranks each as that allows
-        const int64_t fours = (l.rank + 15) / 16 * 16 / kDownRanks;
-        int64_t each = 1;
-        while (each < fours && l.rows * ((fours + each - 1) / each) > 3 * c.sms) ++each;
+    if (l.rows * l.rank <= kDownByCores && (c.p.bf16 || how.tile != 256)) {
+        // three CTAs of 256 threads an SM, with as few ranks each as that allows
+        const int64_t padded = (l.rank + 15) / 16 * 16;
+        int ranks = 4;
+        while (!c.p.bf16 && padded > 8 * ranks && l.rows * (padded / ranks) <= 3 * c.sms) ranks *= 2;
+        const int64_t units = padded / ranks;
+        int64_t each = c.p.bf16 ? 1 : (units + 7) / 8;
+        while (each < units && l.rows * ((units + each - 1) / each) * ranks > 4 * 3 * c.sms) ++each;
+        const unsigned parts = static_cast<unsigned>((units + each - 1) / each);
         const DownParams d = {static_cast<const uint16_t *>(l.x.ptr), static_cast<const uint16_t *>(l.down.ptr), l.x.stride,
                               l.down.stride, l.down.depth_stride, static_cast<uint16_t *>(l.workspace), static_cast<int32_t>(each)};
-        st = launch(lora_down_kernel, dim3(static_cast<unsigned>(l.rows), static_cast<unsigned>((fours + each - 1) / each)),
-                    dim3(256), 0, c.stream, c.p, d);
+        const dim3 grid(static_cast<unsigned>(l.rows), parts);
+        st = c.p.bf16      ? launch(lora_down_kernel<false, 4>, grid, dim3(256), 0, c.stream, c.p, d)
+             : ranks == 4 ? launch_clusters(lora_down_kernel<true, 4>, grid, 256, dim3(1, parts), 0, c.stream, c.p, d)
+             : ranks == 8 ? launch_clusters(lora_down_kernel<true, 8>, grid, 512, dim3(1, parts), 0, c.stream, c.p, d)
+                          : launch_clusters(lora_down_kernel<true, 16>, grid, 1024, dim3(1, parts), 0, c.stream, c.p, d);
     } else {
         Call d = c;
         d.P = l.down;
@@ -519,7 +536,7 @@ Choice choose_lora(const GroupParams &p, int sms, const grouped_options &o) {
 // Requests of many rows: tiles of one request each, the adapter as more of the sum.
 // Requests of few: tiles of any rows, the adapters run by run.
 int lora(Call &c, const Lora &l, const Choice &how) {
-    const int st = lora_down(c, l);
+    const int st = lora_down(c, l, how);
     if (st != GEMM_OK) return st;
     c.P = l.W;
     c.Q = l.x;
@@ -560,7 +577,7 @@ int grouped_gemm_tn(const void *dD, int64_t ldd, const void *A, int64_t lda, con
 int64_t gemm_lora_workspace_size(int64_t rows, int64_t rank) {
     if (rows < 0 || rank < 0) return GEMM_ERR_INVALID_ARG;
     if (rows > kMaxDim || rank > kMaxRank || rank % 8 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
-    return rows * ((rank + 63) / 64 * 64) * 4;  // two 16-bit numbers
+    return rows * ((rank + 63) / 64 * 64 * 4 + 8);  // two 16-bit numbers; of a row, row_scale and some_scaled
 }
 
 int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const void *down, int64_t ld_down,
@@ -640,6 +657,10 @@ int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const v
     p.adapter_count = static_cast<int32_t>(adapter_count);
     p.rank = static_cast<int32_t>(rank);
     p.rank_pad = static_cast<int32_t>((rank + 63) / 64 * 64);
+    if (some) {
+        p.row_scale = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + rows * p.rank_pad * 4);
+        p.some_scaled = reinterpret_cast<int32_t *>(p.row_scale + rows);
+    }
     p.debug_flags = static_cast<uint32_t>(o.debug_flags);
     p.timeout_ns = static_cast<uint64_t>(o.timeout_ns);
     if (rows == 1) l.x.stride = 0;

@@ -30,8 +30,12 @@
 //
 // LORA and DOWN are the two launches of low-rank adapters beside a shared product, with
 // the rows of a request as a group.  DOWN leaves h = scale_a * x * down_a^T as two
-// 16-bit numbers, h rounded and what that rounding left, which hold 16 (bf16) or 22 bits
-// of it; LORA's sum goes on over the ranks, once for each, so the result is rounded once.
+// 16-bit numbers, h rounded and what that rounding left, which hold 16 bits of it (bf16) or, in fp16,
+// 22 of its row's largest: fp16 has few exponents, so there a row of h is held times a power of two of
+// its own where its largest is not in their midst (row_exponent()).  LORA's sum goes on over the ranks,
+// once for each, so the result is rounded once; where rows of a tile have such a power, the ranks' sum
+// goes to the other accumulator, and the epilogue brings each row's back before it adds it (4100
+// tokens of 11 requests, rank 64, 4096 x 4096 fp16: 115 us without such rows, 137 with all).
 // Rows without a request are a group without an adapter, before the first and behind the
 // last.  A request's tile holds its own rows only: what another request's adapter holds
 // cannot reach them.
@@ -88,6 +92,14 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+
+// The first 8 of such columns: registers 0 to 3.
+__device__ __forceinline__ void tmem_ld_16x256b_x1(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 // 32 TMEM lanes x one column.
@@ -195,7 +207,8 @@ struct GroupShape {
     static constexpr int OFF_BAR = OFF_CHOSEN + (ADAPTERS ? LIST : 0);
     // full, empty [STAGES]; accumulator full, empty [2]; drain
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 5) * 8;
-    static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 896;  // from a multiple of 128 bytes to one of 1024
+    static constexpr int OFF_APART = OFF_MISC + 16;  // LORA: whether a stage's tile has its ranks apart, [STAGES]
+    static constexpr int SMEM_ALLOC = OFF_APART + (MODE == kGroupLora ? 4 * STAGES : 0) + 896;  // from a multiple of 128 bytes to one of 1024
     static constexpr int THREADS = 384;
     static_assert(STAGES >= 4 && OFF_BAR % 8 == 0 && SMEM_ALLOC <= 232448, "227 KiB");
     static_assert((CG == 2 && TN == 256) || (CG == 1 && (TN == 32 || TN == 64 || TN == 128)), "tile");
@@ -220,6 +233,10 @@ struct GroupParams {
     int32_t adapter_count, rank;
     int32_t rank_pad;            // rank in whole 64s: h has 2 * rank_pad elements a row
     int32_t follows;             // LORA: behind a launch that leaves h
+    // fp16: what brings each row of h back, and at the first row of each 32 of a request that DOWN had at
+    // once whether that is 1 for all of them
+    float *row_scale;
+    int32_t *some_scaled;
     uint32_t debug_flags;
     uint64_t timeout_ns;
 };
@@ -388,6 +405,21 @@ __device__ __forceinline__ void split_16(bool bf16, float h, uint16_t *high, uin
     *low = static_cast<uint16_t>(b);
 }
 
+// h of fp16 rows: the bits of a magnitude, 0 of infinities and NaN (they stay what they are).
+__device__ __forceinline__ uint32_t finite_bits(float h) {
+    const uint32_t b = __float_as_uint(h) & 0x7fffffffu;
+    return b < 0x7f800000u ? b : 0u;
+}
+// The exponent of the power of two that a row of h is divided by, from its largest finite magnitude: 0
+// where that is from 2^-3 to 2^15 (then the second number's least step, 2^-24, is 2^-21 of it at most),
+// else what brings it to 2^14 to 2^15; from -112 on, as 2^112 and 2^-112 are normal and what is
+// smaller still adds nothing that fp16 shows.
+__device__ __forceinline__ int row_exponent(uint32_t top) {
+    const int e = static_cast<int>(top >> 23) - 127;
+    return top == 0u || (e >= -3 && e <= 14) ? 0 : (e < -98 ? -112 : e - 14);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // TN: P's and Q's maps with boxes of 2^k rows.
 template <int MODE>
 struct GroupTails {};
@@ -434,8 +466,27 @@ __device__ __forceinline__ void load_sum_rows(const GroupParams &p, const CUtens
     }
 }
 
+// Sums of 16 TMEM lanes x 32 columns (as tmem_ld_16x256b_x4 has them), each column's times its row's
+// scale, added to v; `rows` of the columns have one.
+__device__ __forceinline__ void add_scaled(uint32_t taddr, const float *row_scale, int rows, int lane, uint32_t (&v)[16]) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {  // 8 columns at a time: few registers
+        uint32_t more[4];
+        ptxg::tmem_ld_16x256b_x1(taddr + n * 8, more);
+        const int j = 8 * n + 2 * (lane % 4);
+        const float s = j < rows ? row_scale[j] : 0.f, t = j + 1 < rows ? row_scale[j + 1] : 0.f;
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[4 * n + i] = __float_as_uint(fmaf(__uint_as_float(more[i]), i % 2 ? t : s, __uint_as_float(v[4 * n + i])));
+        }
+    }
+}
+
+// LORA in 80 registers, as for two CTAs an SM, to find room beside lora_down_kernel's: 300 rows of rank 24, 4096 x
+// 4096, 25.3 us, else 35.3.
 template <int CG, int TN, int MODE>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(384, MODE == kGroupLora ? 2 : 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                    const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmU,
                    const __grid_constant__ CUtensorMap tmH, const __grid_constant__ GroupTails<MODE> tails, const GroupParams p) {
@@ -454,6 +505,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t bar_tfull = bar_empty + 8 * C::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    volatile int32_t *stage_apart = reinterpret_cast<volatile int32_t *>(smem + C::OFF_APART);
     int32_t *start = reinterpret_cast<int32_t *>(smem + C::OFF_START);
     int32_t *tiles = reinterpret_cast<int32_t *>(smem + C::OFF_TILES);
 
@@ -498,6 +550,19 @@ __global__ void __launch_bounds__(384, 1)
     auto rank_tiles = [&](const GroupTile &w) {
         return MODE == kGroupLora && chosen[w.group] >= 0 ? p.rank_pad / 64 * 2 : 0;
     };
+    // what DOWN has left of a tile's rows, and whether its ranks have an accumulator of their own.  Asked for
+    // at a tile's start and looked at near its end, the answer costs nothing (4100 tokens in fp16 115 us, else 117)
+    constexpr int FLAGS = MODE == kGroupLora ? TN / 32 : 1;
+    auto ask_scaled = [&](const GroupTile &w, int32_t (&some)[FLAGS]) {
+#pragma unroll
+        for (int j = 0; j < FLAGS; ++j) some[j] = j * 32 < w.n ? p.some_scaled[w.j0 + j * 32] : 0;
+    };
+    auto any_scaled = [](const int32_t (&some)[FLAGS]) {
+        int32_t any = 0;
+#pragma unroll
+        for (int j = 0; j < FLAGS; ++j) any |= some[j];
+        return any;
+    };
     // N of a tile's MMAs; a pair's CTAs hold half of these rows of Q each
     auto columns_of = [](const GroupTile &w) { return (w.n + 16 * CG - 1) / (16 * CG) * (16 * CG); };
 
@@ -513,6 +578,9 @@ __global__ void __launch_bounds__(384, 1)
                 const int boxes = (columns_of(w) / CG + C::Q_BOX - 1) / C::Q_BOX;  // of Q, in each CTA
                 // of DOWN's P only the ranks that there are
                 const uint32_t bytes = (MODE == kGroupDown ? p.rank * 128u : C::P_BYTES) + static_cast<uint32_t>(boxes * C::Q_BOX) * 128u;
+                const bool ask = MODE == kGroupLora && !p.bf16 && leader && all_tiles > k_tiles, asked = ask && waited;
+                int32_t some[FLAGS];
+                if (asked) ask_scaled(w, some);
                 for (int kt = 0; kt < all_tiles; ++kt) {
                     if (!wait_bounded(bar_empty + 8 * ring.stage, ring.phase, abort_flag, p.timeout_ns,
                                       kWaitProducer, seq)) {
@@ -526,6 +594,15 @@ __global__ void __launch_bounds__(384, 1)
                         load_sum_rows<CG>(p, tmP, tmQ, tails, w, r, i0, j0, boxes, leader, sp, sq, full);
                         ring.advance();
                         continue;
+                    }
+                    if constexpr (MODE == kGroupLora) {
+                        if (kt >= k_tiles) {
+                            if (!waited) ptx::griddep_wait();
+                            waited = true;
+                            if (kt == k_tiles && ask && !asked) ask_scaled(w, some);
+                            // the issuer reads it behind the stage's barrier
+                            if (kt == k_tiles && leader) stage_apart[s] = ask ? any_scaled(some) : 0;
+                        }
                     }
                     if (leader) ptx::mbar_arrive_expect_tx(full, CG * bytes);
                     if constexpr (CG == 2) full = ptx::mapa(full, 0);
@@ -545,8 +622,6 @@ __global__ void __launch_bounds__(384, 1)
                     };
                     if constexpr (MODE == kGroupLora) {
                         if (kt >= k_tiles) {
-                            if (!waited) ptx::griddep_wait();
-                            waited = true;
                             const int32_t c = (kt - k_tiles) / 2 * 64, rest = (kt - k_tiles) % 2 * p.rank_pad;
                             load_3d(sp, &tmU, c, i0, chosen[w.group]);
                             for (int b = 0; b < boxes; ++b) load_2d(sq + b * C::Q_BOX * 128, &tmH, rest + c, j0 + b * C::Q_BOX);
@@ -586,7 +661,8 @@ __global__ void __launch_bounds__(384, 1)
                 const int k_tiles = (w.r + 63) / 64, all_tiles = k_tiles + rank_tiles(w);
                 if (all_tiles == 0) continue;
                 const uint32_t idesc = group_idesc<CG, MODE>(columns_of(w), p.bf16);
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc.stage * TN);
+                uint32_t d = tmem_base + static_cast<uint32_t>(acc.stage * TN);
+                bool apart = false;
                 if (!wait_bounded(bar_tempty + 8 * acc.stage, acc.phase, abort_flag, p.timeout_ns, kWaitMma,
                                   seq)) {
                     break;
@@ -602,15 +678,32 @@ __global__ void __launch_bounds__(384, 1)
                     const int s = ring.stage;
                     constexpr bool kMnP = MODE == kGroupNN || MODE == kGroupTN, kMnQ = MODE == kGroupTN;
                     const int left = kt < k_tiles ? w.r - kt * 64 : p.rank - (kt - k_tiles) / 2 * 64;
+                    if constexpr (MODE == kGroupLora) {
+                        if (kt == k_tiles && stage_apart[s]) {
+                            apart = true;
+                            PipelineState other = acc;
+                            other.advance();
+                            if (!wait_bounded(bar_tempty + 8 * other.stage, other.phase, abort_flag, p.timeout_ns, kWaitMma, seq)) {
+                                ok = false;
+                                break;
+                            }
+                            ptx::tcgen05_fence_after();
+                            d = tmem_base + static_cast<uint32_t>(other.stage * TN);
+                        }
+                    }
                     ptxg::mma_stage<CG, kMnP ? 128 : 2, kMnQ ? 128 : 2>(
                         d, p_low + static_cast<uint32_t>(s * (C::P_BYTES >> 4)), q_low + static_cast<uint32_t>(s * (C::Q_BYTES >> 4)),
-                        idesc, left >= 64 ? 4 : (left + 15) / 16, kt == 0);
+                        idesc, left >= 64 ? 4 : (left + 15) / 16, kt == 0 || (apart && kt == k_tiles));
                     ptx::mma_commit<CG>(bar_empty + 8 * s, 0x3);
                     ring.advance();
                 }
                 if (!ok) break;
                 ptx::mma_commit<CG>(bar_tfull + 8 * acc.stage, 0x3);
                 acc.advance();
+                if (apart) {
+                    ptx::mma_commit<CG>(bar_tfull + 8 * acc.stage, 0x3);
+                    acc.advance();
+                }
             }
             ptx::mma_commit<CG>(bar_drain, 0x1);
             wait_bounded(bar_drain, 0, abort_flag, p.timeout_ns, kWaitMma, 0xFFFFFFFFu, false);
@@ -632,6 +725,7 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
         PipelineState acc(2, 0u);
+        bool waited = false;
         uint32_t seq = 0;
         for (TileWalk walk(cluster, clusters, p.turn); walk.t() < total; walk.next(), ++seq) {
             const GroupTile w = tile_of(walk.t());
@@ -644,6 +738,13 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 continue;
             }
+            const bool ask = MODE == kGroupLora && !p.bf16 && rank_tiles(w) > 0, asked = ask && waited;
+            bool apart = false;
+            if (asked) {  // before the tile's wait, not behind it
+                int32_t some[FLAGS];
+                ask_scaled(w, some);
+                apart = any_scaled(some) != 0;
+            }
             bool failed = false;
             if (lane == 0) {
                 failed = !wait_bounded(bar_tfull + 8 * acc.stage, acc.phase, abort_flag, p.timeout_ns,
@@ -653,22 +754,71 @@ __global__ void __launch_bounds__(384, 1)
             ptx::tcgen05_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc.stage * TN);
             const int chunks = (w.n + 31) / 32;
+            PipelineState other = acc;  // LORA: the accumulator of ranks apart
+            if constexpr (MODE == kGroupLora) {
+                if (ask && !asked) {  // DOWN has ended, as the tile's sums have come
+                    ptx::griddep_wait();
+                    waited = true;
+                    int32_t some[FLAGS];
+                    ask_scaled(w, some);
+                    apart = any_scaled(some) != 0;
+                }
+                if (apart) {
+                    other.advance();
+                    if (lane == 0) failed = !wait_bounded(bar_tfull + 8 * other.stage, other.phase, abort_flag, p.timeout_ns, kWaitEpilogue, seq);
+                    if (ptxg::any_of_128(barrier, failed)) break;
+                    ptx::tcgen05_fence_after();
+                }
+            }
             if constexpr (MODE == kGroupDown) {
                 // a lane a rank: h and what its rounding left, zeros up to a whole 16
                 const int32_t padded = (p.rank + 15) / 16 * 16, i = quarter * 32 + lane;
                 const float scale = p.scales ? p.scales[chosen[w.group]] : 1.f;
                 uint16_t *to = out + static_cast<int64_t>(w.j0) * p.out_row + i;
 #pragma unroll 1
-                for (int c = team; c < chunks && quarter * 32 < padded; c += 2) {
+                for (int c = team; c < chunks; c += 2) {
                     uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(taddr + c * 32, v);
-                    ptx::tmem_wait_ld();
+                    const bool some = quarter * 32 < padded;
+                    if (some) {
+                        ptx::tmem_ld_32x32b_x32(taddr + c * 32, v);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * scale);
+                    }
+                    float by = 1.f;  // of fp16: what row c * 32 + lane is held times
+                    uint32_t scaled = 0;  // rows for which that is not 1
+                    if (!p.bf16) {
+                        uint32_t top = 0;
+                        if (some) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const uint32_t t = __reduce_max_sync(0xffffffffu, i < p.rank ? finite_bits(__uint_as_float(v[j])) : 0u);
+                                if (lane == j) top = t;
+                            }
+                        }
+                        // the warps have 32 ranks each; the team's staging buffer is not used else
+                        volatile uint32_t *tops = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_D + team * C::BUF);
+                        tops[quarter * 32 + lane] = top;
+                        ptxg::sync_128(barrier);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) top = top > tops[q * 32 + lane] ? top : tops[q * 32 + lane];
+                        const bool there = c * 32 + lane < w.n;
+                        const int e = row_exponent(top);
+                        by = power_of_two(-e);
+                        scaled = __ballot_sync(0xffffffffu, there && e != 0);
+                        if (quarter == 0 && there) p.row_scale[w.j0 + c * 32 + lane] = power_of_two(e);
+                        if (quarter == 0 && lane == 0) p.some_scaled[w.j0 + c * 32] = scaled != 0u;
+                    }
+                    if (!some) continue;
+                    if (scaled != 0u) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * __shfl_sync(0xffffffffu, by, j));
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         if (c * 32 + j >= w.n || i >= padded) continue;
-                        const float h = i < p.rank ? __uint_as_float(v[j]) * scale : 0.f;
                         uint16_t high, low;
-                        split_16(p.bf16, h, &high, &low);
+                        split_16(p.bf16, i < p.rank ? __uint_as_float(v[j]) : 0.f, &high, &low);
                         to[(c * 32 + j) * p.out_row] = high;
                         to[(c * 32 + j) * p.out_row + p.rank_pad] = low;
                     }
@@ -684,6 +834,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (lane == 0) {
                         if constexpr (CG == 2) {
                             ptxg::mbar_arrive_cluster_relaxed(tempty + 8 * acc.stage);
+                            if (apart) ptxg::mbar_arrive_cluster_relaxed(tempty + 8 * other.stage);
                         } else {
                             ptx::mbar_arrive(tempty + 8 * acc.stage);
                         }
@@ -696,6 +847,13 @@ __global__ void __launch_bounds__(384, 1)
                 ptxg::tmem_ld_16x256b_x4(taddr + c * 32, lo);
                 ptxg::tmem_ld_16x256b_x4(taddr + (16u << 16) + c * 32, hi);
                 ptx::tmem_wait_ld();
+                if constexpr (MODE == kGroupLora) {
+                    if (apart) {
+                        const uint32_t ranks = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(other.stage * TN + c * 32);
+                        add_scaled(ranks, p.row_scale + w.j0 + c * 32, w.n - c * 32, lane, lo);
+                        add_scaled(ranks + (16u << 16), p.row_scale + w.j0 + c * 32, w.n - c * 32, lane, hi);
+                    }
+                }
                 if (c + 2 >= chunks) hand_over();
                 const uint32_t buf = base + C::OFF_D + team * C::BUF;
                 if (tid == 0) ptx::bulk_wait_group_read<0>();  // what was in the buffer has left it
@@ -761,6 +919,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
             acc.advance();
+            if (apart) acc.advance();
             }
         }
         if (tid == 0) ptx::bulk_wait_group_read<0>();

@@ -103,7 +103,9 @@ def gemm_lora_nt(x, W, down, up, offsets, adapters, D=None, *, scales=None, stre
     x rows x K, W N x K, down adapters x rank x K, up adapters x N x rank, D rows x N; rank a multiple
     of 8 up to 128; ``adapters`` int32, ``scales`` float32 (None: 1), both on the device, one for each
     request and each adapter.  An adapter out of range (-1) and rows without a request have the
-    shared product alone.  No row's result depends on another row's adapter.
+    shared product alone.  No row's result depends on another row's adapter.  Between its two products
+    scales[a]·x[r]·down[a]ᵀ is held, whatever its size, to 2⁻¹⁶ of itself (bfloat16) or 2⁻²² of the row's
+    largest (float16); the sum is fp32.
     """
     if stream is None and options is None:
         return _linear._native.gemm_lora_nt(x, W, down, up, offsets, adapters, D, scales, 0)

@@ -82,9 +82,9 @@ int grouped_gemm_tn(const void *dD, int64_t ldd, const void *A, int64_t lda, con
  * for the rows r of request e (offsets as above), a = adapters[e] (int32, DEVICE
  * memory); without the second term where a is not in [0, adapter_count) and for rows
  * without a request.  x rows x K, W N x K, down adapter_count matrices of rank x K,
- * up of N x rank, scales fp32 in DEVICE memory (NULL: 1).  scales * (x * down^T) is held
- * as two 16-bit numbers (16 bits of it for LINEAR_BF16, 22 for LINEAR_F16, where it must
- * be below 65520), the sum fp32, D rounded once.  rank is a multiple of 8 up to 128.
+ * up of N x rank, scales fp32 in DEVICE memory (NULL: 1).  scales * (x * down^T), any finite
+ * fp32 number, is held as two 16-bit numbers: of LINEAR_BF16 to 2^-16 of itself, of
+ * LINEAR_F16 to 2^-22 of its row's largest.  The sum is fp32, D rounded once.  rank is a multiple of 8 up to 128.
  * No row's result depends on another row's adapter.  `workspace`
  * (gemm_lora_workspace_size() bytes, 16-byte aligned, no initialisation, not shared
  * by calls that may overlap on the GPU) holds x * down^T; GEMM_ERR_SCRATCH_LIMIT if it

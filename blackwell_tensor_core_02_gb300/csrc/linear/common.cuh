@@ -379,14 +379,19 @@ inline int64_t span_bytes(int64_t rows, int64_t cols, int64_t stride, int64_t si
     return rows <= 0 || cols <= 0 ? 0 : ((rows - 1) * stride + cols) * size;
 }
 
-// Whether rows of `bytes` bytes, `stride` bytes apart, share memory between p and q.
+// Whether p's rows of p_bytes bytes and q's of q_bytes, p_stride and q_stride bytes apart, share memory.
 // Rows of one stride may lie between each other's (two slices of a wider matrix).
-inline bool rows_overlap(const void *p, const void *q, int64_t rows, int64_t bytes, int64_t p_stride, int64_t q_stride) {
-    if (!overlap(p, span_bytes(rows, bytes, p_stride, 1), q, span_bytes(rows, bytes, q_stride, 1))) return false;
-    if (p_stride != q_stride || p_stride < bytes) return true;
+inline bool rows_overlap(const void *p, int64_t p_bytes, int64_t p_stride, const void *q, int64_t q_bytes, int64_t q_stride,
+                         int64_t rows) {
+    if (!overlap(p, span_bytes(rows, p_bytes, p_stride, 1), q, span_bytes(rows, q_bytes, q_stride, 1))) return false;
+    if (p_stride != q_stride || p_stride < p_bytes || p_stride < q_bytes) return true;
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    // from a row of the one that begins first to the next of the other
     const int64_t apart = static_cast<int64_t>((a < b ? b - a : a - b) % static_cast<uintptr_t>(p_stride));
-    return apart < bytes || p_stride - apart < bytes;
+    return a < b ? apart < p_bytes || p_stride - apart < q_bytes : apart < q_bytes || p_stride - apart < p_bytes;
+}
+inline bool rows_overlap(const void *p, const void *q, int64_t rows, int64_t bytes, int64_t p_stride, int64_t q_stride) {
+    return rows_overlap(p, bytes, p_stride, q, bytes, q_stride, rows);
 }
 
 // The current device is a GB300 (checked once per device); its SM count.

@@ -55,11 +55,12 @@ struct Span {
     int64_t bytes;
 };
 
-// Whether an output shares memory with an input or another output.
+// Whether an output shares memory with an input or another output; not the first output with the first
+// input, whose rows may lie between each other's (rows_overlap()).
 template <int OUTS, int INS>
 bool any_overlap(const Span (&outs)[OUTS], const Span (&ins)[INS]) {
     for (int i = 0; i < OUTS; ++i) {
-        for (int j = 0; j < INS; ++j) {
+        for (int j = i == 0 ? 1 : 0; j < INS; ++j) {
             if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return true;
         }
         for (int j = 0; j < i; ++j) {

@@ -365,6 +365,11 @@ int64_t matrix_bytes(const Matrix &m) {
     return 2 * (one + (m.depth > 1 ? (m.depth - 1) * m.depth_stride : 0));
 }
 
+// Whether two matrices of as many rows share memory; rows of one stride may lie between each other's.
+bool rows_shared(const Matrix &m, const Matrix &n) {
+    return rows_overlap(m.ptr, 2 * m.cols, m.rows > 1 ? 2 * m.stride : 0, n.ptr, 2 * n.cols, n.rows > 1 ? 2 * n.stride : 0, m.rows);
+}
+
 // The checks that all three directions share, and the launch.
 int grouped(int mode, Matrix ragged, Matrix other, Matrix out, const void *offsets, int32_t offsets_type, int64_t rows,
             int64_t groups, int64_t N, int64_t K, int32_t type, int32_t zero_rest, void *stream,
@@ -389,7 +394,7 @@ int grouped(int mode, Matrix ragged, Matrix other, Matrix out, const void *offse
     }
     if (!aligned(offsets, offsets_type ? 8 : 4)) return GEMM_ERR_MISALIGNED;
     const int64_t out_bytes = matrix_bytes(out);
-    if (overlap(out.ptr, out_bytes, ragged.ptr, matrix_bytes(ragged)) ||
+    if ((mode == kGroupTN ? overlap(out.ptr, out_bytes, ragged.ptr, matrix_bytes(ragged)) : rows_shared(out, ragged)) ||
         overlap(out.ptr, out_bytes, other.ptr, matrix_bytes(other)) ||
         overlap(out.ptr, out_bytes, offsets, (groups + 1) * (offsets_type ? 8 : 4))) {
         return GEMM_ERR_INVALID_ARG;
@@ -622,7 +627,7 @@ int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const v
         const void *p;
         int64_t bytes;
     } outs[2] = {{D, matrix_bytes(l.D)}, {workspace, some ? gemm_lora_workspace_size(rows, rank) : 0}},
-      ins[7] = {{x, matrix_bytes(l.x)}, {W, matrix_bytes(l.W)}, {down, some ? matrix_bytes(l.down) : 0},
+      ins[6] = {{W, matrix_bytes(l.W)}, {down, some ? matrix_bytes(l.down) : 0},
                 {up, some ? matrix_bytes(l.up) : 0}, {offsets, (requests + 1) * (offsets_type ? 8 : 4)},
                 {adapters, requests * 4}, {scales, adapter_count * 4}};
     for (const auto &out : outs) {
@@ -630,7 +635,10 @@ int gemm_lora_nt(const void *x, int64_t ldx, const void *W, int64_t ldw, const v
             if (overlap(out.p, out.bytes, in.p, in.bytes)) return GEMM_ERR_INVALID_ARG;
         }
     }
-    if (overlap(outs[0].p, outs[0].bytes, outs[1].p, outs[1].bytes)) return GEMM_ERR_INVALID_ARG;
+    if (rows_shared(l.D, l.x) || overlap(workspace, outs[1].bytes, x, matrix_bytes(l.x)) ||
+        overlap(outs[0].p, outs[0].bytes, outs[1].p, outs[1].bytes)) {
+        return GEMM_ERR_INVALID_ARG;
+    }
     Call c = {};
     st = gb300_sms(&c.sms);
     if (st != GEMM_OK) return st;

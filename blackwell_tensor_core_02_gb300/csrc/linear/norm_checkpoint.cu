@@ -435,7 +435,7 @@ int norm_checkpoint_forward(const void *x, int64_t x_stride, const void *weight,
     if (rows == 1 || !y) y_stride = 0;
     const Span outs[4] = {{y, y ? span_bytes(rows, cols, y_stride, size) : 0}, {codes, rows * cols}, {scales, rows * blocks}, {rstd, rows * 4}},
                ins[3] = {{x, span_bytes(rows, cols, x_stride, size)}, {weight, cols * wsize}, {bias, cols * wsize}};
-    if (any_overlap(outs, ins)) return GEMM_ERR_INVALID_ARG;
+    if (rows_overlap(y, x, rows, cols * size, y_stride * size, x_stride * size) || any_overlap(outs, ins)) return GEMM_ERR_INVALID_ARG;
     int sms = 0;
     const int st = gb300_sms(&sms);
     if (st != GEMM_OK) return st;
@@ -459,7 +459,7 @@ int norm_checkpoint_restore(const void *codes, const void *scales, const void *w
     if (rows == 1) y_stride = 0;
     const Span outs[1] = {{y, span_bytes(rows, cols, y_stride, size)}},
                ins[4] = {{codes, rows * cols}, {scales, rows * blocks}, {weight, cols * wsize}, {bias, cols * wsize}};
-    if (any_overlap(outs, ins)) return GEMM_ERR_INVALID_ARG;
+    if (overlap(y, outs[0].bytes, codes, rows * cols) || any_overlap(outs, ins)) return GEMM_ERR_INVALID_ARG;
     int sms = 0;
     const int st = gb300_sms(&sms);
     if (st != GEMM_OK) return st;

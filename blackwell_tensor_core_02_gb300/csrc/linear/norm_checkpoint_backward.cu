@@ -406,7 +406,7 @@ int norm_checkpoint_backward(const void *dy, int64_t dy_stride, const void *code
                           {workspace, need}},
                ins[5] = {{dy, span_bytes(rows, cols, dy_stride, size)}, {codes, rows * cols}, {scales, rows * blocks},
                          {weight, cols * wsize}, {rstd, rows * 4}};
-    if (any_overlap(outs, ins)) return GEMM_ERR_INVALID_ARG;
+    if (rows_overlap(dx, dy, rows, cols * size, dx_stride * size, dy_stride * size) || any_overlap(outs, ins)) return GEMM_ERR_INVALID_ARG;
     int sms = 0;
     const int st = gb300_sms(&sms);
     if (st != GEMM_OK) return st;

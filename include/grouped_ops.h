@@ -13,7 +13,8 @@
  * Types are LINEAR_F16 and LINEAR_BF16; the sums are fp32, results are rounded
  * once.  Widths (N, K) and strides are multiples of 8, pointers 16-byte aligned,
  * row strides at least the rows' width and strides of matrices at least a matrix's
- * extent; up to 1024 groups.
+ * extent; up to 1024 groups.  Rows of operands and results may lie between each
+ * other's at one stride (slices of one wider matrix).
  */
 #ifndef GROUPED_OPS_H
 #define GROUPED_OPS_H

@@ -104,14 +104,14 @@ class PreNormExperts:
         place = torch.empty_like(order).scatter_(0, order, torch.arange(order.numel(), device=order.device))
         bounds = torch.arange(self.weights.shape[0] + 1, device=chosen.device, dtype=experts.dtype)
         offsets = torch.searchsorted(experts[order], bounds)
-        return order // chosen.shape[1], place, offsets
+        return order // max(chosen.shape[1], 1), place, offsets
 
     def forward(self, x, chosen, gates):
         """(y, what ``backward`` needs)."""
         h, rows, rstd = g.layer_norm_checkpoint(x, self.scale, self.shift, self.eps)
         token, place, offsets = self.route(chosen)
         out = g.grouped_gemm_nt(h[token], self.weights, offsets)
-        y = (out[place].view(*chosen.shape, -1).float() * gates.float()[..., None]).sum(1).to(x.dtype)
+        y = (out[place].view(*chosen.shape, out.shape[1]).float() * gates.float()[..., None]).sum(1).to(x.dtype)
         return y, (rows, rstd, token, place, offsets, gates)
 
     def backward(self, dy, kept):
@@ -123,7 +123,7 @@ class PreNormExperts:
         dgates = (dh.float() * h.float()).sum(1)[place].view(gates.shape)
         row_gates = torch.empty_like(gates).view(-1).scatter_(0, place, gates.reshape(-1))
         dweights = g.grouped_gemm_tn((dout.float() * row_gates.float()[:, None]).to(dy.dtype), h, offsets)
-        dh = (dh[place].view(*gates.shape, -1).float() * gates.float()[..., None]).sum(1).to(dy.dtype)
+        dh = (dh[place].view(*gates.shape, dh.shape[1]).float() * gates.float()[..., None]).sum(1).to(dy.dtype)
         dx, dscale, dshift = g.layer_norm_backward_checkpoint(dh, rows, self.scale, rstd)
         return dx, dweights, dscale, dshift, dgates.to(gates.dtype)
 

@@ -1,0 +1,37 @@
+"""The layers of prenorm.py at their edges."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+def _randn(*shape, seed, dtype, size=1.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=gen, device="cuda") * size).to(dtype)
+
+
+def _inputs(tokens, top, experts, seed=4, dtype=torch.bfloat16):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    chosen = torch.rand(tokens, experts, generator=gen, device="cuda").topk(top).indices
+    gates = torch.rand(tokens, top, generator=gen, device="cuda").softmax(1)
+    return _randn(tokens, 256, seed=1, dtype=dtype), _randn(tokens, 128, seed=2, dtype=dtype), chosen, gates
+
+
+def _step(layer, x, dy, chosen, gates):
+    y, kept = layer.forward(x, chosen, gates)
+    return (y, *layer.backward(dy, kept))
+
+
+def test_experts_without_tokens(gpu_lib):
+    """No tokens, or no expert for any: results of those shapes, gradients of the parameters 0."""
+    from blackwell_tensor_core_02_gb300 import prenorm
+
+    layer = prenorm.make_experts(256, 128, 4, seed=3)
+    for tokens, top in ((0, 2), (5, 0)):
+        x, dy, _, _ = _inputs(tokens, 2, 4)
+        chosen = torch.zeros(tokens, top, dtype=torch.int64, device="cuda")
+        y, dx, dweights, dscale, dshift, dgates = _step(layer, x, dy, chosen, torch.zeros(tokens, top, device="cuda"))
+        assert y.shape == (tokens, 128) and dx.shape == x.shape and dgates.shape == (tokens, top)
+        assert dweights.shape == layer.weights.shape
+        assert not any(bool(t.any()) for t in (y, dx, dweights, dscale, dshift, dgates))

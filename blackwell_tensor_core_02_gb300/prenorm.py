@@ -121,7 +121,7 @@ class PreNormExperts:
         dout = dy[token]
         dh = g.grouped_gemm_nn(dout, self.weights, offsets)                 # before the gates
         dgates = (dh.float() * h.float()).sum(1)[place].view(gates.shape)
-        row_gates = torch.empty_like(gates).view(-1).scatter_(0, place, gates.reshape(-1))
+        row_gates = gates.new_empty(gates.numel()).scatter_(0, place, gates.reshape(-1))
         dweights = g.grouped_gemm_tn((dout.float() * row_gates.float()[:, None]).to(dy.dtype), h, offsets)
         dh = (dh[place].view(*gates.shape, dh.shape[1]).float() * gates.float()[..., None]).sum(1).to(dy.dtype)
         dx, dscale, dshift = g.layer_norm_backward_checkpoint(dh, rows, self.scale, rstd)

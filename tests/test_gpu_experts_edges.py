@@ -35,3 +35,19 @@ def test_experts_without_tokens(gpu_lib):
         assert y.shape == (tokens, 128) and dx.shape == x.shape and dgates.shape == (tokens, top)
         assert dweights.shape == layer.weights.shape
         assert not any(bool(t.any()) for t in (y, dx, dweights, dscale, dshift, dgates))
+
+
+def test_gates_and_choices_of_any_layout(gpu_lib):
+    """Transposed, sliced and expanded gates and choices: the results of contiguous ones."""
+    from blackwell_tensor_core_02_gb300 import prenorm
+
+    layer = prenorm.make_experts(256, 128, 4, seed=3)
+    x, dy, chosen, gates = _inputs(40, 2, 4)
+    want = _step(layer, x, dy, chosen, gates)
+    wide = torch.full((40, 5), 7.0, device="cuda")
+    wide[:, 1:3] = gates
+    for c, w in ((chosen.t().contiguous().t(), gates), (chosen, gates.t().contiguous().t()), (chosen, wide[:, 1:3])):
+        assert all(torch.equal(a, b) for a, b in zip(_step(layer, x, dy, c, w), want))
+    even = torch.full((1, 1), 0.5, device="cuda")
+    got, want = (_step(layer, x, dy, chosen, w) for w in (even.expand(40, 2), even.repeat(40, 2)))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

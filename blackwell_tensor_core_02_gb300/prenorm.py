@@ -99,10 +99,10 @@ class PreNormExperts:
     def route(self, chosen):
         """(token of each grouped row, place of each token's row among them, the groups' offsets); an
         expert out of range counts as none: its rows stand before or behind the groups."""
-        experts = chosen.reshape(-1)
+        experts = chosen.reshape(-1).long()  # small types do not hold the number of experts
         order = experts.argsort(stable=True)
         place = torch.empty_like(order).scatter_(0, order, torch.arange(order.numel(), device=order.device))
-        bounds = torch.arange(self.weights.shape[0] + 1, device=chosen.device, dtype=experts.dtype)
+        bounds = torch.arange(self.weights.shape[0] + 1, device=chosen.device)
         offsets = torch.searchsorted(experts[order], bounds)
         return order // max(chosen.shape[1], 1), place, offsets
 

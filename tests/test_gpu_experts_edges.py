@@ -51,3 +51,17 @@ def test_gates_and_choices_of_any_layout(gpu_lib):
     even = torch.full((1, 1), 0.5, device="cuda")
     got, want = (_step(layer, x, dy, chosen, w) for w in (even.expand(40, 2), even.repeat(40, 2)))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.uint8, torch.int16, torch.int32])
+def test_choices_of_any_whole_type(gpu_lib, dtype):
+    """Numbers of experts that the choices' type just holds, or does not: 127 is the last of 128."""
+    from blackwell_tensor_core_02_gb300 import prenorm
+
+    for experts in (128, 256):
+        layer = prenorm.make_experts(256, 16, experts, seed=3)
+        x, dy, chosen, gates = _inputs(40, 2, 128)
+        dy = dy[:, :16].contiguous()
+        chosen[7, 0] = 127
+        want = _step(layer, x, dy, chosen, gates)
+        assert all(torch.equal(a, b) for a, b in zip(_step(layer, x, dy, chosen.to(dtype), gates), want))

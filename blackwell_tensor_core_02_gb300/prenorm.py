@@ -34,7 +34,8 @@ import blackwell_tensor_core_02_gb300 as g
 
 
 class PreNormLinear:
-    """y = layer_norm(x; scale, shift)·Wᵀ for x (tokens × width), W (out × width), all fp16.
+    """y = layer_norm(x; scale, shift)·Wᵀ for x (tokens × width), W (out × width), in fp16; scale and
+    shift have that type or float32, or are None.
 
     ``forward``/``backward`` are a training step's two passes; ``quantize`` makes the 4-bit copy of
     W that ``serve`` uses.  Widths, outputs and, in ``backward``, tokens are multiples of 8
@@ -59,7 +60,7 @@ class PreNormLinear:
         dh = g.gemm_f16_nt(dy, self.weight.t().contiguous())                # dy·W
         if self.checkpoint:
             rows, rstd = kept
-            h = g.layer_norm_restore(rows, self.scale, self.shift)
+            h = g.layer_norm_restore(rows, self.scale, self.shift, dh.dtype)
             dx, dscale, dshift = g.layer_norm_backward_checkpoint(dh, rows, self.scale, rstd)
         else:
             x, h, mean, rstd = kept
@@ -88,9 +89,10 @@ class PreNormLinear:
 class PreNormExperts:
     """y[t] = Σ_j gates[t, j]·layer_norm(x[t]; scale, shift)·W[chosen[t, j]]ᵀ, W (experts × out × width).
 
-    x (tokens × width), scale, shift and W share float16 or bfloat16; ``chosen`` (tokens × top, integers)
-    names each token's experts, ``gates`` weighs them.  Widths and outputs are multiples of 8.  Between the
-    passes the normalised rows stay in 8 bits; each token's rows are gathered from them again.
+    x (tokens × width) and W share float16 or bfloat16, scale and shift have that type or float32, or are
+    None; ``chosen`` (tokens × top, integers) names each token's experts, ``gates`` weighs them.  Widths and
+    outputs are multiples of 8.  Between the passes the normalised rows stay in 8 bits; each token's rows
+    are gathered from them again.
     """
 
     def __init__(self, weights, scale, shift, eps: float = 1e-5):
@@ -117,7 +119,7 @@ class PreNormExperts:
     def backward(self, dy, kept):
         """(dx, dweights, dscale, dshift, dgates) for the gradient dy of y."""
         rows, rstd, token, place, offsets, gates = kept
-        h = g.layer_norm_restore(rows, self.scale, self.shift)[token]
+        h = g.layer_norm_restore(rows, self.scale, self.shift, dy.dtype)[token]
         dout = dy[token]
         dh = g.grouped_gemm_nn(dout, self.weights, offsets)                 # before the gates
         dgates = (dh.float() * h.float()).sum(1)[place].view(gates.shape)

@@ -65,3 +65,41 @@ def test_choices_of_any_whole_type(gpu_lib, dtype):
         chosen[7, 0] = 127
         want = _step(layer, x, dy, chosen, gates)
         assert all(torch.equal(a, b) for a, b in zip(_step(layer, x, dy, chosen.to(dtype), gates), want))
+
+
+@pytest.mark.parametrize("parameters", ["float32", "none"])
+def test_checkpoints_with_other_parameters(gpu_lib, parameters):
+    """Scale and shift in 32 bits, or none, as the layer without checkpoints takes them: the step runs, its
+    matrices' gradients are those of the restored rows, and the rest is near the layer's without."""
+    from blackwell_tensor_core_02_gb300 import prenorm
+
+    def change(layer):
+        if parameters == "none":
+            layer.scale = layer.shift = None
+        else:
+            layer.scale, layer.shift = layer.scale.float(), layer.shift.float()
+        return layer
+
+    layer, plain = (change(prenorm.make_layer(256, 128, seed=5, checkpoint=c)) for c in (True, False))
+    x, dy = _randn(64, 256, seed=1, dtype=torch.float16, size=1.5), _randn(64, 128, seed=2, dtype=torch.float16)
+    y, kept = layer.forward(x)
+    assert torch.equal(y, plain.forward(x)[0])
+    dx, dweight, dscale, dshift = layer.backward(dy, kept)
+    h = gpu_lib.layer_norm_restore(kept[0], layer.scale, layer.shift, torch.float16)
+    assert torch.equal(dweight, gpu_lib.gemm_f16_nt(dy.t().contiguous(), h.t().contiguous()))
+    # the kept rows' elements are off by 2^-4 of themselves at most (an eighth in the top binade)
+    for got, want in zip((dx, dscale, dshift), plain.backward(dy, plain.forward(x)[1])[:1] + plain.backward(dy, plain.forward(x)[1])[2:]):
+        assert (got is None) == (want is None)
+        if got is not None:
+            assert got.dtype == want.dtype
+            assert float((got.double() - want.double()).norm()) <= 0.125 * float(want.double().norm())
+    experts = change(prenorm.make_experts(256, 128, 4, seed=3))
+    x, dy, chosen, gates = _inputs(40, 2, 4)
+    y, kept = experts.forward(x, chosen, gates)
+    dx, dweights, dscale, dshift, dgates = experts.backward(dy, kept)
+    assert dx.dtype == dweights.dtype == torch.bfloat16 and bool(dweights.isfinite().all())
+    rows, _, token, _, offsets, _ = kept
+    h = gpu_lib.layer_norm_restore(rows, experts.scale, experts.shift, torch.bfloat16)
+    order = chosen.reshape(-1).argsort(stable=True)
+    weighed = (dy[token].float() * gates.reshape(-1)[order][:, None]).to(torch.bfloat16)
+    assert torch.equal(dweights, gpu_lib.grouped_gemm_tn(weighed, h[token], offsets))

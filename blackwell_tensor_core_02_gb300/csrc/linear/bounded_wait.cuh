@@ -19,7 +19,7 @@ enum : uint32_t { kWaitProducer = 1, kWaitMma = 2, kWaitEpilogue = 3 };
 // The wait of a thread that found nothing yet (out of line: the roles' loops are short, and
 // what bounds those of small tiles is a thread's instructions).
 static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint64_t timeout_ns,
-                                     uint32_t role, uint32_t seq, bool honor_abort) {
+                                            uint32_t role, uint32_t seq, bool honor_abort) {
     namespace ptx = gemm_f16::ptx;
     const uint64_t begun = ptx::globaltimer_ns();
     for (uint32_t turn = 1; !ptx::mbar_try_wait(bar, parity); ++turn) {

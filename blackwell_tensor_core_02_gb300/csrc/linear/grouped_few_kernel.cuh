@@ -524,10 +524,10 @@ __global__ void __launch_bounds__(192, MODE == kGroupLora ? 1 : 2)
 
 // h[row] = scale_a * x[row] * down_a^T for a row with an adapter, as two 16-bit numbers
 // (split_16; zeros up to a whole 16 ranks), for few rows.  256 threads: two warps a rank and
-// half of K each, four ranks at a time and `each` times four a CTA.  The chain of a single token is the launch, the
+// half of K each, RANKS ranks at a time and `each` times so many a CTA.  The chain of a single token is the launch, the
 // offsets and adapters, what down holds, and the sums; x is on its way from the start.
-// SCALED (fp16): the row's CTAs are a cluster, which agrees on the row's power of two (row_exponent()); of up
-// to 8, so RANKS, those at a time, may be 8 or 16 there, with 64 threads each.
+// SCALED (fp16): the row's CTAs are a cluster, which agrees on the row's power of two (row_exponent()).  RANKS: those
+// at a time, with 64 threads each.
 struct DownParams {
     const uint16_t *x, *down;
     int64_t x_row, down_row, down_matrix;
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(64 * RANKS) lora_down_kernel(const GroupParams
     // the first request that starts behind the row, and its predecessor's adapter
     __shared__ unsigned long long past;
     __shared__ float halves[RANKS];
-    __shared__ float held[SCALED ? 128 : 1];  // this CTA's ranks of h
+    __shared__ float held[2][SCALED ? 128 : 1];  // SCALED: both halves of this CTA's ranks of h
     __shared__ uint32_t top_here;
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
     const int64_t row = blockIdx.x;
@@ -611,27 +611,28 @@ __global__ void __launch_bounds__(64 * RANKS) lora_down_kernel(const GroupParams
         }
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (half && lane == 0) halves[warp % RANKS] = sum;
-        __syncthreads();
-        if (!half && lane == 0 && j < padded) {
-            const float h = j < p.rank ? (sum + halves[warp]) * (p.scales ? p.scales[a] : 1.f) : 0.f;
-            if constexpr (SCALED) {
-                held[q * RANKS + warp] = h;
-            } else {
+        if constexpr (SCALED) {
+            if (lane == 0) held[half][q * RANKS + warp % RANKS] = sum;
+        } else {
+            if (half && lane == 0) halves[warp % RANKS] = sum;
+            __syncthreads();
+            if (!half && lane == 0 && j < padded) {
+                const float h = j < p.rank ? (sum + halves[warp]) * (p.scales ? p.scales[a] : 1.f) : 0.f;
                 uint16_t *to = d.h + row * (2 * p.rank_pad) + j;
                 split_16(p.bf16, h, to, to + p.rank_pad);
             }
+            __syncthreads();
         }
-        __syncthreads();
     }
     if constexpr (SCALED) {
         const int first = static_cast<int>(blockIdx.y) * d.each * RANKS;
         const int count = padded - first < d.each * RANKS ? padded - first : d.each * RANKS;  // none: below 1
-        if (warp == 0) {
-            uint32_t top = 0;
-            for (int i = lane; i < count; i += 32) top = top > finite_bits(held[i]) ? top : finite_bits(held[i]);
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (lane == 0) top_here = top;
+        if (tid == 0) top_here = 0;
+        __syncthreads();
+        const float h = tid < count && first + tid < p.rank ? (held[0][tid] + held[1][tid]) * (p.scales ? p.scales[a] : 1.f) : 0.f;
+        if (warp * 32 < count) {  // up to four warps
+            const uint32_t t = __reduce_max_sync(0xffffffffu, finite_bits(h));
+            if (lane == 0) atomicMax(&top_here, t);
             __syncwarp();
         }
         ptx::cluster_sync();
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(64 * RANKS) lora_down_kernel(const GroupParams
         const int e = row_exponent(top);
         if (tid < count) {
             uint16_t *to = d.h + row * (2 * p.rank_pad) + first + tid;
-            split_16(false, held[tid] * power_of_two(-e), to, to + p.rank_pad);
+            split_16(false, h * power_of_two(-e), to, to + p.rank_pad);
         }
         if (blockIdx.y == 0 && tid == 0) p.row_scale[row] = power_of_two(e);
         __syncwarp();

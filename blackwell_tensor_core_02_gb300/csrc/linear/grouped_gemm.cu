@@ -452,28 +452,34 @@ struct Lora {
 //   2 of 64, 128                    29.1, 23.0    1 of 256, 64  34.0, 24.3
 constexpr int64_t kDownByCores = 12288;
 
-// Of fp16 a row's CTAs agree on the power of two that its h is held in, so they are a cluster, of up to 8, with
-// 8 or 16 ranks at a time where 4 would take more (one row of rank 128 11.2 us, in bf16, of 32 CTAs, 8.7; 64 of rank
-// 16 18.5 and 16.7); and tiles of 256 rows take h from the tensor cores' launch, which leaves what they ask of each 32 rows.
+// Of fp16 a row's CTAs agree on the power of two that its h is held in, so they are a cluster; and tiles of 256 rows
+// take h from the tensor cores' launch, which leaves what they ask of each 32 rows.
 int lora_down(Call &c, const Lora &l, const Choice &how) {
     if (c.p.groups == 0) return GEMM_OK;
     int st;
     if (l.rows * l.rank <= kDownByCores && (c.p.bf16 || how.tile != 256)) {
-        // three CTAs of 256 threads an SM, with as few ranks each as that allows
-        const int64_t padded = (l.rank + 15) / 16 * 16;
-        int ranks = 4;
-        while (!c.p.bf16 && padded > 8 * ranks && l.rows * (padded / ranks) <= 3 * c.sms) ranks *= 2;
-        const int64_t units = padded / ranks;
-        int64_t each = c.p.bf16 ? 1 : (units + 7) / 8;
-        while (each < units && l.rows * ((units + each - 1) / each) * ranks > 4 * 3 * c.sms) ++each;
-        const unsigned parts = static_cast<unsigned>((units + each - 1) / each);
+        // ranks at a time: 16 for one or two rows of many ranks, as a cluster has at most 8 CTAs (fp16, one row of
+        // rank 128: 9.6 us, with 4 10.7; one of rank 64 9.0 and 8.1, 4 of rank 128 12.5 and 11.4)
+        const bool many = !c.p.bf16 && l.rows <= 2 && l.rank > 64;
+        const int64_t units = (l.rank + 15) / 16 * 16 / (many ? 16 : 4);
+        int64_t each = 1, parts = 1;
+        if (c.p.bf16) {
+            // three CTAs an SM, with as few ranks each as that allows
+            while (each < units && l.rows * ((units + each - 1) / each) > 3 * c.sms) ++each;
+            parts = (units + each - 1) / each;
+        } else {
+            // clusters that all run at once, of CTAs with two units at least but where that makes them few: 64 rows of
+            // rank 64, 4 CTAs each 13.8 us, 6 18.6, 8 16.8; 128 of rank 32, 2 15.6, 4 18.4; one of rank 8, 2 7.7, 4 8.0
+            const int64_t least = many ? 1 : 2;
+            while (parts < 8 && 2 * least * parts <= units && 2 * parts * l.rows <= 256) parts *= 2;
+            each = (units + parts - 1) / parts;
+        }
         const DownParams d = {static_cast<const uint16_t *>(l.x.ptr), static_cast<const uint16_t *>(l.down.ptr), l.x.stride,
                               l.down.stride, l.down.depth_stride, static_cast<uint16_t *>(l.workspace), static_cast<int32_t>(each)};
-        const dim3 grid(static_cast<unsigned>(l.rows), parts);
-        st = c.p.bf16      ? launch(lora_down_kernel<false, 4>, grid, dim3(256), 0, c.stream, c.p, d)
-             : ranks == 4 ? launch_clusters(lora_down_kernel<true, 4>, grid, 256, dim3(1, parts), 0, c.stream, c.p, d)
-             : ranks == 8 ? launch_clusters(lora_down_kernel<true, 8>, grid, 512, dim3(1, parts), 0, c.stream, c.p, d)
-                          : launch_clusters(lora_down_kernel<true, 16>, grid, 1024, dim3(1, parts), 0, c.stream, c.p, d);
+        const dim3 grid(static_cast<unsigned>(l.rows), static_cast<unsigned>(parts)), cluster(1, static_cast<unsigned>(parts));
+        st = c.p.bf16 ? launch(lora_down_kernel<false, 4>, grid, dim3(256), 0, c.stream, c.p, d)
+             : many   ? launch_clusters(lora_down_kernel<true, 16>, grid, 1024, cluster, 0, c.stream, c.p, d)
+                      : launch_clusters(lora_down_kernel<true, 4>, grid, 256, cluster, 0, c.stream, c.p, d);
     } else {
         Call d = c;
         d.P = l.down;

@@ -135,6 +135,31 @@ bool encode_tails(const Call &c, GroupTails<MODE> *tails) {
     return true;
 }
 
+// Clusters of a kernel that run at once on the current device, asked once of each; 0: an error.  `fit` is the kernel's.
+template <typename K>
+int clusters_at_once(K *kernel, unsigned ctas, unsigned threads, size_t smem, std::atomic<int> (&fit)[kMaxDevices]) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    int clusters = fit[dev].load(std::memory_order_relaxed);
+    if (clusters > 0) return clusters;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters <= 0) {
+        cudaGetLastError();
+        return 0;
+    }
+    fit[dev].store(clusters, std::memory_order_relaxed);
+    return clusters;
+}
+
 template <int CG, int TN, int MODE>
 int launch_tile(const Call &c) {
     using C = GroupShape<CG, TN, MODE>;
@@ -166,27 +191,8 @@ int launch_tile(const Call &c) {
     int64_t grid = c.sms / CG;
     if constexpr (CG == 2) {
         static std::atomic<int> fit[kMaxDevices];
-        int dev = -1;
-        if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
-        int clusters = fit[dev].load(std::memory_order_relaxed);
-        if (clusters == 0) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(2);
-            cfg.blockDim = dim3(C::THREADS);
-            cfg.dynamicSmemBytes = C::SMEM_ALLOC;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 2;
-            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters <= 0) {
-                cudaGetLastError();
-                return GEMM_ERR_CUDA;
-            }
-            fit[dev].store(clusters, std::memory_order_relaxed);
-        }
-        grid = clusters;
+        grid = clusters_at_once(kernel, 2, C::THREADS, C::SMEM_ALLOC, fit);
+        if (grid == 0) return GEMM_ERR_CUDA;
     }
     if (!p.zero_rest && most < grid) grid = most;
     if (c.max_clusters > 0 && c.max_clusters < grid) grid = c.max_clusters;
@@ -194,11 +200,6 @@ int launch_tile(const Call &c) {
     p.turn = turn_of(MODE, p, TN, grid);
     return launch_cluster(kernel, CG * grid, C::THREADS, CG, C::SMEM_ALLOC, c.stream, tmP, tmQ, tmD, tmU, tmH, tails, p);
 }
-
-// CTAs with an SM each that run at once: a cluster lies within a GPC, and clusters of 8 and 4 leave
-// some SMs of one without.  Past that two share an SM: 1 x 2048 x 4096, 16 clusters of 8, 5.3 us, where
-// the last cluster waits for an SM alone 9.1.
-constexpr int alone_at_once(int cluster, int sms) { return cluster == 8 ? sms * 15 / 19 : (cluster == 4 ? sms * 18 / 19 : sms); }
 
 template <int TN, int KS, int MODE>
 int launch_few(const Call &c) {
@@ -226,7 +227,19 @@ int launch_few(const Call &c) {
         if (!encode(&tmU, c.U, 128) || !encode(&tmH, c.H, 16)) return GEMM_ERR_CUDA;
     }
     const int64_t tiles = most > 0 ? most : 1;  // one for the rows without a group
-    const int stages = MODE == kGroupLora || KS * tiles <= alone_at_once(KS, c.sms) ? C::ALONE : C::PAIRED;
+    int stages = C::ALONE;
+    if constexpr (MODE != kGroupLora) {
+        // An SM for each CTA while all clusters have that at once (one lies within a GPC, and clusters of 8 and 4 leave
+        // some SMs of one without).  Past that two share an SM: 1 x 2048 x 4096, 16 clusters of 8 where 15 have SMs
+        // of their own, 5.3 us; where the last waits for them 9.1.
+        int64_t alone = c.sms;
+        if constexpr (KS > 1) {
+            static std::atomic<int> fit[kMaxDevices];
+            alone = clusters_at_once(kernel, KS, C::THREADS, static_cast<size_t>(C::smem(C::ALONE)), fit);
+            if (alone == 0) return GEMM_ERR_CUDA;
+        }
+        if (tiles > alone) stages = C::PAIRED;
+    }
     return launch_cluster(kernel, KS * tiles, C::THREADS, KS, static_cast<size_t>(C::smem(stages)), c.stream, tmP, tmQ, tmU, tmH, tails,
                           p, stages);
 }
@@ -503,6 +516,7 @@ int lora_down(Call &c, const Lora &l, const Choice &how) {
 //   32 of 64, 16                    128, 1: 93.8                   256, pairs: 113
 //   64 of 4, 32, 1024 x 1024        16, 1: 19.1                    32, 2: 19.4    128, 8: 28.5
 //   1 of 1, 32, 2048 x 2048         16, 4: 6.2                     16, 8: 11.0
+// (Of 152 SMs clusters of 8 and 4 have 120 and 144 at once.)
 double lora_cost(const GroupParams &p, int sms, int tile, int split) {
     const int requests = p.groups > 0 ? p.groups : 1;
     const double rows = p.rows, each = rows / requests, k_tiles = (p.R + 63) / 64;
@@ -515,7 +529,7 @@ double lora_cost(const GroupParams &p, int sms, int tile, int split) {
         return (waves < 3 ? whole(waves) : waves + 0.5) * ((k_tiles + 2 * ranks) * (stage < 450 ? 450 : stage) + 1330) + 3500;
     }
     const int filled = tile < p.rows ? tile : p.rows, q = tile == 16 ? 16 : (filled + 31) / 32 * 32;
-    const int at_once = alone_at_once(split, sms);
+    const int at_once = split == 8 ? sms * 15 / 19 : (split == 4 ? sms * 18 / 19 : sms);
     const double turns = whole(static_cast<double>((static_cast<int64_t>(p.rows) + tile - 1) / tile * ((p.I + 127) / 128) * split) / at_once);
     const double stage = 1.6 * (128 + q);
     double pieces = 0;

@@ -145,3 +145,27 @@ def test_expanded_operands_are_refused(g):
         with pytest.raises(g.GemmError):
             bad()
     assert gref.clamp(s.offsets.tolist(), 9) == [0, 3, 4, 9]
+
+
+def test_first_calls_in_a_graph():
+    """A process whose first call of each operator is captured: tiles, clusters' sizes and shared memory are
+    asked for then, and the graph gives what eager calls do."""
+    import os
+    import subprocess
+    import sys
+
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "import torch, blackwell_tensor_core_02_gb300 as g\n"
+            "from test_gpu_new_ops_together import Step, same, F16, BF16\n"
+            "steps = [Step(1, F16, 1), Step(600, BF16, 2), Step(130, F16, 3)]\n"
+            "torch.cuda.synchronize()\n"
+            "graph = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(graph):\n"
+            "    got = [s.run(g) for s in steps]\n"
+            "graph.replay(); torch.cuda.synchronize()\n"
+            "kept = [[t.clone() for t in r] for r in got]\n"
+            "assert all(same(k, s.run(g)) for k, s in zip(kept, steps)) and g.grouped_device_status()[0] == 0\n"
+            % (os.path.dirname(here), here))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -842,84 +842,84 @@ __global__ void __launch_bounds__(384, MODE == kGroupLora ? 2 : 1)
                 };
                 if (chunks <= team) hand_over();
 #pragma unroll 1
-            for (int c = team; c < chunks; c += 2) {
-                uint32_t lo[16], hi[16];
-                ptxg::tmem_ld_16x256b_x4(taddr + c * 32, lo);
-                ptxg::tmem_ld_16x256b_x4(taddr + (16u << 16) + c * 32, hi);
-                ptx::tmem_wait_ld();
-                if constexpr (MODE == kGroupLora) {
-                    if (apart) {
-                        const uint32_t ranks = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(other.stage * TN + c * 32);
-                        add_scaled(ranks, p.row_scale + w.j0 + c * 32, w.n - c * 32, lane, lo);
-                        add_scaled(ranks + (16u << 16), p.row_scale + w.j0 + c * 32, w.n - c * 32, lane, hi);
-                    }
-                }
-                if (c + 2 >= chunks) hand_over();
-                const uint32_t buf = base + C::OFF_D + team * C::BUF;
-                if (tid == 0) ptx::bulk_wait_group_read<0>();  // what was in the buffer has left it
-                ptxg::sync_128(barrier);
-                // lane l: row l % 8 of matrix l / 8 (columns 8 (n + l / 16) on, lanes 8 (l / 8 % 2) on);
-                // 16-byte unit u of row j lies at u ^ j % 8
-                const uint32_t own = buf + static_cast<uint32_t>(quarter >> 1) * C::BOX +
-                                     static_cast<uint32_t>((lane & 7) + (lane >> 4) * 8) * 128u;
-                const uint32_t unit = static_cast<uint32_t>((quarter & 1) * 4 + (lane >> 3 & 1));
-                const uint32_t low = own + ((unit ^ (lane & 7u)) * 16u), high = own + (((unit + 2) ^ (lane & 7u)) * 16u);
-#pragma unroll
-                for (int n = 0; n < 4; n += 2) {
-                    ptxg::stmatrix_trans(low + n * 8 * 128, pack_pair(p.bf16, lo[4 * n], lo[4 * n + 1]),
-                                         pack_pair(p.bf16, lo[4 * n + 2], lo[4 * n + 3]),
-                                         pack_pair(p.bf16, lo[4 * n + 4], lo[4 * n + 5]),
-                                         pack_pair(p.bf16, lo[4 * n + 6], lo[4 * n + 7]));
-                    ptxg::stmatrix_trans(high + n * 8 * 128, pack_pair(p.bf16, hi[4 * n], hi[4 * n + 1]),
-                                         pack_pair(p.bf16, hi[4 * n + 2], hi[4 * n + 3]),
-                                         pack_pair(p.bf16, hi[4 * n + 4], hi[4 * n + 5]),
-                                         pack_pair(p.bf16, hi[4 * n + 6], hi[4 * n + 7]));
-                }
-                // By the copy engine, which needs no thread, where a tile's MMAs take longer than
-                // its epilogue: weights of 8 groups of 1024 rows, 4096 x 4096, 151 us, by threads
-                // 156.  By threads, which need not wait for it, where the epilogue is what takes
-                // the time: 32 groups of 16 rows, 1416 x 2040, 43 us, by the copy engine 51.
-                if ((MODE == kGroupTN || w.n - c * 32 >= 32) && w.r >= kLongSum) {
-                    ptx::fence_proxy_async_smem();
-                    ptxg::sync_128(barrier);
-                    if (tid == 0) {
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            if (width <= b * 64) continue;
-                            if constexpr (MODE == kGroupTN) {
-                                ptx::tma_store_3d(&tmD, buf + b * C::BOX, i0 + b * 64, w.j0 + c * 32, w.group);
-                            } else {
-                                ptx::tma_store_2d(&tmD, buf + b * C::BOX, i0 + b * 64, w.j0 + c * 32);
-                            }
+                for (int c = team; c < chunks; c += 2) {
+                    uint32_t lo[16], hi[16];
+                    ptxg::tmem_ld_16x256b_x4(taddr + c * 32, lo);
+                    ptxg::tmem_ld_16x256b_x4(taddr + (16u << 16) + c * 32, hi);
+                    ptx::tmem_wait_ld();
+                    if constexpr (MODE == kGroupLora) {
+                        if (apart) {
+                            const uint32_t ranks = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(other.stage * TN + c * 32);
+                            add_scaled(ranks, p.row_scale + w.j0 + c * 32, w.n - c * 32, lane, lo);
+                            add_scaled(ranks + (16u << 16), p.row_scale + w.j0 + c * 32, w.n - c * 32, lane, hi);
                         }
-                        ptx::bulk_commit_group();
                     }
-                    continue;
-                }
-                ptxg::sync_128(barrier);
-                // 16 threads a row, 16 bytes each; rows behind a group's end belong to the next
-                const uint32_t from = buf + static_cast<uint32_t>(x / 8) * C::BOX + static_cast<uint32_t>(y) * 128u +
-                                      ((static_cast<uint32_t>(x & 7) ^ (y & 7u)) * 16u);
-                uint16_t *to = at + (c * 32 + y) * p.out_row + x * 8;
-                const int32_t rows = x * 8 < width ? w.n - c * 32 - y : 0;
-                uint4 v[4];
+                    if (c + 2 >= chunks) hand_over();
+                    const uint32_t buf = base + C::OFF_D + team * C::BUF;
+                    if (tid == 0) ptx::bulk_wait_group_read<0>();  // what was in the buffer has left it
+                    ptxg::sync_128(barrier);
+                    // lane l: row l % 8 of matrix l / 8 (columns 8 (n + l / 16) on, lanes 8 (l / 8 % 2) on);
+                    // 16-byte unit u of row j lies at u ^ j % 8
+                    const uint32_t own = buf + static_cast<uint32_t>(quarter >> 1) * C::BOX +
+                                         static_cast<uint32_t>((lane & 7) + (lane >> 4) * 8) * 128u;
+                    const uint32_t unit = static_cast<uint32_t>((quarter & 1) * 4 + (lane >> 3 & 1));
+                    const uint32_t low = own + ((unit ^ (lane & 7u)) * 16u), high = own + (((unit + 2) ^ (lane & 7u)) * 16u);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = ptx::ld_shared_v4(from + k * 8 * 128);
+                    for (int n = 0; n < 4; n += 2) {
+                        ptxg::stmatrix_trans(low + n * 8 * 128, pack_pair(p.bf16, lo[4 * n], lo[4 * n + 1]),
+                                             pack_pair(p.bf16, lo[4 * n + 2], lo[4 * n + 3]),
+                                             pack_pair(p.bf16, lo[4 * n + 4], lo[4 * n + 5]),
+                                             pack_pair(p.bf16, lo[4 * n + 6], lo[4 * n + 7]));
+                        ptxg::stmatrix_trans(high + n * 8 * 128, pack_pair(p.bf16, hi[4 * n], hi[4 * n + 1]),
+                                             pack_pair(p.bf16, hi[4 * n + 2], hi[4 * n + 3]),
+                                             pack_pair(p.bf16, hi[4 * n + 4], hi[4 * n + 5]),
+                                             pack_pair(p.bf16, hi[4 * n + 6], hi[4 * n + 7]));
+                    }
+                    // By the copy engine, which needs no thread, where a tile's MMAs take longer than
+                    // its epilogue: weights of 8 groups of 1024 rows, 4096 x 4096, 151 us, by threads
+                    // 156.  By threads, which need not wait for it, where the epilogue is what takes
+                    // the time: 32 groups of 16 rows, 1416 x 2040, 43 us, by the copy engine 51.
+                    if ((MODE == kGroupTN || w.n - c * 32 >= 32) && w.r >= kLongSum) {
+                        ptx::fence_proxy_async_smem();
+                        ptxg::sync_128(barrier);
+                        if (tid == 0) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k, to += 8 * p.out_row) {
-                    if (k * 8 >= rows) continue;
-                    if constexpr (MODE == kGroupTN) {
-                        // matrices that are far more than L2 holds leave it first: 32 groups of 16
-                        // rows, 1416 x 2040, 41.8 us, else 42.7 (only zeros, of 16 matrices of 4096 x
-                        // 4096: 84.3, 6.4 TB/s, which is what writes get)
-                        __stcs(reinterpret_cast<uint4 *>(to), v[k]);
-                    } else {
-                        *reinterpret_cast<uint4 *>(to) = v[k];
+                            for (int b = 0; b < 2; ++b) {
+                                if (width <= b * 64) continue;
+                                if constexpr (MODE == kGroupTN) {
+                                    ptx::tma_store_3d(&tmD, buf + b * C::BOX, i0 + b * 64, w.j0 + c * 32, w.group);
+                                } else {
+                                    ptx::tma_store_2d(&tmD, buf + b * C::BOX, i0 + b * 64, w.j0 + c * 32);
+                                }
+                            }
+                            ptx::bulk_commit_group();
+                        }
+                        continue;
+                    }
+                    ptxg::sync_128(barrier);
+                    // 16 threads a row, 16 bytes each; rows behind a group's end belong to the next
+                    const uint32_t from = buf + static_cast<uint32_t>(x / 8) * C::BOX + static_cast<uint32_t>(y) * 128u +
+                                          ((static_cast<uint32_t>(x & 7) ^ (y & 7u)) * 16u);
+                    uint16_t *to = at + (c * 32 + y) * p.out_row + x * 8;
+                    const int32_t rows = x * 8 < width ? w.n - c * 32 - y : 0;
+                    uint4 v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = ptx::ld_shared_v4(from + k * 8 * 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k, to += 8 * p.out_row) {
+                        if (k * 8 >= rows) continue;
+                        if constexpr (MODE == kGroupTN) {
+                            // matrices that are far more than L2 holds leave it first: 32 groups of 16
+                            // rows, 1416 x 2040, 41.8 us, else 42.7 (only zeros, of 16 matrices of 4096 x
+                            // 4096: 84.3, 6.4 TB/s, which is what writes get)
+                            __stcs(reinterpret_cast<uint4 *>(to), v[k]);
+                        } else {
+                            *reinterpret_cast<uint4 *>(to) = v[k];
+                        }
                     }
                 }
-            }
-            acc.advance();
-            if (apart) acc.advance();
+                acc.advance();
+                if (apart) acc.advance();
             }
         }
         if (tid == 0) ptx::bulk_wait_group_read<0>();

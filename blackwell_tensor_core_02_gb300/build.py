@@ -41,6 +41,7 @@ def sources() -> list[str]:
 
 def linear_sources() -> list[str]:
     return sorted(glob.glob(os.path.join(LINEAR_CSRC, "*.cu")) + glob.glob(os.path.join(LINEAR_CSRC, "*.cuh")) +
+                  glob.glob(os.path.join(LINEAR_CSRC, "*.h")) +
                   glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
                   glob.glob(os.path.join(INCLUDE, "*.h")))
 

@@ -26,7 +26,7 @@
 // loaded in boxes of 16, 8, 4, 2 and 1 rows, and the rest of its last step, in such boxes
 // too, from behind the matrix, where the copy engine fills zeros.  (Cleared by a warp in
 // shared memory, between the load's arrival and the MMA, they came too late: 8 groups of
-// 1025 rows, 4096 x 4096, took 189 us, of 1024 153; so 157 to 163.)
+// 1025 rows, 4096 x 4096, took 189 us where those of 1024 took 153; so 152 and 146.)
 //
 // LORA and DOWN are the two launches of low-rank adapters beside a shared product, with
 // the rows of a request as a group.  DOWN leaves h = scale_a * x * down_a^T as two
@@ -52,6 +52,7 @@
 #include "../schedule.h"
 #include "bounded_wait.cuh"
 #include "common.cuh"
+#include "grouped_choice.h"
 #include "grouped_ops.h"
 
 namespace linear_ops {
@@ -176,8 +177,6 @@ __device__ __forceinline__ void sync_128(uint32_t barrier) {
 }
 
 }  // namespace ptxg
-
-enum GroupMode { kGroupNT = 0, kGroupNN = 1, kGroupTN = 2, kGroupLora = 3, kGroupDown = 4 };
 
 // CG: CTAs of a tile; TN: its columns j.  A CTA holds 128 rows of P and TN / CG of Q.
 template <int CG, int TN, int MODE>
@@ -876,9 +875,9 @@ __global__ void __launch_bounds__(384, MODE == kGroupLora ? 2 : 1)
                                              pack_pair(p.bf16, hi[4 * n + 6], hi[4 * n + 7]));
                     }
                     // By the copy engine, which needs no thread, where a tile's MMAs take longer than
-                    // its epilogue: weights of 8 groups of 1024 rows, 4096 x 4096, 151 us, by threads
-                    // 156.  By threads, which need not wait for it, where the epilogue is what takes
-                    // the time: 32 groups of 16 rows, 1416 x 2040, 43 us, by the copy engine 51.
+                    // its epilogue: weights of 8 groups of 1024 rows, 4096 x 4096, 146 us, by threads
+                    // 152.  By threads, which need not wait for it, where the epilogue is what takes
+                    // the time: 32 groups of 16 rows, 1416 x 2040, 41.9 us, by the copy engine 50.7.
                     if ((MODE == kGroupTN || w.n - c * 32 >= 32) && w.r >= kLongSum) {
                         ptx::fence_proxy_async_smem();
                         ptxg::sync_128(barrier);
@@ -910,8 +909,8 @@ __global__ void __launch_bounds__(384, MODE == kGroupLora ? 2 : 1)
                         if (k * 8 >= rows) continue;
                         if constexpr (MODE == kGroupTN) {
                             // matrices that are far more than L2 holds leave it first: 32 groups of 16
-                            // rows, 1416 x 2040, 41.8 us, else 42.7 (only zeros, of 16 matrices of 4096 x
-                            // 4096: 84.3, 6.4 TB/s, which is what writes get)
+                            // rows, 1416 x 2040, 41.9 us, else 42.2 (only zeros, of 16 matrices of 4096 x
+                            // 4096: 82 to 84, 6.4 TB/s, which is what writes get)
                             __stcs(reinterpret_cast<uint4 *>(to), v[k]);
                         } else {
                             *reinterpret_cast<uint4 *>(to) = v[k];

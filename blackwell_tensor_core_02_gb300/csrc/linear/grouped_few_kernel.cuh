@@ -635,14 +635,20 @@ __global__ void __launch_bounds__(64 * RANKS) lora_down_kernel(const GroupParams
             if (lane == 0) atomicMax(&top_here, t);
             __syncwarp();
         }
-        ptx::cluster_sync();
         uint32_t top = 0;
-        for (uint32_t s = 0; s < gridDim.y; ++s) {
-            uint32_t t;
-            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(t) : "r"(ptx::mapa(ptx::smem_u32(&top_here), s)) : "memory");
-            top = top > t ? top : t;
+        const bool alone = gridDim.y == 1;
+        if (alone) {
+            __syncthreads();
+            top = top_here;
+        } else {
+            ptx::cluster_sync();
+            for (uint32_t s = 0; s < gridDim.y; ++s) {
+                uint32_t t;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(t) : "r"(ptx::mapa(ptx::smem_u32(&top_here), s)) : "memory");
+                top = top > t ? top : t;
+            }
+            ptx::cluster_arrive();
         }
-        ptx::cluster_arrive();
         const int e = row_exponent(top);
         if (tid < count) {
             uint16_t *to = d.h + row * (2 * p.rank_pad) + first + tid;
@@ -650,7 +656,7 @@ __global__ void __launch_bounds__(64 * RANKS) lora_down_kernel(const GroupParams
         }
         if (blockIdx.y == 0 && tid == 0) p.row_scale[row] = power_of_two(e);
         __syncwarp();
-        ptx::cluster_wait();  // no CTA leaves while another reads its largest
+        if (!alone) ptx::cluster_wait();  // no CTA leaves while another reads its largest
     }
 }
 

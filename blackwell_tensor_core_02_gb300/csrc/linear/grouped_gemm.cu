@@ -394,28 +394,36 @@ int lora_down(Call &c, const Lora &l, const Choice &how) {
     if (c.p.groups == 0) return GEMM_OK;
     int st;
     if (l.rows * l.rank <= kDownByCores && (c.p.bf16 || how.tile != 256)) {
-        // ranks at a time: 16 for one or two rows of many ranks, as a cluster has at most 8 CTAs (fp16, one row of
-        // rank 128: 9.6 us, with 4 10.7; one of rank 64 9.0 and 8.1, 4 of rank 128 12.5 and 11.4)
-        const bool many = !c.p.bf16 && l.rows <= 2 && l.rank > 64;
-        const int64_t units = (l.rank + 15) / 16 * 16 / (many ? 16 : 4);
-        int64_t each = 1, parts = 1;
+        const int64_t padded = (l.rank + 15) / 16 * 16;
+        int64_t ranks = 4, each = 1, parts = padded / ranks;  // a CTA's at a time, how many times, CTAs of a row
         if (c.p.bf16) {
             // three CTAs an SM, with as few ranks each as that allows
-            while (each < units && l.rows * ((units + each - 1) / each) > 3 * c.sms) ++each;
-            parts = (units + each - 1) / each;
+            while (each < padded / ranks && l.rows * parts > 3 * c.sms) {
+                ++each;
+                parts = (padded / ranks + each - 1) / each;
+            }
+        } else if (l.rows <= 2) {
+            // the chain is what counts: all at once, in a cluster's 8 CTAs.  A stream of calls of one row, rank 16, 10.8 us
+            // (two CTAs with two turns 12.0, one 11.2), rank 64 11.0 (8 with two turns 12.7)
+            while (padded / ranks > 8) ranks *= 2;
+            parts = padded / ranks;
+        } else if (l.rank <= 16 && l.rows <= 32) {
+            // one CTA, which agrees with itself: 16 rows 11.7 us, clusters of 4 13.1
+            ranks = 16, parts = 1;
         } else {
-            // clusters that all run at once, of CTAs with two units at least but where that makes them few: 64 rows of
-            // rank 64, 4 CTAs each 13.8 us, 6 18.6, 8 16.8; 128 of rank 32, 2 15.6, 4 18.4; one of rank 8, 2 7.7, 4 8.0
-            const int64_t least = many ? 1 : 2;
-            while (parts < 8 && 2 * least * parts <= units && 2 * parts * l.rows <= 256) parts *= 2;
+            // clusters that all run at once, of CTAs with two turns at least: 64 rows of rank 64, 4 CTAs each 13.8 us, 6
+            // 18.6, 8 16.8; 128 of rank 32, 2 15.6, 4 18.4
+            const int64_t units = padded / ranks;
+            for (parts = 1; parts < 8 && 4 * parts <= units && 2 * parts * l.rows <= 256;) parts *= 2;
             each = (units + parts - 1) / parts;
         }
         const DownParams d = {static_cast<const uint16_t *>(l.x.ptr), static_cast<const uint16_t *>(l.down.ptr), l.x.stride,
                               l.down.stride, l.down.depth_stride, static_cast<uint16_t *>(l.workspace), static_cast<int32_t>(each)};
         const dim3 grid(static_cast<unsigned>(l.rows), static_cast<unsigned>(parts)), cluster(1, static_cast<unsigned>(parts));
-        st = c.p.bf16 ? launch(lora_down_kernel<false, 4>, grid, dim3(256), 0, c.stream, c.p, d)
-             : many   ? launch_clusters(lora_down_kernel<true, 16>, grid, 1024, cluster, 0, c.stream, c.p, d)
-                      : launch_clusters(lora_down_kernel<true, 4>, grid, 256, cluster, 0, c.stream, c.p, d);
+        st = c.p.bf16      ? launch(lora_down_kernel<false, 4>, grid, dim3(256), 0, c.stream, c.p, d)
+             : ranks == 16 ? launch_clusters(lora_down_kernel<true, 16>, grid, 1024, cluster, 0, c.stream, c.p, d)
+             : ranks == 8  ? launch_clusters(lora_down_kernel<true, 8>, grid, 512, cluster, 0, c.stream, c.p, d)
+                           : launch_clusters(lora_down_kernel<true, 4>, grid, 256, cluster, 0, c.stream, c.p, d);
     } else {
         Call d = c;
         d.P = l.down;

@@ -393,6 +393,7 @@ __device__ __forceinline__ void split_16(bool bf16, float h, uint16_t *high, uin
     uint32_t a, b;
     if (bf16) {
         Pair<__nv_bfloat16>::narrow(make_float2(h, 0.f), &a);
+        if ((a & 0x7fffu) == 0x7f80u && fabsf(h) < INFINITY) --a;  // past the largest bf16, whose rest the second one holds
         const float rest = h - Pair<__nv_bfloat16>::widen(&a).x;
         Pair<__nv_bfloat16>::narrow(make_float2(fabsf(rest) < INFINITY ? rest : 0.f, 0.f), &b);
     } else {

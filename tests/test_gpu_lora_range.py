@@ -132,3 +132,18 @@ def test_large_intermediate_values_of_both_types(g, dtype, value):
         else:
             assert bool((got[:, 0] == right).all())
         assert not bool(got[:, 1:].any())
+
+
+@pytest.mark.parametrize("path", PATHS, ids=PATH_IDS)
+@pytest.mark.parametrize("rows", [1, 130, 1700])
+def test_the_last_fp32_numbers_in_bf16(g, rows, path):
+    """h between bf16's largest and fp32's, which rounds to no bf16: 2^128 - 2^106; up takes 2^121 of it away, and D is off by a rounding (2^-8) and h's two (2^-16)."""
+    bf = torch.bfloat16
+    x, W = torch.ones(rows, 16, device="cuda", dtype=bf), torch.zeros(8, 16, device="cuda", dtype=bf)
+    down, up = torch.zeros(2, 8, 16, device="cuda", dtype=bf), torch.zeros(2, 8, 8, device="cuda", dtype=bf)
+    down[:, 0, 0], up[0, ::2, 0], up[1, ::2, 0] = 1.0, 2.0 ** -121, -(2.0 ** -121)
+    scales = torch.tensor([3.4e38, -3.4e38], device="cuda")
+    o, adapters = torch.tensor([0, rows // 2, rows], device="cuda"), torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    got = g.gemm_lora_nt(x, W, down, up, o, adapters, scales=scales, options=g.GroupedOptions(**path)).double()
+    value = float(scales[0].double()) * 2.0 ** -121
+    assert bool(((got[:, ::2] - value).abs() <= 2.0 ** -7 * value).all()) and not bool(got[:, 1::2].any())

@@ -13,7 +13,9 @@ in the manner of ``linear.py``: float16 and bfloat16, fp32 sums, one rounding; `
 ``offsets`` (int32 or int64, groups + 1 of them on the device): group e has the rows offsets[e] to
 offsets[e + 1] - 1.  No call reads them on the host.  Values are taken as at least 0, at most the
 number of rows and at least the one before.  Rows before the first offset and from the last on have no
-group.  N and K are multiples of 8, rows 16-byte aligned (any number of them); up to 1024 groups.
+group.  N and K are multiples of 8, rows 16-byte aligned (any number of them) and at least a row apart, so
+expanded operands are refused; results may lie between the operands' rows (slices of one matrix).  Up to
+1024 groups.
 """
 from __future__ import annotations
 
